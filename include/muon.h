@@ -65,6 +65,8 @@ typedef enum {
 #define MUON_FLAG_TIMEOUT 0x2u     /* a bounded device wait ran out; results are invalid */
 #define MUON_FLAG_MISALIGNED 0x4u  /* a pointer in a device pointer array was not 16 B aligned;
                                       that matrix was left untouched */
+#define MUON_FLAG_INDEX 0x8u       /* an expert number or an offset in a device array was out of
+                                      range or out of order; it was ignored or cut to the range */
 
 typedef enum { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype_t;
 
@@ -326,6 +328,168 @@ typedef struct {
 muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
                               const muon_adamw_hparams_t* hparams, uint32_t* device_flags,
                               muon_stream_t stream);
+
+/* ---- Gradients of a mixture-of-experts training step -----------------------
+ * The operators below produce gradients that muon_step_batched and
+ * muon_adamw_step consume: the router's balance loss with its counts and
+ * gradient, activations kept between the forward and the backward pass in 8
+ * bits, the gated feed-forward activation on them, and the experts' weight
+ * gradients.  The pages describe the optimizer alone and have no counterpart.
+ *
+ * Unlike the matrices of the step, their inputs need no alignment beyond
+ * their element size and no particular width unless an argument says so:
+ * where every row starts on a 16-byte boundary the kernels use wide accesses,
+ * elsewhere they take element-wise ones.  Strides are in elements. */
+
+/* Router balance loss.  Token t of a sequence s (of n_s valid tokens, N valid
+ * tokens in all) with logits l has the probabilities
+ *   softmax:  p_e = exp(l_e) / sum_j exp(l_j)
+ *   sigmoid:  p_e = sigma(l_e) / sum_j sigma(l_j)
+ * and was sent to the experts chosen[t][0..topk).  With c_se the number of
+ * choices of expert e in sequence s,
+ *   f_se = experts / (topk * n_s) * c_se           (1 = balanced)
+ *   loss = coef / N * sum_s sum_{t in s} sum_e f_se p_te,
+ * the mean of the sequences' losses weighted by their valid tokens.  f is a
+ * constant of the gradient:
+ *   dloss/dl_te = coef / N * p_te (f_se - sum_j f_sj p_tj)   [* (1 - sigma(l_te))].
+ * A logit of -inf (a disabled expert) has probability 0; a row of them alone
+ * has probability 0 everywhere and no gradient. */
+typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score_t;
+
+/* logits: device [tokens][experts], row stride logits_stride >= experts.
+ * chosen: device [tokens][topk] of int32 (chosen_bytes 4) or int64 (8), row
+ * stride chosen_stride >= topk; -1 = not sent anywhere (a dropped token: it
+ * still counts in p), any other value outside [0, experts) is ignored and
+ * sets MUON_FLAG_INDEX.
+ * seq_begin: device [sequences + 1], ascending; sequence s holds the tokens
+ * seq_begin[s] .. seq_begin[s+1] - 1, tokens outside every sequence are not
+ * valid.  NULL = one sequence of all tokens (sequences must be 1).  Values
+ * outside [0, tokens] or out of order set MUON_FLAG_INDEX.
+ * token_mask: device [tokens] of 0/1 (0 = padding: not read, not counted, no
+ * gradient); NULL = all valid.
+ * experts <= 1024; tokens < 2^31. */
+typedef struct {
+  int64_t tokens;
+  int experts, topk;
+  const void* logits;
+  muon_dtype_t dtype;
+  int64_t logits_stride;
+  const void* chosen;
+  int chosen_bytes;
+  int64_t chosen_stride;
+  int sequences;
+  const int32_t* seq_begin;
+  const uint8_t* token_mask;
+  muon_score_t score;
+  float coef;
+} muon_balance_t;
+
+/* Bytes of workspace muon_balance_forward needs.  Host only. */
+muon_status_t muon_balance_workspace_size(int64_t tokens, int experts, int sequences,
+                                          size_t* bytes);
+
+/* loss: device, 1 fp32.  counts: device [experts] int32, the choices of each
+ * expert by the valid tokens of all sequences.  load: device
+ * [sequences][experts] fp32, coef / N * f_se, which the backward pass takes.
+ * Status word in the workspace (muon_get_status).  Sums are fp32 in an order
+ * fixed by the sizes: the same inputs give the same bits. */
+muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t* counts,
+                                   float* load, void* workspace, size_t workspace_bytes,
+                                   muon_stream_t stream);
+
+/* dlogits: device [tokens][experts] of dtype ddt, row stride dlogits_stride;
+ * written (0 for tokens that are not valid), or added to when accumulate is 1.
+ * load: as muon_balance_forward left it.  dloss: device, 1 fp32, the gradient
+ * of the loss itself; NULL = 1.  Reads neither b->chosen nor b->coef; needs
+ * no workspace.  dlogits may be the logits themselves (same stride and type). */
+muon_status_t muon_balance_backward(const muon_balance_t* b, const float* load,
+                                    const float* dloss, void* dlogits, muon_dtype_t ddt,
+                                    int64_t dlogits_stride, int accumulate,
+                                    muon_stream_t stream);
+
+/* An activation of rows x cols held in 8 bits.  Each 32 columns of a row
+ * (the last block of a row may be shorter) share the scale 2^e, e the least
+ * integer >= -126 with 127 * 2^e >= the block's largest magnitude:
+ *   code = round-to-nearest-even(x / 2^e), one int8 in [-127, 127]
+ *   exps = e + 127, one byte a block
+ * (magnitudes above 63.5 * 2^122, where 64 * 2^122 would overflow, get code
+ * 63).  The value code * 2^e has at most 7 significant bits, so it is exact in
+ * bf16.  A block with an infinity or a NaN gets the byte 255 and reads back as
+ * NaN throughout.
+ * codes: device, 16-byte aligned, row r at codes + r * code_stride,
+ * code_stride a multiple of 32 and >= cols; the bytes between cols and the end
+ * of its block of 32 are written as 0.  exps: device, 16-byte aligned, row r
+ * at exps + r * exp_stride, exp_stride a multiple of 16 and >= the blocks of a
+ * row. */
+typedef struct {
+  int64_t rows;
+  int cols;
+  int8_t* codes;
+  int64_t code_stride;
+  uint8_t* exps;
+  int64_t exp_stride;
+} muon_act8_t;
+
+/* Write x (rows x cols, row stride x_stride) into `out`. */
+muon_status_t muon_act8_pack(const void* x, muon_dtype_t xdt, int64_t x_stride,
+                             const muon_act8_t* out, muon_stream_t stream);
+
+/* Read `a` back into x. */
+muon_status_t muon_act8_unpack(const muon_act8_t* a, void* x, muon_dtype_t xdt, int64_t x_stride,
+                               muon_stream_t stream);
+
+/* h = silu(gate) * up with silu(g) = g * sigma(g), in fp32, rounded once to
+ * dt; gate8 and up8 receive gate and up (one pass over the data).  gate, up
+ * and h: rows x cols of dt with row strides; rows and cols are gate8's. */
+muon_status_t muon_act8_swiglu_forward(const void* gate, int64_t gate_stride, const void* up,
+                                       int64_t up_stride, muon_dtype_t dt, void* h,
+                                       int64_t h_stride, const muon_act8_t* gate8,
+                                       const muon_act8_t* up8, muon_stream_t stream);
+
+/* The backward pass from the checkpoints' values g, u:
+ *   dup = dh * g * sigma(g),   dgate = dh * u * sigma(g) * (1 + g * (1 - sigma(g)))
+ * h8: NULL, or a checkpoint that receives silu(g) * u, the input of the down
+ * projection's weight gradient.  dgate or dup may be dh itself (same stride). */
+muon_status_t muon_act8_swiglu_backward(const void* dh, int64_t dh_stride, muon_dtype_t dt,
+                                        const muon_act8_t* gate8, const muon_act8_t* up8,
+                                        void* dgate, int64_t dgate_stride, void* dup,
+                                        int64_t dup_stride, const muon_act8_t* h8,
+                                        muon_stream_t stream);
+
+/* Weight gradients of `experts` projections y = W_e x whose tokens lie one
+ * expert after the other:
+ *   G_e[o][i] (+)= sum_{t = offsets[e]}^{offsets[e+1] - 1} dy[t][o] * x[t][i]
+ * with x read from its checkpoint (exact products, fp32 sums).
+ * dy: device, rows x out, row stride dy_stride, bf16 or fp32.  x: rows x in.
+ * offsets: device [experts + 1], ascending, within [0, rows] (values outside
+ * or out of order are cut and set MUON_FLAG_INDEX); NULL = all rows (experts
+ * must be 1).  An expert without tokens gets 0.
+ * g_ptrs: DEVICE array of `experts` DEVICE pointers (a muon_group_t's g_ptrs),
+ * or NULL: matrix e at g_base + e * g_batch_stride.  G: out x in of g_dtype,
+ * row stride g_stride.  accumulate: 1 = add to what G holds (in fp32, rounded
+ * once).  Results depend on the sizes and the inputs alone. */
+typedef struct {
+  int64_t rows;
+  int out, experts;
+  const void* dy;
+  muon_dtype_t dy_dtype;
+  int64_t dy_stride;
+  muon_act8_t x;
+  const int32_t* offsets;
+  void* const* g_ptrs;
+  void* g_base;
+  int64_t g_batch_stride;
+  int64_t g_stride;
+  muon_dtype_t g_dtype;
+  int accumulate;
+} muon_weight_grad_t;
+
+/* Bytes of workspace muon_act8_weight_grad needs (pointers are not looked at).
+ * Host only. */
+muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, size_t* bytes);
+
+muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace,
+                                    size_t workspace_bytes, muon_stream_t stream);
 
 /* Per-kernel statistics since the last muon_profile_reset.  Launches are
  * always counted.  With profiling on, the library records a CUDA event pair

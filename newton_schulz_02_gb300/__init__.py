@@ -29,15 +29,18 @@ MUON_ERR_TIMEOUT = 6
 MUON_FLAG_NONFINITE = 0x1
 MUON_FLAG_TIMEOUT = 0x2
 MUON_FLAG_MISALIGNED = 0x4
+MUON_FLAG_INDEX = 0x8
 # enums
 MUON_BF16, MUON_F32 = 0, 1
 MUON_NESTEROV_SGD, MUON_NESTEROV_EMA = 0, 1
 MUON_SCALE_SPECTRAL, MUON_SCALE_UNIT_RMS_NORM, MUON_SCALE_NONE = 0, 1, 2
 MUON_NS_BF16, MUON_NS_TF32, MUON_NS_BF16X3 = 0, 1, 2
+MUON_SCORE_SOFTMAX, MUON_SCORE_SIGMOID = 0, 1
 
 _DT = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
 _SCALE = {"spectral": MUON_SCALE_SPECTRAL, "unit_rms_norm": MUON_SCALE_UNIT_RMS_NORM,
           "none": MUON_SCALE_NONE}
+_SCORE = {"softmax": MUON_SCORE_SOFTMAX, "sigmoid": MUON_SCORE_SIGMOID}
 _STYLE = {"sgd": MUON_NESTEROV_SGD, "ema": MUON_NESTEROV_EMA}
 
 
@@ -88,6 +91,27 @@ class muon_adamw_hparams_t(ctypes.Structure):
                 ("weight_decay", c_float), ("t", c_int64)]
 
 
+class muon_balance_t(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("experts", c_int), ("topk", c_int), ("logits", c_void_p),
+                ("dtype", c_int), ("logits_stride", c_int64), ("chosen", c_void_p),
+                ("chosen_bytes", c_int), ("chosen_stride", c_int64), ("sequences", c_int),
+                ("seq_begin", c_void_p), ("token_mask", c_void_p), ("score", c_int),
+                ("coef", c_float)]
+
+
+class muon_act8_t(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int), ("codes", c_void_p), ("code_stride", c_int64),
+                ("exps", c_void_p), ("exp_stride", c_int64)]
+
+
+class muon_weight_grad_t(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("out", c_int), ("experts", c_int), ("dy", c_void_p),
+                ("dy_dtype", c_int), ("dy_stride", c_int64), ("x", muon_act8_t),
+                ("offsets", c_void_p), ("g_ptrs", c_void_p), ("g_base", c_void_p),
+                ("g_batch_stride", c_int64), ("g_stride", c_int64), ("g_dtype", c_int),
+                ("accumulate", c_int)]
+
+
 # C prototypes: name -> (restype, argtypes)
 PROTOTYPES = {
     "muon_ns_hybrid_schedule": (c_int, [POINTER(muon_ns_schedule_t)]),
@@ -115,6 +139,22 @@ PROTOTYPES = {
     "muon_status_string": (c_char_p, [c_int]),
     "muon_adamw_step": (c_int, [POINTER(muon_adamw_group_t), c_int, POINTER(muon_adamw_hparams_t),
                                 c_void_p, c_void_p]),
+    "muon_balance_workspace_size": (c_int, [c_int64, c_int, c_int, POINTER(c_size_t)]),
+    "muon_balance_forward": (c_int, [POINTER(muon_balance_t), c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_size_t, c_void_p]),
+    "muon_balance_backward": (c_int, [POINTER(muon_balance_t), c_void_p, c_void_p, c_void_p,
+                                      c_int, c_int64, c_int, c_void_p]),
+    "muon_act8_pack": (c_int, [c_void_p, c_int, c_int64, POINTER(muon_act8_t), c_void_p]),
+    "muon_act8_unpack": (c_int, [POINTER(muon_act8_t), c_void_p, c_int, c_int64, c_void_p]),
+    "muon_act8_swiglu_forward": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p,
+                                         c_int64, POINTER(muon_act8_t), POINTER(muon_act8_t),
+                                         c_void_p]),
+    "muon_act8_swiglu_backward": (c_int, [c_void_p, c_int64, c_int, POINTER(muon_act8_t),
+                                          POINTER(muon_act8_t), c_void_p, c_int64, c_void_p,
+                                          c_int64, POINTER(muon_act8_t), c_void_p]),
+    "muon_act8_weight_grad_workspace_size": (c_int, [POINTER(muon_weight_grad_t),
+                                                     POINTER(c_size_t)]),
+    "muon_act8_weight_grad": (c_int, [POINTER(muon_weight_grad_t), c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None
@@ -458,3 +498,196 @@ def muon_adamw_step(groups: Sequence[AdamWGroup], hp: muon_adamw_hparams_t,
     _check(load_library().muon_adamw_step(arr, len(groups), ctypes.byref(hp),
                                           flags.data_ptr() if flags is not None else None,
                                           _stream(stream)), "muon_adamw_step")
+
+
+# ---------------------------------------------------------------------------
+# gradients of a mixture-of-experts training step
+# ---------------------------------------------------------------------------
+def _rows2d(t: torch.Tensor, what: str, shape=None) -> int:
+    """Row stride of a 2-D tensor with unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0] > 0):
+        raise ValueError(f"{what} needs two dimensions and unit column stride")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} needs the shape {tuple(shape)}, not {tuple(t.shape)}")
+    # the stride of no row or of the only one is never used; it may be anything
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _DT:
+        raise ValueError(f"{what} must be bfloat16 or float32, not {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _vector(t: torch.Tensor, what: str, dtype: torch.dtype, numel: int) -> int:
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{what} must be {numel} contiguous {dtype}")
+    return t.data_ptr()
+
+
+class Balance:
+    """A router's decisions over a batch of tokens: logits [tokens, experts],
+    chosen [tokens, topk] (int32 or int64 expert numbers, -1 = none), seq_begin
+    (int32 [sequences + 1]; None = one sequence) and mask (bool or uint8
+    [tokens]; None = every token is valid)."""
+
+    def __init__(self, logits: torch.Tensor, chosen: torch.Tensor,
+                 seq_begin: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                 score: str = "softmax", coef: float = 1e-2):
+        tokens, experts = logits.shape
+        ls = _rows2d(logits, "logits")
+        if chosen.dtype not in (torch.int32, torch.int64):
+            raise ValueError("chosen must be int32 or int64")
+        if chosen.dim() != 2 or chosen.shape[0] != tokens:
+            raise ValueError("chosen needs one row of expert numbers for each token")
+        topk = chosen.shape[1]
+        cs = _rows2d(chosen, "chosen")
+        sequences, seq = 1, None
+        if seq_begin is not None:
+            sequences = seq_begin.numel() - 1
+            seq = _vector(seq_begin, "seq_begin", torch.int32, sequences + 1)
+        mp = None
+        if mask is not None:
+            if mask.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("mask must be bool or uint8")
+            mp = _vector(mask, "mask", mask.dtype, tokens)
+        self.tensors = (logits, chosen, seq_begin, mask)
+        self.shape = (tokens, experts)
+        self.sequences = sequences
+        self.c = muon_balance_t(tokens, experts, topk, logits.data_ptr(), _dtype(logits, "logits"),
+                                ls, chosen.data_ptr(), chosen.element_size(), cs, sequences, seq,
+                                mp, _SCORE[score], float(coef))
+
+
+def muon_balance_workspace_size(tokens: int, experts: int, sequences: int = 1) -> int:
+    nb = c_size_t(0)
+    _check(load_library().muon_balance_workspace_size(int(tokens), int(experts), int(sequences),
+                                                      ctypes.byref(nb)),
+           "muon_balance_workspace_size")
+    return nb.value
+
+
+def muon_balance_forward(b: Balance, loss: torch.Tensor, counts: torch.Tensor,
+                         load: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """loss: fp32, one element; counts: int32 [experts]; load: fp32 [sequences, experts]."""
+    experts = b.shape[1]
+    _check(load_library().muon_balance_forward(
+        ctypes.byref(b.c), _vector(loss, "loss", torch.float32, 1),
+        _vector(counts, "counts", torch.int32, experts),
+        _vector(load, "load", torch.float32, b.sequences * experts), ws.data_ptr(), ws.numel(),
+        _stream(stream)), "muon_balance_forward")
+
+
+def muon_balance_backward(b: Balance, load: torch.Tensor, dlogits: torch.Tensor,
+                          dloss: Optional[torch.Tensor] = None, accumulate: bool = False,
+                          stream=None) -> None:
+    """dlogits [tokens, experts] is written, or added to with accumulate."""
+    _check(load_library().muon_balance_backward(
+        ctypes.byref(b.c), _vector(load, "load", torch.float32, b.sequences * b.shape[1]),
+        None if dloss is None else _vector(dloss, "dloss", torch.float32, 1),
+        dlogits.data_ptr(), _dtype(dlogits, "dlogits"), _rows2d(dlogits, "dlogits", b.shape),
+        int(bool(accumulate)), _stream(stream)), "muon_balance_backward")
+
+
+class Act8:
+    """An activation [rows, cols] held in 8 bits: codes (int8, [rows, >= cols],
+    row stride a multiple of 32) and exps (uint8, one biased exponent for each
+    32 columns of a row, row stride a multiple of 16)."""
+
+    def __init__(self, codes: torch.Tensor, exps: torch.Tensor, cols: int):
+        if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
+            raise ValueError("codes are int8, exps uint8")
+        rows = codes.shape[0]
+        if codes.dim() != 2 or exps.dim() != 2 or exps.shape[0] != rows or \
+                codes.shape[1] < cols or exps.shape[1] * 32 < cols:
+            raise ValueError("codes [rows, >= cols] and exps [rows, >= cols / 32] are needed")
+        self.codes, self.exps, self.shape = codes, exps, (rows, int(cols))
+        self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), _rows2d(codes, "codes"),
+                             exps.data_ptr(), _rows2d(exps, "exps"))
+
+
+def act8_empty(rows: int, cols: int, device="cuda") -> Act8:
+    """Memory of a checkpoint of rows x cols (its values are not set)."""
+    blocks = (cols + 31) // 32
+    return Act8(torch.empty(rows, blocks * 32, dtype=torch.int8, device=device),
+                torch.empty(rows, (blocks + 15) // 16 * 16, dtype=torch.uint8, device=device), cols)
+
+
+def muon_act8_pack(x: torch.Tensor, out: Act8, stream=None) -> None:
+    """Write x [rows, cols] (bf16 or fp32) into the checkpoint."""
+    _check(load_library().muon_act8_pack(x.data_ptr(), _dtype(x, "x"), _rows2d(x, "x", out.shape),
+                                         ctypes.byref(out.c), _stream(stream)), "muon_act8_pack")
+
+
+def muon_act8_unpack(a: Act8, out: torch.Tensor, stream=None) -> None:
+    """Read a checkpoint back into out [rows, cols] (bf16 or fp32)."""
+    _check(load_library().muon_act8_unpack(ctypes.byref(a.c), out.data_ptr(), _dtype(out, "out"),
+                                           _rows2d(out, "out", a.shape), _stream(stream)),
+           "muon_act8_unpack")
+
+
+def _one_dtype(first: torch.Tensor, *others: torch.Tensor) -> int:
+    if any(t.dtype != first.dtype for t in others):
+        raise ValueError("the tensors need one dtype")
+    return _dtype(first, "the tensors")
+
+
+def muon_act8_swiglu_forward(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor, gate8: Act8,
+                             up8: Act8, stream=None) -> None:
+    """h = silu(gate) * up; gate8 and up8 keep gate and up for the backward pass."""
+    dt, s = _one_dtype(gate, up, h), gate8.shape
+    _check(load_library().muon_act8_swiglu_forward(
+        gate.data_ptr(), _rows2d(gate, "gate", s), up.data_ptr(), _rows2d(up, "up", s), dt,
+        h.data_ptr(), _rows2d(h, "h", s), ctypes.byref(gate8.c), ctypes.byref(up8.c),
+        _stream(stream)), "muon_act8_swiglu_forward")
+
+
+def muon_act8_swiglu_backward(dh: torch.Tensor, gate8: Act8, up8: Act8, dgate: torch.Tensor,
+                              dup: torch.Tensor, h8: Optional[Act8] = None, stream=None) -> None:
+    """Gradients of gate and up; h8, if given, receives silu(gate) * up."""
+    dt, s = _one_dtype(dh, dgate, dup), gate8.shape
+    _check(load_library().muon_act8_swiglu_backward(
+        dh.data_ptr(), _rows2d(dh, "dh", s), dt, ctypes.byref(gate8.c), ctypes.byref(up8.c),
+        dgate.data_ptr(), _rows2d(dgate, "dgate", s), dup.data_ptr(), _rows2d(dup, "dup", s),
+        None if h8 is None else ctypes.byref(h8.c), _stream(stream)), "muon_act8_swiglu_backward")
+
+
+def muon_act8_weight_grad_workspace_size(rows: int, out: int, inp: int, experts: int = 1,
+                                         dy_dtype: torch.dtype = torch.bfloat16,
+                                         g_dtype: torch.dtype = torch.bfloat16) -> int:
+    x = muon_act8_t(rows, inp, None, (inp + 31) // 32 * 32, None, ((inp + 31) // 32 + 15) // 16 * 16)
+    d = muon_weight_grad_t(rows, out, experts, None, _DT[dy_dtype], out, x, None, None, None,
+                           out * inp, inp, _DT[g_dtype], 0)
+    nb = c_size_t(0)
+    _check(load_library().muon_act8_weight_grad_workspace_size(ctypes.byref(d), ctypes.byref(nb)),
+           "muon_act8_weight_grad_workspace_size")
+    return nb.value
+
+
+def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
+                          offsets: Optional[torch.Tensor] = None, accumulate: bool = False,
+                          stream=None) -> None:
+    """G[e] (+)= dy[offsets[e]:offsets[e+1]]^T x[offsets[e]:offsets[e+1]].
+
+    G: a tensor [experts, out, in] (or [out, in] for one), or a Group whose G
+    matrices receive the gradients.  offsets: int32 [experts + 1] on the
+    device; None = all rows belong to the one expert."""
+    rows, inp = x8.shape
+    out = dy.shape[1] if dy.dim() == 2 else 0
+    ds = _rows2d(dy, "dy", (rows, out))
+    if isinstance(G, Group):
+        v = G.c.view
+        experts, shape, gs, gdt = G.c.batch, (v.rows, v.cols), v.row_stride, G.c.g_dtype
+        ptrs, base, bs = G.c.g_ptrs, None, 0
+    else:
+        g3 = G if G.dim() == 3 else G.unsqueeze(0)
+        experts, shape, gdt = g3.shape[0], tuple(g3.shape[1:]), _dtype(G, "G")
+        gs = _rows2d(g3[0], "G")
+        ptrs, base, bs = None, G.data_ptr(), g3.stride(0)
+    if shape != (out, inp):
+        raise ValueError(f"G needs matrices of {out} x {inp}, not {shape[0]} x {shape[1]}")
+    op = None if offsets is None else _vector(offsets, "offsets", torch.int32, experts + 1)
+    d = muon_weight_grad_t(rows, out, experts, dy.data_ptr(), _dtype(dy, "dy"), ds, x8.c, op, ptrs,
+                           base, bs, gs, gdt, int(bool(accumulate)))
+    _check(load_library().muon_act8_weight_grad(ctypes.byref(d), ws.data_ptr(), ws.numel(),
+                                                _stream(stream)), "muon_act8_weight_grad")

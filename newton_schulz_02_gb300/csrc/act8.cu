@@ -1,0 +1,461 @@
+// Activations held in 8 bits between the forward and the backward pass, and
+// the gated feed-forward activation on them (muon_act8_pack, _unpack,
+// _swiglu_forward, _swiglu_backward).
+//
+// A block of 32 columns of a row shares a power-of-two scale 2^e, so both
+// directions are exact but for the one rounding of x / 2^e to an integer, and
+// a code's value (7 significant bits) is exact in bf16.  A power of two costs
+// up to one of the eight bits against a free scale; in return the code's
+// value needs no rounding where the tensor cores read it.
+//
+// All four passes are bound by HBM: each value is read once and written once.
+// A thread takes V consecutive columns (V = 16: 16-byte accesses throughout,
+// two threads share a block's maximum by one shuffle), or, where some row does
+// not start on a 16-byte boundary, one column (V = 1: a warp reads the 32
+// columns of a block side by side, which coalesces at any alignment).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = 32;   // columns that share a scale
+
+// Quotient by a fixed divisor of numbers below 2^31: with l = ceil(log2 d) and
+// m = ceil(2^(31+l) / d), m*d exceeds 2^(31+l) by less than 2^l, so the
+// product's error stays below one part in n for n < 2^31.
+struct Divider {
+  uint32_t mul, shift, d;
+};
+
+Divider divider(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t{1} << l) < d) ++l;
+  const uint64_t two = uint64_t{1} << (31 + l);
+  return {static_cast<uint32_t>((two + d - 1) / d), 31 + l, d};
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divider& v) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> v.shift);
+}
+
+struct Plane {          // one operand: base of the first row, row stride in elements
+  void* p;
+  int64_t stride;
+};
+
+struct Packed {
+  int8_t* codes;
+  int64_t code_stride;
+  uint8_t* exps;
+  int64_t exp_stride;
+};
+
+struct Act8Args {
+  uint32_t items;       // threads' work items: rows x items of a row
+  int cols;
+  Divider per_row;      // items of a row
+  Plane x, y, z;        // roles by kernel
+  Packed a, b, c;
+};
+
+// ---- V values of a row -----------------------------------------------------
+template <int V, typename T>
+__device__ __forceinline__ void load_values(const Plane& pl, int64_t row, int col, int n,
+                                            float (&x)[V]) {
+  const T* p = static_cast<const T*>(pl.p) + row * pl.stride + col;
+  if constexpr (V == 1) {
+    x[0] = n > 0 ? static_cast<float>(*p) : 0.f;
+  } else if (n >= V) {
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < V / kPer; ++q) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[q];
+      if constexpr (sizeof(T) == 4) {
+        x[4 * q] = __uint_as_float(u.x);
+        x[4 * q + 1] = __uint_as_float(u.y);
+        x[4 * q + 2] = __uint_as_float(u.z);
+        x[4 * q + 3] = __uint_as_float(u.w);
+      } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // a bf16 is the upper half of an fp32
+          x[8 * q + 2 * k] = __uint_as_float(w[k] << 16);
+          x[8 * q + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = k < n ? static_cast<float>(p[k]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <int V, typename T>
+__device__ __forceinline__ void store_values(const Plane& pl, int64_t row, int col, int n,
+                                             const float (&x)[V]) {
+  T* p = static_cast<T*>(pl.p) + row * pl.stride + col;
+  if constexpr (V == 1) {
+    if (n > 0) store_one(p, x[0]);
+  } else if (n >= V) {
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < V / kPer; ++q) {
+      uint4 u;
+      if constexpr (sizeof(T) == 4) {
+        u = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]),
+                       __float_as_uint(x[4 * q + 2]), __float_as_uint(x[4 * q + 3]));
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      reinterpret_cast<uint4*>(p)[q] = u;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k < n) store_one(p + k, x[k]);
+  }
+}
+
+// ---- the code --------------------------------------------------------------
+// Biased exponent of the scale of a block with largest magnitude amax
+// (0 <= amax, or NaN / infinity): with amax = m * 2^k, 1 <= m < 2, and
+// 127 * 2^e = (127/64) 2^(e+6), e is k - 6, and one more where m > 127/64
+// (mantissa bits above 0x7E0000), at least -126.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int b = static_cast<int>((bits + 0x1FFFFu) >> 23) - 6;
+  return bits >= 0x7F800000u ? 255 : max(b, 1);
+}
+
+__device__ __forceinline__ float exponent_value(int b) {   // 2^(b - 127); infinity for 255
+  return __uint_as_float(static_cast<uint32_t>(b) << 23);
+}
+
+// Largest magnitude of a block from its threads' V values each; NaN counts as
+// the largest (the comparison is on the bits).
+template <int V>
+__device__ __forceinline__ float block_amax(const float (&x)[V]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = kBlock / V / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return __uint_as_float(m);
+}
+
+// Quantises the V values of this thread and leaves them in `out`; the lanes
+// of a block must be active together.  The values are replaced by what the
+// codes stand for where BACK is set.
+template <int V>
+__device__ __forceinline__ void write_codes(const Packed& out, int64_t row, int col, int n,
+                                            const float (&x)[V], bool on) {
+  const int b = scale_exponent(block_amax<V>(x));
+  // 2^-e: the biased exponent of the reciprocal is 254 - b, in [5, 253]
+  const float inv = b == 255 ? 0.f : exponent_value(254 - b);
+  const float top = b == 249 ? 63.f : 127.f;   // 64 * 2^122 overflows
+  if (!on) return;
+  int8_t* p = out.codes + row * out.code_stride + col;
+  if constexpr (V == 1) {
+    // columns past the end of the row, up to the block's end, hold 0
+    *p = static_cast<int8_t>(__float2int_rn(fminf(fmaxf(x[0] * inv, -top), top)));
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) {
+      uint32_t u = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = __float2int_rn(fminf(fmaxf(x[4 * q + k] * inv, -top), top));
+        u |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * k);
+      }
+      w[q] = u;
+    }
+#pragma unroll
+    for (int q = 0; q < V / 16; ++q)
+      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+  if (col % kBlock == 0) out.exps[row * out.exp_stride + col / kBlock] = static_cast<uint8_t>(b);
+}
+
+// Values of V codes.  code * 2^e is one exact product; the byte 255 turns the
+// scale into an infinity, and infinity - infinity gives the block's NaN.
+template <int V>
+__device__ __forceinline__ void read_codes(const Packed& in, int64_t row, int col, float (&x)[V]) {
+  const int b = in.exps[row * in.exp_stride + col / kBlock];
+  const float s = exponent_value(b);
+  const float nan = s - s;   // 0, or NaN for 255
+  const int8_t* p = in.codes + row * in.code_stride + col;
+  if constexpr (V == 1) {
+    x[0] = fmaf(static_cast<float>(*p), s, nan);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V / 16; ++q) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[q];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int c = static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)));
+        x[16 * q + k] = fmaf(static_cast<float>(c), s, nan);
+      }
+    }
+  }
+}
+
+struct Place {
+  int64_t row;
+  int col, n;    // n: columns of this item inside the row (<= 0: padding of the last block)
+  bool on;
+};
+
+template <int V>
+__device__ __forceinline__ Place place(const Act8Args& a) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  Place p;
+  p.on = i < a.items;
+  const uint32_t at = p.on ? i : a.items - 1;
+  const uint32_t row = quotient(at, a.per_row);
+  p.row = row;
+  p.col = static_cast<int>(at - row * a.per_row.d) * V;
+  p.n = p.on ? a.cols - p.col : 0;
+  return p;
+}
+
+template <int V, typename T>
+__global__ void __launch_bounds__(kThreads) k_act8_pack(const __grid_constant__ Act8Args a) {
+  const Place p = place<V>(a);
+  float x[V];
+  load_values<V, T>(a.x, p.row, p.col, p.n, x);
+  write_codes<V>(a.a, p.row, p.col, p.n, x, p.on);
+}
+
+template <int V, typename T>
+__global__ void __launch_bounds__(kThreads) k_act8_unpack(const __grid_constant__ Act8Args a) {
+  const Place p = place<V>(a);
+  if (!p.on) return;
+  float x[V];
+  read_codes<V>(a.a, p.row, p.col, x);
+  store_values<V, T>(a.x, p.row, p.col, p.n, x);
+}
+
+__device__ __forceinline__ float sigma(float g) { return 1.f / (1.f + expf(-g)); }
+
+// x = gate, y = up, z = h; a, b = the checkpoints of gate and up.
+template <int V, typename T>
+__global__ void __launch_bounds__(kThreads) k_act8_swiglu_forward(const __grid_constant__ Act8Args a) {
+  const Place p = place<V>(a);
+  float g[V], u[V], h[V];
+  load_values<V, T>(a.x, p.row, p.col, p.n, g);
+  load_values<V, T>(a.y, p.row, p.col, p.n, u);
+  write_codes<V>(a.a, p.row, p.col, p.n, g, p.on);
+  write_codes<V>(a.b, p.row, p.col, p.n, u, p.on);
+#pragma unroll
+  for (int k = 0; k < V; ++k) h[k] = g[k] * sigma(g[k]) * u[k];
+  if (p.on) store_values<V, T>(a.z, p.row, p.col, p.n, h);
+}
+
+// x = dh, y = dgate, z = dup; a, b = the checkpoints of gate and up, c = h8.
+template <int V, typename T, bool H8>
+__global__ void __launch_bounds__(kThreads) k_act8_swiglu_backward(const __grid_constant__ Act8Args a) {
+  const Place p = place<V>(a);
+  float g[V], u[V], d[V], h[H8 ? V : 1];
+  read_codes<V>(a.a, p.row, p.col, g);
+  read_codes<V>(a.b, p.row, p.col, u);
+  load_values<V, T>(a.x, p.row, p.col, p.n, d);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const float s = sigma(g[k]);
+    const float act = g[k] * s;
+    if (H8) h[k] = k < p.n ? act * u[k] : 0.f;
+    const float dg = d[k] * u[k] * fmaf(act, 1.f - s, s);
+    u[k] = d[k] * act;
+    g[k] = dg;
+  }
+  if (p.on) {
+    store_values<V, T>(a.y, p.row, p.col, p.n, g);
+    store_values<V, T>(a.z, p.row, p.col, p.n, u);
+  }
+  if constexpr (H8) write_codes<V>(a.c, p.row, p.col, p.n, h, p.on);
+}
+
+// ---- host ------------------------------------------------------------------
+int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int64_t blocks_of(int cols) { return (static_cast<int64_t>(cols) + kBlock - 1) / kBlock; }
+
+muon_status_t check_act8(const muon_act8_t* a) {
+  if (a == nullptr || a->rows < 0 || a->cols < 1) return MUON_ERR_INVALID_ARG;
+  if (a->cols > (1 << 26)) return MUON_ERR_UNSUPPORTED;
+  if (a->code_stride < a->cols || a->exp_stride < blocks_of(a->cols)) return MUON_ERR_INVALID_ARG;
+  if (a->rows > 0 && (a->codes == nullptr || a->exps == nullptr)) return MUON_ERR_INVALID_ARG;
+  if (a->code_stride % kBlock != 0 || a->exp_stride % 16 != 0 || !at_multiple(a->codes, 16) ||
+      !at_multiple(a->exps, 16))
+    return MUON_ERR_MISALIGNED;
+  return MUON_OK;
+}
+
+muon_status_t check_plane(const void* p, int64_t stride, int dtype, const muon_act8_t* like) {
+  if (dtype != MUON_BF16 && dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
+  if (stride < like->cols || (like->rows > 0 && p == nullptr)) return MUON_ERR_INVALID_ARG;
+  return at_multiple(p, esize(dtype)) ? MUON_OK : MUON_ERR_MISALIGNED;
+}
+
+bool same_size(const muon_act8_t* a, const muon_act8_t* b) {
+  return a->rows == b->rows && a->cols == b->cols;
+}
+
+Packed packed(const muon_act8_t* a) { return {a->codes, a->code_stride, a->exps, a->exp_stride}; }
+
+bool rows_aligned(const Plane& p, int dtype) {
+  return p.p == nullptr || (at_multiple(p.p, 16) && p.stride * esize(dtype) % 16 == 0);
+}
+
+enum Pass { kPack, kUnpack, kForward, kBackward, kBackwardH8 };
+
+template <int V, typename T>
+void launch_pass(Pass pass, unsigned grid, cudaStream_t st, const Act8Args& a) {
+  switch (pass) {
+    case kPack: k_act8_pack<V, T><<<grid, kThreads, 0, st>>>(a); break;
+    case kUnpack: k_act8_unpack<V, T><<<grid, kThreads, 0, st>>>(a); break;
+    case kForward: k_act8_swiglu_forward<V, T><<<grid, kThreads, 0, st>>>(a); break;
+    case kBackward: k_act8_swiglu_backward<V, T, false><<<grid, kThreads, 0, st>>>(a); break;
+    case kBackwardH8: k_act8_swiglu_backward<V, T, true><<<grid, kThreads, 0, st>>>(a); break;
+  }
+}
+
+// Every row's items in one launch, or in several of fewer than 2^30 items.
+muon_status_t run_pass(Pass pass, int dtype, int64_t rows, int cols, Act8Args a, double bytes,
+                       cudaStream_t st) {
+  if (rows == 0) return MUON_OK;
+  const bool wide = rows_aligned(a.x, dtype) && rows_aligned(a.y, dtype) && rows_aligned(a.z, dtype);
+  const int64_t per_row = blocks_of(cols) * (wide ? 2 : kBlock);
+  a.cols = cols;
+  a.per_row = divider(static_cast<uint32_t>(per_row));
+  int64_t most = (int64_t{1} << 30) / per_row;
+  if (most < 1) most = 1;
+  const KernelKind kind = pass == kPack || pass == kUnpack ? kKindAct8 : kKindSwiglu;
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most;
+    Act8Args b = a;
+    b.items = static_cast<uint32_t>(n * per_row);
+    for (Plane* p : {&b.x, &b.y, &b.z})
+      if (p->p != nullptr) p->p = static_cast<char*>(p->p) + r0 * p->stride * esize(dtype);
+    for (Packed* p : {&b.a, &b.b, &b.c})
+      if (p->codes != nullptr) {
+        p->codes += r0 * p->code_stride;
+        p->exps += r0 * p->exp_stride;
+      }
+    const unsigned grid = (b.items + kThreads - 1) / kThreads;
+    prof_begin(kind, st);
+    if (dtype == MUON_F32) {
+      if (wide) launch_pass<16, float>(pass, grid, st, b);
+      else launch_pass<1, float>(pass, grid, st, b);
+    } else {
+      if (wide) launch_pass<16, __nv_bfloat16>(pass, grid, st, b);
+      else launch_pass<1, __nv_bfloat16>(pass, grid, st, b);
+    }
+    prof_end(kind, st, 0.0, bytes * static_cast<double>(n) * cols);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  return MUON_OK;
+}
+
+constexpr double kCodeBytes = 1.0 + 1.0 / kBlock;
+
+Plane plane(const void* p, int64_t stride) { return {const_cast<void*>(p), stride}; }
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status_t muon_act8_pack(const void* x, muon_dtype_t xdt, int64_t x_stride,
+                             const muon_act8_t* out, muon_stream_t stream) {
+  muon_status_t s = check_act8(out);
+  if (s == MUON_OK) s = check_plane(x, x_stride, xdt, out);
+  if (s != MUON_OK) return s;
+  Act8Args a{};
+  a.x = plane(x, x_stride);
+  a.a = packed(out);
+  return run_pass(kPack, xdt, out->rows, out->cols, a, esize(xdt) + kCodeBytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status_t muon_act8_unpack(const muon_act8_t* in, void* x, muon_dtype_t xdt, int64_t x_stride,
+                               muon_stream_t stream) {
+  muon_status_t s = check_act8(in);
+  if (s == MUON_OK) s = check_plane(x, x_stride, xdt, in);
+  if (s != MUON_OK) return s;
+  Act8Args a{};
+  a.x = plane(x, x_stride);
+  a.a = packed(in);
+  return run_pass(kUnpack, xdt, in->rows, in->cols, a, esize(xdt) + kCodeBytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status_t muon_act8_swiglu_forward(const void* gate, int64_t gate_stride, const void* up,
+                                       int64_t up_stride, muon_dtype_t dt, void* h,
+                                       int64_t h_stride, const muon_act8_t* gate8,
+                                       const muon_act8_t* up8, muon_stream_t stream) {
+  muon_status_t s = check_act8(gate8);
+  if (s == MUON_OK) s = check_act8(up8);
+  if (s == MUON_OK) s = check_plane(gate, gate_stride, dt, gate8);
+  if (s == MUON_OK) s = check_plane(up, up_stride, dt, gate8);
+  if (s == MUON_OK) s = check_plane(h, h_stride, dt, gate8);
+  if (s != MUON_OK) return s;
+  if (!same_size(gate8, up8)) return MUON_ERR_INVALID_ARG;
+  Act8Args a{};
+  a.x = plane(gate, gate_stride);
+  a.y = plane(up, up_stride);
+  a.z = plane(h, h_stride);
+  a.a = packed(gate8);
+  a.b = packed(up8);
+  return run_pass(kForward, dt, gate8->rows, gate8->cols, a, 3.0 * esize(dt) + 2 * kCodeBytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+muon_status_t muon_act8_swiglu_backward(const void* dh, int64_t dh_stride, muon_dtype_t dt,
+                                        const muon_act8_t* gate8, const muon_act8_t* up8,
+                                        void* dgate, int64_t dgate_stride, void* dup,
+                                        int64_t dup_stride, const muon_act8_t* h8,
+                                        muon_stream_t stream) {
+  muon_status_t s = check_act8(gate8);
+  if (s == MUON_OK) s = check_act8(up8);
+  if (s == MUON_OK && h8 != nullptr) s = check_act8(h8);
+  if (s == MUON_OK) s = check_plane(dh, dh_stride, dt, gate8);
+  if (s == MUON_OK) s = check_plane(dgate, dgate_stride, dt, gate8);
+  if (s == MUON_OK) s = check_plane(dup, dup_stride, dt, gate8);
+  if (s != MUON_OK) return s;
+  if (!same_size(gate8, up8) || (h8 != nullptr && !same_size(gate8, h8)))
+    return MUON_ERR_INVALID_ARG;
+  Act8Args a{};
+  a.x = plane(dh, dh_stride);
+  a.y = plane(dgate, dgate_stride);
+  a.z = plane(dup, dup_stride);
+  a.a = packed(gate8);
+  a.b = packed(up8);
+  if (h8 != nullptr) a.c = packed(h8);
+  return run_pass(h8 != nullptr ? kBackwardH8 : kBackward, dt, gate8->rows, gate8->cols, a,
+                  3.0 * esize(dt) + (h8 != nullptr ? 3 : 2) * kCodeBytes,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,659 @@
+// Router balance loss: per-expert counts, the loss and the gradient of the
+// logits (muon_balance_forward, muon_balance_backward).
+//
+//   p_t  = softmax(l_t)  or  sigma(l_t) / sum sigma(l_t)
+//   f_se = E / (K n_s) c_se,   loss = coef/N sum_s sum_{t in s} sum_e f_se p_te
+//   dl   = coef/N p (f - sum_j f_j p_j)  [* (1 - sigma(l))]
+//
+// Both passes are bound by the logits' bytes: the forward pass reads them
+// once, the backward pass reads them once and writes the gradient.  A row of
+// logits lives in the registers of LANES lanes (VPT values each), so its
+// maximum, sum and dot product are shuffles and the probabilities are
+// recomputed in the backward pass instead of being stored.  The expert sums
+// over tokens (sum_t p_te and c_se) stay in registers and shared memory over a
+// chunk of tokens of one sequence; each chunk leaves one row of partial sums,
+// which the second kernel adds in index order, so no float atomics are used.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int kFinThreads = 1024;   // finalize: 32 experts x 32 partial rows at a time
+constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks
+
+// Tokens of a chunk: at most ~600 chunks (four blocks on each of 152 SMs), so
+// that the partial rows stay few.  A function of the sizes alone, as the
+// order of the sums follows it.
+int chunk_tokens(int64_t tokens) {
+  const int64_t c = (tokens + 607) / 608;
+  return static_cast<int>(c < 32 ? 32 : c);
+}
+
+// Chunks are cut at absolute multiples of the chunk length and at sequence
+// bounds.  Sequence s that starts at token b owns the chunks b/C + s ...
+// (e-1)/C + s: one number for each (chunk, sequence) pair, ascending, without
+// knowing the bounds on the host.
+int64_t chunk_items(int64_t tokens, int sequences) {
+  return tokens / chunk_tokens(tokens) + sequences;
+}
+
+struct BalanceArgs {
+  int tokens, experts, topk, sequences, chunk, items;
+  const void* logits;
+  int dtype;
+  int64_t logits_stride;
+  const void* chosen;
+  int chosen_bytes;
+  int64_t chosen_stride;
+  const int32_t* seq_begin;   // nullptr: one sequence
+  const uint8_t* mask;        // nullptr: all valid
+  int sigmoid;
+  float coef;
+  int vec;                    // rows may be read four values at a time
+  // forward
+  float* psum;                // [items][experts]
+  int* pcnt;                  // [items][experts]
+  int* pval;                  // [items]: valid tokens
+  int* pflag;                 // [items]: device conditions seen
+  float* lossp;               // [sequences * expert blocks]
+  uint32_t* status;
+  int* ticket;
+  float* loss;
+  int32_t* counts;
+  float* load;
+  // backward
+  const float* dloss;
+  void* dlogits;
+  int ddt;
+  int64_t dlogits_stride;
+  int dvec;
+  int accumulate;
+};
+
+__device__ __forceinline__ int clamp_token(int v, int tokens) { return min(max(v, 0), tokens); }
+
+__device__ __forceinline__ int seq_at(const BalanceArgs& a, int s) {
+  return a.seq_begin == nullptr ? (s == 0 ? 0 : a.tokens)
+                                : clamp_token(__ldg(a.seq_begin + s), a.tokens);
+}
+
+// Largest s whose first chunk is at most `item` (0 if none).
+__device__ int seq_of_item(const BalanceArgs& a, int item) {
+  int lo = 0, hi = a.sequences - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_at(a, mid) / a.chunk + mid <= item)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Largest s with seq_begin[s] <= t, or -1.
+__device__ int seq_of_token(const BalanceArgs& a, int t) {
+  int lo = -1, hi = a.sequences - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_at(a, mid) <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Value j of lane `sub` is column (j / 4) * 4 LANES + 4 sub + j % 4: four
+// consecutive columns a lane, LANES lanes side by side.
+template <int LANES>
+__device__ __forceinline__ int column(int sub, int j) {
+  return (j >> 2) * (4 * LANES) + 4 * sub + (j & 3);
+}
+
+template <int LANES, int VPT>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, int dtype, int n, int vec,
+                                         int sub, float fill, float (&x)[VPT]) {
+#pragma unroll
+  for (int q = 0; q < VPT / 4; ++q) {
+    const int c = column<LANES>(sub, 4 * q);
+    if (vec) {
+      if (c < n) {
+        if (dtype == MUON_F32) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + c);
+          x[4 * q] = v.x; x[4 * q + 1] = v.y; x[4 * q + 2] = v.z; x[4 * q + 3] = v.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + off + c);
+          const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+          const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+          x[4 * q] = f0.x; x[4 * q + 1] = f0.y; x[4 * q + 2] = f1.x; x[4 * q + 3] = f1.y;
+        }
+      } else {
+        x[4 * q] = x[4 * q + 1] = x[4 * q + 2] = x[4 * q + 3] = fill;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[4 * q + k] = fill;
+        if (c + k < n)
+          x[4 * q + k] = dtype == MUON_F32
+                             ? static_cast<const float*>(base)[off + c + k]
+                             : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off + c + k]);
+      }
+    }
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int d = LANES / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// Probabilities of a row in place of its logits; slope (sigmoid only) = 1 - sigma.
+// A row whose scores sum to 0 (every expert disabled) gets 0; NaN stays NaN.
+template <int LANES, int VPT, bool SLOPE>
+__device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
+                                                  float (&slope)[SLOPE ? VPT : 1]) {
+  float z = 0.f;
+  if (sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const float t = expf(-x[j]);
+      const float s = 1.f / (1.f + t);
+      if (SLOPE) slope[j] = t < 1.f ? t * s : 1.f - s;   // no cancellation where sigma is near 1
+      x[j] = s;
+      z += s;
+    }
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) m = fmaxf(m, x[j]);
+    m = group_max<LANES>(m);
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      x[j] = expf(x[j] - m);
+      z += x[j];
+    }
+  }
+  z = group_sum<LANES>(z);
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) x[j] *= inv;
+}
+
+// One chunk of tokens of one sequence per block: sum_t p_te, c_e and the
+// number of valid tokens.
+template <int LANES, int VPT>
+__global__ void __launch_bounds__(kThreads) k_balance_forward(const __grid_constant__ BalanceArgs a) {
+  constexpr int kGroups = kThreads / LANES;
+  constexpr int kCols = LANES * VPT;
+  __shared__ float s_sum[kGroups * kCols];
+  __shared__ int s_cnt[kCols];
+  __shared__ int s_val, s_flag;
+  griddep_launch_dependents();
+  const int item = blockIdx.x;
+  const int s = seq_of_item(a, item);
+  const int64_t c0 = static_cast<int64_t>(item - s) * a.chunk;
+  const int b = seq_at(a, s), e = seq_at(a, s + 1);
+  const int t0 = static_cast<int>(max(static_cast<int64_t>(b), c0));
+  const int t1 = static_cast<int>(min(static_cast<int64_t>(e), c0 + a.chunk));
+  if (item == 0) {
+    for (int i = threadIdx.x; i < a.experts; i += kThreads) a.counts[i] = 0;
+    if (threadIdx.x == 0) *a.ticket = 0;
+  }
+  if (c0 < 0 || t0 >= t1) {   // no sequence has this chunk
+    if (threadIdx.x == 0) a.pval[item] = a.pflag[item] = 0;
+    return;
+  }
+  for (int i = threadIdx.x; i < kCols; i += kThreads) s_cnt[i] = 0;
+  if (threadIdx.x == 0) s_val = s_flag = 0;
+  __syncthreads();
+
+  const int group = threadIdx.x / LANES, sub = threadIdx.x % LANES;
+  float acc[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) acc[j] = 0.f;
+  int valid = 0, bad = 0;
+  for (int tb = t0; tb < t1; tb += kGroups) {   // uniform trip count: shuffles need every lane
+    const int t = tb + group;
+    const bool on = t < t1 && (a.mask == nullptr || a.mask[t] != 0);
+    float x[VPT], none[1];
+    load_row<LANES, VPT>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
+                         on ? a.experts : 0, a.vec, sub, -INFINITY, x);
+    row_probabilities<LANES, VPT, false>(a.sigmoid, x, none);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) acc[j] += x[j];
+    if (on) {
+      valid += sub == 0;
+      for (int k = sub; k < a.topk; k += LANES) {
+        const int64_t at = static_cast<int64_t>(t) * a.chosen_stride + k;
+        const int64_t id = a.chosen_bytes == 4 ? static_cast<const int32_t*>(a.chosen)[at]
+                                               : static_cast<const int64_t*>(a.chosen)[at];
+        if (id >= 0 && id < a.experts)
+          atomicAdd(&s_cnt[id], 1);
+        else if (id != -1)
+          bad = 1;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) s_sum[group * kCols + column<LANES>(sub, j)] = acc[j];
+  if (valid) atomicAdd(&s_val, valid);
+  if (bad) s_flag = 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.experts; i += kThreads) {
+    float v = 0.f;
+    for (int g = 0; g < kGroups; ++g) v += s_sum[g * kCols + i];
+    a.psum[static_cast<int64_t>(item) * a.experts + i] = v;
+    a.pcnt[static_cast<int64_t>(item) * a.experts + i] = s_cnt[i];
+  }
+  if (threadIdx.x == 0) {
+    a.pval[item] = s_val;
+    a.pflag[item] = s_flag;
+  }
+}
+
+__device__ __forceinline__ int block_sum(int v, int* s_warp) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s_warp[threadIdx.x & 31];
+  return __reduce_add_sync(0xffffffffu, v);
+}
+
+// One block per (sequence, 32 experts): adds the chunks' partial rows, writes
+// the load, adds the counts; the last block to finish adds the loss.
+__global__ void __launch_bounds__(kFinThreads) k_balance_finalize(const __grid_constant__ BalanceArgs a) {
+  __shared__ float s_f[32][33];
+  __shared__ int s_i[32][33];
+  __shared__ int s_warp[32];
+  __shared__ int s_last;
+  griddep_wait();
+  const int eblocks = (a.experts + 31) / 32;
+  const int s = blockIdx.x / eblocks, eb = blockIdx.x % eblocks;
+  const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int e = eb * 32 + col;
+  int all = 0, bad = 0;
+  for (int i = threadIdx.x; i < a.items; i += kFinThreads) {
+    all += a.pval[i];
+    bad |= a.pflag[i];
+  }
+  const int total = block_sum(all, s_warp);
+  const int b = seq_at(a, s), end = seq_at(a, s + 1);
+  float p = 0.f;
+  int c = 0, mine = 0;
+  if (b < end) {
+    const int i0 = b / a.chunk + s, i1 = min((end - 1) / a.chunk + s, a.items - 1);
+    if (e < a.experts)
+      for (int i = i0 + row; i <= i1; i += 32) {
+        p += a.psum[static_cast<int64_t>(i) * a.experts + e];
+        c += a.pcnt[static_cast<int64_t>(i) * a.experts + e];
+      }
+    for (int i = i0 + threadIdx.x; i <= i1; i += kFinThreads) mine += a.pval[i];
+  }
+  const int n = block_sum(mine, s_warp);
+  s_f[row][col] = p;
+  s_i[row][col] = c;
+  __syncthreads();
+  float contrib = 0.f;
+  if (row == 0) {
+    p = 0.f;
+    c = 0;
+    for (int r = 0; r < 32; ++r) {
+      p += s_f[r][col];
+      c += s_i[r][col];
+    }
+    if (e < a.experts) {
+      const float scale = n == 0 ? 0.f
+                                 : a.coef / static_cast<float>(total) *
+                                       (static_cast<float>(a.experts) /
+                                        (static_cast<float>(a.topk) * static_cast<float>(n)));
+      const float f = scale * static_cast<float>(c);
+      a.load[static_cast<int64_t>(s) * a.experts + e] = f;
+      if (c) atomicAdd(a.counts + e, c);
+      contrib = f * p;
+    }
+    contrib = group_sum<32>(contrib);
+    if (col == 0) a.lossp[blockIdx.x] = contrib;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  float v = 0.f;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinThreads) v += __ldcg(a.lossp + i);
+  // bounds that do not ascend within [0, tokens]
+  if (a.seq_begin != nullptr)
+    for (int i = threadIdx.x; i <= a.sequences; i += kFinThreads) {
+      const int at = a.seq_begin[i];
+      if (at < 0 || at > a.tokens || (i > 0 && at < a.seq_begin[i - 1])) bad = 1;
+    }
+  v = group_sum<32>(v);
+  bad = __any_sync(0xffffffffu, bad);
+  if (col == 0) {
+    s_f[0][row] = v;
+    s_i[0][row] = bad;
+  }
+  __syncthreads();
+  if (row == 0) {
+    v = group_sum<32>(s_f[0][col]);
+    bad = __any_sync(0xffffffffu, s_i[0][col]);
+    if (col == 0) {
+      *a.loss = v;
+      *a.status = bad ? MUON_FLAG_INDEX : 0u;
+    }
+  }
+}
+
+template <int LANES, int VPT>
+__device__ __forceinline__ void store_row(const BalanceArgs& a, int64_t off, int sub,
+                                          const float (&d)[VPT]) {
+#pragma unroll
+  for (int q = 0; q < VPT / 4; ++q) {
+    const int c = column<LANES>(sub, 4 * q);
+    if (a.dvec) {
+      if (c >= a.experts) continue;
+      if (a.ddt == MUON_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + off + c);
+        float4 v = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
+        if (a.accumulate) {
+          const float4 o = *p;
+          v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+        }
+        *p = v;
+      } else {
+        uint2* p = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.dlogits) + off + c);
+        float v[4] = {d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        if (a.accumulate) {
+          const uint2 o = *p;
+          const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
+          const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
+          v[0] += f0.x; v[1] += f0.y; v[2] += f1.x; v[3] += f1.y;
+        }
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[0], v[1]);
+        const __nv_bfloat162 h1 = __floats2bfloat162_rn(v[2], v[3]);
+        *p = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (c + k >= a.experts) continue;
+        if (a.ddt == MUON_F32) {
+          float* p = static_cast<float*>(a.dlogits) + off + c + k;
+          *p = a.accumulate ? *p + d[4 * q + k] : d[4 * q + k];
+        } else {
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.dlogits) + off + c + k;
+          *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + d[4 * q + k] : d[4 * q + k]);
+        }
+      }
+    }
+  }
+}
+
+constexpr int kRowsPerGroup = 8;   // consecutive rows steps a group keeps its sequence's load for
+
+template <int LANES, int VPT>
+__global__ void __launch_bounds__(kThreads) k_balance_backward(const __grid_constant__ BalanceArgs a) {
+  constexpr int kGroups = kThreads / LANES;
+  const int group = threadIdx.x / LANES, sub = threadIdx.x % LANES;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * kRowsPerGroup);
+  const float scale = a.dloss == nullptr ? 1.f : *a.dloss;
+  int s = -2, s_end = 0;
+  float f[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) f[j] = 0.f;
+  for (int r = 0; r < kRowsPerGroup; ++r) {
+    const int64_t t64 = first + static_cast<int64_t>(r) * kGroups + group;
+    const bool in = t64 < a.tokens;
+    const int t = in ? static_cast<int>(t64) : a.tokens - 1;
+    if (s == -2 || t >= s_end) {
+      s = seq_of_token(a, t);
+      s_end = s + 1 <= a.sequences ? seq_at(a, s + 1) : a.tokens;
+      const bool inside = s >= 0 && t < s_end;
+      if (!inside) s_end = t;   // between sequences: look again at the next token
+      load_row<LANES, VPT>(a.load, static_cast<int64_t>(inside ? s : 0) * a.experts, MUON_F32,
+                           inside ? a.experts : 0, a.experts % 4 == 0 && (reinterpret_cast<uintptr_t>(a.load) & 15) == 0,
+                           sub, 0.f, f);
+      if (!inside) s = -2;
+    }
+    const bool on = in && s >= 0 && (a.mask == nullptr || a.mask[t] != 0);
+    float x[VPT], slope[VPT];
+    load_row<LANES, VPT>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
+                         on ? a.experts : 0, a.vec, sub, -INFINITY, x);
+    row_probabilities<LANES, VPT, true>(a.sigmoid, x, slope);
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) dot = fmaf(f[j], x[j], dot);
+    dot = group_sum<LANES>(dot);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float d = scale * x[j] * (f[j] - dot);
+      if (a.sigmoid) d *= slope[j];
+      x[j] = on ? d : 0.f;
+    }
+    if (in && (on || !a.accumulate))
+      store_row<LANES, VPT>(a, static_cast<int64_t>(t) * a.dlogits_stride, sub, x);
+  }
+}
+
+// Lanes and values a row takes: the narrowest that holds it.
+template <template <int, int> class F>
+cudaError_t by_width(const BalanceArgs& a, cudaStream_t st) {
+  if (a.experts <= 32) return F<8, 4>::run(a, st);
+  if (a.experts <= 64) return F<16, 4>::run(a, st);
+  if (a.experts <= 128) return F<32, 4>::run(a, st);
+  if (a.experts <= 256) return F<32, 8>::run(a, st);
+  if (a.experts <= 512) return F<32, 16>::run(a, st);
+  return F<32, 32>::run(a, st);
+}
+
+template <int LANES, int VPT>
+struct Forward {
+  static cudaError_t run(const BalanceArgs& a, cudaStream_t st) {
+    k_balance_forward<LANES, VPT><<<a.items, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+template <int LANES, int VPT>
+struct Backward {
+  static cudaError_t run(const BalanceArgs& a, cudaStream_t st) {
+    const int64_t rows = (kThreads / LANES) * kRowsPerGroup;
+    k_balance_backward<LANES, VPT>
+        <<<static_cast<unsigned>((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct Layout {
+  size_t psum, pcnt, pval, pflag, lossp, total;
+};
+
+Layout layout(int64_t tokens, int experts, int sequences) {
+  const size_t items = static_cast<size_t>(chunk_items(tokens, sequences));
+  Layout l;
+  l.psum = kHeader;
+  l.pcnt = l.psum + align256(items * experts * 4);
+  l.pval = l.pcnt + align256(items * experts * 4);
+  l.pflag = l.pval + align256(items * 4);
+  l.lossp = l.pflag + align256(items * 4);
+  l.total = l.lossp + align256(static_cast<size_t>(sequences) * ((experts + 31) / 32) * 4);
+  return l;
+}
+
+int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+
+bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Rows that may be read (or written) four values at a time.
+int vectorised(const void* p, int dtype, int64_t stride, int n) {
+  return n % 4 == 0 && stride % 4 == 0 && at_multiple(p, 4 * esize(dtype));
+}
+
+muon_status_t check_sizes(int64_t tokens, int experts, int sequences) {
+  if (tokens < 0 || experts < 1 || sequences < 1) return MUON_ERR_INVALID_ARG;
+  if (experts > kMaxExperts || tokens >= (int64_t{1} << 31) - (1 << 20) || sequences > (1 << 20))
+    return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+muon_status_t check_balance(const muon_balance_t* b) {
+  if (b == nullptr) return MUON_ERR_INVALID_ARG;
+  const muon_status_t s = check_sizes(b->tokens, b->experts, b->sequences);
+  if (s != MUON_OK) return s;
+  if (b->dtype != MUON_BF16 && b->dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
+  if (b->score != MUON_SCORE_SOFTMAX && b->score != MUON_SCORE_SIGMOID) return MUON_ERR_INVALID_ARG;
+  if (b->logits_stride < b->experts) return MUON_ERR_INVALID_ARG;
+  if (b->tokens > 0 && b->logits == nullptr) return MUON_ERR_INVALID_ARG;
+  if (b->seq_begin == nullptr && b->sequences != 1) return MUON_ERR_INVALID_ARG;
+  if (!at_multiple(b->logits, esize(b->dtype)) || !at_multiple(b->seq_begin, 4))
+    return MUON_ERR_MISALIGNED;
+  return MUON_OK;
+}
+
+BalanceArgs base_args(const muon_balance_t* b) {
+  BalanceArgs a{};
+  a.tokens = static_cast<int>(b->tokens);
+  a.experts = b->experts;
+  a.topk = b->topk;
+  a.sequences = b->sequences;
+  a.chunk = chunk_tokens(b->tokens);
+  a.items = static_cast<int>(chunk_items(b->tokens, b->sequences));
+  a.logits = b->logits;
+  a.dtype = b->dtype;
+  a.logits_stride = b->logits_stride;
+  a.chosen = b->chosen;
+  a.chosen_bytes = b->chosen_bytes;
+  a.chosen_stride = b->chosen_stride;
+  a.seq_begin = b->seq_begin;
+  a.mask = b->token_mask;
+  a.sigmoid = b->score == MUON_SCORE_SIGMOID;
+  a.coef = b->coef;
+  a.vec = vectorised(b->logits, b->dtype, b->logits_stride, b->experts);
+  return a;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status_t muon_balance_workspace_size(int64_t tokens, int experts, int sequences,
+                                          size_t* bytes) {
+  if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  const muon_status_t s = check_sizes(tokens, experts, sequences);
+  if (s != MUON_OK) return s;
+  *bytes = layout(tokens, experts, sequences).total;
+  return MUON_OK;
+}
+
+muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t* counts,
+                                   float* load, void* workspace, size_t workspace_bytes,
+                                   muon_stream_t stream) {
+  muon_status_t s = check_balance(b);
+  if (s != MUON_OK) return s;
+  if (b->topk < 1 || b->topk > b->experts || !std::isfinite(b->coef)) return MUON_ERR_INVALID_ARG;
+  if (b->chosen_bytes != 4 && b->chosen_bytes != 8) return MUON_ERR_INVALID_ARG;
+  if (b->chosen_stride < b->topk || (b->tokens > 0 && b->chosen == nullptr))
+    return MUON_ERR_INVALID_ARG;
+  if (loss == nullptr || counts == nullptr || load == nullptr || workspace == nullptr)
+    return MUON_ERR_INVALID_ARG;
+  if (!at_multiple(b->chosen, b->chosen_bytes) || !at_multiple(loss, 4) ||
+      !at_multiple(counts, 4) || !at_multiple(load, 4) || !at_multiple(workspace, 256))
+    return MUON_ERR_MISALIGNED;
+  const Layout l = layout(b->tokens, b->experts, b->sequences);
+  if (workspace_bytes < l.total) return MUON_ERR_WORKSPACE_TOO_SMALL;
+
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  BalanceArgs a = base_args(b);
+  a.psum = reinterpret_cast<float*>(ws + l.psum);
+  a.pcnt = reinterpret_cast<int*>(ws + l.pcnt);
+  a.pval = reinterpret_cast<int*>(ws + l.pval);
+  a.pflag = reinterpret_cast<int*>(ws + l.pflag);
+  a.lossp = reinterpret_cast<float*>(ws + l.lossp);
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.ticket = reinterpret_cast<int*>(ws) + 1;
+  a.loss = loss;
+  a.counts = counts;
+  a.load = load;
+  const double rows = static_cast<double>(b->tokens);
+  prof_begin(kKindBalance, st);
+  cudaError_t e = by_width<Forward>(a, st);
+  prof_end(kKindBalance, st, 0.0,
+           rows * (b->experts * esize(b->dtype) + b->topk * b->chosen_bytes));
+  if (e != cudaSuccess) return MUON_ERR_CUDA;
+  // a programmatic dependent of the first kernel (it waits for the partial rows)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(b->sequences) * ((b->experts + 31) / 32));
+  cfg.blockDim = dim3(kFinThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  prof_begin(kKindBalance, st);
+  e = cudaLaunchKernelEx(&cfg, k_balance_finalize, a);
+  prof_end(kKindBalance, st, 0.0, 4.0 * b->sequences * b->experts);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+muon_status_t muon_balance_backward(const muon_balance_t* b, const float* load,
+                                    const float* dloss, void* dlogits, muon_dtype_t ddt,
+                                    int64_t dlogits_stride, int accumulate,
+                                    muon_stream_t stream) {
+  const muon_status_t s = check_balance(b);
+  if (s != MUON_OK) return s;
+  if (ddt != MUON_BF16 && ddt != MUON_F32) return MUON_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return MUON_ERR_INVALID_ARG;
+  if (dlogits_stride < b->experts || load == nullptr || (b->tokens > 0 && dlogits == nullptr))
+    return MUON_ERR_INVALID_ARG;
+  if (!at_multiple(load, 4) || !at_multiple(dloss, 4) || !at_multiple(dlogits, esize(ddt)))
+    return MUON_ERR_MISALIGNED;
+  if (b->tokens == 0) return MUON_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  BalanceArgs a = base_args(b);
+  a.load = const_cast<float*>(load);
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.ddt = ddt;
+  a.dlogits_stride = dlogits_stride;
+  a.dvec = vectorised(dlogits, ddt, dlogits_stride, b->experts);
+  a.accumulate = accumulate;
+  prof_begin(kKindBalance, st);
+  const cudaError_t e = by_width<Backward>(a, st);
+  prof_end(kKindBalance, st, 0.0,
+           static_cast<double>(b->tokens) * b->experts *
+               (esize(b->dtype) + esize(ddt) * (accumulate ? 2 : 1)));
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -157,6 +157,10 @@ enum KernelKind : int {
   kKindAdamW,
   kKindGramPoly,
   kKindChain,
+  kKindBalance,
+  kKindAct8,
+  kKindSwiglu,
+  kKindWeightGrad,
   kKindCount
 };
 void prof_begin(KernelKind k, cudaStream_t st);
@@ -191,6 +195,9 @@ struct AdamWScalars {
 
 cudaError_t launch_adamw(AdamWGroupArgs* groups, int n_groups, const AdamWScalars& s,
                          uint32_t* flags, cudaStream_t st);
+
+// Limit of the bounded device waits (muon_set_wait_timeout_ns).
+uint64_t wait_timeout_ns();
 
 cudaError_t launch_wait_timeout_check(uint32_t* status, uint64_t timeout_ns, cudaStream_t st);
 cudaError_t launch_occupy(int blocks, size_t smem_bytes, uint64_t ns, cudaStream_t st);

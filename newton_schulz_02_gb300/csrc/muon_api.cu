@@ -315,6 +315,8 @@ muon_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
 
 }  // namespace
 
+uint64_t muon::wait_timeout_ns() { return g_timeout_ns.load(); }
+
 extern "C" {
 
 muon_status_t muon_ns_hybrid_schedule(muon_ns_schedule_t* out) {

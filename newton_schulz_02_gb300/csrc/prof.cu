@@ -27,7 +27,8 @@ struct Pending {
 
 const char* const kNames[kKindCount] = {"prepare", "finalize_norm", "ns_gram", "ns_poly",
                                         "ns_update", "apply", "timeout_check", "adamw",
-                                        "ns_gram_poly", "ns_chain"};
+                                        "ns_gram_poly", "ns_chain", "balance", "act8", "act8_swiglu",
+                                        "act8_weight_grad"};
 
 std::mutex g_mu;
 bool g_timing = false;

@@ -1,0 +1,190 @@
+"""Refusals of the balance, checkpoint, gated-activation and weight-gradient
+entry points, struct layouts and workspace sizes (no GPU: every case returns
+before the library touches CUDA)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import newton_schulz_02_gb300 as m
+from newton_schulz_02_gb300 import build as nbuild
+from tests.conftest import ROOT
+
+INVALID, MISALIGNED, UNSUPPORTED, SMALL = (m.MUON_ERR_INVALID_ARG, m.MUON_ERR_MISALIGNED,
+                                           m.MUON_ERR_UNSUPPORTED, m.MUON_ERR_WORKSPACE_TOO_SMALL)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    nbuild.build()
+    return m.load_library()
+
+
+def test_struct_layouts_match_c(tmp_path):
+    structs = ["muon_balance_t", "muon_act8_t", "muon_weight_grad_t"]
+    lines = [f'printf("{s} %zu\\n", sizeof({s}));' for s in structs]
+    lines += [f'printf("{s}.{f[0]} %zu\\n", offsetof({s}, {f[0]}));'
+              for s in structs for f in getattr(m, s)._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "muon.h"\nint main(void){'
+                   + "".join(lines) + "return 0;}\n")
+    exe = tmp_path / "layout"
+    subprocess.check_call(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o",
+                           str(exe)])
+    for line in subprocess.check_output([str(exe)], text=True).splitlines():
+        key, val = line.split()
+        s, _, f = key.partition(".")
+        got = getattr(getattr(m, s), f).offset if f else ctypes.sizeof(getattr(m, s))
+        assert got == int(val), key
+
+
+def changed(c, **kw):
+    d = type(c).from_buffer_copy(c)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def balance(**kw):
+    b = m.muon_balance_t(100, 16, 2, 0x10000, m.MUON_BF16, 16, 0x20000, 4, 2, 3, 0x30000, None,
+                         m.MUON_SCORE_SOFTMAX, 0.01)
+    return changed(b, **kw)
+
+
+def test_balance_refusals(lib):
+    need = m.muon_balance_workspace_size(100, 16, 3)
+
+    def fwd(b, loss=0x40000, counts=0x50000, load=0x60000, ws=0x100000, n=need):
+        return lib.muon_balance_forward(ctypes.byref(b), loss, counts, load, ws, n, None)
+
+    def bwd(b, load=0x60000, dloss=None, dl=0x70000, ddt=m.MUON_BF16, stride=16, acc=0):
+        return lib.muon_balance_backward(ctypes.byref(b), load, dloss, dl, ddt, stride, acc, None)
+
+    for bad in (dict(tokens=-1), dict(experts=0), dict(sequences=0), dict(dtype=7), dict(score=2),
+                dict(logits_stride=15), dict(logits=None), dict(seq_begin=None)):
+        assert fwd(balance(**bad)) == INVALID and bwd(balance(**bad)) == INVALID, bad
+    for bad in (dict(topk=0), dict(topk=17), dict(chosen_bytes=2), dict(chosen_stride=1),
+                dict(chosen=None), dict(coef=float("nan"))):
+        assert fwd(balance(**bad)) == INVALID, bad
+    for big in (dict(experts=1025, logits_stride=1025), dict(tokens=1 << 31)):
+        assert fwd(balance(**big)) == UNSUPPORTED and bwd(balance(**big), stride=2000) == UNSUPPORTED
+    assert fwd(balance(), loss=None) == INVALID and fwd(balance(), load=None) == INVALID
+    assert fwd(balance(), counts=None) == INVALID and fwd(balance(), ws=None) == INVALID
+    assert fwd(balance(), ws=0x100010) == MISALIGNED and fwd(balance(), n=need - 1) == SMALL
+    assert fwd(balance(logits=0x10001)) == MISALIGNED and fwd(balance(chosen=0x20002)) == MISALIGNED
+    assert fwd(balance(seq_begin=0x30002)) == MISALIGNED
+    assert bwd(balance(), ddt=5) == INVALID and bwd(balance(), acc=2) == INVALID
+    assert bwd(balance(), stride=15) == INVALID and bwd(balance(), dl=None) == INVALID
+    assert bwd(balance(), dl=0x70001) == MISALIGNED and bwd(balance(), dloss=0x70002) == MISALIGNED
+    assert lib.muon_balance_forward(None, 0, 0, 0, 0, 0, None) == INVALID
+    # a backward pass over no tokens enqueues nothing
+    assert bwd(balance(tokens=0, logits=None, chosen=None), dl=None) == m.MUON_OK
+    assert lib.muon_balance_workspace_size(10, 4, 1, None) == INVALID
+
+
+def act8(**kw):
+    return changed(m.muon_act8_t(8, 100, 0x10000, 128, 0x20000, 16), **kw)
+
+
+def test_act8_refusals(lib):
+    r = ctypes.byref
+    pack = lambda a, x=0x40000, dt=m.MUON_BF16, s=100: lib.muon_act8_pack(x, dt, s, r(a), None)
+    unpack = lambda a, x=0x40000, dt=m.MUON_BF16, s=100: lib.muon_act8_unpack(r(a), x, dt, s, None)
+    for f in (pack, unpack):
+        for bad in (dict(rows=-1), dict(cols=0), dict(code_stride=96), dict(codes=None),
+                    dict(exps=None), dict(exp_stride=3)):
+            assert f(act8(**bad)) == INVALID, bad
+        for bad in (dict(code_stride=130), dict(exp_stride=17), dict(codes=0x10008),
+                    dict(exps=0x20004)):
+            assert f(act8(**bad)) == MISALIGNED, bad
+        assert f(act8(), dt=3) == INVALID and f(act8(), s=99) == INVALID
+        assert f(act8(), x=None) == INVALID and f(act8(), x=0x40001) == MISALIGNED
+        assert f(act8(cols=(1 << 26) + 1, code_stride=1 << 27, exp_stride=1 << 22)) == UNSUPPORTED
+        assert f(act8(rows=0, codes=None, exps=None), x=None) == m.MUON_OK
+
+
+def test_swiglu_refusals(lib):
+    r = ctypes.byref
+
+    def fwd(g8=act8(), u8=act8(), gate=0x40000, up=0x50000, h=0x60000, gs=100, us=100, hs=100, dt=0):
+        return lib.muon_act8_swiglu_forward(gate, gs, up, us, dt, h, hs, r(g8), r(u8), None)
+
+    def bwd(g8=act8(), u8=act8(), h8=act8(), dh=0x40000, dg=0x50000, du=0x60000, s=100, dt=0):
+        return lib.muon_act8_swiglu_backward(dh, s, dt, r(g8), r(u8), dg, 100, du, 100,
+                                             None if h8 is None else r(h8), None)
+
+    for bad in (dict(g8=act8(rows=7)), dict(u8=act8(cols=99)), dict(dt=2), dict(g8=act8(codes=None))):
+        assert fwd(**bad) == INVALID and bwd(**bad) == INVALID, bad
+    for bad in (dict(gate=None), dict(up=None), dict(h=None), dict(gs=99), dict(us=0), dict(hs=-1)):
+        assert fwd(**bad) == INVALID, bad
+    for bad in (dict(dh=None), dict(dg=None), dict(du=None), dict(s=99), dict(h8=act8(rows=9)),
+                dict(h8=act8(exps=None))):
+        assert bwd(**bad) == INVALID, bad
+    assert fwd(h=0x60001) == MISALIGNED and bwd(du=0x60001) == MISALIGNED
+    assert bwd(u8=act8(exps=0x20001)) == MISALIGNED
+    none = act8(rows=0, codes=None, exps=None)
+    assert fwd(none, none, None, None, None) == m.MUON_OK
+    assert bwd(none, none, None, None, None, None) == m.MUON_OK
+
+
+def test_weight_grad_refusals(lib):
+    base = m.muon_weight_grad_t(8, 64, 2, 0x40000, m.MUON_BF16, 64, act8(), 0x50000, None, 0x60000,
+                                6400, 100, m.MUON_BF16, 0)
+    nb = ctypes.c_size_t()
+    assert lib.muon_act8_weight_grad_workspace_size(ctypes.byref(base), ctypes.byref(nb)) == m.MUON_OK
+
+    def call(ws=0x100000, n=nb.value, **kw):
+        return lib.muon_act8_weight_grad(ctypes.byref(changed(base, **kw)), ws, n, None)
+
+    for bad in (dict(rows=-1), dict(out=0), dict(experts=0), dict(dy_dtype=2), dict(g_dtype=9),
+                dict(rows=9), dict(dy=None), dict(dy_stride=63), dict(g_stride=99),
+                dict(accumulate=2), dict(offsets=None), dict(g_base=None),
+                dict(x=act8(codes=None)), dict(x=act8(code_stride=96)), dict(x=act8(exp_stride=3))):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(dy=0x40001), dict(offsets=0x50002), dict(g_base=0x60001),
+                dict(x=act8(codes=0x10004)), dict(x=act8(exp_stride=20)), dict(g_ptrs=0x70004)):
+        assert call(**bad) == MISALIGNED, bad
+    assert call(ws=None) == INVALID and call(ws=0x100010) == MISALIGNED
+    assert call(n=nb.value - 1) == SMALL
+    assert call(experts=70000) == UNSUPPORTED
+    assert lib.muon_act8_weight_grad(None, 0x100000, 256, None) == INVALID
+    assert lib.muon_act8_weight_grad_workspace_size(ctypes.byref(base), None) == INVALID
+
+
+def test_binding_refusals(lib):
+    """What the binding itself refuses, on CPU tensors (nothing is enqueued)."""
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        m.Balance(z(4, 8, dtype=torch.float16), z(4, 2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        m.Balance(z(4, 8), z(3, 2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        m.Balance(z(4, 8), z(4, 2, dtype=torch.int16))
+    with pytest.raises(ValueError):
+        m.Balance(z(8, 4).t(), z(4, 2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        m.Balance(z(4, 8), z(4, 2, dtype=torch.int64), mask=z(5, dtype=torch.bool))
+    with pytest.raises(ValueError):
+        m.Balance(z(4, 8), z(4, 2, dtype=torch.int64), seq_begin=z(3))
+    a = m.act8_empty(4, 70, device="cpu")
+    assert a.codes.shape == (4, 96) and a.exps.shape == (4, 16) and a.shape == (4, 70)
+    with pytest.raises(ValueError):
+        m.muon_act8_pack(z(4, 71), a, stream=0)
+    with pytest.raises(ValueError):
+        m.muon_act8_pack(z(4, 70, dtype=torch.float64), a, stream=0)
+    with pytest.raises(ValueError):
+        m.muon_act8_swiglu_forward(z(4, 70), z(4, 70, dtype=torch.bfloat16), z(4, 70), a, a, stream=0)
+    with pytest.raises(ValueError):
+        m.Act8(z(4, 96, dtype=torch.uint8), a.exps, 70)
+    with pytest.raises(ValueError):
+        m.Act8(a.codes, a.exps, 97)
+    ws = z(512, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        m.muon_act8_weight_grad(z(4, 8), a, z(2, 8, 71), ws, stream=0)
+    with pytest.raises(ValueError):
+        m.muon_act8_weight_grad(z(3, 8), a, z(2, 8, 70), ws, stream=0)
+    with pytest.raises(ValueError):
+        m.muon_act8_weight_grad(z(4, 8), a, z(2, 8, 70), ws, stream=0,
+                                offsets=z(2, dtype=torch.int32))
