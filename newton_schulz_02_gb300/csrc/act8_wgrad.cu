@@ -3,15 +3,35 @@
 //
 //   G_e[o][i] = sum_{t in expert e} dy[t][o] * code[t][i] * 2^(e[t][i/32])
 //
-// A block computes a 64 x 64 tile of one expert's G: 16 tokens at a time of
-// dy and of the decoded x go through shared memory, each thread accumulates
-// 4 x 4 sums in fp32.
+// A code's value has at most 7 significant bits, so it is exact in bf16 and
+// the product runs on the bf16 tensor cores without losing anything of x:
+// dy^T (MN-major A) and x (MN-major B), contracted over the tokens, fp32
+// accumulators in tensor memory.
+//
+// k_wgrad_pair: a CTA pair computes 256 x 256 of G (tcgen05 cta_group::2; each
+// CTA holds 128 output columns of dy and 128 input columns of x).  Per 64
+// tokens one thread fetches the dy tile, the codes and the exponents by TMA;
+// eight warps turn the codes into the swizzled bf16 operand (2.5 operations a
+// code); one thread of the pair issues the MMAs; eight warps drain the
+// accumulators, of which there are two, while the next tile runs.  The ranges
+// of tokens are ragged: rows of the last block that belong to the next expert
+// are zeroed in both operands (a zero times their NaN would be NaN).
+//
+// k_wgrad_simt (fp32 dy, rows of dy off the 16-byte boundaries TMA needs): a
+// block computes a 64 x 64 tile in fp32, 16 tokens at a time through shared
+// memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace muon {
 namespace {
@@ -34,8 +54,10 @@ struct WgradArgs {
   void* g_base;
   int64_t g_batch_stride, g_stride;
   int g_dtype, accumulate;
-  int tiles_o, tiles_i;
+  int tiles_o, tiles_i;   // 256 x 256 tiles of a matrix
+  int units;              // tiles of all experts
   uint32_t* status;
+  uint64_t timeout_ns;
 };
 
 __device__ __forceinline__ void span_of(const WgradArgs& a, int e, int& b, int& n) {
@@ -48,7 +70,7 @@ __device__ __forceinline__ void span_of(const WgradArgs& a, int e, int& b, int& 
   n = min(max(a.offsets[e + 1], b), a.rows) - b;
 }
 
-__global__ void __launch_bounds__(kThreads) k_act8_wgrad(const __grid_constant__ WgradArgs a) {
+__global__ void __launch_bounds__(kThreads) k_wgrad_simt(const __grid_constant__ WgradArgs a) {
   __shared__ float sy[kTok][kTile + 4], sx[kTok][kTile + 4];
   const int e = blockIdx.z;
   int begin, n;
@@ -115,6 +137,383 @@ __global__ void __launch_bounds__(kThreads) k_act8_wgrad(const __grid_constant__
     }
 }
 
+// ---- 256 x 256 tiles on CTA pairs -------------------------------------------
+constexpr int kBK = 64;                          // tokens per block of the contraction
+constexpr int kStages = 6;                       // dy, codes and exponents in flight
+constexpr int kSlots = 3;                        // decoded blocks
+constexpr int kConvWarps = 8, kEpiWarps = 8;
+constexpr int kPairThreads = 32 * (2 + kConvWarps + kEpiWarps);
+constexpr uint32_t kDyBytes = kBK * 128 * 2;     // two 64-column atoms of 128-byte rows
+constexpr uint32_t kCodeBytes = kBK * 128;
+constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four of them used
+constexpr uint32_t kStageBytes = kDyBytes + kCodeBytes + kExpBytes;
+constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
+constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
+constexpr size_t kPairSmem = kStages * kStageBytes + kSlots * kSlotBytes + 1024 + 512;
+constexpr uint32_t kTmemCols = 512;              // two accumulators of 256 columns
+// D fp32, A and B bf16, both MN-major, M = 256, N = 256
+constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, true) | (1u << 15);
+constexpr int kGroupO = 8;                       // tiles walked down before the next column
+
+// Unit u of the walk: expert, and the tile's first row and column.  Within an
+// expert, columns of kGroupO tiles are walked side by side, so that the tiles
+// in flight share operands in L2.
+struct Unit {
+  int e, o0, i0, begin, n;
+};
+
+__device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u) {
+  const int per = a.tiles_o * a.tiles_i;
+  Unit t;
+  t.e = u / per;
+  const int r = u - t.e * per;
+  const int band = r / (kGroupO * a.tiles_i);
+  const int rows = min(kGroupO, a.tiles_o - band * kGroupO);
+  const int q = r - band * kGroupO * a.tiles_i;
+  t.o0 = (band * kGroupO + q % rows) * 256;
+  t.i0 = (q / rows) * 256;
+  span_of(a, t.e, t.begin, t.n);
+  return t;
+}
+
+// Waits, like mbar_wait_bounded, for a barrier the pair's CTAs arrive on.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, uint32_t* status,
+                                           uint64_t timeout_ns) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity))
+    if (global_timer_ns() - t0 > timeout_ns) {
+      atomicOr(status, kFlagTimeout);
+      return;
+    }
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t* bar, int32_t x,
+                                            int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Two int8 codes in the low bytes of p's halves as bf16.  0x4300 is 128 in
+// bf16 and its 7 mantissa bits count units, so 0x4300 | (c & 127) is 128 + (c
+// & 127); what is subtracted is 128 for c >= 0 and 256 for c < 0, which
+// 0x4300 | (c & 128) spells.  Every step is exact.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t p, __nv_bfloat162 scale) {
+  const uint32_t hi = (p & 0x007F007Fu) | 0x43004300u;
+  const uint32_t lo = (p & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&lo)),
+                                   scale);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 consecutive columns of one row of G.
+__device__ __forceinline__ void store_chunk(const WgradArgs& a, void* g, bool vec, int o, int i,
+                                            float (&v)[32]) {
+  if (o >= a.out || i >= a.in) return;
+  const int64_t at = static_cast<int64_t>(o) * a.g_stride + i;
+  if (vec && i + 32 <= a.in) {
+    if (a.g_dtype == MUON_F32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(g) + at);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float4 w = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        if (a.accumulate) {
+          const float4 old = p[k];
+          w.x += old.x; w.y += old.y; w.z += old.z; w.w += old.w;
+        }
+        p[k] = w;
+      }
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g) + at);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (a.accumulate) {
+          const uint4 old = p[k];
+          const uint32_t w[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[8 * k + 2 * j] += __uint_as_float(w[j] << 16);
+            v[8 * k + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+        }
+        p[k] = make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]),
+                          pack2(v[8 * k + 4], v[8 * k + 5]), pack2(v[8 * k + 6], v[8 * k + 7]));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    if (i + k >= a.in) break;
+    if (a.g_dtype == MUON_F32) {
+      float* p = static_cast<float*>(g) + at + k;
+      *p = a.accumulate ? *p + v[k] : v[k];
+    } else {
+      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g) + at + k;
+      *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + v[k] : v[k]);
+    }
+  }
+}
+
+__device__ __forceinline__ void* matrix_of(const WgradArgs& a, int e) {
+  return a.g_ptrs != nullptr ? a.g_ptrs[e]
+                             : static_cast<char*>(a.g_base) +
+                                   e * a.g_batch_stride * (a.g_dtype == MUON_F32 ? 4 : 2);
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_wgrad_pair(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_codes,
+                 const __grid_constant__ CUtensorMap tm_exps, const __grid_constant__ WgradArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
+  uint8_t* sm_x = sm_dy + kStages * kDyBytes;               // decoded, swizzled
+  uint8_t* sm_codes = sm_x + kSlots * kSlotBytes;
+  uint8_t* sm_exps = sm_codes + kStages * kCodeBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm_exps + kStages * kExpBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* ready = empty + kStages;
+  uint64_t* tfull = ready + kSlots;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit0 = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);                   // this CTA's loads
+      mbar_init(&empty[s], 1);                  // the pair's MMA commit, multicast
+    }
+    for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], 2 * kConvWarps);   // both CTAs' warps
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t c = 0;   // blocks of 64 tokens since the start
+      bool ok = true;
+      for (int u = unit0; ok && u < a.units; u += step) {
+        const Unit t = unit_of(a, u);
+        const int o = t.o0 + static_cast<int>(rank) * 128, i = t.i0 + static_cast<int>(rank) * 128;
+        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+          const uint32_t s = c % kStages;
+          if (!mbar_wait_bounded(&empty[s], (c / kStages & 1u) ^ 1u, abort_flag, a.status,
+                                 a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], kStageBytes);
+          uint8_t* d = sm_dy + s * kDyBytes;
+          tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
+          tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
+          tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
+          tma_load_2d(sm_exps + s * kExpBytes, &tm_exps, &full[s], (i / 32) & ~15, t.begin + k0);
+        }
+      }
+      // every load has landed before the CTA exits
+      for (uint32_t k = c > kStages ? c - kStages : 0; k < c; ++k)
+        wait_drain(&full[k % kStages], k / kStages & 1u, a.status, a.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // -------------------------------------------------------- MMA issuer
+      uint32_t c = 0, tile = 0;
+      bool ok = true;
+      for (int u = unit0; ok && u < a.units; u += step) {
+        const Unit t = unit_of(a, u);
+        if (t.n == 0) continue;
+        const uint32_t acc = tile & 1u;
+        if (!mbar_wait_bounded(&tempty[acc], (tile >> 1 & 1u) ^ 1u, abort_flag, a.status,
+                               a.timeout_ns))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * 256u;
+        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+          const uint32_t s = c % kStages, b = c % kSlots;
+          if (!mbar_wait_acquire_cluster(&ready[b], c / kSlots & 1u, abort_flag, a.status,
+                                         a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(sm_dy + s * kDyBytes);
+          const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
+#pragma unroll
+          for (int ks = 0; ks < kBK / 16; ++ks)
+            tc_mma_bf16_pair(d, smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
+                             smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
+                             (k0 | ks) != 0 ? 1u : 0u);
+          tc_commit_pair_multicast(&empty[s], 0x3);
+        }
+        if (!ok) break;
+        tc_commit_pair_multicast(&tfull[acc], 0x3);
+        ++tile;
+      }
+      tc_commit_pair_multicast(drain, 0x1);
+      wait_drain(drain, 0, a.status, a.timeout_ns);
+    }
+  } else if (warp < 2 + kConvWarps) {
+    // ---------------------------------------------------------- converters
+    // Thread -> row r of the block and 32 columns (one exponent).  The halves
+    // of the 32 columns are taken in the order that makes the eight threads of
+    // a shared-memory phase hit eight different 16-byte columns, on the codes'
+    // side (rows of 128 bytes) as on the swizzled operand's.
+    const int ct = threadIdx.x - 64;
+    const int r = ct >> 2, j = ct & 3;
+    const int first = (j >> 1) ^ (r & 1);
+    const uint32_t ready0 = mapa_shared(&ready[0], 0);
+    const uint32_t atom = smem_u32(sm_x) + (j >> 1) * kAtomBytes + r * 128;
+    uint32_t c = 0;
+    for (int u = unit0; u < a.units; u += step) {
+      const Unit t = unit_of(a, u);
+      const int blk = (t.i0 + static_cast<int>(rank) * 128) / 32;
+      bool ok = true;
+      for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+        const uint32_t s = c % kStages, b = c % kSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], c / kStages & 1u, abort_flag,
+                                                       a.status, a.timeout_ns));
+        if (!ok) break;
+        const uint32_t e = sm_exps[s * kExpBytes + r * 16 + (blk & 15) + j];
+        const uint4* src = reinterpret_cast<const uint4*>(sm_codes + s * kCodeBytes + r * 128 + j * 32);
+        uint4 w[2];
+        w[0] = src[first];
+        w[1] = src[first ^ 1];
+        const int left = t.n - k0;
+        if (r >= left) {
+          w[0] = w[1] = make_uint4(0, 0, 0, 0);
+        }
+        // 2^(e - 127); a block that held something not finite (255) gives NaN
+        const uint32_t sb = r >= left ? 0x3F80u : e == 255u ? 0x7FC0u : e << 7;
+        const uint32_t sp = sb | sb << 16;
+        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&sp);
+        if (c >= kSlots) {   // the MMAs that read this slot are done
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&empty[(c - kSlots) % kStages],
+                                            (c - kSlots) / kStages & 1u, abort_flag, a.status,
+                                            a.timeout_ns));
+          if (!ok) break;
+        }
+        const uint32_t dst = atom + b * kSlotBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t q[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+          const int base = (j & 1) * 4 + ((h ^ first) << 1);   // 16-byte column before swizzling
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t v0 = codes_to_bf16(__byte_perm(q[2 * p], 0, 0x4140), scale);
+            const uint32_t v1 = codes_to_bf16(__byte_perm(q[2 * p], 0, 0x4342), scale);
+            const uint32_t v2 = codes_to_bf16(__byte_perm(q[2 * p + 1], 0, 0x4140), scale);
+            const uint32_t v3 = codes_to_bf16(__byte_perm(q[2 * p + 1], 0, 0x4342), scale);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             dst + (((base + p) ^ (r & 7)) << 4)),
+                         "r"(v0), "r"(v1), "r"(v2), "r"(v3)
+                         : "memory");
+          }
+        }
+        if (r >= left) {   // dy's rows of the next expert, this thread's quarter of the row
+          uint4* p = reinterpret_cast<uint4*>(sm_dy + s * kDyBytes + (j >> 1) * kAtomBytes + r * 128 +
+                                              (j & 1) * 64);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[k] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(ready0 + b * 8u);
+      }
+      if (!ok) break;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;                              // tensor-memory lanes 32 q ..
+    const int c0 = (warp - 2 - kConvWarps) >> 2;         // columns 128 c0 ..
+    const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
+    uint32_t tile = 0;
+    for (int u = unit0; u < a.units; u += step) {
+      const Unit t = unit_of(a, u);
+      const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      void* g = matrix_of(a, t.e);
+      const int esz = a.g_dtype == MUON_F32 ? 4 : 2;
+      const bool vec = (reinterpret_cast<uintptr_t>(g) & 15u) == 0 && a.g_stride * esz % 16 == 0;
+      if (t.n == 0) {   // an expert without tokens
+        if (!a.accumulate)
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            store_chunk(a, g, vec, o, t.i0 + c0 * 128 + ch * 32, v);
+          }
+        continue;
+      }
+      const uint32_t acc = tile & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile >> 1 & 1u, abort_flag,
+                                                     a.status, a.timeout_ns)))
+        break;
+      tc_fence_after();
+      const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + c0 * 128u;
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t raw[32];
+        tmem_ld_32x32b_x32(src + ch * 32, raw);
+        tmem_ld_wait(raw);
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
+        store_chunk(a, g, vec, o, t.i0 + c0 * 128 + ch * 32, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8u);
+      ++tile;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+  // offsets that do not ascend within [0, rows]
+  if (a.offsets != nullptr && blockIdx.x == 0)
+    for (int e = threadIdx.x; e < a.experts; e += kPairThreads)
+      if (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows)
+        atomicOr(a.status, MUON_FLAG_INDEX);
+}
+
 int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 
 bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -128,6 +527,99 @@ muon_status_t check_sizes(const muon_weight_grad_t* d) {
       d->experts > 65535)
     return MUON_ERR_UNSUPPORTED;
   return MUON_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A [rows][cols] operand of element size esz, boxes of box_cols x kBK rows.
+// Columns and rows past the operand's read as 0.
+bool map_rows(CUtensorMap* m, CUtensorMapDataType type, int esz, const void* base, int64_t rows,
+              int64_t cols, int64_t stride, int box_cols, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * esz};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), kBK};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that fit the current device at once (asked once per device).
+cudaError_t resident_pairs(int* out) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_wgrad_pair, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kPairSmem));
+  if (e != cudaSuccess) return e;
+  if (dev < kDevices && (*out = known[dev].load()) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad_pair, &cfg);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  if (dev < kDevices) known[dev].store(n);
+  *out = n;
+  return cudaSuccess;
+}
+
+cudaError_t launch_pair(const WgradArgs& a, cudaStream_t st) {
+  int pairs = 0;
+  cudaError_t e = resident_pairs(&pairs);
+  if (e != cudaSuccess) return e;
+  CUtensorMap dy{}, codes{}, exps{};
+  if (a.rows > 0) {
+    if (encode_fn() == nullptr) return cudaErrorNotSupported;
+    const int64_t blocks = (static_cast<int64_t>(a.in) + 31) / 32;
+    if (!map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dy, a.rows, a.out, a.dy_stride, 64,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_rows(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.codes, a.rows, a.in, a.code_stride, 128,
+                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !map_rows(&exps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.exps, a.rows, blocks, a.exp_stride, 16,
+                  CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min(a.units, pairs)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, k_wgrad_pair, dy, codes, exps, a);
+}
+
+cudaError_t launch_simt(const WgradArgs& a, cudaStream_t st) {
+  const dim3 grid((a.in + kTile - 1) / kTile, (a.out + kTile - 1) / kTile, a.experts);
+  k_wgrad_simt<<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -189,16 +681,22 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
   a.g_dtype = d->g_dtype;
   a.accumulate = d->accumulate;
   a.status = static_cast<uint32_t*>(workspace);
-  const dim3 grid((x.cols + kTile - 1) / kTile, (d->out + kTile - 1) / kTile, d->experts);
-  if (grid.y > 65535) return MUON_ERR_UNSUPPORTED;
+  a.timeout_ns = wait_timeout_ns();
+  a.tiles_o = (d->out + 255) / 256;
+  a.tiles_i = (x.cols + 255) / 256;
+  const int64_t units = static_cast<int64_t>(a.tiles_o) * a.tiles_i * d->experts;
+  if (units >= (int64_t{1} << 30)) return MUON_ERR_UNSUPPORTED;
+  a.units = static_cast<int>(units);
+  // TMA takes dy's rows where they start on 16-byte boundaries
+  const bool pair = d->dy_dtype == MUON_BF16 && at_multiple(d->dy, 16) && d->dy_stride % 8 == 0;
   const double rows = static_cast<double>(d->rows);
   prof_begin(kKindWeightGrad, st);
-  k_act8_wgrad<<<grid, kThreads, 0, st>>>(a);
+  const cudaError_t e = pair ? launch_pair(a, st) : launch_simt(a, st);
   prof_end(kKindWeightGrad, st, 2.0 * rows * d->out * x.cols,
            rows * (d->out * esize(d->dy_dtype) + x.cols * (1.0 + 1.0 / 32)) +
                static_cast<double>(d->experts) * d->out * x.cols * esize(d->g_dtype) *
                    (d->accumulate ? 2 : 1));
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 }  // extern "C"
