@@ -139,25 +139,28 @@ __global__ void __launch_bounds__(kThreads) k_wgrad_simt(const __grid_constant__
 
 // ---- 256 x 256 tiles on CTA pairs -------------------------------------------
 constexpr int kBK = 64;                          // tokens per block of the contraction
-constexpr int kStages = 6;                       // dy, codes and exponents in flight
-constexpr int kSlots = 3;                        // decoded blocks
-constexpr int kConvWarps = 8, kEpiWarps = 8;
-constexpr int kPairThreads = 32 * (2 + kConvWarps + kEpiWarps);
+constexpr int kDyStages = 6;                     // dy tiles in flight or in use
+constexpr int kCodeStages = 4;                   // codes and exponents in flight
+constexpr int kSlots = 4;                        // decoded blocks, one per group of converters
+constexpr int kConvWarps = 4, kEpiWarps = 8;     // converter warps of one group
+constexpr int kConv0 = 4, kEpi0 = kConv0 + kSlots * kConvWarps;   // first warps
+constexpr int kPairThreads = 32 * (kEpi0 + kEpiWarps);
 constexpr uint32_t kDyBytes = kBK * 128 * 2;     // two 64-column atoms of 128-byte rows
 constexpr uint32_t kCodeBytes = kBK * 128;
 constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four of them used
-constexpr uint32_t kStageBytes = kDyBytes + kCodeBytes + kExpBytes;
 constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
 constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
-constexpr size_t kPairSmem = kStages * kStageBytes + kSlots * kSlotBytes + 1024 + 512;
+constexpr int kUnits = 4;                        // units announced ahead
+constexpr size_t kPairSmem = kDyStages * kDyBytes + kSlots * kSlotBytes +
+                             kCodeStages * (kCodeBytes + kExpBytes) + 1024 + 512;
 constexpr uint32_t kTmemCols = 512;              // two accumulators of 256 columns
 // D fp32, A and B bf16, both MN-major, M = 256, N = 256
 constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, true) | (1u << 15);
 constexpr int kGroupO = 8;                       // tiles walked down before the next column
 
-// Unit u of the walk: expert, and the tile's first row and column.  Within an
-// expert, columns of kGroupO tiles are walked side by side, so that the tiles
-// in flight share operands in L2.
+// Unit u of the walk: expert (-1: no more), the tile's first row and column,
+// the expert's tokens.  Within an expert, columns of kGroupO tiles are walked
+// side by side, so that the tiles in flight share operands in L2.
 struct Unit {
   int e, o0, i0, begin, n;
 };
@@ -176,7 +179,38 @@ __device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u) {
   return t;
 }
 
-// Waits, like mbar_wait_bounded, for a barrier the pair's CTAs arrive on.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P1, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// mbar_wait_bounded for a barrier that the pair's other CTA arrives on too
+// (acquire at cluster scope); the timer is read only when the wait is not
+// over at once.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             uint32_t* status, uint64_t timeout_ns) {
+  const uint32_t a = smem_u32(bar);
+  if (try_wait_cluster(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (try_wait_cluster(a, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > timeout_ns) {
+      *abort = 1;
+      atomicOr(status, kFlagTimeout);
+      return false;
+    }
+  }
+}
+
+// Waits for what is still in flight when a role ends, whatever became of the others.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, uint32_t* status,
                                            uint64_t timeout_ns) {
   const uint32_t a = smem_u32(bar);
@@ -197,10 +231,10 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// Two int8 codes in the low bytes of p's halves as bf16.  0x4300 is 128 in
-// bf16 and its 7 mantissa bits count units, so 0x4300 | (c & 127) is 128 + (c
-// & 127); what is subtracted is 128 for c >= 0 and 256 for c < 0, which
-// 0x4300 | (c & 128) spells.  Every step is exact.
+// Codes 0 and 2 of the four int8 in p as a pair of bf16 (with p >> 8: codes 1
+// and 3).  0x4300 is 128 in bf16 and its 7 mantissa bits count units, so
+// 0x4300 | (c & 127) is 128 + (c & 127); what is subtracted is 128 for c >= 0
+// and 256 for c < 0, which 0x4300 | (c & 128) spells.  Every step is exact.
 __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t p, __nv_bfloat162 scale) {
   const uint32_t hi = (p & 0x007F007Fu) | 0x43004300u;
   const uint32_t lo = (p & 0x00800080u) | 0x43004300u;
@@ -210,49 +244,71 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t p, __nv_bfloat162 sca
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 16 lanes x 64 fp32 columns: registers 4b .. 4b+3 of lane l hold columns 8b +
+// 2 (l % 4) + {0, 1} of tensor-memory lane l / 4, then of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 consecutive columns of one row of G.
-__device__ __forceinline__ void store_chunk(const WgradArgs& a, void* g, bool vec, int o, int i,
-                                            float (&v)[32]) {
+// 16 consecutive columns of one row of G.
+__device__ __forceinline__ void store16(const WgradArgs& a, void* g, bool vec, int o, int i,
+                                        float (&v)[16]) {
   if (o >= a.out || i >= a.in) return;
   const int64_t at = static_cast<int64_t>(o) * a.g_stride + i;
-  if (vec && i + 32 <= a.in) {
+  if (vec && i + 16 <= a.in) {   // whole 32-byte sectors
     if (a.g_dtype == MUON_F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(g) + at);
+      float* p = static_cast<float*>(g) + at;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float4 w = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int k = 0; k < 16; k += 8) {
         if (a.accumulate) {
-          const float4 old = p[k];
-          w.x += old.x; w.y += old.y; w.z += old.z; w.w += old.w;
+          uint4 x, y;
+          ld_global_v8(p + k, x, y);
+          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[k + j] += __uint_as_float(w[j]);
         }
-        p[k] = w;
+        st_global_v8(p + k,
+                     make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
+                                __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])),
+                     make_uint4(__float_as_uint(v[k + 4]), __float_as_uint(v[k + 5]),
+                                __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7])));
       }
     } else {
-      uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g) + at);
+      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g) + at;
+      if (a.accumulate) {
+        uint4 x, y;
+        ld_global_v8(p, x, y);
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (a.accumulate) {
-          const uint4 old = p[k];
-          const uint32_t w[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[8 * k + 2 * j] += __uint_as_float(w[j] << 16);
-            v[8 * k + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-          }
+        for (int j = 0; j < 8; ++j) {
+          v[2 * j] += __uint_as_float(w[j] << 16);
+          v[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
         }
-        p[k] = make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]),
-                          pack2(v[8 * k + 4], v[8 * k + 5]), pack2(v[8 * k + 6], v[8 * k + 7]));
       }
+      st_global_v8(p,
+                   make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
+                              pack2(v[6], v[7])),
+                   make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]),
+                              pack2(v[14], v[15])));
     }
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
+  for (int k = 0; k < 16; ++k) {
     if (i + k >= a.in) break;
     if (a.g_dtype == MUON_F32) {
       float* p = static_cast<float*>(g) + at + k;
@@ -277,26 +333,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
-  uint8_t* sm_x = sm_dy + kStages * kDyBytes;               // decoded, swizzled
+  uint8_t* sm_x = sm_dy + kDyStages * kDyBytes;             // decoded, swizzled
   uint8_t* sm_codes = sm_x + kSlots * kSlotBytes;
-  uint8_t* sm_exps = sm_codes + kStages * kCodeBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm_exps + kStages * kExpBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* ready = empty + kStages;
-  uint64_t* tfull = ready + kSlots;
+  uint8_t* sm_exps = sm_codes + kCodeStages * kCodeBytes;
+  uint64_t* dy_full = reinterpret_cast<uint64_t*>(sm_exps + kCodeStages * kExpBytes);
+  uint64_t* dy_empty = dy_full + kDyStages;
+  uint64_t* code_full = dy_empty + kDyStages;
+  uint64_t* code_empty = code_full + kCodeStages;
+  uint64_t* ready = code_empty + kCodeStages;
+  uint64_t* unit_full = ready + kSlots;
+  uint64_t* unit_empty = unit_full + kUnits;
+  uint64_t* tfull = unit_empty + kUnits;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* sm_units = reinterpret_cast<int*>(drain + 2);   // [kUnits][8]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int unit0 = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);                   // this CTA's loads
-      mbar_init(&empty[s], 1);                  // the pair's MMA commit, multicast
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(&unit_full[s], 1);
+      // producers, converters, epilogue; the MMA issuer in the even CTA
+      mbar_init(&unit_empty[s], 2 + kSlots * kConvWarps + kEpiWarps + (rank == 0 ? 1 : 0));
+    }
+    for (int s = 0; s < kDyStages; ++s) {
+      mbar_init(&dy_full[s], 1);                // this CTA's loads
+      mbar_init(&dy_empty[s], 1);               // the pair's MMA commit, multicast
+    }
+    for (int s = 0; s < kCodeStages; ++s) {
+      mbar_init(&code_full[s], 1);
+      mbar_init(&code_empty[s], kConvWarps);    // read into registers
     }
     for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], 2 * kConvWarps);   // both CTAs' warps
     for (int s = 0; s < 2; ++s) {
@@ -318,40 +387,71 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
+  // One thread works out the units ahead of the other roles, which take them
+  // from a ring in the same order and number the blocks of 64 tokens c = 0, 1,
+  // ... since the start.
+  uint32_t taken = 0;
+  const auto take = [&](Unit& t, bool whole_warp) {
+    const uint32_t k = taken % kUnits;
+    bool ok = mbar_wait_bounded(&unit_full[k], taken / kUnits & 1u, abort_flag, a.status, a.timeout_ns);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    const int4 v = *reinterpret_cast<const int4*>(sm_units + 8 * k);
+    t.e = v.x;
+    t.o0 = v.y;
+    t.i0 = v.z;
+    t.begin = v.w;
+    t.n = sm_units[8 * k + 4];
+    if (whole_warp) __syncwarp();
+    if (lane == 0) mbar_arrive(&unit_empty[k]);
+    ++taken;
+    return t.e >= 0;
+  };
+
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      uint32_t c = 0;   // blocks of 64 tokens since the start
+      // ------------------------------------- producers: dy, codes + exponents
+      const bool is_dy = warp == 0;
+      uint64_t* full = is_dy ? dy_full : code_full;
+      uint64_t* empty = is_dy ? dy_empty : code_empty;
+      const uint32_t stages = is_dy ? kDyStages : kCodeStages;
+      uint32_t c = 0, s = 0, phase = 0;
       bool ok = true;
-      for (int u = unit0; ok && u < a.units; u += step) {
-        const Unit t = unit_of(a, u);
+      Unit t;
+      while (ok && take(t, false)) {
         const int o = t.o0 + static_cast<int>(rank) * 128, i = t.i0 + static_cast<int>(rank) * 128;
         for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-          const uint32_t s = c % kStages;
-          if (!mbar_wait_bounded(&empty[s], (c / kStages & 1u) ^ 1u, abort_flag, a.status,
-                                 a.timeout_ns)) {
+          if (!mbar_wait_bounded(&empty[s], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], kStageBytes);
-          uint8_t* d = sm_dy + s * kDyBytes;
-          tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
-          tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
-          tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
-          tma_load_2d(sm_exps + s * kExpBytes, &tm_exps, &full[s], (i / 32) & ~15, t.begin + k0);
+          if (is_dy) {
+            mbar_arrive_expect_tx(&full[s], kDyBytes);
+            uint8_t* d = sm_dy + s * kDyBytes;
+            tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
+            tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
+          } else {
+            mbar_arrive_expect_tx(&full[s], kCodeBytes + kExpBytes);
+            tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
+            tma_load_2d(sm_exps + s * kExpBytes, &tm_exps, &full[s], (i / 32) & ~15, t.begin + k0);
+          }
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
       // every load has landed before the CTA exits
-      for (uint32_t k = c > kStages ? c - kStages : 0; k < c; ++k)
-        wait_drain(&full[k % kStages], k / kStages & 1u, a.status, a.timeout_ns);
+      for (uint32_t k = c > stages ? c - stages : 0; k < c; ++k)
+        wait_drain(&full[k % stages], k / stages & 1u, a.status, a.timeout_ns);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // -------------------------------------------------------- MMA issuer
-      uint32_t c = 0, tile = 0;
+      uint32_t c = 0, s = 0, tile = 0;
       bool ok = true;
-      for (int u = unit0; ok && u < a.units; u += step) {
-        const Unit t = unit_of(a, u);
+      Unit t;
+      while (ok && take(t, false)) {
         if (t.n == 0) continue;
         const uint32_t acc = tile & 1u;
         if (!mbar_wait_bounded(&tempty[acc], (tile >> 1 & 1u) ^ 1u, abort_flag, a.status,
@@ -360,9 +460,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + acc * 256u;
         for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-          const uint32_t s = c % kStages, b = c % kSlots;
-          if (!mbar_wait_acquire_cluster(&ready[b], c / kSlots & 1u, abort_flag, a.status,
-                                         a.timeout_ns)) {
+          const uint32_t b = c % kSlots;
+          if (!wait_cluster(&ready[b], c / kSlots & 1u, abort_flag, a.status, a.timeout_ns)) {
             ok = false;
             break;
           }
@@ -374,7 +473,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc_mma_bf16_pair(d, smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
                              smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
                              (k0 | ks) != 0 ? 1u : 0u);
-          tc_commit_pair_multicast(&empty[s], 0x3);
+          tc_commit_pair_multicast(&dy_empty[s], 0x3);
+          if (++s == kDyStages) s = 0;
         }
         if (!ok) break;
         tc_commit_pair_multicast(&tfull[acc], 0x3);
@@ -383,115 +483,162 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc_commit_pair_multicast(drain, 0x1);
       wait_drain(drain, 0, a.status, a.timeout_ns);
     }
-  } else if (warp < 2 + kConvWarps) {
+  } else if (warp == 3) {
+    if (lane == 0) {
+      // ----------------------------------------------------------- walker
+      const int step = static_cast<int>(gridDim.x >> 1);
+      uint32_t k = 0;
+      for (int u = static_cast<int>(blockIdx.x >> 1);; u += step, ++k) {
+        Unit t{-1, 0, 0, 0, 0};
+        if (u < a.units) t = unit_of(a, u);
+        int* p = sm_units + 8 * (k % kUnits);
+        if (!mbar_wait_bounded(&unit_empty[k % kUnits], (k / kUnits & 1u) ^ 1u, abort_flag, a.status,
+                               a.timeout_ns))
+          break;
+        *reinterpret_cast<int4*>(p) = make_int4(t.e, t.o0, t.i0, t.begin);
+        p[4] = t.n;
+        mbar_arrive(&unit_full[k % kUnits]);
+        if (t.e < 0) break;
+      }
+    }
+  } else if (warp < kEpi0) {
     // ---------------------------------------------------------- converters
-    // Thread -> row r of the block and 32 columns (one exponent).  The halves
-    // of the 32 columns are taken in the order that makes the eight threads of
-    // a shared-memory phase hit eight different 16-byte columns, on the codes'
-    // side (rows of 128 bytes) as on the swizzled operand's.
-    const int ct = threadIdx.x - 64;
-    const int r = ct >> 2, j = ct & 3;
-    const int first = (j >> 1) ^ (r & 1);
-    const uint32_t ready0 = mapa_shared(&ready[0], 0);
-    const uint32_t atom = smem_u32(sm_x) + (j >> 1) * kAtomBytes + r * 128;
-    uint32_t c = 0;
-    for (int u = unit0; u < a.units; u += step) {
-      const Unit t = unit_of(a, u);
+    // Group g decodes the blocks c = g, g + 4, ... into slot g, so that the
+    // latencies of one block's chain (wait, read, decode, write, fence, arrive)
+    // overlap with the others'; the codes are decoded in registers before the
+    // slot is free.  Thread -> row r of the block and 64 columns (two
+    // exponents, one swizzled row of the operand).
+    //
+    // The 64 columns go into the operand in an order of their own: position
+    // 8b + 2q + i holds column 16q + 4 (b / 2) + b % 2 + 2i.  Decoding then
+    // takes codes 0, 2 and 1, 3 of a word as they lie, and a thread of the
+    // epilogue, which reads positions 8b + 2q + {0, 1} of every b, ends up with
+    // 16 consecutive columns of G.
+    const int g = (warp - kConv0) / kConvWarps;
+    const int wi = (warp - kConv0) % kConvWarps;
+    const int r = (wi & 1) * 32 + lane, j = wi >> 1;
+    const uint32_t ready_g = mapa_shared(&ready[g], 0);
+    const uint32_t dst = smem_u32(sm_x) + g * kSlotBytes + j * kAtomBytes + r * 128 + ((r & 7) << 4);
+    const uint32_t src = smem_u32(sm_codes) + r * 128 + ((j * 4 ^ (r & 7)) << 4);
+    uint32_t c0 = 0;   // blocks before this unit
+    bool ok = true;
+    Unit t;
+    while (ok && take(t, true)) {
       const int blk = (t.i0 + static_cast<int>(rank) * 128) / 32;
-      bool ok = true;
-      for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-        const uint32_t s = c % kStages, b = c % kSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], c / kStages & 1u, abort_flag,
-                                                       a.status, a.timeout_ns));
+      const uint32_t blocks = static_cast<uint32_t>((t.n + kBK - 1) / kBK);
+      for (uint32_t k = (g - c0) % kSlots; k < blocks; k += kSlots) {
+        const uint32_t c = c0 + k, s = c % kCodeStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&code_full[s], c / kCodeStages & 1u,
+                                                       abort_flag, a.status, a.timeout_ns));
         if (!ok) break;
-        const uint32_t e = sm_exps[s * kExpBytes + r * 16 + (blk & 15) + j];
-        const uint4* src = reinterpret_cast<const uint4*>(sm_codes + s * kCodeBytes + r * 128 + j * 32);
-        uint4 w[2];
-        w[0] = src[first];
-        w[1] = src[first ^ 1];
-        const int left = t.n - k0;
-        if (r >= left) {
-          w[0] = w[1] = make_uint4(0, 0, 0, 0);
-        }
-        // 2^(e - 127); a block that held something not finite (255) gives NaN
-        const uint32_t sb = r >= left ? 0x3F80u : e == 255u ? 0x7FC0u : e << 7;
-        const uint32_t sp = sb | sb << 16;
-        const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&sp);
-        if (c >= kSlots) {   // the MMAs that read this slot are done
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&empty[(c - kSlots) % kStages],
-                                            (c - kSlots) / kStages & 1u, abort_flag, a.status,
-                                            a.timeout_ns));
-          if (!ok) break;
-        }
-        const uint32_t dst = atom + b * kSlotBytes;
+        uint32_t w[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3])
+                       : "r"((src ^ (q << 4)) + s * kCodeBytes)
+                       : "memory");
+        const uint32_t ee = *reinterpret_cast<const uint16_t*>(sm_exps + s * kExpBytes + r * 16 +
+                                                               (blk & 15) + 2 * j);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&code_empty[s]);
+        const bool out = static_cast<int>(k) * kBK + r >= t.n;   // a row of the next expert
+        uint32_t sb[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t q[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
-          const int base = (j & 1) * 4 + ((h ^ first) << 1);   // 16-byte column before swizzling
+          const uint32_t e = ee >> (8 * h) & 255u;
+          // 2^(e - 127); a block that held something not finite (255) gives NaN
+          const uint32_t v = e == 255u ? 0x7FC0u : e << 7;
+          sb[h] = out ? 0u : v | v << 16;
+        }
+        uint32_t v[8][4];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint32_t v0 = codes_to_bf16(__byte_perm(q[2 * p], 0, 0x4140), scale);
-            const uint32_t v1 = codes_to_bf16(__byte_perm(q[2 * p], 0, 0x4342), scale);
-            const uint32_t v2 = codes_to_bf16(__byte_perm(q[2 * p + 1], 0, 0x4140), scale);
-            const uint32_t v3 = codes_to_bf16(__byte_perm(q[2 * p + 1], 0, 0x4342), scale);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             dst + (((base + p) ^ (r & 7)) << 4)),
-                         "r"(v0), "r"(v1), "r"(v2), "r"(v3)
-                         : "memory");
+        for (int q = 0; q < 4; ++q) {
+          const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&sb[q >> 1]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            v[2 * b][q] = codes_to_bf16(w[q][b], scale);
+            v[2 * b + 1][q] = codes_to_bf16(w[q][b] >> 8, scale);
           }
         }
-        if (r >= left) {   // dy's rows of the next expert, this thread's quarter of the row
-          uint4* p = reinterpret_cast<uint4*>(sm_dy + s * kDyBytes + (j >> 1) * kAtomBytes + r * 128 +
-                                              (j & 1) * 64);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) p[k] = make_uint4(0, 0, 0, 0);
+        if (c >= kSlots) {   // the MMAs that read this slot are done
+          const uint32_t done = c - kSlots;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&dy_empty[done % kDyStages], done / kDyStages & 1u,
+                                            abort_flag, a.status, a.timeout_ns));
+          if (!ok) break;
         }
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ (b << 4)),
+                       "r"(v[b][0]), "r"(v[b][1]), "r"(v[b][2]), "r"(v[b][3])
+                       : "memory");
+        const uint32_t ds = c % kDyStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_full[ds], c / kDyStages & 1u, abort_flag,
+                                                       a.status, a.timeout_ns));
+        if (!ok) break;
+        if (out) {   // its dy too, this thread's half of the row
+          uint4* p = reinterpret_cast<uint4*>(sm_dy + ds * kDyBytes + j * kAtomBytes + r * 128);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) p[z] = make_uint4(0, 0, 0, 0);
+        }
+        // The readers are the tensor cores, which see this CTA's shared memory as
+        // the proxy fence left it; a cluster-scope release on the arrival adds
+        // nothing to that and costs the chain of a slot a quarter of its time.
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(ready0 + b * 8u);
+        if (lane == 0) mbar_arrive_cluster(ready_g);
       }
-      if (!ok) break;
+      c0 += blocks;
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;                              // tensor-memory lanes 32 q ..
-    const int c0 = (warp - 2 - kConvWarps) >> 2;         // columns 128 c0 ..
+    // A warp drains 32 rows x 128 columns in four pieces of 16 x 64: a thread
+    // gets 16 consecutive columns of two rows, four threads 64 columns, so that
+    // a store of the warp fills eight whole 128-byte lines.
+    const int q = warp & 3;                    // tensor-memory lanes 32 q ..
+    const int half = (warp - kEpi0) >> 2;      // columns 128 half ..
     const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
     uint32_t tile = 0;
-    for (int u = unit0; u < a.units; u += step) {
-      const Unit t = unit_of(a, u);
-      const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+    Unit t;
+    while (take(t, true)) {
+      if (t.n == 0 && a.accumulate) continue;
+      const uint32_t acc = tile & 1u;
+      if (t.n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile >> 1 & 1u, abort_flag,
+                                                       a.status, a.timeout_ns)))
+          break;
+        tc_fence_after();
+      }
       void* g = matrix_of(a, t.e);
       const int esz = a.g_dtype == MUON_F32 ? 4 : 2;
-      const bool vec = (reinterpret_cast<uintptr_t>(g) & 15u) == 0 && a.g_stride * esz % 16 == 0;
-      if (t.n == 0) {   // an expert without tokens
-        if (!a.accumulate)
+      const bool vec = (reinterpret_cast<uintptr_t>(g) & 31u) == 0 && a.g_stride * esz % 32 == 0;
+      const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32 + (lane >> 2);
+      const int i = t.i0 + half * 128 + 16 * (lane & 3);
+      const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            float v[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-            store_chunk(a, g, vec, o, t.i0 + c0 * 128 + ch * 32, v);
-          }
-        continue;
-      }
-      const uint32_t acc = tile & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile >> 1 & 1u, abort_flag,
-                                                     a.status, a.timeout_ns)))
-        break;
-      tc_fence_after();
-      const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + c0 * 128u;
-#pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
+      for (int piece = 0; piece < 4; ++piece) {
+        const int dr = (piece & 1) * 16, dc = (piece >> 1) * 64;
         uint32_t raw[32];
-        tmem_ld_32x32b_x32(src + ch * 32, raw);
-        tmem_ld_wait(raw);
-        float v[32];
+        if (t.n > 0) {
+          tmem_ld_16x256b_x8(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
+          tmem_ld_wait(raw);
+        } else {   // an expert without tokens
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(raw[k]);
-        store_chunk(a, g, vec, o, t.i0 + c0 * 128 + ch * 32, v);
+          for (int k = 0; k < 32; ++k) raw[k] = 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[16];
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              v[4 * (b >> 1) + (b & 1) + 2 * k] = __uint_as_float(raw[4 * b + 2 * h + k]);
+          store16(a, g, vec, o + dr + 8 * h, i + dc, v);
+        }
       }
+      if (t.n == 0) continue;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8u);
@@ -597,7 +744,7 @@ cudaError_t launch_pair(const WgradArgs& a, cudaStream_t st) {
     if (!map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dy, a.rows, a.out, a.dy_stride, 64,
                   CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_rows(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.codes, a.rows, a.in, a.code_stride, 128,
-                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_rows(&exps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.exps, a.rows, blocks, a.exp_stride, 16,
                   CU_TENSOR_MAP_SWIZZLE_NONE))
       return cudaErrorInvalidValue;
