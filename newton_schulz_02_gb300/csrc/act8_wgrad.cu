@@ -8,18 +8,21 @@
 // dy^T (MN-major A) and x (MN-major B), contracted over the tokens, fp32
 // accumulators in tensor memory.
 //
-// k_wgrad_pair: a CTA pair computes 256 x 256 of G (tcgen05 cta_group::2; each
-// CTA holds 128 output columns of dy and 128 input columns of x).  Per 64
-// tokens one thread fetches the dy tile, the codes and the exponents by TMA;
-// eight warps turn the codes into the swizzled bf16 operand (2.5 operations a
-// code); one thread of the pair issues the MMAs; eight warps drain the
-// accumulators, of which there are two, while the next tile runs.  The ranges
-// of tokens are ragged: rows of the last block that belong to the next expert
-// are zeroed in both operands (a zero times their NaN would be NaN).
+// k_wgrad: a CTA pair computes 256 x 256 of G (tcgen05 cta_group::2; each CTA
+// holds 128 output columns of dy and 128 input columns of x).  Per 64 tokens
+// the dy tile, the codes and the exponents come by TMA; groups of four warps
+// turn the codes into the swizzled bf16 operand (2.25 operations a code); one
+// thread of the pair issues the MMAs; eight warps drain the accumulators, of
+// which there are two, while the next tile runs.  The ranges of tokens are
+// ragged: rows of the last block that belong to the next expert are zeroed in
+// both operands (a zero times their NaN would be NaN).
 //
-// k_wgrad_simt (fp32 dy, rows of dy off the 16-byte boundaries TMA needs): a
-// block computes a 64 x 64 tile in fp32, 16 tokens at a time through shared
-// memory.
+// Where TMA cannot fetch dy (fp32, or rows off 16-byte boundaries), eight warps
+// load it instead.  An fp32 value is split into three bf16 of 8 bits each,
+// whose sum it is, and the MMA runs once for each: products stay exact.
+//
+// Few tiles and many tokens: the tokens of a tile are cut into slices that
+// leave fp32 partial sums in the workspace, which k_wgrad_join adds in order.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -36,26 +39,27 @@
 namespace muon {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64, kTok = 16;
-constexpr size_t kHeader = 256;
+constexpr size_t kHeader = 256;   // status word
+
+// Where sums go: G itself, or slices of partial sums.
+struct Matrices {
+  void* const* ptrs;      // device pointers, or nullptr: base + e * batch_stride
+  void* base;
+  int64_t batch_stride, stride;
+  int rows, cols;         // of a matrix
+  int dtype, accumulate;
+};
 
 struct WgradArgs {
   int rows, out, in, experts;
   const void* dy;
-  int dy_dtype;
   int64_t dy_stride;
-  const int8_t* codes;
-  int64_t code_stride;
-  const uint8_t* exps;
-  int64_t exp_stride;
+  int dy_vec;             // dy's rows may be read four values at a time
   const int32_t* offsets;
-  void* const* g_ptrs;
-  void* g_base;
-  int64_t g_batch_stride, g_stride;
-  int g_dtype, accumulate;
+  Matrices g;
   int tiles_o, tiles_i;   // 256 x 256 tiles of a matrix
-  int units;              // tiles of all experts
+  int slices;             // of a tile's tokens; slice s of expert e goes to matrix s * experts + e
+  int units;              // tiles x slices of all experts
   uint32_t* status;
   uint64_t timeout_ns;
 };
@@ -70,89 +74,61 @@ __device__ __forceinline__ void span_of(const WgradArgs& a, int e, int& b, int& 
   n = min(max(a.offsets[e + 1], b), a.rows) - b;
 }
 
-__global__ void __launch_bounds__(kThreads) k_wgrad_simt(const __grid_constant__ WgradArgs a) {
-  __shared__ float sy[kTok][kTile + 4], sx[kTok][kTile + 4];
-  const int e = blockIdx.z;
-  int begin, n;
-  span_of(a, e, begin, n);
-  if (a.offsets != nullptr && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) {
-    const int b = a.offsets[e], c = a.offsets[e + 1];
-    if (b < 0 || c < b || c > a.rows) atomicOr(a.status, MUON_FLAG_INDEX);
-  }
-  const int o0 = blockIdx.y * kTile, i0 = blockIdx.x * kTile;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int t0 = 0; t0 < n; t0 += kTok) {
-    for (int v = threadIdx.x; v < kTok * kTile; v += kThreads) {
-      const int r = v / kTile, c = v % kTile;
-      const int64_t t = begin + t0 + r;
-      float y = 0.f, x = 0.f;
-      if (t0 + r < n) {
-        if (o0 + c < a.out)
-          y = a.dy_dtype == MUON_F32
-                  ? static_cast<const float*>(a.dy)[t * a.dy_stride + o0 + c]
-                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.dy)[t * a.dy_stride + o0 + c]);
-        if (i0 + c < a.in) {
-          const float s = __uint_as_float(
-              static_cast<uint32_t>(a.exps[t * a.exp_stride + (i0 + c) / 32]) << 23);
-          x = fmaf(static_cast<float>(a.codes[t * a.code_stride + i0 + c]), s, s - s);
-        }
-      }
-      sy[r][c] = y;
-      sx[r][c] = x;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kTok; ++r) {
-      float y[4], x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        y[k] = sy[r][ty * 4 + k];
-        x[k] = sx[r][tx * 4 + k];
-      }
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[p][q] = fmaf(y[p], x[q], acc[p][q]);
-    }
-    __syncthreads();
-  }
-  void* g = a.g_ptrs != nullptr ? a.g_ptrs[e]
-                                : static_cast<char*>(a.g_base) +
-                                      e * a.g_batch_stride * (a.g_dtype == MUON_F32 ? 4 : 2);
-#pragma unroll
-  for (int p = 0; p < 4; ++p)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int o = o0 + ty * 4 + p, i = i0 + tx * 4 + q;
-      if (o >= a.out || i >= a.in) continue;
-      const int64_t at = o * a.g_stride + i;
-      if (a.g_dtype == MUON_F32) {
-        float* w = static_cast<float*>(g) + at;
-        *w = a.accumulate ? *w + acc[p][q] : acc[p][q];
-      } else {
-        __nv_bfloat16* w = static_cast<__nv_bfloat16*>(g) + at;
-        *w = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*w) + acc[p][q] : acc[p][q]);
-      }
-    }
-}
-
 // ---- 256 x 256 tiles on CTA pairs -------------------------------------------
 constexpr int kBK = 64;                          // tokens per block of the contraction
-constexpr int kDyStages = 6;                     // dy tiles in flight or in use
-constexpr int kCodeStages = 4;                   // codes and exponents in flight
-constexpr int kSlots = 4;                        // decoded blocks, one per group of converters
 constexpr int kConvWarps = 4, kEpiWarps = 8;     // converter warps of one group
-constexpr int kConv0 = 4, kEpi0 = kConv0 + kSlots * kConvWarps;   // first warps
-constexpr int kPairThreads = 32 * (kEpi0 + kEpiWarps);
-constexpr uint32_t kDyBytes = kBK * 128 * 2;     // two 64-column atoms of 128-byte rows
+constexpr uint32_t kDyBytes = kBK * 128 * 2;     // a plane: two 64-column atoms of 128-byte rows
+constexpr uint32_t kRawBytes = kBK * 128 * 4;
 constexpr uint32_t kCodeBytes = kBK * 128;
 constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four of them used
 constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
 constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
 constexpr int kUnits = 4;                        // units announced ahead
-constexpr size_t kPairSmem = kDyStages * kDyBytes + kSlots * kSlotBytes +
-                             kCodeStages * (kCodeBytes + kExpBytes) + 1024 + 512;
+
+// How dy comes: kTma (bf16), kTma32 (fp32 by TMA, split by eight warps), kLoad16
+// and kLoad32 (the same warps load it themselves, for rows off the boundaries
+// that TMA needs).  Six dy stages and four decoded blocks cover the latency of
+// a load (about 1 us under load, a block's MMAs take 0.3); with three planes
+// a block's MMAs take three times as long and two do.
+enum DyMode { kTma, kTma32, kLoad16, kLoad32 };
+
+template <DyMode MODE>
+struct Cfg {
+  static constexpr int kPlanes = MODE == kTma32 || MODE == kLoad32 ? 3 : 1;
+  static constexpr int kRawStages = MODE == kTma32 ? 2 : 0;  // fp32 tiles in flight
+  static constexpr int kDyStages = MODE == kTma ? 6 : 2;     // dy tiles in flight or in use
+  static constexpr int kSlots = MODE == kTma ? 4 : 2;        // decoded blocks, a converter group each
+  static constexpr int kLoadWarps = MODE == kTma ? 0 : 8;
+  static constexpr int kConv0 = 4, kLoad0 = kConv0 + kSlots * kConvWarps;   // first warps
+  static constexpr int kEpi0 = kLoad0 + kLoadWarps;
+  static constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
+  static constexpr uint32_t kStageBytes = kPlanes * kDyBytes;
+
+  // What the roles of a CTA share besides the operands.  An mbarrier's parity
+  // tells only the current phase from the one before, so every role that waits
+  // for phase f of a barrier has seen phase f - 1 end: it waited for it itself,
+  // or for something that came after.  A converter group waits for every phase
+  // of its code stage (as many stages as groups); block c - kDyStages is over
+  // when the MMAs of block c - kSlots are (at least as many dy stages as slots).
+  struct Shared {
+    uint64_t dy_full[kDyStages], dy_empty[kDyStages];     // loads landed; MMAs on the stage done
+    uint64_t raw_full[2], raw_empty[2];                   // the same of fp32 tiles
+    uint64_t code_full[kSlots], code_empty[kSlots];       // loads landed; read into registers
+    uint64_t ready[kSlots];                               // both operands of a block in place
+    uint64_t unit_full[kUnits], unit_empty[kUnits];
+    uint64_t tfull[2], tempty[2];                         // accumulator summed; drained
+    uint64_t drain;
+    uint32_t tmem_slot;
+    int abort;
+    alignas(16) int units[8 * kUnits];
+  };
+  static constexpr size_t kSmem = kDyStages * kStageBytes + kRawStages * kRawBytes +
+                                  kSlots * (kSlotBytes + kCodeBytes + kExpBytes) +
+                                  sizeof(Shared) + 1024;
+};
+static_assert(Cfg<kTma>::kThreads <= 1024 && Cfg<kTma32>::kThreads <= 1024, "");
+static_assert(Cfg<kTma>::kSmem <= 232448 && Cfg<kTma32>::kSmem <= 232448, "");
+
 constexpr uint32_t kTmemCols = 512;              // two accumulators of 256 columns
 // D fp32, A and B bf16, both MN-major, M = 256, N = 256
 constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, true) | (1u << 15);
@@ -163,9 +139,12 @@ constexpr int kGroupO = 8;                       // tiles walked down before the
 // side by side, so that the tiles in flight share operands in L2.
 struct Unit {
   int e, o0, i0, begin, n;
+  int m;   // matrix the sums go to
 };
 
 __device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u) {
+  const int slice = u % a.slices;
+  u /= a.slices;
   const int per = a.tiles_o * a.tiles_i;
   Unit t;
   t.e = u / per;
@@ -176,6 +155,14 @@ __device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u) {
   t.o0 = (band * kGroupO + q % rows) * 256;
   t.i0 = (q / rows) * 256;
   span_of(a, t.e, t.begin, t.n);
+  t.m = slice * a.experts + t.e;
+  if (a.slices > 1) {   // whole blocks, as even as can be
+    const int blocks = (t.n + kBK - 1) / kBK;
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * slice / a.slices);
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (slice + 1) / a.slices);
+    t.n = min(t.n, b1 * kBK) - b0 * kBK;
+    t.begin += b0 * kBK;
+  }
   return t;
 }
 
@@ -265,12 +252,12 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 
 // 16 consecutive columns of one row of G.
-__device__ __forceinline__ void store16(const WgradArgs& a, void* g, bool vec, int o, int i,
+__device__ __forceinline__ void store16(const Matrices& a, void* g, bool vec, int o, int i,
                                         float (&v)[16]) {
-  if (o >= a.out || i >= a.in) return;
-  const int64_t at = static_cast<int64_t>(o) * a.g_stride + i;
-  if (vec && i + 16 <= a.in) {   // whole 32-byte sectors
-    if (a.g_dtype == MUON_F32) {
+  if (o >= a.rows || i >= a.cols) return;
+  const int64_t at = static_cast<int64_t>(o) * a.stride + i;
+  if (vec && i + 16 <= a.cols) {   // whole 32-byte sectors
+    if (a.dtype == MUON_F32) {
       float* p = static_cast<float*>(g) + at;
 #pragma unroll
       for (int k = 0; k < 16; k += 8) {
@@ -309,8 +296,8 @@ __device__ __forceinline__ void store16(const WgradArgs& a, void* g, bool vec, i
   }
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-    if (i + k >= a.in) break;
-    if (a.g_dtype == MUON_F32) {
+    if (i + k >= a.cols) break;
+    if (a.dtype == MUON_F32) {
       float* p = static_cast<float*>(g) + at + k;
       *p = a.accumulate ? *p + v[k] : v[k];
     } else {
@@ -320,35 +307,81 @@ __device__ __forceinline__ void store16(const WgradArgs& a, void* g, bool vec, i
   }
 }
 
-__device__ __forceinline__ void* matrix_of(const WgradArgs& a, int e) {
-  return a.g_ptrs != nullptr ? a.g_ptrs[e]
-                             : static_cast<char*>(a.g_base) +
-                                   e * a.g_batch_stride * (a.g_dtype == MUON_F32 ? 4 : 2);
+__device__ __forceinline__ char* matrix_of(const Matrices& g, int m) {
+  return static_cast<char*>(g.ptrs != nullptr
+                                ? g.ptrs[m]
+                                : static_cast<char*>(g.base) +
+                                      m * g.batch_stride * (g.dtype == MUON_F32 ? 4 : 2));
 }
 
-__global__ void __launch_bounds__(kPairThreads, 1)
-    k_wgrad_pair(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_codes,
+template <DyMode MODE>
+struct DyType {
+  using type = __nv_bfloat16;
+};
+template <>
+struct DyType<kTma32> {
+  using type = float;
+};
+template <>
+struct DyType<kLoad32> {
+  using type = float;
+};
+
+// Four consecutive values of a row of dy (0 past the row's end).
+template <typename T>
+__device__ __forceinline__ void load_dy4(const T* row, int col, int cols, bool vec, float (&v)[4]) {
+  if (vec && col + 4 <= cols) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 w = *reinterpret_cast<const float4*>(row + col);
+      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(row + col);
+      v[0] = __uint_as_float(w.x << 16);
+      v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16);
+      v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = col + k < cols ? static_cast<float>(row[col + k]) : 0.f;
+  }
+}
+
+// The upper 8 significant bits of v as bf16 in the upper half of a word; v
+// becomes the rest, exactly.  An infinity or a NaN leaves 0.
+__device__ __forceinline__ uint32_t take_upper(float& v) {
+  const uint32_t u = __float_as_uint(v);
+  if ((u & 0x7F800000u) == 0x7F800000u) {
+    v = 0.f;
+    return (u & 0x007FFFFFu) != 0 ? 0x7FC00000u : u;
+  }
+  v -= __uint_as_float(u & 0xFFFF0000u);
+  return u & 0xFFFF0000u;
+}
+
+template <DyMode MODE>
+__global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_codes,
                  const __grid_constant__ CUtensorMap tm_exps, const __grid_constant__ WgradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  using C = Cfg<MODE>;
+  constexpr int kDyStages = C::kDyStages, kSlots = C::kSlots;
+  constexpr bool kTmaDy = MODE == kTma || MODE == kTma32;
   uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
-  uint8_t* sm_x = sm_dy + kDyStages * kDyBytes;             // decoded, swizzled
-  uint8_t* sm_codes = sm_x + kSlots * kSlotBytes;
-  uint8_t* sm_exps = sm_codes + kCodeStages * kCodeBytes;
-  uint64_t* dy_full = reinterpret_cast<uint64_t*>(sm_exps + kCodeStages * kExpBytes);
-  uint64_t* dy_empty = dy_full + kDyStages;
-  uint64_t* code_full = dy_empty + kDyStages;
-  uint64_t* code_empty = code_full + kCodeStages;
-  uint64_t* ready = code_empty + kCodeStages;
-  uint64_t* unit_full = ready + kSlots;
-  uint64_t* unit_empty = unit_full + kUnits;
-  uint64_t* tfull = unit_empty + kUnits;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* sm_units = reinterpret_cast<int*>(drain + 2);   // [kUnits][8]
+  uint8_t* sm_x = sm_dy + kDyStages * C::kStageBytes;       // decoded, swizzled
+  uint8_t* sm_raw = sm_x + kSlots * kSlotBytes;             // fp32, rows of 512 bytes
+  uint8_t* sm_codes = sm_raw + C::kRawStages * kRawBytes;   // swizzled
+  uint8_t* sm_exps = sm_codes + kSlots * kCodeBytes;
+  typename C::Shared& bars = *reinterpret_cast<typename C::Shared*>(sm_exps + kSlots * kExpBytes);
+  uint64_t *dy_full = bars.dy_full, *dy_empty = bars.dy_empty, *code_full = bars.code_full,
+           *code_empty = bars.code_empty, *ready = bars.ready, *unit_full = bars.unit_full,
+           *unit_empty = bars.unit_empty, *tfull = bars.tfull, *tempty = bars.tempty,
+           *drain = &bars.drain;
+  volatile int* abort_flag = &bars.abort;
+  uint32_t* tmem_slot = &bars.tmem_slot;
+  int* sm_units = bars.units;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -356,18 +389,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&unit_full[s], 1);
-      // producers, converters, epilogue; the MMA issuer in the even CTA
-      mbar_init(&unit_empty[s], 2 + kSlots * kConvWarps + kEpiWarps + (rank == 0 ? 1 : 0));
+      // TMA threads, converters, loaders, epilogue; the MMA issuer in the even CTA
+      mbar_init(&unit_empty[s], (kTmaDy ? 2 : 1) + kSlots * kConvWarps + C::kLoadWarps +
+                                    kEpiWarps + (rank == 0 ? 1 : 0));
     }
     for (int s = 0; s < kDyStages; ++s) {
       mbar_init(&dy_full[s], 1);                // this CTA's loads
       mbar_init(&dy_empty[s], 1);               // the pair's MMA commit, multicast
     }
-    for (int s = 0; s < kCodeStages; ++s) {
+    for (int s = 0; s < C::kRawStages; ++s) {
+      mbar_init(&bars.raw_full[s], 1);
+      mbar_init(&bars.raw_empty[s], C::kLoadWarps);
+    }
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&code_full[s], 1);
       mbar_init(&code_empty[s], kConvWarps);    // read into registers
+      mbar_init(&ready[s], 2 * (kConvWarps + C::kLoadWarps));   // both CTAs' warps
     }
-    for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], 2 * kConvWarps);   // both CTAs' warps
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
       mbar_init(&tempty[s], 2 * kEpiWarps);
@@ -401,20 +439,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     t.o0 = v.y;
     t.i0 = v.z;
     t.begin = v.w;
-    t.n = sm_units[8 * k + 4];
+    const int2 w = *reinterpret_cast<const int2*>(sm_units + 8 * k + 4);
+    t.n = w.x;
+    t.m = w.y;
     if (whole_warp) __syncwarp();
     if (lane == 0) mbar_arrive(&unit_empty[k]);
     ++taken;
     return t.e >= 0;
   };
 
-  if (warp == 0 || warp == 2) {
+  if ((warp == 0 && kTmaDy) || warp == 2) {
     if (lane == 0) {
-      // ------------------------------------- producers: dy, codes + exponents
+      // ----------------------------------- TMA: dy (warp 0), codes + exponents
       const bool is_dy = warp == 0;
-      uint64_t* full = is_dy ? dy_full : code_full;
-      uint64_t* empty = is_dy ? dy_empty : code_empty;
-      const uint32_t stages = is_dy ? kDyStages : kCodeStages;
+      uint64_t* full = !is_dy ? code_full : MODE == kTma ? dy_full : bars.raw_full;
+      uint64_t* empty = !is_dy ? code_empty : MODE == kTma ? dy_empty : bars.raw_empty;
+      const uint32_t stages = !is_dy ? kSlots : MODE == kTma ? kDyStages : C::kRawStages;
       uint32_t c = 0, s = 0, phase = 0;
       bool ok = true;
       Unit t;
@@ -425,7 +465,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             ok = false;
             break;
           }
-          if (is_dy) {
+          if (is_dy && MODE == kTma32) {
+            mbar_arrive_expect_tx(&full[s], kRawBytes);
+            tma_load_2d(sm_raw + s * kRawBytes, &tm_dy, &full[s], o, t.begin + k0);
+          } else if (is_dy) {
             mbar_arrive_expect_tx(&full[s], kDyBytes);
             uint8_t* d = sm_dy + s * kDyBytes;
             tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
@@ -466,13 +509,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(sm_dy + s * kDyBytes);
           const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
 #pragma unroll
-          for (int ks = 0; ks < kBK / 16; ++ks)
-            tc_mma_bf16_pair(d, smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
-                             smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
-                             (k0 | ks) != 0 ? 1u : 0u);
+          for (int p = C::kPlanes - 1; p >= 0; --p) {   // the smallest parts first
+            const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kDyBytes);
+#pragma unroll
+            for (int ks = 0; ks < kBK / 16; ++ks)
+              tc_mma_bf16_pair(d, smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
+                               smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
+                               k0 == 0 && p == C::kPlanes - 1 && ks == 0 ? 0u : 1u);
+          }
           tc_commit_pair_multicast(&dy_empty[s], 0x3);
           if (++s == kDyStages) s = 0;
         }
@@ -489,21 +535,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int step = static_cast<int>(gridDim.x >> 1);
       uint32_t k = 0;
       for (int u = static_cast<int>(blockIdx.x >> 1);; u += step, ++k) {
-        Unit t{-1, 0, 0, 0, 0};
+        Unit t{-1, 0, 0, 0, 0, 0};
         if (u < a.units) t = unit_of(a, u);
         int* p = sm_units + 8 * (k % kUnits);
         if (!mbar_wait_bounded(&unit_empty[k % kUnits], (k / kUnits & 1u) ^ 1u, abort_flag, a.status,
                                a.timeout_ns))
           break;
         *reinterpret_cast<int4*>(p) = make_int4(t.e, t.o0, t.i0, t.begin);
-        p[4] = t.n;
+        *reinterpret_cast<int2*>(p + 4) = make_int2(t.n, t.m);
         mbar_arrive(&unit_full[k % kUnits]);
         if (t.e < 0) break;
       }
     }
-  } else if (warp < kEpi0) {
+  } else if (warp >= C::kConv0 && warp < C::kLoad0) {
     // ---------------------------------------------------------- converters
-    // Group g decodes the blocks c = g, g + 4, ... into slot g, so that the
+    // Group g decodes the blocks c = g, g + kSlots, ... into slot g, so that the
     // latencies of one block's chain (wait, read, decode, write, fence, arrive)
     // overlap with the others'; the codes are decoded in registers before the
     // slot is free.  Thread -> row r of the block and 64 columns (two
@@ -514,8 +560,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // takes codes 0, 2 and 1, 3 of a word as they lie, and a thread of the
     // epilogue, which reads positions 8b + 2q + {0, 1} of every b, ends up with
     // 16 consecutive columns of G.
-    const int g = (warp - kConv0) / kConvWarps;
-    const int wi = (warp - kConv0) % kConvWarps;
+    const int g = (warp - C::kConv0) / kConvWarps;
+    const int wi = (warp - C::kConv0) % kConvWarps;
     const int r = (wi & 1) * 32 + lane, j = wi >> 1;
     const uint32_t ready_g = mapa_shared(&ready[g], 0);
     const uint32_t dst = smem_u32(sm_x) + g * kSlotBytes + j * kAtomBytes + r * 128 + ((r & 7) << 4);
@@ -527,8 +573,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int blk = (t.i0 + static_cast<int>(rank) * 128) / 32;
       const uint32_t blocks = static_cast<uint32_t>((t.n + kBK - 1) / kBK);
       for (uint32_t k = (g - c0) % kSlots; k < blocks; k += kSlots) {
-        const uint32_t c = c0 + k, s = c % kCodeStages;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&code_full[s], c / kCodeStages & 1u,
+        const uint32_t c = c0 + k, s = c % kSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&code_full[s], c / kSlots & 1u,
                                                        abort_flag, a.status, a.timeout_ns));
         if (!ok) break;
         uint32_t w[4][4];
@@ -573,14 +619,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ (b << 4)),
                        "r"(v[b][0]), "r"(v[b][1]), "r"(v[b][2]), "r"(v[b][3])
                        : "memory");
-        const uint32_t ds = c % kDyStages;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_full[ds], c / kDyStages & 1u, abort_flag,
-                                                       a.status, a.timeout_ns));
-        if (!ok) break;
-        if (out) {   // its dy too, this thread's half of the row
-          uint4* p = reinterpret_cast<uint4*>(sm_dy + ds * kDyBytes + j * kAtomBytes + r * 128);
+        if constexpr (MODE == kTma) {
+          const uint32_t ds = c % kDyStages;
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_full[ds], c / kDyStages & 1u, abort_flag,
+                                                         a.status, a.timeout_ns));
+          if (!ok) break;
+          if (out) {   // its dy too, this thread's half of the row
+            uint4* p = reinterpret_cast<uint4*>(sm_dy + ds * kDyBytes + j * kAtomBytes + r * 128);
 #pragma unroll
-          for (int z = 0; z < 8; ++z) p[z] = make_uint4(0, 0, 0, 0);
+            for (int z = 0; z < 8; ++z) p[z] = make_uint4(0, 0, 0, 0);
+          }
         }
         // The readers are the tensor cores, which see this CTA's shared memory as
         // the proxy fence left it; a cluster-scope release on the arrival adds
@@ -591,18 +639,91 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       c0 += blocks;
     }
-  } else {
+  } else if (warp >= C::kLoad0 && warp < C::kEpi0) {
+    // ------------------------------------------------------------- loaders
+    // dy through registers: a warp takes a row of 128 columns, four a thread,
+    // from memory (a block ahead) or from TMA's fp32 tile, and writes them (as
+    // planes) where TMA puts a bf16 tile.  Rows of the next expert and columns
+    // past the end are zeros.
+    if constexpr (MODE != kTma) {
+      using T = typename DyType<MODE>::type;
+      const int lw = warp - C::kLoad0;
+      const int col4 = 4 * lane;   // within the CTA's 128 columns
+      const uint32_t ready0 = mapa_shared(&ready[0], 0);
+      uint32_t c = 0;
+      bool ok = true;
+      Unit t;
+      while (ok && take(t, true)) {
+        const int o = t.o0 + static_cast<int>(rank) * 128 + col4;
+        float v[8][4];
+        const auto fetch = [&](int k0) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = q * C::kLoadWarps + lw;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[q][k] = 0.f;
+            if (k0 + r >= t.n) continue;
+            if constexpr (MODE == kTma32) {
+              const float4 w = *reinterpret_cast<const float4*>(sm_raw + c % 2 * kRawBytes + r * 512 +
+                                                                lane * 16);
+              v[q][0] = w.x; v[q][1] = w.y; v[q][2] = w.z; v[q][3] = w.w;
+            } else {
+              load_dy4(static_cast<const T*>(a.dy) + static_cast<int64_t>(t.begin + k0 + r) * a.dy_stride,
+                       o, a.out, a.dy_vec != 0, v[q]);
+            }
+          }
+        };
+        if (MODE != kTma32 && t.n > 0) fetch(0);
+        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+          const uint32_t s = c % kDyStages;
+          if constexpr (MODE == kTma32) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars.raw_full[c % 2], c / 2 & 1u, abort_flag,
+                                                           a.status, a.timeout_ns));
+            if (!ok) break;
+            fetch(k0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.raw_empty[c % 2]);
+          }
+          if (c >= kDyStages) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(&dy_empty[s], (c / kDyStages & 1u) ^ 1u, abort_flag,
+                                              a.status, a.timeout_ns));
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = q * C::kLoadWarps + lw;
+            uint8_t* at = sm_dy + s * C::kStageBytes + (lane >> 4) * kAtomBytes + r * 128 +
+                          ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+            for (int p = 0; p < C::kPlanes; ++p) {
+              uint32_t u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                u[k] = C::kPlanes == 1 ? __float_as_uint(v[q][k]) : take_upper(v[q][k]);
+              *reinterpret_cast<uint2*>(at + p * kDyBytes) =
+                  make_uint2(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(ready0 + c % kSlots * 8u);
+          if (MODE != kTma32 && k0 + kBK < t.n) fetch(k0 + kBK);
+        }
+      }
+    }
+  } else if (warp >= C::kEpi0) {
     // ------------------------------------------------------------ epilogue
     // A warp drains 32 rows x 128 columns in four pieces of 16 x 64: a thread
     // gets 16 consecutive columns of two rows, four threads 64 columns, so that
     // a store of the warp fills eight whole 128-byte lines.
     const int q = warp & 3;                    // tensor-memory lanes 32 q ..
-    const int half = (warp - kEpi0) >> 2;      // columns 128 half ..
+    const int half = (warp - C::kEpi0) >> 2;      // columns 128 half ..
     const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
     uint32_t tile = 0;
     Unit t;
     while (take(t, true)) {
-      if (t.n == 0 && a.accumulate) continue;
+      if (t.n == 0 && a.g.accumulate) continue;
       const uint32_t acc = tile & 1u;
       if (t.n > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile >> 1 & 1u, abort_flag,
@@ -610,9 +731,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           break;
         tc_fence_after();
       }
-      void* g = matrix_of(a, t.e);
-      const int esz = a.g_dtype == MUON_F32 ? 4 : 2;
-      const bool vec = (reinterpret_cast<uintptr_t>(g) & 31u) == 0 && a.g_stride * esz % 32 == 0;
+      char* g = matrix_of(a.g, t.m);
+      const int esz = a.g.dtype == MUON_F32 ? 4 : 2;
+      const bool vec = (reinterpret_cast<uintptr_t>(g) & 31u) == 0 && a.g.stride * esz % 32 == 0;
       const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32 + (lane >> 2);
       const int i = t.i0 + half * 128 + 16 * (lane & 3);
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
@@ -620,6 +741,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int piece = 0; piece < 4; ++piece) {
         const int dr = (piece & 1) * 16, dc = (piece >> 1) * 64;
         uint32_t raw[32];
+        __syncwarp();   // tcgen05.ld takes the warp together
         if (t.n > 0) {
           tmem_ld_16x256b_x8(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
           tmem_ld_wait(raw);
@@ -635,7 +757,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               v[4 * (b >> 1) + (b & 1) + 2 * k] = __uint_as_float(raw[4 * b + 2 * h + k]);
-          store16(a, g, vec, o + dr + 8 * h, i + dc, v);
+          store16(a.g, g, vec, o + dr + 8 * h, i + dc, v);
         }
       }
       if (t.n == 0) continue;
@@ -656,25 +778,43 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   // offsets that do not ascend within [0, rows]
   if (a.offsets != nullptr && blockIdx.x == 0)
-    for (int e = threadIdx.x; e < a.experts; e += kPairThreads)
+    for (int e = threadIdx.x; e < a.experts; e += C::kThreads)
       if (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows)
         atomicOr(a.status, MUON_FLAG_INDEX);
+}
+
+// G (+)= the slices' partial sums, added in order.  parts: [slices][experts]
+// [rows][stride] fp32.  Four columns of a row per thread.
+__global__ void __launch_bounds__(256)
+    k_wgrad_join(const float* parts, int slices, int64_t slice_stride, int64_t matrix_stride,
+                 int64_t stride, const __grid_constant__ Matrices g) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int o = blockIdx.y, e = blockIdx.z;
+  if (i >= g.cols) return;
+  const float* p = parts + e * matrix_stride + o * stride + i;
+  float v[4] = {};
+  for (int s = 0; s < slices; ++s) {
+    const float4 w = *reinterpret_cast<const float4*>(p + s * slice_stride);
+    v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+  }
+  char* m = matrix_of(g, e);
+  const int64_t at = o * g.stride + i;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (i + k >= g.cols) break;
+    if (g.dtype == MUON_F32) {
+      float* w = reinterpret_cast<float*>(m) + at + k;
+      *w = g.accumulate ? *w + v[k] : v[k];
+    } else {
+      __nv_bfloat16* w = reinterpret_cast<__nv_bfloat16*>(m) + at + k;
+      *w = __float2bfloat16_rn(g.accumulate ? __bfloat162float(*w) + v[k] : v[k]);
+    }
+  }
 }
 
 int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
 
 bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-muon_status_t check_sizes(const muon_weight_grad_t* d) {
-  if (d == nullptr || d->rows < 0 || d->out < 1 || d->experts < 1 || d->x.cols < 1)
-    return MUON_ERR_INVALID_ARG;
-  if (d->dy_dtype != MUON_BF16 && d->dy_dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
-  if (d->g_dtype != MUON_BF16 && d->g_dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
-  if (d->rows >= (int64_t{1} << 31) - (1 << 20) || d->out > (1 << 22) || d->x.cols > (1 << 22) ||
-      d->experts > 65535)
-    return MUON_ERR_UNSUPPORTED;
-  return MUON_OK;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -704,28 +844,17 @@ bool map_rows(CUtensorMap* m, CUtensorMapDataType type, int esz, const void* bas
 }
 
 // CTA pairs that fit the current device at once (asked once per device).
-cudaError_t resident_pairs(int* out) {
+template <DyMode MODE>
+cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_wgrad_pair, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kPairSmem));
-  if (e != cudaSuccess) return e;
   if (dev < kDevices && (*out = known[dev].load()) > 0) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad_pair, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad<MODE>, &cfg);
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
   if (dev < kDevices) known[dev].store(n);
@@ -733,22 +862,12 @@ cudaError_t resident_pairs(int* out) {
   return cudaSuccess;
 }
 
-cudaError_t launch_pair(const WgradArgs& a, cudaStream_t st) {
-  int pairs = 0;
-  cudaError_t e = resident_pairs(&pairs);
+template <DyMode MODE>
+cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
+  using C = Cfg<MODE>;
+  cudaError_t e = cudaFuncSetAttribute(k_wgrad<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
-  CUtensorMap dy{}, codes{}, exps{};
-  if (a.rows > 0) {
-    if (encode_fn() == nullptr) return cudaErrorNotSupported;
-    const int64_t blocks = (static_cast<int64_t>(a.in) + 31) / 32;
-    if (!map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dy, a.rows, a.out, a.dy_stride, 64,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_rows(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.codes, a.rows, a.in, a.code_stride, 128,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_rows(&exps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.exps, a.rows, blocks, a.exp_stride, 16,
-                  CU_TENSOR_MAP_SWIZZLE_NONE))
-      return cudaErrorInvalidValue;
-  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -756,17 +875,78 @@ cudaError_t launch_pair(const WgradArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min(a.units, pairs)));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, k_wgrad_pair, dy, codes, exps, a);
+  int pairs = 0;
+  e = resident_pairs<MODE>(cfg, &pairs);
+  if (e != cudaSuccess) return e;
+  CUtensorMap dy{}, codes{}, exps{};
+  if (a.rows > 0) {
+    if (encode_fn() == nullptr) return cudaErrorNotSupported;
+    const int64_t blocks = (static_cast<int64_t>(a.in) + 31) / 32;
+    if ((MODE == kTma && !map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dy, a.rows, a.out,
+                                   a.dy_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (MODE == kTma32 && !map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.dy, a.rows, a.out,
+                                     a.dy_stride, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) ||
+        !map_rows(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, a.rows, a.in, x.code_stride, 128,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_rows(&exps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.exps, a.rows, blocks, x.exp_stride, 16,
+                  CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min(a.units, pairs)));
+  return cudaLaunchKernelEx(&cfg, k_wgrad<MODE>, dy, codes, exps, a);
 }
 
-cudaError_t launch_simt(const WgradArgs& a, cudaStream_t st) {
-  const dim3 grid((a.in + kTile - 1) / kTile, (a.out + kTile - 1) / kTile, a.experts);
-  k_wgrad_simt<<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+muon_status_t check_sizes(const muon_weight_grad_t* d) {
+  if (d == nullptr || d->rows < 0 || d->out < 1 || d->experts < 1 || d->x.cols < 1)
+    return MUON_ERR_INVALID_ARG;
+  if (d->dy_dtype != MUON_BF16 && d->dy_dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
+  if (d->g_dtype != MUON_BF16 && d->g_dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
+  if (d->rows >= (int64_t{1} << 31) - (1 << 20) || d->out > (1 << 22) || d->x.cols > (1 << 22) ||
+      d->experts > 65535)
+    return MUON_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>((d->out + 255) / 256) * ((d->x.cols + 255) / 256) * d->experts >=
+      (int64_t{1} << 26))
+    return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+// Slices of a tile's tokens.  With `tiles` tiles on 76 CTA pairs the last wave
+// leaves pairs idle; s slices shorten the longest pair's share to
+// ceil(tiles * s / 76) / s of a tile.  A slice costs its partial sums (256 KB
+// written and read, about two blocks' time), so slices have at least 16 blocks
+// of the average expert, and none are made for less than a fifth.
+int slices_of(int64_t tiles, int64_t rows, int experts) {
+  constexpr int kPairs = 76;
+  const int64_t blocks = (rows / experts + kBK - 1) / kBK;
+  int best = 1;
+  double least = static_cast<double>((tiles + kPairs - 1) / kPairs) * 0.8;
+  for (int s = 2; s <= 76 && s * 16 <= blocks; ++s) {
+    const double share = static_cast<double>((tiles * s + kPairs - 1) / kPairs) / s +
+                         2.0 * s / static_cast<double>(blocks);
+    if (share < least) {
+      least = share;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int tiles_o, tiles_i, slices;
+  size_t part_bytes;
+};
+
+Plan plan_of(const muon_weight_grad_t* d) {
+  Plan p;
+  p.tiles_o = (d->out + 255) / 256;
+  p.tiles_i = (d->x.cols + 255) / 256;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_o) * p.tiles_i * d->experts;
+  p.slices = slices_of(tiles, d->rows, d->experts);
+  p.part_bytes = p.slices > 1 ? static_cast<size_t>(tiles) * p.slices * 256 * 256 * 4 : 0;
+  return p;
 }
 
 }  // namespace
@@ -780,17 +960,17 @@ muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, 
   if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
   const muon_status_t s = check_sizes(d);
   if (s != MUON_OK) return s;
-  *bytes = kHeader;
+  *bytes = kHeader + plan_of(d).part_bytes;
   return MUON_OK;
 }
 
 muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace,
                                     size_t workspace_bytes, muon_stream_t stream) {
-  size_t need = 0;
-  muon_status_t s = muon_act8_weight_grad_workspace_size(d, &need);
+  muon_status_t s = check_sizes(d);
   if (s != MUON_OK) return s;
   const muon_act8_t& x = d->x;
-  if (x.rows != d->rows || x.code_stride < x.cols || x.exp_stride * 32 < x.cols)
+  if (x.rows != d->rows || x.code_stride < x.cols ||
+      x.exp_stride < (static_cast<int64_t>(x.cols) + 31) / 32)
     return MUON_ERR_INVALID_ARG;
   if (d->rows > 0 && (d->dy == nullptr || x.codes == nullptr || x.exps == nullptr))
     return MUON_ERR_INVALID_ARG;
@@ -804,46 +984,60 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
       !at_multiple(d->offsets, 4) || !at_multiple(d->g_ptrs, 8) ||
       !at_multiple(d->g_base, esize(d->g_dtype)) || !at_multiple(workspace, 256))
     return MUON_ERR_MISALIGNED;
-  if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
+  const Plan p = plan_of(d);
+  if (workspace_bytes < kHeader + p.part_bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, kHeader, st) != cudaSuccess) return MUON_ERR_CUDA;
+  if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st) != cudaSuccess) return MUON_ERR_CUDA;
+  const Matrices g{d->g_ptrs, d->g_base, d->g_batch_stride, d->g_stride, d->out, x.cols, d->g_dtype,
+                   d->accumulate};
   WgradArgs a{};
   a.rows = static_cast<int>(d->rows);
   a.out = d->out;
   a.in = x.cols;
   a.experts = d->experts;
   a.dy = d->dy;
-  a.dy_dtype = d->dy_dtype;
   a.dy_stride = d->dy_stride;
-  a.codes = x.codes;
-  a.code_stride = x.code_stride;
-  a.exps = x.exps;
-  a.exp_stride = x.exp_stride;
   a.offsets = d->offsets;
-  a.g_ptrs = d->g_ptrs;
-  a.g_base = d->g_base;
-  a.g_batch_stride = d->g_batch_stride;
-  a.g_stride = d->g_stride;
-  a.g_dtype = d->g_dtype;
-  a.accumulate = d->accumulate;
+  a.g = g;
+  a.tiles_o = p.tiles_o;
+  a.tiles_i = p.tiles_i;
+  a.slices = p.slices;
+  a.units = p.tiles_o * p.tiles_i * d->experts * p.slices;
   a.status = static_cast<uint32_t*>(workspace);
   a.timeout_ns = wait_timeout_ns();
-  a.tiles_o = (d->out + 255) / 256;
-  a.tiles_i = (x.cols + 255) / 256;
-  const int64_t units = static_cast<int64_t>(a.tiles_o) * a.tiles_i * d->experts;
-  if (units >= (int64_t{1} << 30)) return MUON_ERR_UNSUPPORTED;
-  a.units = static_cast<int>(units);
-  // TMA takes dy's rows where they start on 16-byte boundaries
-  const bool pair = d->dy_dtype == MUON_BF16 && at_multiple(d->dy, 16) && d->dy_stride % 8 == 0;
+  const int64_t part_stride = static_cast<int64_t>(p.tiles_i) * 256;
+  const int64_t part_matrix = part_stride * p.tiles_o * 256;
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
+  if (p.slices > 1)
+    a.g = Matrices{nullptr, parts, part_matrix, part_stride, p.tiles_o * 256, p.tiles_i * 256,
+                   MUON_F32, 0};
   const double rows = static_cast<double>(d->rows);
   prof_begin(kKindWeightGrad, st);
-  const cudaError_t e = pair ? launch_pair(a, st) : launch_simt(a, st);
+  cudaError_t e;
+  if (d->dy_dtype == MUON_F32) {
+    e = at_multiple(d->dy, 16) && d->dy_stride % 4 == 0 ? launch<kTma32>(a, x, st)
+                                                        : launch<kLoad32>(a, x, st);
+  } else if (at_multiple(d->dy, 16) && d->dy_stride % 8 == 0) {
+    e = launch<kTma>(a, x, st);
+  } else {
+    a.dy_vec = at_multiple(d->dy, 8) && d->dy_stride % 4 == 0;
+    e = launch<kLoad16>(a, x, st);
+  }
   prof_end(kKindWeightGrad, st, 2.0 * rows * d->out * x.cols,
            rows * (d->out * esize(d->dy_dtype) + x.cols * (1.0 + 1.0 / 32)) +
                static_cast<double>(d->experts) * d->out * x.cols * esize(d->g_dtype) *
                    (d->accumulate ? 2 : 1));
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  if (e != cudaSuccess) return MUON_ERR_CUDA;
+  if (p.slices > 1) {
+    prof_begin(kKindWeightGrad, st);
+    const dim3 grid((x.cols + 1023) / 1024, d->out, d->experts);
+    k_wgrad_join<<<grid, 256, 0, st>>>(parts, p.slices, part_matrix * d->experts, part_matrix,
+                                       part_stride, g);
+    prof_end(kKindWeightGrad, st, 0.0, 0.0);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  return MUON_OK;
 }
 
 }  // extern "C"
