@@ -195,8 +195,8 @@ def _check(code: int, where: str) -> None:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without an object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -505,12 +505,17 @@ def muon_adamw_step(groups: Sequence[AdamWGroup], hp: muon_adamw_hparams_t,
 # ---------------------------------------------------------------------------
 def _rows2d(t: torch.Tensor, what: str, shape=None) -> int:
     """Row stride of a 2-D tensor with unit column stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0] > 0):
-        raise ValueError(f"{what} needs two dimensions and unit column stride")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} needs the shape {tuple(shape)}, not {tuple(t.shape)}")
-    # the stride of no row or of the only one is never used; it may be anything
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    got = t.shape
+    if shape is not None and got != shape:
+        raise ValueError(f"{what} needs the shape {tuple(shape)}, not {tuple(got)}")
+    if len(got) != 2:
+        raise ValueError(f"{what} needs two dimensions")
+    if got[0] <= 1 and (got[1] <= 1 or got[0] == 0 or t.stride(1) == 1):
+        return got[1]   # the stride of no row or of the only one is never used; it may be anything
+    rs, cs = t.stride()
+    if cs != 1 and got[1] > 1:
+        raise ValueError(f"{what} needs unit column stride")
+    return rs
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
@@ -594,6 +599,8 @@ class Act8:
     row stride a multiple of 32) and exps (uint8, one biased exponent for each
     32 columns of a row, row stride a multiple of 16)."""
 
+    __slots__ = ("shape", "c", "ref", "_codes", "_exps", "_memory")
+
     def __init__(self, codes: torch.Tensor, exps: torch.Tensor, cols: int):
         if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
             raise ValueError("codes are int8, exps uint8")
@@ -601,27 +608,54 @@ class Act8:
         if codes.dim() != 2 or exps.dim() != 2 or exps.shape[0] != rows or \
                 codes.shape[1] < cols or exps.shape[1] * 32 < cols:
             raise ValueError("codes [rows, >= cols] and exps [rows, >= cols / 32] are needed")
-        self.codes, self.exps, self.shape = codes, exps, (rows, int(cols))
+        self.shape = (rows, int(cols))
+        self._codes, self._exps, self._memory = codes, exps, None
         self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), _rows2d(codes, "codes"),
                              exps.data_ptr(), _rows2d(exps, "exps"))
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda") -> "Act8":
+        """Memory of a checkpoint of rows x cols (its values are not set)."""
+        self = cls.__new__(cls)
+        blocks = (cols + 31) // 32
+        cs, es = blocks * 32, (blocks + 15) // 16 * 16
+        # one piece of memory; every exponent row starts on a 16-byte boundary
+        self._memory = torch.empty(rows * (cs + es), dtype=torch.int8, device=device)
+        self._codes = self._exps = None
+        self.shape = (rows, int(cols))
+        base = self._memory.data_ptr()
+        self.c = muon_act8_t(rows, int(cols), base, cs, base + rows * cs, es)
+        self.ref = ctypes.byref(self.c)
+        return self
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = self.shape[0] * self.c.code_stride
+            self._codes = self._memory[:n].view(self.shape[0], self.c.code_stride)
+        return self._codes
+
+    @property
+    def exps(self) -> torch.Tensor:
+        if self._exps is None:
+            n = self.shape[0] * self.c.code_stride
+            self._exps = self._memory[n:].view(torch.uint8).view(self.shape[0], self.c.exp_stride)
+        return self._exps
 
 
-def act8_empty(rows: int, cols: int, device="cuda") -> Act8:
-    """Memory of a checkpoint of rows x cols (its values are not set)."""
-    blocks = (cols + 31) // 32
-    return Act8(torch.empty(rows, blocks * 32, dtype=torch.int8, device=device),
-                torch.empty(rows, (blocks + 15) // 16 * 16, dtype=torch.uint8, device=device), cols)
+act8_empty = Act8.empty
 
 
 def muon_act8_pack(x: torch.Tensor, out: Act8, stream=None) -> None:
     """Write x [rows, cols] (bf16 or fp32) into the checkpoint."""
     _check(load_library().muon_act8_pack(x.data_ptr(), _dtype(x, "x"), _rows2d(x, "x", out.shape),
-                                         ctypes.byref(out.c), _stream(stream)), "muon_act8_pack")
+                                         out.ref, _stream(stream)), "muon_act8_pack")
 
 
 def muon_act8_unpack(a: Act8, out: torch.Tensor, stream=None) -> None:
     """Read a checkpoint back into out [rows, cols] (bf16 or fp32)."""
-    _check(load_library().muon_act8_unpack(ctypes.byref(a.c), out.data_ptr(), _dtype(out, "out"),
+    _check(load_library().muon_act8_unpack(a.ref, out.data_ptr(), _dtype(out, "out"),
                                            _rows2d(out, "out", a.shape), _stream(stream)),
            "muon_act8_unpack")
 
@@ -638,7 +672,7 @@ def muon_act8_swiglu_forward(gate: torch.Tensor, up: torch.Tensor, h: torch.Tens
     dt, s = _one_dtype(gate, up, h), gate8.shape
     _check(load_library().muon_act8_swiglu_forward(
         gate.data_ptr(), _rows2d(gate, "gate", s), up.data_ptr(), _rows2d(up, "up", s), dt,
-        h.data_ptr(), _rows2d(h, "h", s), ctypes.byref(gate8.c), ctypes.byref(up8.c),
+        h.data_ptr(), _rows2d(h, "h", s), gate8.ref, up8.ref,
         _stream(stream)), "muon_act8_swiglu_forward")
 
 
@@ -647,9 +681,9 @@ def muon_act8_swiglu_backward(dh: torch.Tensor, gate8: Act8, up8: Act8, dgate: t
     """Gradients of gate and up; h8, if given, receives silu(gate) * up."""
     dt, s = _one_dtype(dh, dgate, dup), gate8.shape
     _check(load_library().muon_act8_swiglu_backward(
-        dh.data_ptr(), _rows2d(dh, "dh", s), dt, ctypes.byref(gate8.c), ctypes.byref(up8.c),
+        dh.data_ptr(), _rows2d(dh, "dh", s), dt, gate8.ref, up8.ref,
         dgate.data_ptr(), _rows2d(dgate, "dgate", s), dup.data_ptr(), _rows2d(dup, "dup", s),
-        None if h8 is None else ctypes.byref(h8.c), _stream(stream)), "muon_act8_swiglu_backward")
+        None if h8 is None else h8.ref, _stream(stream)), "muon_act8_swiglu_backward")
 
 
 def muon_act8_weight_grad_workspace_size(rows: int, out: int, inp: int, experts: int = 1,

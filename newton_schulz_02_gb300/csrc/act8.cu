@@ -146,72 +146,81 @@ __device__ __forceinline__ float exponent_value(int b) {   // 2^(b - 127); infin
   return __uint_as_float(static_cast<uint32_t>(b) << 23);
 }
 
-// Largest magnitude of a block from its threads' V values each; NaN counts as
-// the largest (the comparison is on the bits).
-template <int V>
-__device__ __forceinline__ float block_amax(const float (&x)[V]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < V; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int d = kBlock / V / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return __uint_as_float(m);
+// max(|a|, |b|), with a sign that the caller drops; NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float m;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
-// Quantises the V values of this thread and leaves them in `out`; the lanes
-// of a block must be active together.  The values are replaced by what the
-// codes stand for where BACK is set.
+// Largest magnitude of a block from its threads' V values each; NaN if one is.
 template <int V>
-__device__ __forceinline__ void write_codes(const Packed& out, int64_t row, int col, int n,
+__device__ __forceinline__ float block_amax(const float (&x)[V]) {
+  float m = x[0];
+#pragma unroll
+  for (int k = 1; k < V; ++k) m = max_magnitude(m, x[k]);
+#pragma unroll
+  for (int d = kBlock / V / 2; d > 0; d >>= 1)
+    m = max_magnitude(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return fabsf(m);
+}
+
+// Quantises the V values of this thread; the lanes of a block must be active
+// together.  x / 2^e is exact, and adding 1.5 * 2^23 rounds it to the nearest
+// integer, ties to even, whose two's complement is the sum's low byte.
+template <int V>
+__device__ __forceinline__ void write_codes(const Packed& out, int64_t row, int col,
                                             const float (&x)[V], bool on) {
   const int b = scale_exponent(block_amax<V>(x));
   // 2^-e: the biased exponent of the reciprocal is 254 - b, in [5, 253]
   const float inv = b == 255 ? 0.f : exponent_value(254 - b);
-  const float top = b == 249 ? 63.f : 127.f;   // 64 * 2^122 overflows
   if (!on) return;
+  uint32_t c[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) c[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
+  if (b == 249) {   // 64 * 2^122 would overflow
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      c[k] = __float_as_uint(fminf(fmaxf(x[k] * inv, -63.f), 63.f) + 12582912.f);
+  }
   int8_t* p = out.codes + row * out.code_stride + col;
   if constexpr (V == 1) {
-    // columns past the end of the row, up to the block's end, hold 0
-    *p = static_cast<int8_t>(__float2int_rn(fminf(fmaxf(x[0] * inv, -top), top)));
+    *p = static_cast<int8_t>(c[0]);   // columns past the row's end, up to the block's, hold 0
   } else {
-    uint32_t w[V / 4];
 #pragma unroll
-    for (int q = 0; q < V / 4; ++q) {
-      uint32_t u = 0;
+    for (int q = 0; q < V / 16; ++q) {
+      uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int c = __float2int_rn(fminf(fmaxf(x[4 * q + k] * inv, -top), top));
-        u |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * k);
+        const uint32_t* d = c + 16 * q + 4 * k;
+        w[k] = __byte_perm(__byte_perm(d[0], d[1], 0x0040), __byte_perm(d[2], d[3], 0x0040), 0x5410);
       }
-      w[q] = u;
+      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-#pragma unroll
-    for (int q = 0; q < V / 16; ++q)
-      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   }
   if (col % kBlock == 0) out.exps[row * out.exp_stride + col / kBlock] = static_cast<uint8_t>(b);
 }
 
-// Values of V codes.  code * 2^e is one exact product; the byte 255 turns the
-// scale into an infinity, and infinity - infinity gives the block's NaN.
+// Values of V codes.  Biased by 128 a code is the low byte of 2^23 + 128 +
+// code, so a byte permute and a subtraction make the float (the conversion
+// unit is needed for the exponentials), and times 2^e is exact.
 template <int V>
 __device__ __forceinline__ void read_codes(const Packed& in, int64_t row, int col, float (&x)[V]) {
   const int b = in.exps[row * in.exp_stride + col / kBlock];
-  const float s = exponent_value(b);
-  const float nan = s - s;   // 0, or NaN for 255
+  const float s = b == 255 ? __uint_as_float(0x7FC00000u) : exponent_value(b);
   const int8_t* p = in.codes + row * in.code_stride + col;
   if constexpr (V == 1) {
-    x[0] = fmaf(static_cast<float>(*p), s, nan);
+    x[0] = static_cast<float>(*p) * s;
   } else {
 #pragma unroll
     for (int q = 0; q < V / 16; ++q) {
       const uint4 u = reinterpret_cast<const uint4*>(p)[q];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u,
+                             u.w ^ 0x80808080u};
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int c = static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)));
-        x[16 * q + k] = fmaf(static_cast<float>(c), s, nan);
-      }
+      for (int k = 0; k < 16; ++k)
+        x[16 * q + k] =
+            (__uint_as_float(__byte_perm(w[k / 4], 0x4B000000u, 0x7440 + k % 4)) - 8388736.f) * s;
     }
   }
 }
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_pack(const __grid_constant__ 
   const Place p = place<V>(a);
   float x[V];
   load_values<V, T>(a.x, p.row, p.col, p.n, x);
-  write_codes<V>(a.a, p.row, p.col, p.n, x, p.on);
+  write_codes<V>(a.a, p.row, p.col, x, p.on);
 }
 
 template <int V, typename T>
@@ -252,7 +261,9 @@ __global__ void __launch_bounds__(kThreads) k_act8_unpack(const __grid_constant_
   store_values<V, T>(a.x, p.row, p.col, p.n, x);
 }
 
-__device__ __forceinline__ float sigma(float g) { return 1.f / (1.f + expf(-g)); }
+// 1 / (1 + e^-g) with the fast exponential and reciprocal: an error of a few
+// units plus (1 - sigma) |g| units in the last place.
+__device__ __forceinline__ float sigma(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // x = gate, y = up, z = h; a, b = the checkpoints of gate and up.
 template <int V, typename T>
@@ -261,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) k_act8_swiglu_forward(const __grid_c
   float g[V], u[V], h[V];
   load_values<V, T>(a.x, p.row, p.col, p.n, g);
   load_values<V, T>(a.y, p.row, p.col, p.n, u);
-  write_codes<V>(a.a, p.row, p.col, p.n, g, p.on);
-  write_codes<V>(a.b, p.row, p.col, p.n, u, p.on);
+  write_codes<V>(a.a, p.row, p.col, g, p.on);
+  write_codes<V>(a.b, p.row, p.col, u, p.on);
 #pragma unroll
   for (int k = 0; k < V; ++k) h[k] = g[k] * sigma(g[k]) * u[k];
   if (p.on) store_values<V, T>(a.z, p.row, p.col, p.n, h);
@@ -289,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_swiglu_backward(const __grid_
     store_values<V, T>(a.y, p.row, p.col, p.n, g);
     store_values<V, T>(a.z, p.row, p.col, p.n, u);
   }
-  if constexpr (H8) write_codes<V>(a.c, p.row, p.col, p.n, h, p.on);
+  if constexpr (H8) write_codes<V>(a.c, p.row, p.col, h, p.on);
 }
 
 // ---- host ------------------------------------------------------------------

@@ -84,6 +84,8 @@ constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four
 constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
 constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
 constexpr int kUnits = 4;                        // units announced ahead
+constexpr int kStagePitch = 64 + 4;
+constexpr int kStageFloats = 4 * kStagePitch;
 
 // How dy comes: kTma (bf16), kTma32 (fp32 by TMA, split by eight warps), kLoad16
 // and kLoad32 (the same warps load it themselves, for rows off the boundaries
@@ -121,6 +123,7 @@ struct Cfg {
     uint32_t tmem_slot;
     int abort;
     alignas(16) int units[8 * kUnits];
+    alignas(16) float stage[kEpiWarps][kStageFloats];     // four rows of 64 columns a warp
   };
   static constexpr size_t kSmem = kDyStages * kStageBytes + kRawStages * kRawBytes +
                                   kSlots * (kSlotBytes + kCodeBytes + kExpBytes) +
@@ -246,39 +249,73 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// The same of 32 columns, 16 registers.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 16 consecutive columns of one row of G.
-__device__ __forceinline__ void store16(const Matrices& a, void* g, bool vec, int o, int i,
-                                        float (&v)[16]) {
-  if (o >= a.rows || i >= a.cols) return;
-  const int64_t at = static_cast<int64_t>(o) * a.stride + i;
-  if (vec && i + 16 <= a.cols) {   // whole 32-byte sectors
+// 32 bytes of G: whole sectors in one access where rows start on 32-byte
+// boundaries, else in two.
+__device__ __forceinline__ void load32(const void* p, bool whole, uint4& x, uint4& y) {
+  if (whole) {
+    ld_global_v8(p, x, y);
+  } else {
+    x = static_cast<const uint4*>(p)[0];
+    y = static_cast<const uint4*>(p)[1];
+  }
+}
+
+__device__ __forceinline__ void store32(void* p, bool whole, const uint4& x, const uint4& y) {
+  if (whole) {
+    st_global_v8(p, x, y);
+  } else {
+    static_cast<uint4*>(p)[0] = x;
+    static_cast<uint4*>(p)[1] = y;
+  }
+}
+
+// 8 rows x 64 columns of G from a warp: lane l has 16 consecutive columns, 16 (l
+// % 4) on, of row l / 4.  align: what divides the rows' addresses.
+__device__ __forceinline__ void store_8x64(const Matrices& a, char* g, int align, int o, int i,
+                                           int lane, float (&v)[16], float* stage) {
+  if (i >= a.cols || o >= a.rows) return;   // the whole warp
+  if (align >= 16 && i + 64 <= a.cols) {
+    const bool whole = align >= 32;
+    if (o + (lane >> 2) >= a.rows) return;
+    const int64_t at = static_cast<int64_t>(o + (lane >> 2)) * a.stride + i + 16 * (lane & 3);
     if (a.dtype == MUON_F32) {
-      float* p = static_cast<float*>(g) + at;
+      float* p = reinterpret_cast<float*>(g) + at;
 #pragma unroll
       for (int k = 0; k < 16; k += 8) {
         if (a.accumulate) {
           uint4 x, y;
-          ld_global_v8(p + k, x, y);
+          load32(p + k, whole, x, y);
           const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[k + j] += __uint_as_float(w[j]);
         }
-        st_global_v8(p + k,
-                     make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
+        store32(p + k, whole,
+                make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
                                 __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])),
                      make_uint4(__float_as_uint(v[k + 4]), __float_as_uint(v[k + 5]),
                                 __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7])));
       }
     } else {
-      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g) + at;
+      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g) + at;
       if (a.accumulate) {
         uint4 x, y;
-        ld_global_v8(p, x, y);
+        load32(p, whole, x, y);
         const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -286,24 +323,40 @@ __device__ __forceinline__ void store16(const Matrices& a, void* g, bool vec, in
           v[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
         }
       }
-      st_global_v8(p,
-                   make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
+      store32(p, whole,
+              make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
                               pack2(v[6], v[7])),
                    make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]),
                               pack2(v[14], v[15])));
     }
     return;
   }
+  // The last columns of a matrix, or rows off 16-byte boundaries: through
+  // shared memory, so that the warp writes consecutive columns of one row.
+#pragma unroll 1
+  for (int part = 0; part < 8; part += 4) {
+    if ((lane >> 4) * 4 == part) {
+      float4* p = reinterpret_cast<float4*>(stage + (lane >> 2 & 3) * kStagePitch + 16 * (lane & 3));
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    if (i + k >= a.cols) break;
-    if (a.dtype == MUON_F32) {
-      float* p = static_cast<float*>(g) + at + k;
-      *p = a.accumulate ? *p + v[k] : v[k];
-    } else {
-      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(g) + at + k;
-      *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + v[k] : v[k]);
+      for (int k = 0; k < 4; ++k) p[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = o + part + (k >> 1), col = i + (k & 1) * 32 + lane;
+      const float x = stage[(k >> 1) * kStagePitch + (k & 1) * 32 + lane];
+      if (row < a.rows && col < a.cols) {
+        const int64_t at = static_cast<int64_t>(row) * a.stride + col;
+        if (a.dtype == MUON_F32) {
+          float* p = reinterpret_cast<float*>(g) + at;
+          *p = a.accumulate ? *p + x : x;
+        } else {
+          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g) + at;
+          *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + x : x);
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -369,6 +422,11 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
   using C = Cfg<MODE>;
   constexpr int kDyStages = C::kDyStages, kSlots = C::kSlots;
   constexpr bool kTmaDy = MODE == kTma || MODE == kTma32;
+  // Two accumulators take turns; with three planes one takes the sums of the
+  // upper parts and the other those of the rest.  The tensor core's additions
+  // truncate: apart, the long sum is added to a third as often, and the error of
+  // 32 blocks against 64 bits falls from 6e-6 to 2e-6.
+  constexpr uint32_t kAccs = C::kPlanes == 1 ? 2 : 1;
   uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
   uint8_t* sm_x = sm_dy + kDyStages * C::kStageBytes;       // decoded, swizzled
   uint8_t* sm_raw = sm_x + kSlots * kSlotBytes;             // fp32, rows of 512 bytes
@@ -496,8 +554,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       Unit t;
       while (ok && take(t, false)) {
         if (t.n == 0) continue;
-        const uint32_t acc = tile & 1u;
-        if (!mbar_wait_bounded(&tempty[acc], (tile >> 1 & 1u) ^ 1u, abort_flag, a.status,
+        const uint32_t acc = tile % kAccs;
+        if (!mbar_wait_bounded(&tempty[acc], (tile / kAccs & 1u) ^ 1u, abort_flag, a.status,
                                a.timeout_ns))
           break;
         tc_fence_after();
@@ -511,13 +569,14 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
           tc_fence_after();
           const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
 #pragma unroll
-          for (int p = C::kPlanes - 1; p >= 0; --p) {   // the smallest parts first
+          for (int p = C::kPlanes - 1; p >= 0; --p) {
             const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kDyBytes);
 #pragma unroll
             for (int ks = 0; ks < kBK / 16; ++ks)
-              tc_mma_bf16_pair(d, smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
+              tc_mma_bf16_pair(d + (p > 0 ? 256u : 0u),
+                               smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
                                smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
-                               k0 == 0 && p == C::kPlanes - 1 && ks == 0 ? 0u : 1u);
+                               k0 == 0 && (p == 0 || p == C::kPlanes - 1) && ks == 0 ? 0u : 1u);
           }
           tc_commit_pair_multicast(&dy_empty[s], 0x3);
           if (++s == kDyStages) s = 0;
@@ -720,22 +779,24 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
     const int q = warp & 3;                    // tensor-memory lanes 32 q ..
     const int half = (warp - C::kEpi0) >> 2;      // columns 128 half ..
     const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
+    float* stage = bars.stage[warp - C::kEpi0];
     uint32_t tile = 0;
     Unit t;
     while (take(t, true)) {
       if (t.n == 0 && a.g.accumulate) continue;
-      const uint32_t acc = tile & 1u;
+      const uint32_t acc = tile % kAccs;
       if (t.n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile >> 1 & 1u, abort_flag,
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile / kAccs & 1u, abort_flag,
                                                        a.status, a.timeout_ns)))
           break;
         tc_fence_after();
       }
       char* g = matrix_of(a.g, t.m);
       const int esz = a.g.dtype == MUON_F32 ? 4 : 2;
-      const bool vec = (reinterpret_cast<uintptr_t>(g) & 31u) == 0 && a.g.stride * esz % 32 == 0;
-      const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32 + (lane >> 2);
-      const int i = t.i0 + half * 128 + 16 * (lane & 3);
+      const uint64_t bits = reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(a.g.stride * esz);
+      const int align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+      const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32;
+      const int i = t.i0 + half * 128;
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
 #pragma unroll 1
       for (int piece = 0; piece < 4; ++piece) {
@@ -743,8 +804,21 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
         uint32_t raw[32];
         __syncwarp();   // tcgen05.ld takes the warp together
         if (t.n > 0) {
-          tmem_ld_16x256b_x8(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
+          const uint32_t at = src + (static_cast<uint32_t>(dr) << 16) + dc;
+          tmem_ld_16x256b_x8(at, raw);
           tmem_ld_wait(raw);
+          if constexpr (C::kPlanes > 1) {
+#pragma unroll
+            for (int b = 0; b < 32; b += 16) {
+              uint32_t rest[16];
+              tmem_ld_16x256b_x4(at + 256u + 2 * b, rest);
+              tmem_ld_wait();
+              tmem_ld_tie(rest);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                raw[b + k] = __float_as_uint(__uint_as_float(raw[b + k]) + __uint_as_float(rest[k]));
+            }
+          }
         } else {   // an expert without tokens
 #pragma unroll
           for (int k = 0; k < 32; ++k) raw[k] = 0u;
@@ -757,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               v[4 * (b >> 1) + (b & 1) + 2 * k] = __uint_as_float(raw[4 * b + 2 * h + k]);
-          store16(a.g, g, vec, o + dr + 8 * h, i + dc, v);
+          store_8x64(a.g, g, align, o + dr + 8 * h, i + dc, lane, v, stage);
         }
       }
       if (t.n == 0) continue;

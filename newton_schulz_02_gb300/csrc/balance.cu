@@ -30,11 +30,13 @@ constexpr int kMaxExperts = 1024;
 constexpr int kFinThreads = 1024;   // finalize: 32 experts x 32 partial rows at a time
 constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks
 
-// Tokens of a chunk: at most ~600 chunks (four blocks on each of 152 SMs), so
-// that the partial rows stay few.  A function of the sizes alone, as the
-// order of the sums follows it.
-int chunk_tokens(int64_t tokens) {
-  const int64_t c = (tokens + 607) / 608;
+// Tokens of a chunk.  Chunks and the cuts at sequence bounds together make up
+// to 608 blocks, four on each of 152 SMs at once (one block more would be a
+// second wave); with many sequences there are up to 304 beside their cuts.  A
+// function of the sizes alone, as the order of the sums follows it.
+int chunk_tokens(int64_t tokens, int sequences) {
+  const int64_t most = 608 - (sequences < 304 ? sequences : 304);
+  const int64_t c = tokens / most + 1;
   return static_cast<int>(c < 32 ? 32 : c);
 }
 
@@ -43,7 +45,7 @@ int chunk_tokens(int64_t tokens) {
 // (e-1)/C + s: one number for each (chunk, sequence) pair, ascending, without
 // knowing the bounds on the host.
 int64_t chunk_items(int64_t tokens, int sequences) {
-  return tokens / chunk_tokens(tokens) + sequences;
+  return tokens / chunk_tokens(tokens, sequences) + sequences;
 }
 
 struct BalanceArgs {
@@ -77,6 +79,7 @@ struct BalanceArgs {
   int64_t dlogits_stride;
   int dvec;
   int accumulate;
+  int row_steps;              // rows a group of lanes walks
 };
 
 __device__ __forceinline__ int clamp_token(int v, int tokens) { return min(max(v, 0), tokens); }
@@ -166,7 +169,8 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// Probabilities of a row in place of its logits; slope (sigmoid only) = 1 - sigma.
+// Probabilities of a row in place of its logits (the fast exponential's error
+// is a few units plus |x| units, below what the logits' own rounding means); slope (sigmoid only) = 1 - sigma.
 // A row whose scores sum to 0 (every expert disabled) gets 0; NaN stays NaN.
 template <int LANES, int VPT, bool SLOPE>
 __device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
@@ -175,8 +179,8 @@ __device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
   if (sigmoid) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const float t = expf(-x[j]);
-      const float s = 1.f / (1.f + t);
+      const float t = __expf(-x[j]);
+      const float s = __fdividef(1.f, 1.f + t);
       if (SLOPE) slope[j] = t < 1.f ? t * s : 1.f - s;   // no cancellation where sigma is near 1
       x[j] = s;
       z += s;
@@ -189,7 +193,7 @@ __device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      x[j] = expf(x[j] - m);
+      x[j] = __expf(x[j] - m);
       z += x[j];
     }
   }
@@ -271,100 +275,103 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const __grid_const
   }
 }
 
-__device__ __forceinline__ int block_sum(int v, int* s_warp) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_warp[threadIdx.x & 31];
-  return __reduce_add_sync(0xffffffffu, v);
-}
-
 // One block per (sequence, 32 experts): adds the chunks' partial rows, writes
 // the load, adds the counts; the last block to finish adds the loss.
 __global__ void __launch_bounds__(kFinThreads) k_balance_finalize(const __grid_constant__ BalanceArgs a) {
   __shared__ float s_f[32][33];
   __shared__ int s_i[32][33];
-  __shared__ int s_warp[32];
+  __shared__ int s_all[32], s_mine[32], s_bad[32];
   __shared__ int s_last;
-  griddep_wait();
   const int eblocks = (a.experts + 31) / 32;
   const int s = blockIdx.x / eblocks, eb = blockIdx.x % eblocks;
-  const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int e = eb * 32 + col;
-  int all = 0, bad = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = seq_at(a, s), end = seq_at(a, s + 1);
+  const int i0 = b / a.chunk + s, i1 = b < end ? min((end - 1) / a.chunk + s, a.items - 1) : i0 - 1;
+  griddep_wait();
+  // partial rows: warp w takes every 32nd, a lane one expert
+  float p = 0.f;
+  int c = 0;
+  if (eb * 32 + lane < a.experts) {
+    const int64_t at = static_cast<int64_t>(eb) * 32 + lane;
+    for (int i = i0 + warp; i <= i1; i += 32) {
+      p += a.psum[i * static_cast<int64_t>(a.experts) + at];
+      c += a.pcnt[i * static_cast<int64_t>(a.experts) + at];
+    }
+  }
+  // valid tokens of the batch and of this sequence, device conditions
+  int all = 0, mine = 0, bad = 0;
   for (int i = threadIdx.x; i < a.items; i += kFinThreads) {
-    all += a.pval[i];
+    const int n = a.pval[i];
+    all += n;
+    if (i >= i0 && i <= i1) mine += n;
     bad |= a.pflag[i];
   }
-  const int total = block_sum(all, s_warp);
-  const int b = seq_at(a, s), end = seq_at(a, s + 1);
-  float p = 0.f;
-  int c = 0, mine = 0;
-  if (b < end) {
-    const int i0 = b / a.chunk + s, i1 = min((end - 1) / a.chunk + s, a.items - 1);
-    if (e < a.experts)
-      for (int i = i0 + row; i <= i1; i += 32) {
-        p += a.psum[static_cast<int64_t>(i) * a.experts + e];
-        c += a.pcnt[static_cast<int64_t>(i) * a.experts + e];
-      }
-    for (int i = i0 + threadIdx.x; i <= i1; i += kFinThreads) mine += a.pval[i];
+  all = __reduce_add_sync(0xffffffffu, all);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  bad = __any_sync(0xffffffffu, bad);
+  s_f[warp][lane] = p;
+  s_i[warp][lane] = c;
+  if (lane == 0) {
+    s_all[warp] = all;
+    s_mine[warp] = mine;
+    s_bad[warp] = bad;
   }
-  const int n = block_sum(mine, s_warp);
-  s_f[row][col] = p;
-  s_i[row][col] = c;
   __syncthreads();
+  // warp w: expert 32 eb + w
+  const int e = eb * 32 + warp;
+  p = group_sum<32>(s_f[lane][warp]);
+  c = __reduce_add_sync(0xffffffffu, s_i[lane][warp]);
+  all = __reduce_add_sync(0xffffffffu, s_all[lane]);
+  mine = __reduce_add_sync(0xffffffffu, s_mine[lane]);
+  bad = __any_sync(0xffffffffu, s_bad[lane]);
   float contrib = 0.f;
-  if (row == 0) {
-    p = 0.f;
-    c = 0;
-    for (int r = 0; r < 32; ++r) {
-      p += s_f[r][col];
-      c += s_i[r][col];
-    }
-    if (e < a.experts) {
-      const float scale = n == 0 ? 0.f
-                                 : a.coef / static_cast<float>(total) *
-                                       (static_cast<float>(a.experts) /
-                                        (static_cast<float>(a.topk) * static_cast<float>(n)));
-      const float f = scale * static_cast<float>(c);
+  if (e < a.experts) {
+    const float scale = mine == 0 ? 0.f
+                                  : a.coef / static_cast<float>(all) *
+                                        (static_cast<float>(a.experts) /
+                                         (static_cast<float>(a.topk) * static_cast<float>(mine)));
+    const float f = scale * static_cast<float>(c);
+    contrib = f * p;
+    if (lane == 0) {
       a.load[static_cast<int64_t>(s) * a.experts + e] = f;
       if (c) atomicAdd(a.counts + e, c);
-      contrib = f * p;
     }
-    contrib = group_sum<32>(contrib);
-    if (col == 0) a.lossp[blockIdx.x] = contrib;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (lane == 0) s_f[0][warp] = contrib;
+  __syncthreads();
+  if (warp != 0) {
+    if (gridDim.x == 1) return;
+  } else {
+    contrib = group_sum<32>(s_f[0][lane]);
+  }
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      a.lossp[blockIdx.x] = contrib;
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
     __threadfence();
-    s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    float v = 0.f;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinThreads) v += __ldcg(a.lossp + i);
+    v = group_sum<32>(v);
+    if (lane == 0) s_f[1][warp] = v;
+    __syncthreads();
+    if (warp != 0) return;
+    contrib = group_sum<32>(s_f[1][lane]);
   }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  float v = 0.f;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinThreads) v += __ldcg(a.lossp + i);
   // bounds that do not ascend within [0, tokens]
   if (a.seq_begin != nullptr)
-    for (int i = threadIdx.x; i <= a.sequences; i += kFinThreads) {
+    for (int i = lane; i <= a.sequences; i += 32) {
       const int at = a.seq_begin[i];
       if (at < 0 || at > a.tokens || (i > 0 && at < a.seq_begin[i - 1])) bad = 1;
     }
-  v = group_sum<32>(v);
   bad = __any_sync(0xffffffffu, bad);
-  if (col == 0) {
-    s_f[0][row] = v;
-    s_i[0][row] = bad;
-  }
-  __syncthreads();
-  if (row == 0) {
-    v = group_sum<32>(s_f[0][col]);
-    bad = __any_sync(0xffffffffu, s_i[0][col]);
-    if (col == 0) {
-      *a.loss = v;
-      *a.status = bad ? MUON_FLAG_INDEX : 0u;
-    }
+  if (lane == 0) {
+    *a.loss = contrib;
+    *a.status = bad ? MUON_FLAG_INDEX : 0u;
   }
 }
 
@@ -413,20 +420,19 @@ __device__ __forceinline__ void store_row(const BalanceArgs& a, int64_t off, int
   }
 }
 
-constexpr int kRowsPerGroup = 8;   // consecutive rows steps a group keeps its sequence's load for
-
 template <int LANES, int VPT>
 __global__ void __launch_bounds__(kThreads) k_balance_backward(const __grid_constant__ BalanceArgs a) {
   constexpr int kGroups = kThreads / LANES;
   const int group = threadIdx.x / LANES, sub = threadIdx.x % LANES;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * kRowsPerGroup);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * a.row_steps);
   const float scale = a.dloss == nullptr ? 1.f : *a.dloss;
   int s = -2, s_end = 0;
   float f[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) f[j] = 0.f;
-  for (int r = 0; r < kRowsPerGroup; ++r) {
-    const int64_t t64 = first + static_cast<int64_t>(r) * kGroups + group;
+  for (int r = 0; r < a.row_steps; ++r) {
+    if (first + r * kGroups >= a.tokens) break;   // the whole block
+    const int64_t t64 = first + r * kGroups + group;
     const bool in = t64 < a.tokens;
     const int t = in ? static_cast<int>(t64) : a.tokens - 1;
     if (s == -2 || t >= s_end) {
@@ -459,13 +465,17 @@ __global__ void __launch_bounds__(kThreads) k_balance_backward(const __grid_cons
   }
 }
 
-// Lanes and values a row takes: the narrowest that holds it.
+// Lanes and values a row takes: the narrowest that holds it, with up to 16
+// values a lane before more lanes (a value costs its share of the row's three
+// reductions, which take log2(lanes) shuffles each).
 template <template <int, int> class F>
 cudaError_t by_width(const BalanceArgs& a, cudaStream_t st) {
   if (a.experts <= 32) return F<8, 4>::run(a, st);
-  if (a.experts <= 64) return F<16, 4>::run(a, st);
-  if (a.experts <= 128) return F<32, 4>::run(a, st);
-  if (a.experts <= 256) return F<32, 8>::run(a, st);
+  if (a.experts <= 64) return F<8, 8>::run(a, st);
+  if (a.experts <= 128) return F<8, 16>::run(a, st);
+  if (a.experts <= 192) return F<16, 12>::run(a, st);
+  if (a.experts <= 256) return F<16, 16>::run(a, st);
+  if (a.experts <= 384) return F<32, 12>::run(a, st);
   if (a.experts <= 512) return F<32, 16>::run(a, st);
   return F<32, 32>::run(a, st);
 }
@@ -481,9 +491,15 @@ struct Forward {
 template <int LANES, int VPT>
 struct Backward {
   static cudaError_t run(const BalanceArgs& a, cudaStream_t st) {
-    const int64_t rows = (kThreads / LANES) * kRowsPerGroup;
+    // a group keeps its sequence's load over up to 8 rows, fewer where the
+    // tokens would not fill 152 SMs eight times over
+    constexpr int kGroups = kThreads / LANES;
+    BalanceArgs b = a;
+    const int steps = a.tokens / (kGroups * 152 * 8);
+    b.row_steps = steps < 1 ? 1 : steps > 8 ? 8 : steps;
+    const int64_t rows = static_cast<int64_t>(kGroups) * b.row_steps;
     k_balance_backward<LANES, VPT>
-        <<<static_cast<unsigned>((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(a);
+        <<<static_cast<unsigned>((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(b);
     return cudaGetLastError();
   }
 };
@@ -542,7 +558,7 @@ BalanceArgs base_args(const muon_balance_t* b) {
   a.experts = b->experts;
   a.topk = b->topk;
   a.sequences = b->sequences;
-  a.chunk = chunk_tokens(b->tokens);
+  a.chunk = chunk_tokens(b->tokens, b->sequences);
   a.items = static_cast<int>(chunk_items(b->tokens, b->sequences));
   a.logits = b->logits;
   a.dtype = b->dtype;
