@@ -60,7 +60,7 @@ struct BalanceArgs {
   const uint8_t* mask;        // nullptr: all valid
   int sigmoid;
   float coef;
-  int vec;                    // rows may be read four values at a time
+  int vec, lvec;              // rows of logits, of load, may be read four values at a time
   // forward
   float* psum;                // [items][experts]
   int* pcnt;                  // [items][experts]
@@ -122,35 +122,44 @@ __device__ __forceinline__ int column(int sub, int j) {
   return (j >> 2) * (4 * LANES) + 4 * sub + (j & 3);
 }
 
-template <int LANES, int VPT>
+// Columns column(sub, 0..VPT-1) of a row of n values; columns from n on are
+// `fill`.  FULL: n = LANES * VPT.
+template <int LANES, int VPT, bool FULL>
 __device__ __forceinline__ void load_row(const void* base, int64_t off, int dtype, int n, int vec,
                                          int sub, float fill, float (&x)[VPT]) {
+  if (vec && dtype == MUON_F32) {
+    const float* p = static_cast<const float*>(base) + off;
 #pragma unroll
-  for (int q = 0; q < VPT / 4; ++q) {
-    const int c = column<LANES>(sub, 4 * q);
-    if (vec) {
-      if (c < n) {
-        if (dtype == MUON_F32) {
-          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + c);
-          x[4 * q] = v.x; x[4 * q + 1] = v.y; x[4 * q + 2] = v.z; x[4 * q + 3] = v.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + off + c);
-          const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-          const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-          x[4 * q] = f0.x; x[4 * q + 1] = f0.y; x[4 * q + 2] = f1.x; x[4 * q + 3] = f1.y;
-        }
-      } else {
-        x[4 * q] = x[4 * q + 1] = x[4 * q + 2] = x[4 * q + 3] = fill;
-      }
-    } else {
+    for (int q = 0; q < VPT / 4; ++q) {
+      const int c = column<LANES>(sub, 4 * q);
+      float4 v = make_float4(fill, fill, fill, fill);
+      if (FULL || c < n) v = *reinterpret_cast<const float4*>(p + c);
+      x[4 * q] = v.x; x[4 * q + 1] = v.y; x[4 * q + 2] = v.z; x[4 * q + 3] = v.w;
+    }
+  } else if (vec) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + off;
+    uint2 w[VPT / 4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[4 * q + k] = fill;
-        if (c + k < n)
-          x[4 * q + k] = dtype == MUON_F32
-                             ? static_cast<const float*>(base)[off + c + k]
-                             : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off + c + k]);
-      }
+    for (int q = 0; q < VPT / 4; ++q) {
+      const int c = column<LANES>(sub, 4 * q);
+      if (FULL || c < n) w[q] = *reinterpret_cast<const uint2*>(p + c);
+    }
+#pragma unroll
+    for (int q = 0; q < VPT / 4; ++q) {
+      const bool in = FULL || column<LANES>(sub, 4 * q) < n;
+      x[4 * q] = in ? __uint_as_float(w[q].x << 16) : fill;
+      x[4 * q + 1] = in ? __uint_as_float(w[q].x & 0xFFFF0000u) : fill;
+      x[4 * q + 2] = in ? __uint_as_float(w[q].y << 16) : fill;
+      x[4 * q + 3] = in ? __uint_as_float(w[q].y & 0xFFFF0000u) : fill;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = column<LANES>(sub, j);
+      x[j] = fill;
+      if (c < n)
+        x[j] = dtype == MUON_F32 ? static_cast<const float*>(base)[off + c]
+                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[off + c]);
     }
   }
 }
@@ -169,20 +178,28 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// Probabilities of a row in place of its logits (the fast exponential's error
-// is a few units plus |x| units, below what the logits' own rounding means); slope (sigmoid only) = 1 - sigma.
-// A row whose scores sum to 0 (every expert disabled) gets 0; NaN stays NaN.
-template <int LANES, int VPT, bool SLOPE>
-__device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
-                                                  float (&slope)[SLOPE ? VPT : 1]) {
+// 2^y, flushed to 0 below the normal range.
+__device__ __forceinline__ float exp2_fast(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// Scores of a row in place of its logits, up to the factor that makes them
+// probabilities, which is returned: softmax exp(l - max); sigmoid 1 / (1 + t),
+// or with KEEP_T the t = exp(-l) itself.  A row whose scores sum to 0 (every
+// expert disabled) gets the factor 0; NaN stays NaN.
+template <int LANES, int VPT, bool KEEP_T>
+__device__ __forceinline__ float row_scores(int sigmoid, float (&x)[VPT]) {
   float z = 0.f;
   if (sigmoid) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const float t = __expf(-x[j]);
+      const float t = exp2_fast(-kLog2e * x[j]);
       const float s = __fdividef(1.f, 1.f + t);
-      if (SLOPE) slope[j] = t < 1.f ? t * s : 1.f - s;   // no cancellation where sigma is near 1
-      x[j] = s;
+      x[j] = KEEP_T ? t : s;
       z += s;
     }
   } else {
@@ -193,20 +210,19 @@ __device__ __forceinline__ void row_probabilities(int sigmoid, float (&x)[VPT],
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      x[j] = __expf(x[j] - m);
+      x[j] = exp2_fast(kLog2e * (x[j] - m));
       z += x[j];
     }
   }
   z = group_sum<LANES>(z);
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) x[j] *= inv;
+  return z == 0.f ? 0.f : 1.f / z;
 }
 
 // One chunk of tokens of one sequence per block: sum_t p_te, c_e and the
 // number of valid tokens.
-template <int LANES, int VPT>
-__global__ void __launch_bounds__(kThreads) k_balance_forward(const __grid_constant__ BalanceArgs a) {
+template <int LANES, int VPT, bool FULL>
+__global__ void __launch_bounds__(kThreads, VPT <= 16 ? 4 : 2)
+    k_balance_forward(const __grid_constant__ BalanceArgs a) {
   constexpr int kGroups = kThreads / LANES;
   constexpr int kCols = LANES * VPT;
   __shared__ float s_sum[kGroups * kCols];
@@ -236,21 +252,36 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const __grid_const
 #pragma unroll
   for (int j = 0; j < VPT; ++j) acc[j] = 0.f;
   int valid = 0, bad = 0;
+  const auto is_on = [&](int t) { return t < t1 && (a.mask == nullptr || a.mask[t] != 0); };
+  const auto choice = [&](int t, int k) {
+    const int64_t at = static_cast<int64_t>(t) * a.chosen_stride + k;
+    return a.chosen_bytes == 4 ? static_cast<int64_t>(static_cast<const int32_t*>(a.chosen)[at])
+                               : static_cast<const int64_t*>(a.chosen)[at];
+  };
+  // A row's loads depend on its mask, which is fetched a row ahead; the choices
+  // are fetched beside the logits.
+  bool next_on = is_on(t0 + group);
   for (int tb = t0; tb < t1; tb += kGroups) {   // uniform trip count: shuffles need every lane
     const int t = tb + group;
-    const bool on = t < t1 && (a.mask == nullptr || a.mask[t] != 0);
-    float x[VPT], none[1];
-    load_row<LANES, VPT>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
-                         on ? a.experts : 0, a.vec, sub, -INFINITY, x);
-    row_probabilities<LANES, VPT, false>(a.sigmoid, x, none);
+    const bool on = next_on;
+    next_on = is_on(t + kGroups);
+    int64_t id = -1;
+    float x[VPT];
+    if (on) {
+      load_row<LANES, VPT, FULL>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
+                                 a.experts, a.vec, sub, -INFINITY, x);
+      if (sub < a.topk) id = choice(t, sub);
+    } else {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) acc[j] += x[j];
+      for (int j = 0; j < VPT; ++j) x[j] = -INFINITY;
+    }
+    const float inv = row_scores<LANES, VPT, false>(a.sigmoid, x);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) acc[j] = fmaf(x[j], inv, acc[j]);
     if (on) {
       valid += sub == 0;
       for (int k = sub; k < a.topk; k += LANES) {
-        const int64_t at = static_cast<int64_t>(t) * a.chosen_stride + k;
-        const int64_t id = a.chosen_bytes == 4 ? static_cast<const int32_t*>(a.chosen)[at]
-                                               : static_cast<const int64_t*>(a.chosen)[at];
+        if (k != sub) id = choice(t, k);
         if (id >= 0 && id < a.experts)
           atomicAdd(&s_cnt[id], 1);
         else if (id != -1)
@@ -265,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_forward(const __grid_const
   __syncthreads();
   for (int i = threadIdx.x; i < a.experts; i += kThreads) {
     float v = 0.f;
+#pragma unroll 8
     for (int g = 0; g < kGroups; ++g) v += s_sum[g * kCols + i];
     a.psum[static_cast<int64_t>(item) * a.experts + i] = v;
     a.pcnt[static_cast<int64_t>(item) * a.experts + i] = s_cnt[i];
@@ -375,14 +407,14 @@ __global__ void __launch_bounds__(kFinThreads) k_balance_finalize(const __grid_c
   }
 }
 
-template <int LANES, int VPT>
+template <int LANES, int VPT, bool FULL>
 __device__ __forceinline__ void store_row(const BalanceArgs& a, int64_t off, int sub,
                                           const float (&d)[VPT]) {
 #pragma unroll
   for (int q = 0; q < VPT / 4; ++q) {
     const int c = column<LANES>(sub, 4 * q);
     if (a.dvec) {
-      if (c >= a.experts) continue;
+      if (!FULL && c >= a.experts) continue;
       if (a.ddt == MUON_F32) {
         float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + off + c);
         float4 v = make_float4(d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]);
@@ -420,75 +452,102 @@ __device__ __forceinline__ void store_row(const BalanceArgs& a, int64_t off, int
   }
 }
 
-template <int LANES, int VPT>
-__global__ void __launch_bounds__(kThreads) k_balance_backward(const __grid_constant__ BalanceArgs a) {
+template <int LANES, int VPT, bool FULL>
+__global__ void __launch_bounds__(kThreads, VPT <= 16 ? 4 : 2)
+    k_balance_backward(const __grid_constant__ BalanceArgs a) {
   constexpr int kGroups = kThreads / LANES;
   const int group = threadIdx.x / LANES, sub = threadIdx.x % LANES;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * a.row_steps);
+  const int64_t last = first + static_cast<int64_t>(a.row_steps) * kGroups;
+  const int stop = static_cast<int>(last < a.tokens ? last : a.tokens);
   const float scale = a.dloss == nullptr ? 1.f : *a.dloss;
   int s = -2, s_end = 0;
   float f[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) f[j] = 0.f;
-  for (int r = 0; r < a.row_steps; ++r) {
-    if (first + r * kGroups >= a.tokens) break;   // the whole block
-    const int64_t t64 = first + r * kGroups + group;
-    const bool in = t64 < a.tokens;
-    const int t = in ? static_cast<int>(t64) : a.tokens - 1;
+  const auto is_on = [&](int t) { return t < stop && (a.mask == nullptr || a.mask[t] != 0); };
+  bool next_on = is_on(static_cast<int>(first) + group);   // fetched a row ahead, as in the forward pass
+  for (int tb = static_cast<int>(first); tb < stop; tb += kGroups) {   // the whole block together
+    const bool in = tb + group < stop;
+    const int t = in ? tb + group : stop - 1;
     if (s == -2 || t >= s_end) {
       s = seq_of_token(a, t);
       s_end = s + 1 <= a.sequences ? seq_at(a, s + 1) : a.tokens;
       const bool inside = s >= 0 && t < s_end;
       if (!inside) s_end = t;   // between sequences: look again at the next token
-      load_row<LANES, VPT>(a.load, static_cast<int64_t>(inside ? s : 0) * a.experts, MUON_F32,
-                           inside ? a.experts : 0, a.experts % 4 == 0 && (reinterpret_cast<uintptr_t>(a.load) & 15) == 0,
-                           sub, 0.f, f);
+      load_row<LANES, VPT, FULL>(a.load, static_cast<int64_t>(inside ? s : 0) * a.experts, MUON_F32,
+                                 a.experts, a.lvec, sub, 0.f, f);
       if (!inside) s = -2;
     }
-    const bool on = in && s >= 0 && (a.mask == nullptr || a.mask[t] != 0);
-    float x[VPT], slope[VPT];
-    load_row<LANES, VPT>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
-                         on ? a.experts : 0, a.vec, sub, -INFINITY, x);
-    row_probabilities<LANES, VPT, true>(a.sigmoid, x, slope);
+    const bool on = next_on && s >= 0;
+    next_on = is_on(tb + group + kGroups);
+    float x[VPT];
+    if (on) {
+      load_row<LANES, VPT, FULL>(a.logits, static_cast<int64_t>(t) * a.logits_stride, a.dtype,
+                                 a.experts, a.vec, sub, -INFINITY, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) x[j] = -INFINITY;
+    }
+    const float inv = row_scores<LANES, VPT, true>(a.sigmoid, x);
+    const float by = scale * inv;
     float dot = 0.f;
+    if (a.sigmoid) {
+      // x holds t = exp(-l): the score is s = 1 / (1 + t), its slope s (1 - s) with
+      // 1 - s = t s where s is near 1 (no cancellation)
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) dot = fmaf(f[j], x[j], dot);
-    dot = group_sum<LANES>(dot);
+      for (int j = 0; j < VPT; ++j) dot = fmaf(f[j], __fdividef(1.f, 1.f + x[j]), dot);
+      dot = group_sum<LANES>(dot) * inv;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      float d = scale * x[j] * (f[j] - dot);
-      if (a.sigmoid) d *= slope[j];
-      x[j] = on ? d : 0.f;
+      for (int j = 0; j < VPT; ++j) {
+        const float r = __fdividef(1.f, 1.f + x[j]);
+        const float slope = x[j] < 1.f ? x[j] * r : 1.f - r;
+        x[j] = by * r * slope * (f[j] - dot);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) dot = fmaf(f[j], x[j], dot);
+      dot = group_sum<LANES>(dot) * inv;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) x[j] = by * x[j] * (f[j] - dot);
+    }
+    if (!on) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) x[j] = 0.f;
     }
     if (in && (on || !a.accumulate))
-      store_row<LANES, VPT>(a, static_cast<int64_t>(t) * a.dlogits_stride, sub, x);
+      store_row<LANES, VPT, FULL>(a, static_cast<int64_t>(t) * a.dlogits_stride, sub, x);
   }
 }
 
 // Lanes and values a row takes: the narrowest that holds it, with up to 16
 // values a lane before more lanes (a value costs its share of the row's three
 // reductions, which take log2(lanes) shuffles each).
-template <template <int, int> class F>
-cudaError_t by_width(const BalanceArgs& a, cudaStream_t st) {
-  if (a.experts <= 32) return F<8, 4>::run(a, st);
-  if (a.experts <= 64) return F<8, 8>::run(a, st);
-  if (a.experts <= 128) return F<8, 16>::run(a, st);
-  if (a.experts <= 192) return F<16, 12>::run(a, st);
-  if (a.experts <= 256) return F<16, 16>::run(a, st);
-  if (a.experts <= 384) return F<32, 12>::run(a, st);
-  if (a.experts <= 512) return F<32, 16>::run(a, st);
-  return F<32, 32>::run(a, st);
+template <template <int, int, bool> class F, int LANES, int VPT>
+cudaError_t full_or_not(const BalanceArgs& a, cudaStream_t st) {
+  return a.experts == LANES * VPT ? F<LANES, VPT, true>::run(a, st) : F<LANES, VPT, false>::run(a, st);
 }
 
-template <int LANES, int VPT>
+template <template <int, int, bool> class F>
+cudaError_t by_width(const BalanceArgs& a, cudaStream_t st) {
+  if (a.experts <= 32) return full_or_not<F, 8, 4>(a, st);
+  if (a.experts <= 64) return full_or_not<F, 8, 8>(a, st);
+  if (a.experts <= 128) return full_or_not<F, 8, 16>(a, st);
+  if (a.experts <= 256) return full_or_not<F, 16, 16>(a, st);
+  if (a.experts <= 384) return full_or_not<F, 32, 12>(a, st);
+  if (a.experts <= 512) return full_or_not<F, 32, 16>(a, st);
+  return F<32, 32, false>::run(a, st);
+}
+
+template <int LANES, int VPT, bool FULL>
 struct Forward {
   static cudaError_t run(const BalanceArgs& a, cudaStream_t st) {
-    k_balance_forward<LANES, VPT><<<a.items, kThreads, 0, st>>>(a);
+    k_balance_forward<LANES, VPT, FULL><<<a.items, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
 };
 
-template <int LANES, int VPT>
+template <int LANES, int VPT, bool FULL>
 struct Backward {
   static cudaError_t run(const BalanceArgs& a, cudaStream_t st) {
     // a group keeps its sequence's load over up to 8 rows, fewer where the
@@ -498,7 +557,7 @@ struct Backward {
     const int steps = a.tokens / (kGroups * 152 * 8);
     b.row_steps = steps < 1 ? 1 : steps > 8 ? 8 : steps;
     const int64_t rows = static_cast<int64_t>(kGroups) * b.row_steps;
-    k_balance_backward<LANES, VPT>
+    k_balance_backward<LANES, VPT, FULL>
         <<<static_cast<unsigned>((a.tokens + rows - 1) / rows), kThreads, 0, st>>>(b);
     return cudaGetLastError();
   }
@@ -662,6 +721,7 @@ muon_status_t muon_balance_backward(const muon_balance_t* b, const float* load,
   a.dlogits = dlogits;
   a.ddt = ddt;
   a.dlogits_stride = dlogits_stride;
+  a.lvec = vectorised(load, MUON_F32, b->experts, b->experts);
   a.dvec = vectorised(dlogits, ddt, dlogits_stride, b->experts);
   a.accumulate = accumulate;
   prof_begin(kKindBalance, st);
