@@ -83,7 +83,7 @@ constexpr uint32_t kCodeBytes = kBK * 128;
 constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four of them used
 constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
 constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
-constexpr int kUnits = 4;                        // units announced ahead
+constexpr int kUnits = 16;                       // units announced at a time, two batches ahead
 constexpr int kStagePitch = 64 + 4;
 constexpr int kStageFloats = 4 * kStagePitch;
 
@@ -117,19 +117,19 @@ struct Cfg {
     uint64_t raw_full[2], raw_empty[2];                   // the same of fp32 tiles
     uint64_t code_full[kSlots], code_empty[kSlots];       // loads landed; read into registers
     uint64_t ready[kSlots];                               // both operands of a block in place
-    uint64_t unit_full[kUnits], unit_empty[kUnits];
+    uint64_t unit_full[2], unit_empty[2];                 // a batch of units announced; taken
     uint64_t tfull[2], tempty[2];                         // accumulator summed; drained
     uint64_t drain;
     uint32_t tmem_slot;
     int abort;
-    alignas(16) int units[8 * kUnits];
+    alignas(16) int units[2 * kUnits][8];
     alignas(16) float stage[kEpiWarps][kStageFloats];     // four rows of 64 columns a warp
   };
   static constexpr size_t kSmem = kDyStages * kStageBytes + kRawStages * kRawBytes +
                                   kSlots * (kSlotBytes + kCodeBytes + kExpBytes) +
                                   sizeof(Shared) + 1024;
 };
-static_assert(Cfg<kTma>::kThreads <= 1024 && Cfg<kTma32>::kThreads <= 1024, "");
+static_assert(Cfg<kTma>::kThreads == 896 && Cfg<kTma32>::kThreads == 896, "see the register split");
 static_assert(Cfg<kTma>::kSmem <= 232448 && Cfg<kTma32>::kSmem <= 232448, "");
 
 constexpr uint32_t kTmemCols = 512;              // two accumulators of 256 columns
@@ -265,98 +265,174 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 bytes of G: whole sectors in one access where rows start on 32-byte
-// boundaries, else in two.
-__device__ __forceinline__ void load32(const void* p, bool whole, uint4& x, uint4& y) {
-  if (whole) {
-    ld_global_v8(p, x, y);
-  } else {
-    x = static_cast<const uint4*>(p)[0];
-    y = static_cast<const uint4*>(p)[1];
-  }
-}
-
-__device__ __forceinline__ void store32(void* p, bool whole, const uint4& x, const uint4& y) {
-  if (whole) {
-    st_global_v8(p, x, y);
-  } else {
-    static_cast<uint4*>(p)[0] = x;
-    static_cast<uint4*>(p)[1] = y;
-  }
-}
-
-// 8 rows x 64 columns of G from a warp: lane l has 16 consecutive columns, 16 (l
-// % 4) on, of row l / 4.  align: what divides the rows' addresses.
-__device__ __forceinline__ void store_8x64(const Matrices& a, char* g, int align, int o, int i,
-                                           int lane, float (&v)[16], float* stage) {
-  if (i >= a.cols || o >= a.rows) return;   // the whole warp
-  if (align >= 16 && i + 64 <= a.cols) {
-    const bool whole = align >= 32;
-    if (o + (lane >> 2) >= a.rows) return;
-    const int64_t at = static_cast<int64_t>(o + (lane >> 2)) * a.stride + i + 16 * (lane & 3);
-    if (a.dtype == MUON_F32) {
-      float* p = reinterpret_cast<float*>(g) + at;
+// 16 rows x 64 columns of an accumulator as fp32 bits (two accumulators' sum
+// with three planes): registers 4b + 2h + k of lane l are row l / 4 + 8h,
+// position 8b + 2 (l % 4) + k.
+template <int PLANES>
+__device__ __forceinline__ void load_piece(uint32_t at, uint32_t (&raw)[32]) {
+  tmem_ld_16x256b_x8(at, raw);
+  tmem_ld_wait(raw);
+  if constexpr (PLANES > 1) {
 #pragma unroll
-      for (int k = 0; k < 16; k += 8) {
-        if (a.accumulate) {
-          uint4 x, y;
-          load32(p + k, whole, x, y);
-          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    for (int b = 0; b < 32; b += 16) {
+      uint32_t rest[16];
+      tmem_ld_16x256b_x4(at + 256u + 2 * b, rest);
+      tmem_ld_wait();
+      tmem_ld_tie(rest);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[k + j] += __uint_as_float(w[j]);
-        }
-        store32(p + k, whole,
-                make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]),
-                                __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3])),
-                     make_uint4(__float_as_uint(v[k + 4]), __float_as_uint(v[k + 5]),
-                                __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7])));
-      }
-    } else {
-      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g) + at;
-      if (a.accumulate) {
-        uint4 x, y;
-        load32(p, whole, x, y);
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[2 * j] += __uint_as_float(w[j] << 16);
-          v[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-      }
-      store32(p, whole,
-              make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
-                              pack2(v[6], v[7])),
-                   make_uint4(pack2(v[8], v[9]), pack2(v[10], v[11]), pack2(v[12], v[13]),
-                              pack2(v[14], v[15])));
+      for (int k = 0; k < 16; ++k)
+        raw[b + k] = __float_as_uint(__uint_as_float(raw[b + k]) + __uint_as_float(rest[k]));
     }
-    return;
   }
-  // The last columns of a matrix, or rows off 16-byte boundaries: through
-  // shared memory, so that the warp writes consecutive columns of one row.
+}
+
+// Register of column c (0..15) of row l / 4 + 8h (see the order of the operand's columns).
+__host__ __device__ constexpr int reg_of(int h, int c) {
+  return 4 * (2 * (c >> 2) + (c & 1)) + 2 * h + ((c >> 1) & 1);
+}
+
+// 32 rows x 128 columns of G that lie inside the matrix, rows on 32-byte
+// boundaries.  p: this lane's 16 columns of row l / 4.
+template <int PLANES, bool F32, bool ADD>
+__device__ __forceinline__ void drain_whole(uint32_t src, char* p, int64_t row_bytes) {
 #pragma unroll 1
-  for (int part = 0; part < 8; part += 4) {
-    if ((lane >> 4) * 4 == part) {
-      float4* p = reinterpret_cast<float4*>(stage + (lane >> 2 & 3) * kStagePitch + 16 * (lane & 3));
+  for (int dr = 0; dr < 32; dr += 16) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    }
-    __syncwarp();
+    for (int dc = 0; dc < 128; dc += 64) {
+      uint32_t raw[32];
+      load_piece<PLANES>(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int row = o + part + (k >> 1), col = i + (k & 1) * 32 + lane;
-      const float x = stage[(k >> 1) * kStagePitch + (k & 1) * 32 + lane];
-      if (row < a.rows && col < a.cols) {
-        const int64_t at = static_cast<int64_t>(row) * a.stride + col;
-        if (a.dtype == MUON_F32) {
-          float* p = reinterpret_cast<float*>(g) + at;
-          *p = a.accumulate ? *p + x : x;
+      for (int h = 0; h < 2; ++h) {
+        char* at = p + h * 8 * row_bytes + dc * (F32 ? 4 : 2);
+        if constexpr (F32) {
+#pragma unroll
+          for (int c = 0; c < 16; c += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = raw[reg_of(h, c + k)];
+            if constexpr (ADD) {
+              uint4 x, y;
+              ld_global_v8(at + 4 * c, x, y);
+              const uint32_t old[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(old[k]));
+            }
+            st_global_v8(at + 4 * c, make_uint4(w[0], w[1], w[2], w[3]),
+                         make_uint4(w[4], w[5], w[6], w[7]));
+          }
         } else {
-          __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g) + at;
-          *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + x : x);
+          uint32_t w[8];
+          uint32_t old[8];
+          if constexpr (ADD) {
+            uint4 x, y;
+            ld_global_v8(at, x, y);
+            old[0] = x.x; old[1] = x.y; old[2] = x.z; old[3] = x.w;
+            old[4] = y.x; old[5] = y.y; old[6] = y.z; old[7] = y.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float lo = __uint_as_float(raw[reg_of(h, 2 * k)]);
+            float hi = __uint_as_float(raw[reg_of(h, 2 * k + 1)]);
+            if constexpr (ADD) {
+              lo += __uint_as_float(old[k] << 16);
+              hi += __uint_as_float(old[k] & 0xFFFF0000u);
+            }
+            w[k] = pack2(lo, hi);
+          }
+          st_global_v8(at, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
         }
       }
     }
-    __syncwarp();
+    p += 16 * row_bytes;
+  }
+}
+
+// The same for any tile: 32 rows from o, 128 columns from i, of which some may
+// lie outside the matrix.  Rows on 16-byte boundaries are written 16 bytes at a
+// time; others, and a matrix's last columns, through shared memory, so that
+// the warp writes consecutive columns of one row.  empty: all zeros.
+template <int PLANES>
+__device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g, int o, int i,
+                                       bool empty, float* stage) {
+  const int lane = threadIdx.x & 31;
+  const int esz = a.dtype == MUON_F32 ? 4 : 2;
+  const bool wide = ((reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(a.stride * esz)) & 15u) == 0;
+#pragma unroll 1
+  for (int piece = 0; piece < 4; ++piece) {
+    const int dr = (piece & 1) * 16, dc = (piece >> 1) * 64;
+    const int row0 = o + dr, col0 = i + dc;
+    if (row0 >= a.rows || col0 >= a.cols) continue;   // the whole warp
+    uint32_t raw[32];
+    __syncwarp();   // tcgen05.ld takes the warp together
+    if (empty) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) raw[k] = 0u;
+    } else {
+      load_piece<PLANES>(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (wide && col0 + 64 <= a.cols) {
+        const int row = row0 + 8 * h + (lane >> 2);
+        if (row < a.rows) {
+          char* at = g + (static_cast<int64_t>(row) * a.stride + col0 + 16 * (lane & 3)) * esz;
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(raw[reg_of(h, c + k)]);
+            if (a.dtype == MUON_F32) {
+              float4* q = reinterpret_cast<float4*>(at + 4 * c);
+              if (a.accumulate) {
+                const float4 x = *q;
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+              }
+              *q = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+              uint2* q = reinterpret_cast<uint2*>(at + 2 * c);
+              if (a.accumulate) {
+                const uint2 x = *q;
+                v[0] += __uint_as_float(x.x << 16);
+                v[1] += __uint_as_float(x.x & 0xFFFF0000u);
+                v[2] += __uint_as_float(x.y << 16);
+                v[3] += __uint_as_float(x.y & 0xFFFF0000u);
+              }
+              *q = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+            }
+          }
+        }
+        continue;
+      }
+#pragma unroll 1
+      for (int part = 0; part < 8; part += 4) {
+        if ((lane >> 4) * 4 == part) {
+          float4* q = reinterpret_cast<float4*>(stage + (lane >> 2 & 3) * kStagePitch + 16 * (lane & 3));
+#pragma unroll
+          for (int c = 0; c < 16; c += 4)
+            q[c / 4] = make_float4(__uint_as_float(raw[reg_of(h, c)]), __uint_as_float(raw[reg_of(h, c + 1)]),
+                                   __uint_as_float(raw[reg_of(h, c + 2)]),
+                                   __uint_as_float(raw[reg_of(h, c + 3)]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = row0 + 8 * h + part + (k >> 1), col = col0 + (k & 1) * 32 + lane;
+          const float x = stage[(k >> 1) * kStagePitch + (k & 1) * 32 + lane];
+          if (row < a.rows && col < a.cols) {
+            const int64_t at = static_cast<int64_t>(row) * a.stride + col;
+            if (a.dtype == MUON_F32) {
+              float* q = reinterpret_cast<float*>(g) + at;
+              *q = a.accumulate ? *q + x : x;
+            } else {
+              __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(g) + at;
+              *q = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*q) + x : x);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
   }
 }
 
@@ -439,13 +515,12 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
            *drain = &bars.drain;
   volatile int* abort_flag = &bars.abort;
   uint32_t* tmem_slot = &bars.tmem_slot;
-  int* sm_units = bars.units;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kUnits; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&unit_full[s], 1);
       // TMA threads, converters, loaders, epilogue; the MMA issuer in the even CTA
       mbar_init(&unit_empty[s], (kTmaDy ? 2 : 1) + kSlots * kConvWarps + C::kLoadWarps +
@@ -483,130 +558,142 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // One thread works out the units ahead of the other roles, which take them
-  // from a ring in the same order and number the blocks of 64 tokens c = 0, 1,
-  // ... since the start.
+  // One warp works out the units, a batch at a time, ahead of the other roles,
+  // which take them in the same order and number the blocks of 64 tokens c = 0,
+  // 1, ... since the start.
   uint32_t taken = 0;
   const auto take = [&](Unit& t, bool whole_warp) {
-    const uint32_t k = taken % kUnits;
-    bool ok = mbar_wait_bounded(&unit_full[k], taken / kUnits & 1u, abort_flag, a.status, a.timeout_ns);
-    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
-    const int4 v = *reinterpret_cast<const int4*>(sm_units + 8 * k);
+    const uint32_t at = taken % (2 * kUnits), batch = at / kUnits;
+    if (at % kUnits == 0) {
+      bool ok = mbar_wait_bounded(&unit_full[batch], taken / (2 * kUnits) & 1u, abort_flag, a.status,
+                                  a.timeout_ns);
+      if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return false;
+    }
+    const int4 v = *reinterpret_cast<const int4*>(bars.units[at]);
+    const int2 w = *reinterpret_cast<const int2*>(bars.units[at] + 4);
     t.e = v.x;
     t.o0 = v.y;
     t.i0 = v.z;
     t.begin = v.w;
-    const int2 w = *reinterpret_cast<const int2*>(sm_units + 8 * k + 4);
     t.n = w.x;
     t.m = w.y;
-    if (whole_warp) __syncwarp();
-    if (lane == 0) mbar_arrive(&unit_empty[k]);
+    if (at % kUnits == kUnits - 1) {
+      if (whole_warp) __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[batch]);
+    }
     ++taken;
     return t.e >= 0;
   };
 
-  if ((warp == 0 && kTmaDy) || warp == 2) {
-    if (lane == 0) {
-      // ----------------------------------- TMA: dy (warp 0), codes + exponents
-      const bool is_dy = warp == 0;
-      uint64_t* full = !is_dy ? code_full : MODE == kTma ? dy_full : bars.raw_full;
-      uint64_t* empty = !is_dy ? code_empty : MODE == kTma ? dy_empty : bars.raw_empty;
-      const uint32_t stages = !is_dy ? kSlots : MODE == kTma ? kDyStages : C::kRawStages;
-      uint32_t c = 0, s = 0, phase = 0;
-      bool ok = true;
-      Unit t;
-      while (ok && take(t, false)) {
-        const int o = t.o0 + static_cast<int>(rank) * 128, i = t.i0 + static_cast<int>(rank) * 128;
-        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-          if (!mbar_wait_bounded(&empty[s], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          if (is_dy && MODE == kTma32) {
-            mbar_arrive_expect_tx(&full[s], kRawBytes);
-            tma_load_2d(sm_raw + s * kRawBytes, &tm_dy, &full[s], o, t.begin + k0);
-          } else if (is_dy) {
-            mbar_arrive_expect_tx(&full[s], kDyBytes);
-            uint8_t* d = sm_dy + s * kDyBytes;
-            tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
-            tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
-          } else {
-            mbar_arrive_expect_tx(&full[s], kCodeBytes + kExpBytes);
-            tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
-            tma_load_2d(sm_exps + s * kExpBytes, &tm_exps, &full[s], (i / 32) & ~15, t.begin + k0);
-          }
-          if (++s == stages) {
-            s = 0;
-            phase ^= 1u;
+  // The single-thread roles hand registers to the epilogue: 7 warpgroups of 72
+  // a thread at launch = 40 + 4 x 72 + 2 x 88.
+  if (warp < C::kConv0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if ((warp == 0 && kTmaDy) || warp == 2) {
+      if (lane == 0) {
+        // ----------------------------------- TMA: dy (warp 0), codes + exponents
+        const bool is_dy = warp == 0;
+        uint64_t* full = !is_dy ? code_full : MODE == kTma ? dy_full : bars.raw_full;
+        uint64_t* empty = !is_dy ? code_empty : MODE == kTma ? dy_empty : bars.raw_empty;
+        const uint32_t stages = !is_dy ? kSlots : MODE == kTma ? kDyStages : C::kRawStages;
+        uint32_t c = 0, s = 0, phase = 0;
+        bool ok = true;
+        Unit t;
+        while (ok && take(t, false)) {
+          const int o = t.o0 + static_cast<int>(rank) * 128, i = t.i0 + static_cast<int>(rank) * 128;
+          for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+            if (!mbar_wait_bounded(&empty[s], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
+              ok = false;
+              break;
+            }
+            if (is_dy && MODE == kTma32) {
+              mbar_arrive_expect_tx(&full[s], kRawBytes);
+              tma_load_2d(sm_raw + s * kRawBytes, &tm_dy, &full[s], o, t.begin + k0);
+            } else if (is_dy) {
+              mbar_arrive_expect_tx(&full[s], kDyBytes);
+              uint8_t* d = sm_dy + s * kDyBytes;
+              tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
+              tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
+            } else {
+              mbar_arrive_expect_tx(&full[s], kCodeBytes + kExpBytes);
+              tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
+              tma_load_2d(sm_exps + s * kExpBytes, &tm_exps, &full[s], (i / 32) & ~15, t.begin + k0);
+            }
+            if (++s == stages) {
+              s = 0;
+              phase ^= 1u;
+            }
           }
         }
+        // every load has landed before the CTA exits
+        for (uint32_t k = c > stages ? c - stages : 0; k < c; ++k)
+          wait_drain(&full[k % stages], k / stages & 1u, a.status, a.timeout_ns);
       }
-      // every load has landed before the CTA exits
-      for (uint32_t k = c > stages ? c - stages : 0; k < c; ++k)
-        wait_drain(&full[k % stages], k / stages & 1u, a.status, a.timeout_ns);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // -------------------------------------------------------- MMA issuer
-      uint32_t c = 0, s = 0, tile = 0;
-      bool ok = true;
-      Unit t;
-      while (ok && take(t, false)) {
-        if (t.n == 0) continue;
-        const uint32_t acc = tile % kAccs;
-        if (!mbar_wait_bounded(&tempty[acc], (tile / kAccs & 1u) ^ 1u, abort_flag, a.status,
-                               a.timeout_ns))
-          break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + acc * 256u;
-        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-          const uint32_t b = c % kSlots;
-          if (!wait_cluster(&ready[b], c / kSlots & 1u, abort_flag, a.status, a.timeout_ns)) {
-            ok = false;
+    } else if (warp == 1) {
+      if (lane == 0 && rank == 0) {
+        // -------------------------------------------------------- MMA issuer
+        uint32_t c = 0, s = 0, tile = 0;
+        bool ok = true;
+        Unit t;
+        while (ok && take(t, false)) {
+          if (t.n == 0) continue;
+          const uint32_t acc = tile % kAccs;
+          if (!mbar_wait_bounded(&tempty[acc], (tile / kAccs & 1u) ^ 1u, abort_flag, a.status,
+                                 a.timeout_ns))
             break;
-          }
           tc_fence_after();
-          const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
+          const uint32_t d = tmem_base + acc * 256u;
+          for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
+            const uint32_t b = c % kSlots;
+            if (!wait_cluster(&ready[b], c / kSlots & 1u, abort_flag, a.status, a.timeout_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
 #pragma unroll
-          for (int p = C::kPlanes - 1; p >= 0; --p) {
-            const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kDyBytes);
+            for (int p = C::kPlanes - 1; p >= 0; --p) {
+              const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kDyBytes);
 #pragma unroll
-            for (int ks = 0; ks < kBK / 16; ++ks)
-              tc_mma_bf16_pair(d + (p > 0 ? 256u : 0u),
-                               smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
-                               smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
-                               k0 == 0 && (p == 0 || p == C::kPlanes - 1) && ks == 0 ? 0u : 1u);
+              for (int ks = 0; ks < kBK / 16; ++ks)
+                tc_mma_bf16_pair(d + (p > 0 ? 256u : 0u),
+                                 smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
+                                 smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
+                                 k0 == 0 && (p == 0 || p == C::kPlanes - 1) && ks == 0 ? 0u : 1u);
+            }
+            tc_commit_pair_multicast(&dy_empty[s], 0x3);
+            if (++s == kDyStages) s = 0;
           }
-          tc_commit_pair_multicast(&dy_empty[s], 0x3);
-          if (++s == kDyStages) s = 0;
+          if (!ok) break;
+          tc_commit_pair_multicast(&tfull[acc], 0x3);
+          ++tile;
         }
-        if (!ok) break;
-        tc_commit_pair_multicast(&tfull[acc], 0x3);
-        ++tile;
+        tc_commit_pair_multicast(drain, 0x1);
+        wait_drain(drain, 0, a.status, a.timeout_ns);
       }
-      tc_commit_pair_multicast(drain, 0x1);
-      wait_drain(drain, 0, a.status, a.timeout_ns);
-    }
-  } else if (warp == 3) {
-    if (lane == 0) {
-      // ----------------------------------------------------------- walker
+    } else if (warp == 3) {
+      // ------------------------------------------------------------- walker
       const int step = static_cast<int>(gridDim.x >> 1);
-      uint32_t k = 0;
-      for (int u = static_cast<int>(blockIdx.x >> 1);; u += step, ++k) {
+      int u = static_cast<int>(blockIdx.x >> 1) + lane * step;   // of this lane
+      for (uint32_t k = 0;; ++k, u += kUnits * step) {
         Unit t{-1, 0, 0, 0, 0, 0};
-        if (u < a.units) t = unit_of(a, u);
-        int* p = sm_units + 8 * (k % kUnits);
-        if (!mbar_wait_bounded(&unit_empty[k % kUnits], (k / kUnits & 1u) ^ 1u, abort_flag, a.status,
-                               a.timeout_ns))
+        if (lane < kUnits && u < a.units) t = unit_of(a, u);
+        const bool end = __any_sync(0xffffffffu, lane < kUnits && t.e < 0);
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&unit_empty[k % 2], (k / 2 & 1u) ^ 1u, abort_flag,
+                                                       a.status, a.timeout_ns)))
           break;
-        *reinterpret_cast<int4*>(p) = make_int4(t.e, t.o0, t.i0, t.begin);
-        *reinterpret_cast<int2*>(p + 4) = make_int2(t.n, t.m);
-        mbar_arrive(&unit_full[k % kUnits]);
-        if (t.e < 0) break;
+        if (lane < kUnits) {
+          int* p = bars.units[k % 2 * kUnits + lane];
+          *reinterpret_cast<int4*>(p) = make_int4(t.e, t.o0, t.i0, t.begin);
+          *reinterpret_cast<int2*>(p + 4) = make_int2(t.n, t.m);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&unit_full[k % 2]);
+        if (end) break;
       }
     }
-  } else if (warp >= C::kConv0 && warp < C::kLoad0) {
+  } else if (warp < C::kLoad0) {
     // ---------------------------------------------------------- converters
     // Group g decodes the blocks c = g, g + kSlots, ... into slot g, so that the
     // latencies of one block's chain (wait, read, decode, write, fence, arrive)
@@ -698,7 +785,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       }
       c0 += blocks;
     }
-  } else if (warp >= C::kLoad0 && warp < C::kEpi0) {
+  } else if (warp < C::kEpi0) {
     // ------------------------------------------------------------- loaders
     // dy through registers: a warp takes a row of 128 columns, four a thread,
     // from memory (a block ahead) or from TMA's fp32 tile, and writes them (as
@@ -771,8 +858,9 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
         }
       }
     }
-  } else if (warp >= C::kEpi0) {
+  } else {
     // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // A warp drains 32 rows x 128 columns in four pieces of 16 x 64: a thread
     // gets 16 consecutive columns of two rows, four threads 64 columns, so that
     // a store of the warp fills eight whole 128-byte lines.
@@ -793,46 +881,35 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       }
       char* g = matrix_of(a.g, t.m);
       const int esz = a.g.dtype == MUON_F32 ? 4 : 2;
-      const uint64_t bits = reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(a.g.stride * esz);
-      const int align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+      const int64_t row_bytes = a.g.stride * esz;
       const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32;
       const int i = t.i0 + half * 128;
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
-#pragma unroll 1
-      for (int piece = 0; piece < 4; ++piece) {
-        const int dr = (piece & 1) * 16, dc = (piece >> 1) * 64;
-        uint32_t raw[32];
-        __syncwarp();   // tcgen05.ld takes the warp together
-        if (t.n > 0) {
-          const uint32_t at = src + (static_cast<uint32_t>(dr) << 16) + dc;
-          tmem_ld_16x256b_x8(at, raw);
-          tmem_ld_wait(raw);
-          if constexpr (C::kPlanes > 1) {
-#pragma unroll
-            for (int b = 0; b < 32; b += 16) {
-              uint32_t rest[16];
-              tmem_ld_16x256b_x4(at + 256u + 2 * b, rest);
-              tmem_ld_wait();
-              tmem_ld_tie(rest);
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                raw[b + k] = __float_as_uint(__uint_as_float(raw[b + k]) + __uint_as_float(rest[k]));
+      const bool whole = o + 32 <= a.g.rows && i + 128 <= a.g.cols &&
+                         ((reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes)) & 31u) == 0;
+      __syncwarp();   // tcgen05.ld takes the warp together
+      if (whole) {
+        char* p = g + (o + (lane >> 2)) * row_bytes + (i + 16 * (lane & 3)) * esz;
+        if (t.n == 0) {   // an expert without tokens
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int r = 0; r < 32; r += 8, p += 8 * row_bytes)
+            for (int c = 0; c < 128 * esz; c += 64 * esz) {
+              st_global_v8(p + c, zero, zero);
+              if (esz == 4) st_global_v8(p + c + 32, zero, zero);
             }
-          }
-        } else {   // an expert without tokens
-#pragma unroll
-          for (int k = 0; k < 32; ++k) raw[k] = 0u;
+        } else if (a.g.dtype == MUON_F32) {
+          if (a.g.accumulate)
+            drain_whole<C::kPlanes, true, true>(src, p, row_bytes);
+          else
+            drain_whole<C::kPlanes, true, false>(src, p, row_bytes);
+        } else {
+          if (a.g.accumulate)
+            drain_whole<C::kPlanes, false, true>(src, p, row_bytes);
+          else
+            drain_whole<C::kPlanes, false, false>(src, p, row_bytes);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[16];
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              v[4 * (b >> 1) + (b & 1) + 2 * k] = __uint_as_float(raw[4 * b + 2 * h + k]);
-          store_8x64(a.g, g, align, o + dr + 8 * h, i + dc, lane, v, stage);
-        }
+      } else {
+        drain_any<C::kPlanes>(src, a.g, g, o, i, t.n == 0, stage);
       }
       if (t.n == 0) continue;
       tc_fence_before();

@@ -280,12 +280,13 @@ __global__ void __launch_bounds__(kThreads, VPT <= 16 ? 4 : 2)
     for (int j = 0; j < VPT; ++j) acc[j] = fmaf(x[j], inv, acc[j]);
     if (on) {
       valid += sub == 0;
-      for (int k = sub; k < a.topk; k += LANES) {
-        if (k != sub) id = choice(t, k);
+      for (int k = sub; k < a.topk;) {
         if (id >= 0 && id < a.experts)
           atomicAdd(&s_cnt[id], 1);
         else if (id != -1)
           bad = 1;
+        k += LANES;
+        if (k < a.topk) id = choice(t, k);
       }
     }
   }
