@@ -465,7 +465,8 @@ muon_status_t muon_act8_swiglu_backward(const void* dh, int64_t dh_stride, muon_
  * or out of order are cut and set MUON_FLAG_INDEX); NULL = all rows (experts
  * must be 1).  An expert without tokens gets 0.
  * g_ptrs: DEVICE array of `experts` DEVICE pointers (a muon_group_t's g_ptrs),
- * or NULL: matrix e at g_base + e * g_batch_stride.  G: out x in of g_dtype,
+ * each 16-byte aligned (else MUON_FLAG_MISALIGNED, and that matrix is left
+ * untouched), or NULL: matrix e at g_base + e * g_batch_stride.  G: out x in of g_dtype,
  * row stride g_stride.  accumulate: 1 = add to what G holds (in fp32, rounded
  * once).  Results depend on the sizes and the inputs alone. */
 typedef struct {

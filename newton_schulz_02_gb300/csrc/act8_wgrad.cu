@@ -291,19 +291,43 @@ __host__ __device__ constexpr int reg_of(int h, int c) {
   return 4 * (2 * (c >> 2) + (c & 1)) + 2 * h + ((c >> 1) & 1);
 }
 
-// 32 rows x 128 columns of G that lie inside the matrix, rows on 32-byte
-// boundaries.  p: this lane's 16 columns of row l / 4.
-template <int PLANES, bool F32, bool ADD>
+// 32 bytes of G: a whole sector in one access (rows on 32-byte boundaries), or
+// two of 16.
+template <bool SECTOR>
+__device__ __forceinline__ void load32(const char* p, uint4& x, uint4& y) {
+  if constexpr (SECTOR) {
+    ld_global_v8(p, x, y);
+  } else {
+    x = reinterpret_cast<const uint4*>(p)[0];
+    y = reinterpret_cast<const uint4*>(p)[1];
+  }
+}
+
+template <bool SECTOR>
+__device__ __forceinline__ void store32(char* p, const uint4& x, const uint4& y) {
+  if constexpr (SECTOR) {
+    st_global_v8(p, x, y);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = x;
+    reinterpret_cast<uint4*>(p)[1] = y;
+  }
+}
+
+// 32 rows x 128 columns of G that lie inside the matrix, rows on 16-byte
+// boundaries.  p: this lane's 16 columns of row l / 4.  Not unrolled: the roles
+// share the instruction caches, and 1510 against 1310 us is what the unrolled
+// form costs 256 experts of 16 tokens.
+template <int PLANES, bool F32, bool ADD, bool SECTOR>
 __device__ __forceinline__ void drain_whole(uint32_t src, char* p, int64_t row_bytes) {
 #pragma unroll 1
-  for (int dr = 0; dr < 32; dr += 16) {
-#pragma unroll
-    for (int dc = 0; dc < 128; dc += 64) {
+  for (int dc = 0; dc < 128; dc += 64) {
+#pragma unroll 1
+    for (int dr = 0; dr < 32; dr += 16) {
       uint32_t raw[32];
       load_piece<PLANES>(src + (static_cast<uint32_t>(dr) << 16) + dc, raw);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        char* at = p + h * 8 * row_bytes + dc * (F32 ? 4 : 2);
+        char* at = p + (h * 8 + dr) * row_bytes + dc * (F32 ? 4 : 2);
         if constexpr (F32) {
 #pragma unroll
           for (int c = 0; c < 16; c += 8) {
@@ -312,21 +336,21 @@ __device__ __forceinline__ void drain_whole(uint32_t src, char* p, int64_t row_b
             for (int k = 0; k < 8; ++k) w[k] = raw[reg_of(h, c + k)];
             if constexpr (ADD) {
               uint4 x, y;
-              ld_global_v8(at + 4 * c, x, y);
+              load32<SECTOR>(at + 4 * c, x, y);
               const uint32_t old[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(old[k]));
             }
-            st_global_v8(at + 4 * c, make_uint4(w[0], w[1], w[2], w[3]),
-                         make_uint4(w[4], w[5], w[6], w[7]));
+            store32<SECTOR>(at + 4 * c, make_uint4(w[0], w[1], w[2], w[3]),
+                            make_uint4(w[4], w[5], w[6], w[7]));
           }
         } else {
           uint32_t w[8];
           uint32_t old[8];
           if constexpr (ADD) {
             uint4 x, y;
-            ld_global_v8(at, x, y);
+            load32<SECTOR>(at, x, y);
             old[0] = x.x; old[1] = x.y; old[2] = x.z; old[3] = x.w;
             old[4] = y.x; old[5] = y.y; old[6] = y.z; old[7] = y.w;
           }
@@ -340,18 +364,44 @@ __device__ __forceinline__ void drain_whole(uint32_t src, char* p, int64_t row_b
             }
             w[k] = pack2(lo, hi);
           }
-          st_global_v8(at, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+          store32<SECTOR>(at, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
         }
       }
     }
-    p += 16 * row_bytes;
+  }
+}
+
+// The same of an expert without tokens, and the choice among the forms.
+template <int PLANES, bool SECTOR>
+__device__ __forceinline__ void drain_inside(uint32_t src, const Matrices& g, char* p, int64_t row_bytes,
+                                             bool empty) {
+  const bool f32 = g.dtype == MUON_F32;
+  if (empty) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int r = 0; r < 32; r += 8, p += 8 * row_bytes)
+#pragma unroll 1
+      for (int c = 0; c < (f32 ? 512 : 256); c += f32 ? 256 : 128) {
+        store32<SECTOR>(p + c, zero, zero);
+        if (f32) store32<SECTOR>(p + c + 32, zero, zero);
+      }
+  } else if (f32) {
+    if (g.accumulate)
+      drain_whole<PLANES, true, true, SECTOR>(src, p, row_bytes);
+    else
+      drain_whole<PLANES, true, false, SECTOR>(src, p, row_bytes);
+  } else {
+    if (g.accumulate)
+      drain_whole<PLANES, false, true, SECTOR>(src, p, row_bytes);
+    else
+      drain_whole<PLANES, false, false, SECTOR>(src, p, row_bytes);
   }
 }
 
 // The same for any tile: 32 rows from o, 128 columns from i, of which some may
-// lie outside the matrix.  Rows on 16-byte boundaries are written 16 bytes at a
-// time; others, and a matrix's last columns, through shared memory, so that
-// the warp writes consecutive columns of one row.  empty: all zeros.
+// lie outside the matrix.  Where rows are off 16-byte boundaries, and at a
+// matrix's last columns, values go through shared memory, so that the warp
+// writes consecutive columns of one row.  empty: all zeros.
 template <int PLANES>
 __device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g, int o, int i,
                                        bool empty, float* stage) {
@@ -488,7 +538,10 @@ __device__ __forceinline__ uint32_t take_upper(float& v) {
   return u & 0xFFFF0000u;
 }
 
-template <DyMode MODE>
+// EDGE: some 32 x 128 piece of G may lie partly outside it, or off 16-byte
+// boundaries.  (A kernel of its own, as the call that drains such a piece costs
+// the other one registers: 469 against 438 us for 64 experts of 256 tokens.)
+template <DyMode MODE, bool EDGE>
 __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_codes,
                  const __grid_constant__ CUtensorMap tm_exps, const __grid_constant__ WgradArgs a) {
@@ -885,30 +938,17 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32;
       const int i = t.i0 + half * 128;
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
-      const bool whole = o + 32 <= a.g.rows && i + 128 <= a.g.cols &&
-                         ((reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes)) & 31u) == 0;
+      const uint64_t bits = reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes);
+      const bool inside = o + 32 <= a.g.rows && i + 128 <= a.g.cols;
+      char* p = g + (o + (lane >> 2)) * row_bytes + (i + 16 * (lane & 3)) * esz;
       __syncwarp();   // tcgen05.ld takes the warp together
-      if (whole) {
-        char* p = g + (o + (lane >> 2)) * row_bytes + (i + 16 * (lane & 3)) * esz;
-        if (t.n == 0) {   // an expert without tokens
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          for (int r = 0; r < 32; r += 8, p += 8 * row_bytes)
-            for (int c = 0; c < 128 * esz; c += 64 * esz) {
-              st_global_v8(p + c, zero, zero);
-              if (esz == 4) st_global_v8(p + c + 32, zero, zero);
-            }
-        } else if (a.g.dtype == MUON_F32) {
-          if (a.g.accumulate)
-            drain_whole<C::kPlanes, true, true>(src, p, row_bytes);
-          else
-            drain_whole<C::kPlanes, true, false>(src, p, row_bytes);
-        } else {
-          if (a.g.accumulate)
-            drain_whole<C::kPlanes, false, true>(src, p, row_bytes);
-          else
-            drain_whole<C::kPlanes, false, false>(src, p, row_bytes);
-        }
-      } else {
+      if (a.g.ptrs != nullptr && reinterpret_cast<uintptr_t>(g) % 16 != 0) {
+        if (lane == 0) atomicOr(a.status, kFlagMisaligned);   // left untouched
+      } else if (inside && bits % 32 == 0) {
+        drain_inside<C::kPlanes, true>(src, a.g, p, row_bytes, t.n == 0);
+      } else if (inside && (!EDGE || bits % 16 == 0)) {
+        drain_inside<C::kPlanes, false>(src, a.g, p, row_bytes, t.n == 0);
+      } else if constexpr (EDGE) {
         drain_any<C::kPlanes>(src, a.g, g, o, i, t.n == 0, stage);
       }
       if (t.n == 0) continue;
@@ -995,7 +1035,7 @@ bool map_rows(CUtensorMap* m, CUtensorMapDataType type, int esz, const void* bas
 }
 
 // CTA pairs that fit the current device at once (asked once per device).
-template <DyMode MODE>
+template <DyMode MODE, bool EDGE>
 cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
@@ -1005,7 +1045,7 @@ cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   if (dev < kDevices && (*out = known[dev].load()) > 0) return cudaSuccess;
   cfg.gridDim = dim3(2);
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad<MODE>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad<MODE, EDGE>, &cfg);
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
   if (dev < kDevices) known[dev].store(n);
@@ -1013,10 +1053,10 @@ cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   return cudaSuccess;
 }
 
-template <DyMode MODE>
-cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
+template <DyMode MODE, bool EDGE>
+cudaError_t launch_mode(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
   using C = Cfg<MODE>;
-  cudaError_t e = cudaFuncSetAttribute(k_wgrad<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_wgrad<MODE, EDGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1030,7 +1070,7 @@ cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   int pairs = 0;
-  e = resident_pairs<MODE>(cfg, &pairs);
+  e = resident_pairs<MODE, EDGE>(cfg, &pairs);
   if (e != cudaSuccess) return e;
   CUtensorMap dy{}, codes{}, exps{};
   if (a.rows > 0) {
@@ -1047,7 +1087,18 @@ cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min(a.units, pairs)));
-  return cudaLaunchKernelEx(&cfg, k_wgrad<MODE>, dy, codes, exps, a);
+  return cudaLaunchKernelEx(&cfg, k_wgrad<MODE, EDGE>, dy, codes, exps, a);
+}
+
+template <DyMode MODE>
+cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
+  // pointers in a device array are on 16-byte boundaries, or their matrix is left alone
+  const int esz = a.g.dtype == MUON_F32 ? 4 : 2;
+  const uint64_t bits = reinterpret_cast<uintptr_t>(a.g.base) |
+                        static_cast<uint64_t>((a.g.ptrs != nullptr ? 0 : a.g.batch_stride) * esz) |
+                        static_cast<uint64_t>(a.g.stride * esz);
+  const bool edge = a.g.rows % 32 != 0 || a.g.cols % 128 != 0 || bits % 16 != 0;
+  return edge ? launch_mode<MODE, true>(a, x, st) : launch_mode<MODE, false>(a, x, st);
 }
 
 muon_status_t check_sizes(const muon_weight_grad_t* d) {
