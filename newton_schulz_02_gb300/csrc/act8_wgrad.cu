@@ -526,16 +526,29 @@ __device__ __forceinline__ void load_dy4(const T* row, int col, int cols, bool v
   }
 }
 
-// The upper 8 significant bits of v as bf16 in the upper half of a word; v
-// becomes the rest, exactly.  An infinity or a NaN leaves 0.
-__device__ __forceinline__ uint32_t take_upper(float& v) {
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7F800000u) == 0x7F800000u) {
-    v = 0.f;
-    return (u & 0x007FFFFFu) != 0 ? 0x7FC00000u : u;
+// Four values as PLANES planes of bf16: with three, the upper 8 significant
+// bits, the next 8 and the last 8, whose sum is the value.  An infinity or a
+// NaN is the first plane alone.
+template <int PLANES>
+__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&out)[PLANES]) {
+  uint32_t u[PLANES][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t b = __float_as_uint(v[k]);
+    u[0][k] = b;
+    if constexpr (PLANES == 3) {
+      const float r = v[k] - __uint_as_float(b & 0xFFFF0000u);
+      u[1][k] = __float_as_uint(r);
+      u[2][k] = __float_as_uint(r - __uint_as_float(u[1][k] & 0xFFFF0000u));
+      if ((b & 0x7F800000u) == 0x7F800000u) {
+        if ((b & 0x007FFFFFu) != 0) u[0][k] = 0x7FC00000u;
+        u[1][k] = u[2][k] = 0u;
+      }
+    }
   }
-  v -= __uint_as_float(u & 0xFFFF0000u);
-  return u & 0xFFFF0000u;
+#pragma unroll
+  for (int p = 0; p < PLANES; ++p)
+    out[p] = make_uint2(__byte_perm(u[p][0], u[p][1], 0x7632), __byte_perm(u[p][2], u[p][3], 0x7632));
 }
 
 // EDGE: some 32 x 128 piece of G may lie partly outside it, or off 16-byte
@@ -855,33 +868,39 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       while (ok && take(t, true)) {
         const int o = t.o0 + static_cast<int>(rank) * 128 + col4;
         float v[8][4];
-        const auto fetch = [&](int k0) {
+        const auto fetch = [&](int k0) {   // from memory
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const int r = q * C::kLoadWarps + lw;
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[q][k] = 0.f;
-            if (k0 + r >= t.n) continue;
-            if constexpr (MODE == kTma32) {
-              const float4 w = *reinterpret_cast<const float4*>(sm_raw + c % 2 * kRawBytes + r * 512 +
-                                                                lane * 16);
-              v[q][0] = w.x; v[q][1] = w.y; v[q][2] = w.z; v[q][3] = w.w;
-            } else {
+            if (k0 + r < t.n)
               load_dy4(static_cast<const T*>(a.dy) + static_cast<int64_t>(t.begin + k0 + r) * a.dy_stride,
                        o, a.out, a.dy_vec != 0, v[q]);
-            }
           }
         };
         if (MODE != kTma32 && t.n > 0) fetch(0);
         for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
           const uint32_t s = c % kDyStages;
+          uint2 w[8][C::kPlanes];   // split before the stage is free
           if constexpr (MODE == kTma32) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars.raw_full[c % 2], c / 2 & 1u, abort_flag,
                                                            a.status, a.timeout_ns));
             if (!ok) break;
-            fetch(k0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int r = q * C::kLoadWarps + lw;
+              const float4 x = *reinterpret_cast<const float4*>(sm_raw + c % 2 * kRawBytes + r * 512 +
+                                                                lane * 16);
+              const bool in = k0 + r < t.n;
+              const float y[4] = {in ? x.x : 0.f, in ? x.y : 0.f, in ? x.z : 0.f, in ? x.w : 0.f};
+              split4<C::kPlanes>(y, w[q]);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.raw_empty[c % 2]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) split4<C::kPlanes>(v[q], w[q]);
           }
           if (c >= kDyStages) {
             ok = __all_sync(0xffffffffu,
@@ -895,14 +914,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
             uint8_t* at = sm_dy + s * C::kStageBytes + (lane >> 4) * kAtomBytes + r * 128 +
                           ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
 #pragma unroll
-            for (int p = 0; p < C::kPlanes; ++p) {
-              uint32_t u[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                u[k] = C::kPlanes == 1 ? __float_as_uint(v[q][k]) : take_upper(v[q][k]);
-              *reinterpret_cast<uint2*>(at + p * kDyBytes) =
-                  make_uint2(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
-            }
+            for (int p = 0; p < C::kPlanes; ++p) *reinterpret_cast<uint2*>(at + p * kDyBytes) = w[q][p];
           }
           fence_proxy_async_smem();
           __syncwarp();
