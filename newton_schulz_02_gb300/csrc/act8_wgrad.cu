@@ -408,16 +408,16 @@ __device__ __forceinline__ void drain_inside(uint32_t src, const Matrices& g, ch
 // matrix's last columns, values go through shared memory, so that the warp
 // writes consecutive columns of one row.  empty: all zeros.
 template <int PLANES>
-__device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g, int o, int i,
-                                       bool empty, bool add, float* stage) {
+__device__ __noinline__ void drain_any(uint32_t src, char* g, int64_t row_bytes, int rows, int cols,
+                                       bool f32, bool empty, bool add, float* stage) {
+  // g: the piece's first element; rows, cols: of the matrix from there on
   const int lane = threadIdx.x & 31;
-  const int esz = a.dtype == MUON_F32 ? 4 : 2;
-  const bool wide = ((reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(a.stride * esz)) & 15u) == 0;
+  const int shift = f32 ? 2 : 1;
+  const bool wide = ((reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes)) & 15u) == 0;
 #pragma unroll 1
   for (int piece = 0; piece < 4; ++piece) {
     const int dr = (piece & 1) * 16, dc = (piece >> 1) * 64;
-    const int row0 = o + dr, col0 = i + dc;
-    if (row0 >= a.rows || col0 >= a.cols) continue;   // the whole warp
+    if (dr >= rows || dc >= cols) continue;   // the whole warp
     uint32_t raw[32];
     __syncwarp();   // tcgen05.ld takes the warp together
     if (empty) {
@@ -428,16 +428,16 @@ __device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g,
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (wide && col0 + 64 <= a.cols) {
-        const int row = row0 + 8 * h + (lane >> 2);
-        if (row < a.rows) {
-          char* at = g + (static_cast<int64_t>(row) * a.stride + col0 + 16 * (lane & 3)) * esz;
+      if (wide && dc + 64 <= cols) {
+        const int row = dr + 8 * h + (lane >> 2);
+        if (row < rows) {
+          char* at = g + row * row_bytes + (static_cast<int64_t>(dc + 16 * (lane & 3)) << shift);
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(raw[reg_of(h, c + k)]);
-            if (a.dtype == MUON_F32) {
+            if (f32) {
               float4* q = reinterpret_cast<float4*>(at + 4 * c);
               if (add) {
                 const float4 x = *q;
@@ -459,9 +459,9 @@ __device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g,
         }
         continue;
       }
-#pragma unroll 1
-      for (int part = 0; part < 8; part += 4) {
-        if ((lane >> 4) * 4 == part) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {   // four rows
+        if (lane >> 4 == part) {
           float4* q = reinterpret_cast<float4*>(stage + (lane >> 2 & 3) * kStagePitch + 16 * (lane & 3));
 #pragma unroll
           for (int c = 0; c < 16; c += 4)
@@ -470,22 +470,26 @@ __device__ __noinline__ void drain_any(uint32_t src, const Matrices& a, char* g,
                                    __uint_as_float(raw[reg_of(h, c + 3)]));
         }
         __syncwarp();
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = stage[(k >> 1) * kStagePitch + (k & 1) * 32 + lane];
+        __syncwarp();
+        const int row0 = dr + 8 * h + 4 * part;
+        char* at = g + row0 * row_bytes + (static_cast<int64_t>(dc + lane) << shift);
+        const bool in0 = dc + lane < cols, in1 = dc + 32 + lane < cols;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int row = row0 + 8 * h + part + (k >> 1), col = col0 + (k & 1) * 32 + lane;
-          const float x = stage[(k >> 1) * kStagePitch + (k & 1) * 32 + lane];
-          if (row < a.rows && col < a.cols) {
-            const int64_t at = static_cast<int64_t>(row) * a.stride + col;
-            if (a.dtype == MUON_F32) {
-              float* q = reinterpret_cast<float*>(g) + at;
-              *q = add ? *q + x : x;
+          if (row0 + (k >> 1) < rows && (k & 1 ? in1 : in0)) {
+            char* q = at + (k >> 1) * row_bytes + ((k & 1) ? 32 << shift : 0);
+            if (f32) {
+              float* w = reinterpret_cast<float*>(q);
+              *w = add ? *w + x[k] : x[k];
             } else {
-              __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(g) + at;
-              *q = __float2bfloat16_rn(add ? __bfloat162float(*q) + x : x);
+              __nv_bfloat16* w = reinterpret_cast<__nv_bfloat16*>(q);
+              *w = __float2bfloat16_rn(add ? __bfloat162float(*w) + x[k] : x[k]);
             }
           }
         }
-        __syncwarp();
       }
     }
   }
@@ -969,7 +973,8 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       } else if (inside && (!EDGE || bits % 16 == 0)) {
         drain_inside<C::kPlanes, false>(src, a.g, p, row_bytes, t.n == 0, add);
       } else if constexpr (EDGE) {
-        drain_any<C::kPlanes>(src, a.g, g, o, i, t.n == 0, add, stage);
+        drain_any<C::kPlanes>(src, g + o * row_bytes + static_cast<int64_t>(i) * esz, row_bytes,
+                                 a.g.rows - o, a.g.cols - i, a.g.dtype == MUON_F32, t.n == 0, add, stage);
       }
       if (t.n == 0) continue;
       tc_fence_before();
