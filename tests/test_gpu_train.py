@@ -542,3 +542,94 @@ def test_weight_grad_against_differences():
     _, size = R.weight_grads(ds, xs, [0, rows])
     tol = float((wgrad_bound(size, f64(G), [0, rows], U) * np.abs(V)).sum())
     assert abs(float((f64(G)[0] * V).sum()) - (f(0.5 * V) - f(-0.5 * V))) <= tol
+
+
+@pytest.mark.parametrize("grad", ["bf16", "f32"])
+@pytest.mark.parametrize("dy", ["bf16", "f32"])
+@pytest.mark.parametrize("offsets,out,inp", [([0, 9000], 256, 512), ([0, 5000, 5001, 12000], 320, 384),
+                                             ([0, 40000], 32, 128), ([0, 3000, 6100], 700, 1000)])
+def test_weight_grad_many_tokens(offsets, out, inp, dy, grad):
+    """Long sums: tokens cut into slices (few tiles) and chunks (fp32 sums), with
+    and without what G holds already."""
+    rows = offsets[-1]
+    d, x8, off, ds, xs = wgrad_case(rows, offsets, rows, out, inp, dy, "dense")
+    want, size = R.weight_grads(ds, xs, offsets)
+    E = len(offsets) - 1
+    start = torch.randn(E, out, inp, device=DEV).to(DT[grad])
+    for acc in (False, True):
+        G = start.clone()
+        assert run_wgrad(d, x8, G, off, acc=acc) == 0
+        total = want + f64(start) if acc else want
+        # a chunk's sum is added to G with a rounding of its own
+        extra = (np.diff(offsets) / 1024 + 2)[:, None, None] * U * (size + np.abs(total))
+        within(f64(G), total, wgrad_bound(size, total, offsets, HALF[grad]) + extra)
+
+
+def test_weight_grad_long_fp32_sums_stay_exact():
+    """32000 tokens: the error against 64 bits stays below 3e-6 of the result
+    (128 truncating additions of the tensor core lose 1.4e-6, chunks add with
+    rounding)."""
+    rows, out, inp = 32000, 256, 256
+    d, x8, off, ds, xs = wgrad_case(7, [0, rows], rows, out, inp, "bf16", "dense")
+    G = torch.empty(1, out, inp, device=DEV)
+    run_wgrad(d, x8, G, off)
+    want = ds.T @ xs
+    assert np.linalg.norm(f64(G)[0] - want) <= 3e-6 * np.linalg.norm(want)
+
+
+def test_weight_grad_pointer_array_alignment():
+    """Pointers of a device array: 16-byte steps are written, others flagged and
+    their matrices left alone."""
+    offsets, rows, out, inp = [0, 40, 90, 130], 130, 64, 128
+    d, x8, off, ds, xs = wgrad_case(8, offsets, rows, out, inp, "bf16", "dense")
+    want, size = R.weight_grads(ds, xs, offsets)
+    buf = torch.full((3 * out * inp + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+    n = out * inp
+    for lead, flag in (((0, 8, 24), 0), ((0, 8, 17), m.MUON_FLAG_MISALIGNED)):
+        buf.fill_(7.0)
+        mats = [buf[e * n + lead[e]:][:n].view(out, inp) for e in range(3)]
+        grp = m.Group(mats, mats, mats)
+        ws = m.workspace(m.muon_act8_weight_grad_workspace_size(rows, out, inp, 3))
+        m.muon_act8_weight_grad(d, x8, grp, ws, offsets=off)
+        code, flags = m.muon_get_status(ws)
+        assert code == m.MUON_OK and flags == flag
+        for e in range(3):
+            if flag and e == 2:
+                assert (mats[e] == 7.0).all()
+            else:
+                within(f64(mats[e]), want[e], wgrad_bound(size, want, offsets, HALF["bf16"])[e])
+
+
+def test_step_from_router_to_muon():
+    """The operators in one step: counts -> offsets -> expert gradients into a
+    group's G, which the optimizer step takes; the dense form in fp32 agrees."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    T, E, D, F = 192, 4, 64, 128
+    x = torch.randn(T, D, generator=g, device=DEV).bfloat16()
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    chosen = logits.argmax(dim=1, keepdim=True)
+    loss, counts = torch.empty(1, device=DEV), torch.empty(E, dtype=torch.int32, device=DEV)
+    load = torch.empty(1, E, device=DEV)
+    ws = m.workspace(m.muon_balance_workspace_size(T, E))
+    m.muon_balance_forward(m.Balance(logits, chosen), loss, counts, load, ws)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:] = torch.cumsum(counts, 0)
+    order = torch.argsort(chosen[:, 0], stable=True)
+    assert counts.sum().item() == T
+    xs, dy = x[order], torch.randn(T, F, generator=g, device=DEV).bfloat16()
+    x8 = m.act8_empty(T, D)
+    m.muon_act8_pack(xs, x8)
+    W, M = torch.randn(E, F, D, device=DEV), torch.zeros(E, F, D, device=DEV)
+    G = torch.empty(E, F, D, dtype=torch.bfloat16, device=DEV)
+    grp = m.Group.stacked(W, G, M)
+    wg = m.workspace(m.muon_act8_weight_grad_workspace_size(T, F, D, E))
+    m.muon_act8_weight_grad(dy, x8, grp, wg, offsets=offsets)
+    back = torch.empty(T, D, device=DEV)
+    m.muon_act8_unpack(x8, back)
+    want, size = R.weight_grads(f64(dy), f64(back), offsets.tolist())
+    within(f64(G), want, wgrad_bound(size, want, offsets.tolist(), HALF["bf16"]))
+    before = W.clone()
+    wm = m.workspace(m.muon_step_workspace_size([grp]))
+    m.muon_step_batched([grp], m.hparams(), wm)
+    assert m.muon_get_status(wm) == (m.MUON_OK, 0)
+    assert torch.equal(M, G.float()) and not torch.equal(W, before)
