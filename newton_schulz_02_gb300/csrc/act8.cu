@@ -9,22 +9,33 @@
 // value needs no rounding where the tensor cores read it.
 //
 // All four passes are bound by HBM: each value is read once and written once.
-// A thread takes V consecutive columns (V = 16: 16-byte accesses throughout,
-// two threads share a block's maximum by one shuffle), or, where some row does
-// not start on a 16-byte boundary, one column (V = 1: a warp reads the 32
-// columns of a block side by side, which coalesces at any alignment).
+// A thread takes 16 consecutive columns; two threads share a block's maximum by
+// one shuffle.  Where every row starts on a 32-byte boundary a thread writes
+// whole 32-byte sectors.  Elsewhere (an odd width, a shifted view) it reads the
+// 16-byte pieces that hold its columns and shifts them into place, and writes
+// the 16-byte pieces that begin in its columns, with the next thread's first
+// values in the last.  One column a thread coalesces at any alignment too, and
+// took 3 to 6 times as long.  Measured at 16384 rows, in us (and the share of
+// the copy rate):
+//                       pack        unpack      forward     backward with h8
+//   7168 bf16           57 (92%)    55 (96%)    155 (90%)   165 (96%)
+//   7001 bf16           63 (82%)    69 (75%)    174 (78%)   209 (74%)
+//   7168 fp32           86 (102%)   89 (98%)    235 (103%)  255 (102%)
+//   7001 fp32           86 (98%)    116 (73%)   249 (95%)   292 (87%)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 32;   // columns that share a scale
+constexpr int kCols = 16;    // columns a thread
 
 // Quotient by a fixed divisor of numbers below 2^31: with l = ceil(log2 d) and
 // m = ceil(2^(31+l) / d), m*d exceeds 2^(31+l) by less than 2^l, so the
@@ -64,70 +75,145 @@ struct Act8Args {
   Packed a, b, c;
 };
 
-// ---- V values of a row -----------------------------------------------------
-template <int V, typename T>
+// ---- 16 values of a row ------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void to_floats(const uint32_t* w, float (&x)[kCols]) {
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    if constexpr (sizeof(T) == 4)
+      x[k] = __uint_as_float(w[k]);
+    else   // a bf16 is the upper half of an fp32
+      x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void to_words(const float (&x)[kCols], uint32_t* w) {
+#pragma unroll
+  for (int k = 0; k < kCols; k += 4 / sizeof(T)) {
+    if constexpr (sizeof(T) == 4) {
+      w[k] = __float_as_uint(x[k]);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[k], x[k + 1]);
+      w[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
+
+// Words from byte `by` of w on (by < 16, a multiple of sizeof(T)); 4 words more
+// than N come in.
+template <typename T, int N>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t by) {
+#pragma unroll
+  for (int k = 0; k < N + 2; ++k) w[k] = by & 8 ? w[k + 2] : w[k];
+#pragma unroll
+  for (int k = 0; k < N + 1; ++k) w[k] = by & 4 ? w[k + 1] : w[k];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = by & 2 ? __byte_perm(w[k], w[k + 1], 0x5432) : w[k];
+  }
+}
+
+// Columns col .. col + 15 of a row, of which n are in the row (the others are
+// 0).  WHOLE: rows start on 32-byte boundaries.
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void load_values(const Plane& pl, int64_t row, int col, int n,
-                                            float (&x)[V]) {
+                                            float (&x)[kCols]) {
+  constexpr int kWords = kCols * sizeof(T) / 4;
   const T* p = static_cast<const T*>(pl.p) + row * pl.stride + col;
-  if constexpr (V == 1) {
-    x[0] = n > 0 ? static_cast<float>(*p) : 0.f;
-  } else if (n >= V) {
-    constexpr int kPer = 16 / sizeof(T);
+  if constexpr (WHOLE) {
+    if (n >= kCols) {
+      uint32_t w[kWords];
 #pragma unroll
-    for (int q = 0; q < V / kPer; ++q) {
-      const uint4 u = reinterpret_cast<const uint4*>(p)[q];
-      if constexpr (sizeof(T) == 4) {
-        x[4 * q] = __uint_as_float(u.x);
-        x[4 * q + 1] = __uint_as_float(u.y);
-        x[4 * q + 2] = __uint_as_float(u.z);
-        x[4 * q + 3] = __uint_as_float(u.w);
-      } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {   // a bf16 is the upper half of an fp32
-          x[8 * q + 2 * k] = __uint_as_float(w[k] << 16);
-          x[8 * q + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
+      for (int q = 0; q < kWords; q += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + q);
+        w[q] = u.x; w[q + 1] = u.y; w[q + 2] = u.z; w[q + 3] = u.w;
       }
+      to_floats<T>(w, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) x[k] = k < n ? static_cast<float>(p[k]) : 0.f;
     }
   } else {
+    // the 16-byte pieces that hold a byte of the row (a piece may begin before the
+    // row or end after it; those bytes are shifted out or cleared)
+    const uint32_t by = reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - by);
+    uint32_t w[kWords + 4];
 #pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = k < n ? static_cast<float>(p[k]) : 0.f;
+    for (int c = 0; c <= kWords / 4; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (16 * c < static_cast<int>(by) + min(n, kCols) * static_cast<int>(sizeof(T)) && n > 0) u = q[c];
+      w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
+    }
+    shift_words<T, kWords>(w, by);
+    to_floats<T>(w, x);
+    if (n < kCols) {
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) x[k] = k < n ? x[k] : 0.f;
+    }
   }
 }
 
 __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <int V, typename T>
+// The reverse; the whole warp calls it (n <= 0: nothing of this thread's is in the row).
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void store_values(const Plane& pl, int64_t row, int col, int n,
-                                             const float (&x)[V]) {
+                                             const float (&x)[kCols]) {
+  constexpr int kWords = kCols * sizeof(T) / 4;
   T* p = static_cast<T*>(pl.p) + row * pl.stride + col;
-  if constexpr (V == 1) {
-    if (n > 0) store_one(p, x[0]);
-  } else if (n >= V) {
-    constexpr int kPer = 16 / sizeof(T);
+  if constexpr (WHOLE) {
+    if (n >= kCols) {
+      uint32_t w[kWords];
+      to_words<T>(x, w);
 #pragma unroll
-    for (int q = 0; q < V / kPer; ++q) {
-      uint4 u;
-      if constexpr (sizeof(T) == 4) {
-        u = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]),
-                       __float_as_uint(x[4 * q + 2]), __float_as_uint(x[4 * q + 3]));
-      } else {
-        uint32_t w[4];
+      for (int q = 0; q < kWords; q += 8)
+        st_global_v8(reinterpret_cast<uint32_t*>(p) + q, make_uint4(w[q], w[q + 1], w[q + 2], w[q + 3]),
+                     make_uint4(w[q + 4], w[q + 5], w[q + 6], w[q + 7]));
+    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        u = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      reinterpret_cast<uint4*>(p)[q] = u;
+      for (int k = 0; k < kCols; ++k)
+        if (k < n) store_one(p + k, x[k]);
     }
   } else {
+    uint32_t w[kWords + 4];
+    {
+      uint32_t mine[kWords];
+      to_words<T>(x, mine);
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (k < n) store_one(p + k, x[k]);
+      for (int k = 0; k < kWords; ++k) w[k] = mine[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[kWords + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+    if (n <= 0) return;
+    const int lane = threadIdx.x & 31;
+    const uint32_t head = -reinterpret_cast<uintptr_t>(p) & 15u;   // bytes before the first whole piece
+    if (n < kCols) {
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        if (k < n) store_one(p + k, x[k]);
+      return;
+    }
+    // neighbours in the row (and the warp) that hold 16 columns too
+    const bool before = lane > 0 && col > 0, after = lane < 31 && n >= 2 * kCols;
+    shift_words<T, kWords>(w, head);
+    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) + head);
+#pragma unroll
+    for (int c = 0; c < kWords / 4; ++c)
+      if (c + 1 < kWords / 4 || head == 0 || after)
+        q[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    if (head != 0 && !before) {   // nobody else writes the first bytes
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(16 / sizeof(T)); ++k)
+        if (k * sizeof(T) < head) store_one(p + k, x[k]);
+    }
+    if (head != 0 && !after) {    // nor the last
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(16 / sizeof(T)); ++k)
+        if (k * sizeof(T) >= head) store_one(p + kCols - 16 / sizeof(T) + k, x[kCols - 16 / sizeof(T) + k]);
+    }
   }
 }
 
@@ -153,76 +239,51 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
   return m;
 }
 
-// Largest magnitude of a block from its threads' V values each; NaN if one is.
-template <int V>
-__device__ __forceinline__ float block_amax(const float (&x)[V]) {
+// Largest magnitude of a block from its two threads' values; NaN if one is.
+__device__ __forceinline__ float block_amax(const float (&x)[kCols]) {
   float m = x[0];
 #pragma unroll
-  for (int k = 1; k < V; ++k) m = max_magnitude(m, x[k]);
-#pragma unroll
-  for (int d = kBlock / V / 2; d > 0; d >>= 1)
-    m = max_magnitude(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return fabsf(m);
+  for (int k = 1; k < kCols; ++k) m = max_magnitude(m, x[k]);
+  return fabsf(max_magnitude(m, __shfl_xor_sync(0xffffffffu, m, 1)));
 }
 
-// Quantises the V values of this thread; the lanes of a block must be active
-// together.  x / 2^e is exact, and adding 1.5 * 2^23 rounds it to the nearest
-// integer, ties to even, whose two's complement is the sum's low byte.
-template <int V>
+// Quantises the values of this thread; the whole warp calls it.  x / 2^e is
+// exact, and adding 1.5 * 2^23 rounds it to the nearest integer, ties to even,
+// whose two's complement is the sum's low byte.
 __device__ __forceinline__ void write_codes(const Packed& out, int64_t row, int col,
-                                            const float (&x)[V], bool on) {
-  const int b = scale_exponent(block_amax<V>(x));
+                                            const float (&x)[kCols], bool on) {
+  const int b = scale_exponent(block_amax(x));
   // 2^-e: the biased exponent of the reciprocal is 254 - b, in [5, 253]
   const float inv = b == 255 ? 0.f : exponent_value(254 - b);
   if (!on) return;
-  uint32_t c[V];
+  uint32_t c[kCols];
 #pragma unroll
-  for (int k = 0; k < V; ++k) c[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
+  for (int k = 0; k < kCols; ++k) c[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
   if (b == 249) {   // 64 * 2^122 would overflow
 #pragma unroll
-    for (int k = 0; k < V; ++k)
+    for (int k = 0; k < kCols; ++k)
       c[k] = __float_as_uint(fminf(fmaxf(x[k] * inv, -63.f), 63.f) + 12582912.f);
   }
-  int8_t* p = out.codes + row * out.code_stride + col;
-  if constexpr (V == 1) {
-    *p = static_cast<int8_t>(c[0]);   // columns past the row's end, up to the block's, hold 0
-  } else {
+  uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < V / 16; ++q) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t* d = c + 16 * q + 4 * k;
-        w[k] = __byte_perm(__byte_perm(d[0], d[1], 0x0040), __byte_perm(d[2], d[3], 0x0040), 0x5410);
-      }
-      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
+  for (int k = 0; k < 4; ++k)
+    w[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040),
+                       __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040), 0x5410);
+  *reinterpret_cast<uint4*>(out.codes + row * out.code_stride + col) = make_uint4(w[0], w[1], w[2], w[3]);
   if (col % kBlock == 0) out.exps[row * out.exp_stride + col / kBlock] = static_cast<uint8_t>(b);
 }
 
-// Values of V codes.  Biased by 128 a code is the low byte of 2^23 + 128 +
+// Values of 16 codes.  Biased by 128 a code is the low byte of 2^23 + 128 +
 // code, so a byte permute and a subtraction make the float (the conversion
 // unit is needed for the exponentials), and times 2^e is exact.
-template <int V>
-__device__ __forceinline__ void read_codes(const Packed& in, int64_t row, int col, float (&x)[V]) {
+__device__ __forceinline__ void read_codes(const Packed& in, int64_t row, int col, float (&x)[kCols]) {
   const int b = in.exps[row * in.exp_stride + col / kBlock];
   const float s = b == 255 ? __uint_as_float(0x7FC00000u) : exponent_value(b);
-  const int8_t* p = in.codes + row * in.code_stride + col;
-  if constexpr (V == 1) {
-    x[0] = static_cast<float>(*p) * s;
-  } else {
+  const uint4 u = *reinterpret_cast<const uint4*>(in.codes + row * in.code_stride + col);
+  const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
 #pragma unroll
-    for (int q = 0; q < V / 16; ++q) {
-      const uint4 u = reinterpret_cast<const uint4*>(p)[q];
-      const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u,
-                             u.w ^ 0x80808080u};
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        x[16 * q + k] =
-            (__uint_as_float(__byte_perm(w[k / 4], 0x4B000000u, 0x7440 + k % 4)) - 8388736.f) * s;
-    }
-  }
+  for (int k = 0; k < kCols; ++k)
+    x[k] = (__uint_as_float(__byte_perm(w[k / 4], 0x4B000000u, 0x7440 + k % 4)) - 8388736.f) * s;
 }
 
 struct Place {
@@ -231,7 +292,6 @@ struct Place {
   bool on;
 };
 
-template <int V>
 __device__ __forceinline__ Place place(const Act8Args& a) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   Place p;
@@ -239,26 +299,25 @@ __device__ __forceinline__ Place place(const Act8Args& a) {
   const uint32_t at = p.on ? i : a.items - 1;
   const uint32_t row = quotient(at, a.per_row);
   p.row = row;
-  p.col = static_cast<int>(at - row * a.per_row.d) * V;
+  p.col = static_cast<int>(at - row * a.per_row.d) * kCols;
   p.n = p.on ? a.cols - p.col : 0;
   return p;
 }
 
-template <int V, typename T>
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) k_act8_pack(const __grid_constant__ Act8Args a) {
-  const Place p = place<V>(a);
-  float x[V];
-  load_values<V, T>(a.x, p.row, p.col, p.n, x);
-  write_codes<V>(a.a, p.row, p.col, x, p.on);
+  const Place p = place(a);
+  float x[kCols];
+  load_values<T, WHOLE>(a.x, p.row, p.col, p.n, x);
+  write_codes(a.a, p.row, p.col, x, p.on);
 }
 
-template <int V, typename T>
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) k_act8_unpack(const __grid_constant__ Act8Args a) {
-  const Place p = place<V>(a);
-  if (!p.on) return;
-  float x[V];
-  read_codes<V>(a.a, p.row, p.col, x);
-  store_values<V, T>(a.x, p.row, p.col, p.n, x);
+  const Place p = place(a);
+  float x[kCols];
+  read_codes(a.a, p.row, p.col, x);
+  store_values<T, WHOLE>(a.x, p.row, p.col, p.n, x);
 }
 
 // 1 / (1 + e^-g) with the fast exponential and reciprocal: an error of a few
@@ -266,29 +325,31 @@ __global__ void __launch_bounds__(kThreads) k_act8_unpack(const __grid_constant_
 __device__ __forceinline__ float sigma(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // x = gate, y = up, z = h; a, b = the checkpoints of gate and up.
-template <int V, typename T>
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) k_act8_swiglu_forward(const __grid_constant__ Act8Args a) {
-  const Place p = place<V>(a);
-  float g[V], u[V], h[V];
-  load_values<V, T>(a.x, p.row, p.col, p.n, g);
-  load_values<V, T>(a.y, p.row, p.col, p.n, u);
-  write_codes<V>(a.a, p.row, p.col, g, p.on);
-  write_codes<V>(a.b, p.row, p.col, u, p.on);
+  const Place p = place(a);
+  float g[kCols], u[kCols], h[kCols];
+  load_values<T, WHOLE>(a.x, p.row, p.col, p.n, g);
+  load_values<T, WHOLE>(a.y, p.row, p.col, p.n, u);
+  write_codes(a.a, p.row, p.col, g, p.on);
+  write_codes(a.b, p.row, p.col, u, p.on);
 #pragma unroll
-  for (int k = 0; k < V; ++k) h[k] = g[k] * sigma(g[k]) * u[k];
-  if (p.on) store_values<V, T>(a.z, p.row, p.col, p.n, h);
+  for (int k = 0; k < kCols; ++k) h[k] = g[k] * sigma(g[k]) * u[k];
+  store_values<T, WHOLE>(a.z, p.row, p.col, p.n, h);
 }
 
 // x = dh, y = dgate, z = dup; a, b = the checkpoints of gate and up, c = h8.
-template <int V, typename T, bool H8>
-__global__ void __launch_bounds__(kThreads) k_act8_swiglu_backward(const __grid_constant__ Act8Args a) {
-  const Place p = place<V>(a);
-  float g[V], u[V], d[V], h[H8 ? V : 1];
-  read_codes<V>(a.a, p.row, p.col, g);
-  read_codes<V>(a.b, p.row, p.col, u);
-  load_values<V, T>(a.x, p.row, p.col, p.n, d);
+// Four blocks an SM (64 registers): with the 66 to 80 that fp32 rows and rows
+// off the boundary take otherwise, 342 us instead of 255 (16384 x 7168 fp32).
+template <typename T, bool WHOLE, bool H8>
+__global__ void __launch_bounds__(kThreads, 4) k_act8_swiglu_backward(const __grid_constant__ Act8Args a) {
+  const Place p = place(a);
+  float g[kCols], u[kCols], d[kCols], h[H8 ? kCols : 1];
+  read_codes(a.a, p.row, p.col, g);
+  read_codes(a.b, p.row, p.col, u);
+  load_values<T, WHOLE>(a.x, p.row, p.col, p.n, d);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
+  for (int k = 0; k < kCols; ++k) {
     const float s = sigma(g[k]);
     const float act = g[k] * s;
     if (H8) h[k] = k < p.n ? act * u[k] : 0.f;
@@ -296,11 +357,12 @@ __global__ void __launch_bounds__(kThreads) k_act8_swiglu_backward(const __grid_
     u[k] = d[k] * act;
     g[k] = dg;
   }
-  if (p.on) {
-    store_values<V, T>(a.y, p.row, p.col, p.n, g);
-    store_values<V, T>(a.z, p.row, p.col, p.n, u);
+  if constexpr (!WHOLE) __syncwarp();   // dh may be dgate or dup: the warp's reads are over
+  if (!WHOLE || p.on) {   // the others exchange their ends: the whole warp
+    store_values<T, WHOLE>(a.y, p.row, p.col, p.n, g);
+    store_values<T, WHOLE>(a.z, p.row, p.col, p.n, u);
   }
-  if constexpr (H8) write_codes<V>(a.c, p.row, p.col, h, p.on);
+  if constexpr (H8) write_codes(a.c, p.row, p.col, h, p.on);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -334,19 +396,19 @@ bool same_size(const muon_act8_t* a, const muon_act8_t* b) {
 Packed packed(const muon_act8_t* a) { return {a->codes, a->code_stride, a->exps, a->exp_stride}; }
 
 bool rows_aligned(const Plane& p, int dtype) {
-  return p.p == nullptr || (at_multiple(p.p, 16) && p.stride * esize(dtype) % 16 == 0);
+  return p.p == nullptr || (at_multiple(p.p, 32) && p.stride * esize(dtype) % 32 == 0);
 }
 
 enum Pass { kPack, kUnpack, kForward, kBackward, kBackwardH8 };
 
-template <int V, typename T>
+template <typename T, bool WHOLE>
 void launch_pass(Pass pass, unsigned grid, cudaStream_t st, const Act8Args& a) {
   switch (pass) {
-    case kPack: k_act8_pack<V, T><<<grid, kThreads, 0, st>>>(a); break;
-    case kUnpack: k_act8_unpack<V, T><<<grid, kThreads, 0, st>>>(a); break;
-    case kForward: k_act8_swiglu_forward<V, T><<<grid, kThreads, 0, st>>>(a); break;
-    case kBackward: k_act8_swiglu_backward<V, T, false><<<grid, kThreads, 0, st>>>(a); break;
-    case kBackwardH8: k_act8_swiglu_backward<V, T, true><<<grid, kThreads, 0, st>>>(a); break;
+    case kPack: k_act8_pack<T, WHOLE><<<grid, kThreads, 0, st>>>(a); break;
+    case kUnpack: k_act8_unpack<T, WHOLE><<<grid, kThreads, 0, st>>>(a); break;
+    case kForward: k_act8_swiglu_forward<T, WHOLE><<<grid, kThreads, 0, st>>>(a); break;
+    case kBackward: k_act8_swiglu_backward<T, WHOLE, false><<<grid, kThreads, 0, st>>>(a); break;
+    case kBackwardH8: k_act8_swiglu_backward<T, WHOLE, true><<<grid, kThreads, 0, st>>>(a); break;
   }
 }
 
@@ -354,8 +416,8 @@ void launch_pass(Pass pass, unsigned grid, cudaStream_t st, const Act8Args& a) {
 muon_status_t run_pass(Pass pass, int dtype, int64_t rows, int cols, Act8Args a, double bytes,
                        cudaStream_t st) {
   if (rows == 0) return MUON_OK;
-  const bool wide = rows_aligned(a.x, dtype) && rows_aligned(a.y, dtype) && rows_aligned(a.z, dtype);
-  const int64_t per_row = blocks_of(cols) * (wide ? 2 : kBlock);
+  const bool whole = rows_aligned(a.x, dtype) && rows_aligned(a.y, dtype) && rows_aligned(a.z, dtype);
+  const int64_t per_row = blocks_of(cols) * (kBlock / kCols);
   a.cols = cols;
   a.per_row = divider(static_cast<uint32_t>(per_row));
   int64_t most = (int64_t{1} << 30) / per_row;
@@ -375,11 +437,11 @@ muon_status_t run_pass(Pass pass, int dtype, int64_t rows, int cols, Act8Args a,
     const unsigned grid = (b.items + kThreads - 1) / kThreads;
     prof_begin(kind, st);
     if (dtype == MUON_F32) {
-      if (wide) launch_pass<16, float>(pass, grid, st, b);
-      else launch_pass<1, float>(pass, grid, st, b);
+      if (whole) launch_pass<float, true>(pass, grid, st, b);
+      else launch_pass<float, false>(pass, grid, st, b);
     } else {
-      if (wide) launch_pass<16, __nv_bfloat16>(pass, grid, st, b);
-      else launch_pass<1, __nv_bfloat16>(pass, grid, st, b);
+      if (whole) launch_pass<__nv_bfloat16, true>(pass, grid, st, b);
+      else launch_pass<__nv_bfloat16, false>(pass, grid, st, b);
     }
     prof_end(kind, st, 0.0, bytes * static_cast<double>(n) * cols);
     if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
