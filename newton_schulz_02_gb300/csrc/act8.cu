@@ -29,13 +29,13 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 32;   // columns that share a scale
-constexpr int kCols = 16;    // columns a thread
 
 // Quotient by a fixed divisor of numbers below 2^31: with l = ceil(log2 d) and
 // m = ceil(2^(31+l) / d), m*d exceeds 2^(31+l) by less than 2^l, so the
@@ -76,44 +76,6 @@ struct Act8Args {
 };
 
 // ---- 16 values of a row ------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ void to_floats(const uint32_t* w, float (&x)[kCols]) {
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) {
-    if constexpr (sizeof(T) == 4)
-      x[k] = __uint_as_float(w[k]);
-    else   // a bf16 is the upper half of an fp32
-      x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void to_words(const float (&x)[kCols], uint32_t* w) {
-#pragma unroll
-  for (int k = 0; k < kCols; k += 4 / sizeof(T)) {
-    if constexpr (sizeof(T) == 4) {
-      w[k] = __float_as_uint(x[k]);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[k], x[k + 1]);
-      w[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-}
-
-// Words from byte `by` of w on (by < 16, a multiple of sizeof(T)); 4 words more
-// than N come in.
-template <typename T, int N>
-__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t by) {
-#pragma unroll
-  for (int k = 0; k < N + 2; ++k) w[k] = by & 8 ? w[k + 2] : w[k];
-#pragma unroll
-  for (int k = 0; k < N + 1; ++k) w[k] = by & 4 ? w[k + 1] : w[k];
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) w[k] = by & 2 ? __byte_perm(w[k], w[k + 1], 0x5432) : w[k];
-  }
-}
-
 // Columns col .. col + 15 of a row, of which n are in the row (the others are
 // 0).  WHOLE: rows start on 32-byte boundaries.
 template <typename T, bool WHOLE>
@@ -135,28 +97,9 @@ __device__ __forceinline__ void load_values(const Plane& pl, int64_t row, int co
       for (int k = 0; k < kCols; ++k) x[k] = k < n ? static_cast<float>(p[k]) : 0.f;
     }
   } else {
-    // the 16-byte pieces that hold a byte of the row (a piece may begin before the
-    // row or end after it; those bytes are shifted out or cleared)
-    const uint32_t by = reinterpret_cast<uintptr_t>(p) & 15u;
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - by);
-    uint32_t w[kWords + 4];
-#pragma unroll
-    for (int c = 0; c <= kWords / 4; ++c) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (16 * c < static_cast<int>(by) + min(n, kCols) * static_cast<int>(sizeof(T)) && n > 0) u = q[c];
-      w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
-    }
-    shift_words<T, kWords>(w, by);
-    to_floats<T>(w, x);
-    if (n < kCols) {
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) x[k] = k < n ? x[k] : 0.f;
-    }
+    load_shifted(p, n, x);
   }
 }
-
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // The reverse; the whole warp calls it (n <= 0: nothing of this thread's is in the row).
 template <typename T, bool WHOLE>
@@ -178,42 +121,8 @@ __device__ __forceinline__ void store_values(const Plane& pl, int64_t row, int c
         if (k < n) store_one(p + k, x[k]);
     }
   } else {
-    uint32_t w[kWords + 4];
-    {
-      uint32_t mine[kWords];
-      to_words<T>(x, mine);
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) w[k] = mine[k];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[kWords + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
-    if (n <= 0) return;
     const int lane = threadIdx.x & 31;
-    const uint32_t head = -reinterpret_cast<uintptr_t>(p) & 15u;   // bytes before the first whole piece
-    if (n < kCols) {
-#pragma unroll
-      for (int k = 0; k < kCols; ++k)
-        if (k < n) store_one(p + k, x[k]);
-      return;
-    }
-    // neighbours in the row (and the warp) that hold 16 columns too
-    const bool before = lane > 0 && col > 0, after = lane < 31 && n >= 2 * kCols;
-    shift_words<T, kWords>(w, head);
-    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) + head);
-#pragma unroll
-    for (int c = 0; c < kWords / 4; ++c)
-      if (c + 1 < kWords / 4 || head == 0 || after)
-        q[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    if (head != 0 && !before) {   // nobody else writes the first bytes
-#pragma unroll
-      for (int k = 0; k < static_cast<int>(16 / sizeof(T)); ++k)
-        if (k * sizeof(T) < head) store_one(p + k, x[k]);
-    }
-    if (head != 0 && !after) {    // nor the last
-#pragma unroll
-      for (int k = 0; k < static_cast<int>(16 / sizeof(T)); ++k)
-        if (k * sizeof(T) >= head) store_one(p + kCols - 16 / sizeof(T) + k, x[kCols - 16 / sizeof(T) + k]);
-    }
+    store_shifted(p, n, lane > 0 && col > 0, lane < 31 ? min(max(n - kCols, 0), kCols) : 0, x);
   }
 }
 
