@@ -55,7 +55,6 @@ struct WgradArgs {
   int rows, out, in, experts;
   const void* dy;
   int64_t dy_stride;
-  int dy_vec;             // dy's rows may be read four values at a time
   const int32_t* offsets;
   Matrices g;
   int tiles_o, tiles_i;   // 256 x 256 tiles of a matrix
@@ -101,6 +100,7 @@ struct Cfg {
   static constexpr int kDyStages = MODE == kTma ? 6 : 2;     // dy tiles in flight or in use
   static constexpr int kSlots = MODE == kTma ? 4 : 2;        // decoded blocks, a converter group each
   static constexpr int kLoadWarps = MODE == kTma ? 0 : 8;
+  static constexpr int kBlockLoadWarps = MODE == kLoad16 ? 4 : kLoadWarps;   // of one block
   static constexpr int kConv0 = 4, kLoad0 = kConv0 + kSlots * kConvWarps;   // first warps
   static constexpr int kEpi0 = kLoad0 + kLoadWarps;
   static constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
@@ -466,61 +466,25 @@ __device__ __forceinline__ char* matrix_of(const Matrices& g, int m) {
                                       m * g.batch_stride * (g.dtype == MUON_F32 ? 4 : 2));
 }
 
-template <DyMode MODE>
-struct DyType {
-  using type = __nv_bfloat16;
-};
-template <>
-struct DyType<kTma32> {
-  using type = float;
-};
-template <>
-struct DyType<kLoad32> {
-  using type = float;
-};
-
-// Four consecutive values of a row of dy (0 past the row's end).
-template <typename T>
-__device__ __forceinline__ void load_dy4(const T* row, int col, int cols, bool vec, float (&v)[4]) {
-  if (vec && col + 4 <= cols) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(row + col);
-      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(row + col);
-      v[0] = __uint_as_float(w.x << 16);
-      v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(w.y << 16);
-      v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = col + k < cols ? static_cast<float>(row[col + k]) : 0.f;
-  }
-}
-
-// Four values as PLANES planes of bf16: with three, the upper 8 significant
+// Four fp32 values as three planes of bf16: the upper 8 significant
 // bits, the next 8 and the last 8, whose sum is the value.  An infinity or a
 // NaN is the first plane alone.
-template <int PLANES>
-__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&out)[PLANES]) {
-  uint32_t u[PLANES][4];
+__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&out)[3]) {
+  uint32_t u[3][4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t b = __float_as_uint(v[k]);
+    const float r = v[k] - __uint_as_float(b & 0xFFFF0000u);
     u[0][k] = b;
-    if constexpr (PLANES == 3) {
-      const float r = v[k] - __uint_as_float(b & 0xFFFF0000u);
-      u[1][k] = __float_as_uint(r);
-      u[2][k] = __float_as_uint(r - __uint_as_float(u[1][k] & 0xFFFF0000u));
-      if ((b & 0x7F800000u) == 0x7F800000u) {
-        if ((b & 0x007FFFFFu) != 0) u[0][k] = 0x7FC00000u;
-        u[1][k] = u[2][k] = 0u;
-      }
+    u[1][k] = __float_as_uint(r);
+    u[2][k] = __float_as_uint(r - __uint_as_float(u[1][k] & 0xFFFF0000u));
+    if ((b & 0x7F800000u) == 0x7F800000u) {
+      if ((b & 0x007FFFFFu) != 0) u[0][k] = 0x7FC00000u;
+      u[1][k] = u[2][k] = 0u;
     }
   }
 #pragma unroll
-  for (int p = 0; p < PLANES; ++p)
+  for (int p = 0; p < 3; ++p)
     out[p] = make_uint2(__byte_perm(u[p][0], u[p][1], 0x7632), __byte_perm(u[p][2], u[p][3], 0x7632));
 }
 
@@ -576,7 +540,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&code_full[s], 1);
       mbar_init(&code_empty[s], kConvWarps);    // read into registers
-      mbar_init(&ready[s], 2 * (kConvWarps + C::kLoadWarps));   // both CTAs' warps
+      mbar_init(&ready[s], 2 * (kConvWarps + C::kBlockLoadWarps));   // both CTAs' warps
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
@@ -828,12 +792,81 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
     }
   } else if (warp < C::kEpi0) {
     // ------------------------------------------------------------- loaders
-    // dy through registers: a warp takes a row of 128 columns, four a thread,
-    // from memory (a block ahead) or from TMA's fp32 tile, and writes them (as
-    // planes) where TMA puts a bf16 tile.  Rows of the next expert and columns
-    // past the end are zeros.
-    if constexpr (MODE != kTma) {
-      using T = typename DyType<MODE>::type;
+    // dy through registers, written where TMA puts a bf16 tile.  Rows of the next
+    // expert and columns past the end are zeros.
+    if constexpr (MODE == kLoad16) {
+      // Two groups of four warps take the blocks in turn.  A thread takes 16 columns
+      // of every 16th row: the 16-byte pieces that hold them, its next block's
+      // fetched ahead, shifted into place (8192 tokens, 4097 x 4096: 417 us, 500 with
+      // one group; 199 for the 4096 that TMA fetches).
+      static_assert(kDyStages == 2 && kSlots == 2, "a stage and a slot for each group");
+      constexpr int kRows = 4;   // of a thread
+      const int tid = threadIdx.x - 32 * C::kLoad0;
+      const int lg = tid >> 7, tr = (tid & 127) >> 3, j = tid & 7;
+      const uint32_t ready_g = mapa_shared(&ready[lg], 0);
+      uint32_t c0 = 0;   // blocks before this unit
+      bool ok = true;
+      Unit t;
+      while (ok && take(t, true)) {
+        const int o = t.o0 + static_cast<int>(rank) * 128 + 16 * j;
+        const int cols = min(a.out - o, kCols);
+        uint32_t w[kRows][12];   // 16 columns at any alignment
+        uint32_t by[kRows];
+        const auto fetch = [&](uint32_t k) {   // block k of the unit
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            const int r = static_cast<int>(k) * kBK + tr + 16 * q;
+            const uintptr_t p = reinterpret_cast<uintptr_t>(a.dy) +
+                                2 * (static_cast<int64_t>(t.begin + r) * a.dy_stride + o);
+            const int n = r < t.n ? cols : 0;
+            by[q] = static_cast<uint32_t>(p) & 15u;
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+              uint4 u = make_uint4(0, 0, 0, 0);
+              if (n > 0 && 16 * x < static_cast<int>(by[q]) + 2 * n)
+                u = reinterpret_cast<const uint4*>(p - by[q])[x];
+              w[q][4 * x] = u.x; w[q][4 * x + 1] = u.y; w[q][4 * x + 2] = u.z; w[q][4 * x + 3] = u.w;
+            }
+          }
+        };
+        const uint32_t blocks = static_cast<uint32_t>((t.n + kBK - 1) / kBK);
+        uint32_t k = (lg - c0) % 2u;
+        if (k < blocks) fetch(k);
+        for (; k < blocks; k += 2) {
+          const uint32_t turn = (c0 + k) / 2;   // this group's blocks before
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            shift_words<__nv_bfloat16, 8>(w[q], by[q]);
+            if (cols < kCols) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                w[q][x] = 2 * x + 1 < cols ? w[q][x] : 2 * x < cols ? w[q][x] & 0xFFFFu : 0u;
+            }
+          }
+          if (turn > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_empty[lg], (turn & 1u) ^ 1u, abort_flag,
+                                                           a.status, a.timeout_ns));
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int q = 0; q < kRows; ++q) {
+            const int r = tr + 16 * q;
+            uint8_t* at = sm_dy + lg * C::kStageBytes + (j >> 2) * kAtomBytes + r * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4*>(at + (((2 * (j & 3) + h) ^ (r & 7)) << 4)) =
+                  make_uint4(w[q][4 * h], w[q][4 * h + 1], w[q][4 * h + 2], w[q][4 * h + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(ready_g);
+          if (k + 2 < blocks) fetch(k + 2);
+        }
+        c0 += blocks;
+      }
+    } else if constexpr (MODE != kTma) {
+      // fp32: a warp takes a row of 128 columns, four a thread, from memory (a block
+      // ahead) or from TMA's tile, and writes them as planes.
       const int lw = warp - C::kLoad0;
       const int col4 = 4 * lane;   // within the CTA's 128 columns
       const uint32_t ready0 = mapa_shared(&ready[0], 0);
@@ -847,11 +880,10 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const int r = q * C::kLoadWarps + lw;
+            const float* row =
+                static_cast<const float*>(a.dy) + static_cast<int64_t>(t.begin + k0 + r) * a.dy_stride;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[q][k] = 0.f;
-            if (k0 + r < t.n)
-              load_dy4(static_cast<const T*>(a.dy) + static_cast<int64_t>(t.begin + k0 + r) * a.dy_stride,
-                       o, a.out, a.dy_vec != 0, v[q]);
+            for (int k = 0; k < 4; ++k) v[q][k] = k0 + r < t.n && o + k < a.out ? row[o + k] : 0.f;
           }
         };
         if (MODE != kTma32 && t.n > 0) fetch(0);
@@ -869,13 +901,13 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
                                                                 lane * 16);
               const bool in = k0 + r < t.n;
               const float y[4] = {in ? x.x : 0.f, in ? x.y : 0.f, in ? x.z : 0.f, in ? x.w : 0.f};
-              split4<C::kPlanes>(y, w[q]);
+              split4(y, w[q]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.raw_empty[c % 2]);
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) split4<C::kPlanes>(v[q], w[q]);
+            for (int q = 0; q < 8; ++q) split4(v[q], w[q]);
           }
           if (c >= kDyStages) {
             ok = __all_sync(0xffffffffu,
@@ -1227,7 +1259,6 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
   } else if (at_multiple(d->dy, 16) && d->dy_stride % 8 == 0) {
     e = launch<kTma>(a, x, st);
   } else {
-    a.dy_vec = at_multiple(d->dy, 8) && d->dy_stride % 4 == 0;
     e = launch<kLoad16>(a, x, st);
   }
   prof_end(kKindWeightGrad, st, 2.0 * rows * d->out * x.cols,
