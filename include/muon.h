@@ -485,8 +485,10 @@ typedef struct {
   int accumulate;
 } muon_weight_grad_t;
 
-/* Bytes of workspace muon_act8_weight_grad needs (pointers are not looked at).
- * Host only. */
+/* Bytes of workspace muon_act8_weight_grad needs (pointers are not looked at):
+ * a header, partial sums where the tokens are cut into slices, and room for a
+ * copy of dy, which is made where dy's rows do not start on 16-byte boundaries
+ * (2 bytes a value) or are fp32 (three bf16 a value).  Host only. */
 muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, size_t* bytes);
 
 muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace,

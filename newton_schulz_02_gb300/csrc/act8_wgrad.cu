@@ -17,9 +17,10 @@
 // ragged: rows of the last block that belong to the next expert are zeroed in
 // both operands (a zero times their NaN would be NaN).
 //
-// Where TMA cannot fetch dy (fp32, or rows off 16-byte boundaries), eight warps
-// load it instead.  An fp32 value is split into three bf16 of 8 bits each,
-// whose sum it is, and the MMA runs once for each: products stay exact.
+// Where TMA cannot fetch dy (rows off 16-byte boundaries, fp32), k_wgrad_dy
+// writes it to the workspace first, on such boundaries.  An fp32 value becomes
+// three bf16 of 8 bits each, whose sum it is, and the MMA runs once for each:
+// products stay exact.
 //
 // Few tiles and many tokens: the tokens of a tile are cut into slices that
 // leave fp32 partial sums in the workspace, which k_wgrad_join adds in order.
@@ -53,8 +54,6 @@ struct Matrices {
 
 struct WgradArgs {
   int rows, out, in, experts;
-  const void* dy;
-  int64_t dy_stride;
   const int32_t* offsets;
   Matrices g;
   int tiles_o, tiles_i;   // 256 x 256 tiles of a matrix
@@ -79,32 +78,22 @@ __device__ __forceinline__ void span_of(const WgradArgs& a, int e, int& b, int& 
 constexpr int kBK = 64;                          // tokens per block of the contraction
 constexpr int kConvWarps = 4, kEpiWarps = 8;     // converter warps of one group
 constexpr uint32_t kDyBytes = kBK * 128 * 2;     // a plane: two 64-column atoms of 128-byte rows
-constexpr uint32_t kRawBytes = kBK * 128 * 4;
 constexpr uint32_t kCodeBytes = kBK * 128;
 constexpr uint32_t kExpBytes = kBK * 16;         // 16 blocks' bytes a row, four of them used
 constexpr uint32_t kAtomBytes = kBK * 128;       // 64 columns x kBK rows
 constexpr uint32_t kSlotBytes = 2 * kAtomBytes;
 constexpr int kUnits = 16;                       // units announced at a time, two batches ahead
 
-// How dy comes: kTma (bf16), kTma32 (fp32 by TMA, split by eight warps), kLoad16
-// and kLoad32 (the same warps load it themselves, for rows off the boundaries
-// that TMA needs).  Six dy stages and four decoded blocks cover the latency of
-// a load (about 1 us under load, a block's MMAs take 0.3); with three planes
-// a block's MMAs take three times as long and two do.
-enum DyMode { kTma, kTma32, kLoad16, kLoad32 };
-
-template <DyMode MODE>
+// PLANES: of dy.  Six dy stages and four decoded blocks cover the latency of a
+// load (about 1 us under load, a block's MMAs take 0.3); with three planes a
+// block's MMAs take three times as long, and three and two do.
+template <int PLANES>
 struct Cfg {
-  static constexpr int kPlanes = MODE == kTma32 || MODE == kLoad32 ? 3 : 1;
-  static constexpr int kRawStages = MODE == kTma32 ? 2 : 0;  // fp32 tiles in flight
-  static constexpr int kDyStages = MODE == kTma ? 6 : 2;     // dy tiles in flight or in use
-  static constexpr int kSlots = MODE == kTma ? 4 : 2;        // decoded blocks, a converter group each
-  static constexpr int kLoadWarps = MODE == kTma ? 0 : 8;
-  static constexpr int kBlockLoadWarps = MODE == kLoad16 ? 4 : kLoadWarps;   // of one block
-  static constexpr int kConv0 = 4, kLoad0 = kConv0 + kSlots * kConvWarps;   // first warps
-  static constexpr int kEpi0 = kLoad0 + kLoadWarps;
+  static constexpr int kDyStages = PLANES == 1 ? 6 : 3;   // dy tiles in flight or in use
+  static constexpr int kSlots = PLANES == 1 ? 4 : 2;      // decoded blocks, a converter group each
+  static constexpr int kConv0 = 4, kEpi0 = kConv0 + kSlots * kConvWarps;   // first warps
   static constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
-  static constexpr uint32_t kStageBytes = kPlanes * kDyBytes;
+  static constexpr uint32_t kStageBytes = PLANES * kDyBytes;   // 64 columns of every plane, 64 more
 
   // What the roles of a CTA share besides the operands.  An mbarrier's parity
   // tells only the current phase from the one before, so every role that waits
@@ -114,7 +103,6 @@ struct Cfg {
   // when the MMAs of block c - kSlots are (at least as many dy stages as slots).
   struct Shared {
     uint64_t dy_full[kDyStages], dy_empty[kDyStages];     // loads landed; MMAs on the stage done
-    uint64_t raw_full[2], raw_empty[2];                   // the same of fp32 tiles
     uint64_t code_full[kSlots], code_empty[kSlots];       // loads landed; read into registers
     uint64_t ready[kSlots];                               // both operands of a block in place
     uint64_t unit_full[2], unit_empty[2];                 // a batch of units announced; taken
@@ -124,12 +112,12 @@ struct Cfg {
     int abort;
     alignas(16) int units[2 * kUnits][8];
   };
-  static constexpr size_t kSmem = kDyStages * kStageBytes + kRawStages * kRawBytes +
+  static constexpr size_t kSmem = kDyStages * kStageBytes +
                                   kSlots * (kSlotBytes + kCodeBytes + kExpBytes) +
                                   sizeof(Shared) + 1024;
 };
-static_assert(Cfg<kTma>::kThreads == 896 && Cfg<kTma32>::kThreads == 896, "see the register split");
-static_assert(Cfg<kTma>::kSmem <= 232448 && Cfg<kTma32>::kSmem <= 232448, "");
+static_assert(Cfg<1>::kThreads == 896, "see the register split");
+static_assert(Cfg<1>::kSmem <= 232448 && Cfg<3>::kSmem <= 232448, "");
 
 constexpr uint32_t kTmemCols = 512;              // two accumulators of 256 columns
 // D fp32, A and B bf16, both MN-major, M = 256, N = 256
@@ -221,6 +209,15 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int32_t x,
+                                            int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -466,50 +463,81 @@ __device__ __forceinline__ char* matrix_of(const Matrices& g, int m) {
                                       m * g.batch_stride * (g.dtype == MUON_F32 ? 4 : 2));
 }
 
-// Four fp32 values as three planes of bf16: the upper 8 significant
-// bits, the next 8 and the last 8, whose sum is the value.  An infinity or a
-// NaN is the first plane alone.
-__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&out)[3]) {
-  uint32_t u[3][4];
+// dy [rows][out] as planes of bf16 [rows][pitch] at `to`, `plane` values apart
+// (pitch: out rounded up to 16; columns past out are 0).  bf16: one plane, the
+// values themselves.  fp32: three, the upper 8 significant bits, the next 8 and
+// the last 8, whose sum is the value; an infinity or a NaN is the first alone.
+// 16 columns a thread; bound by HBM.  Clears the call's status word too, before
+// k_wgrad may start.  (Loading, splitting and shifting dy in k_wgrad instead, by
+// eight warps of its own, cost more than this pass: 16384 tokens, 256 x 7168
+// fp32 158 us against 127; 8192 tokens, 4097 x 4096 bf16 417 against 215.)
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_wgrad_dy(const T* dy, int64_t stride, int64_t items, int out, __nv_bfloat16* to, int pitch, int64_t plane,
+               uint32_t* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *status = 0;
+    __threadfence();
+  }
+  griddep_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= items) return;
+  const uint32_t per = static_cast<uint32_t>(pitch) / kCols;   // items of a row
+  const int64_t row = items >> 32 == 0 ? static_cast<uint32_t>(i) / per : i / per;
+  const int col = static_cast<int>(i - row * per) * kCols;
+  float x[kCols];
+  load_shifted(dy + row * stride + col, out - col, x);
+  __nv_bfloat16* p = to + row * pitch + col;
+  const auto store = [](__nv_bfloat16* q, const uint32_t (&w)[8]) {
+    st_global_v8(q, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+  };
+  uint32_t w[8];
+  if constexpr (sizeof(T) == 2) {
+    to_words<T>(x, w);
+    store(p, w);
+  } else {
+    uint32_t u[3][kCols];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t b = __float_as_uint(v[k]);
-    const float r = v[k] - __uint_as_float(b & 0xFFFF0000u);
-    u[0][k] = b;
-    u[1][k] = __float_as_uint(r);
-    u[2][k] = __float_as_uint(r - __uint_as_float(u[1][k] & 0xFFFF0000u));
-    if ((b & 0x7F800000u) == 0x7F800000u) {
-      if ((b & 0x007FFFFFu) != 0) u[0][k] = 0x7FC00000u;
-      u[1][k] = u[2][k] = 0u;
+    for (int k = 0; k < kCols; ++k) {
+      const uint32_t b = __float_as_uint(x[k]);
+      const float r = x[k] - __uint_as_float(b & 0xFFFF0000u);
+      u[0][k] = b;
+      u[1][k] = __float_as_uint(r);
+      u[2][k] = __float_as_uint(r - __uint_as_float(u[1][k] & 0xFFFF0000u));
+      if ((b & 0x7F800000u) == 0x7F800000u) {
+        if ((b & 0x007FFFFFu) != 0) u[0][k] = 0x7FC00000u;
+        u[1][k] = u[2][k] = 0u;
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __byte_perm(u[z][2 * k], u[z][2 * k + 1], 0x7632);
+      store(p + z * plane, w);
     }
   }
-#pragma unroll
-  for (int p = 0; p < 3; ++p)
-    out[p] = make_uint2(__byte_perm(u[p][0], u[p][1], 0x7632), __byte_perm(u[p][2], u[p][3], 0x7632));
 }
 
 // EDGE: some 32 x 128 piece of G may lie partly outside it, or off 16-byte
 // boundaries.  (A kernel of its own, as the call that drains such a piece costs
 // the other one registers: 469 against 438 us for 64 experts of 256 tokens.)
-template <DyMode MODE, bool EDGE>
-__global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
+template <int PLANES, bool EDGE>
+__global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_codes,
                  const __grid_constant__ CUtensorMap tm_exps, const __grid_constant__ WgradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  using C = Cfg<MODE>;
+  using C = Cfg<PLANES>;
   constexpr int kDyStages = C::kDyStages, kSlots = C::kSlots;
-  constexpr bool kTmaDy = MODE == kTma || MODE == kTma32;
   // Two accumulators take turns; with three planes one takes the sums of the
   // upper parts and the other those of the rest.  The tensor core's additions
   // truncate: apart, the long sum is added to a third as often, and the error of
   // 32 blocks against 64 bits falls from 6e-6 to 2e-6.
-  constexpr uint32_t kAccs = C::kPlanes == 1 ? 2 : 1;
+  constexpr uint32_t kAccs = PLANES == 1 ? 2 : 1;
   uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
   uint8_t* sm_x = sm_dy + kDyStages * C::kStageBytes;       // decoded, swizzled
-  uint8_t* sm_raw = sm_x + kSlots * kSlotBytes;             // fp32, rows of 512 bytes
-  uint8_t* sm_codes = sm_raw + C::kRawStages * kRawBytes;   // swizzled
+  uint8_t* sm_codes = sm_x + kSlots * kSlotBytes;           // swizzled
   uint8_t* sm_exps = sm_codes + kSlots * kCodeBytes;
   typename C::Shared& bars = *reinterpret_cast<typename C::Shared*>(sm_exps + kSlots * kExpBytes);
   uint64_t *dy_full = bars.dy_full, *dy_empty = bars.dy_empty, *code_full = bars.code_full,
@@ -525,22 +553,17 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&unit_full[s], 1);
-      // TMA threads, converters, loaders, epilogue; the MMA issuer in the even CTA
-      mbar_init(&unit_empty[s], (kTmaDy ? 2 : 1) + kSlots * kConvWarps + C::kLoadWarps +
-                                    kEpiWarps + (rank == 0 ? 1 : 0));
+      // TMA threads, converters, epilogue; the MMA issuer in the even CTA
+      mbar_init(&unit_empty[s], 2 + kSlots * kConvWarps + kEpiWarps + (rank == 0 ? 1 : 0));
     }
     for (int s = 0; s < kDyStages; ++s) {
       mbar_init(&dy_full[s], 1);                // this CTA's loads
       mbar_init(&dy_empty[s], 1);               // the pair's MMA commit, multicast
     }
-    for (int s = 0; s < C::kRawStages; ++s) {
-      mbar_init(&bars.raw_full[s], 1);
-      mbar_init(&bars.raw_empty[s], C::kLoadWarps);
-    }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&code_full[s], 1);
       mbar_init(&code_empty[s], kConvWarps);    // read into registers
-      mbar_init(&ready[s], 2 * (kConvWarps + C::kBlockLoadWarps));   // both CTAs' warps
+      mbar_init(&ready[s], 2 * kConvWarps);     // both CTAs' warps
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
@@ -591,16 +614,18 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
   };
 
   // The single-thread roles hand registers to the epilogue: 7 warpgroups of 72
-  // a thread at launch = 40 + 4 x 72 + 2 x 88.
+  // a thread at launch = 40 + 4 x 72 + 2 x 88.  (With three planes there are 5 of
+  // 96.)
   if (warp < C::kConv0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if ((warp == 0 && kTmaDy) || warp == 2) {
+    if constexpr (PLANES == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 || warp == 2) {
       if (lane == 0) {
         // ----------------------------------- TMA: dy (warp 0), codes + exponents
         const bool is_dy = warp == 0;
-        uint64_t* full = !is_dy ? code_full : MODE == kTma ? dy_full : bars.raw_full;
-        uint64_t* empty = !is_dy ? code_empty : MODE == kTma ? dy_empty : bars.raw_empty;
-        const uint32_t stages = !is_dy ? kSlots : MODE == kTma ? kDyStages : C::kRawStages;
+        uint64_t* full = is_dy ? dy_full : code_full;
+        uint64_t* empty = is_dy ? dy_empty : code_empty;
+        const uint32_t stages = is_dy ? kDyStages : kSlots;
+        if (is_dy) griddep_wait();   // k_wgrad_dy's planes
         uint32_t c = 0, s = 0, phase = 0;
         bool ok = true;
         Unit t;
@@ -611,14 +636,11 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
               ok = false;
               break;
             }
-            if (is_dy && MODE == kTma32) {
-              mbar_arrive_expect_tx(&full[s], kRawBytes);
-              tma_load_2d(sm_raw + s * kRawBytes, &tm_dy, &full[s], o, t.begin + k0);
-            } else if (is_dy) {
-              mbar_arrive_expect_tx(&full[s], kDyBytes);
-              uint8_t* d = sm_dy + s * kDyBytes;
-              tma_load_2d(d, &tm_dy, &full[s], o, t.begin + k0);
-              tma_load_2d(d + kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0);
+            if (is_dy) {
+              mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+              uint8_t* d = sm_dy + s * C::kStageBytes;
+              tma_load_3d(d, &tm_dy, &full[s], o, t.begin + k0, 0);
+              tma_load_3d(d + PLANES * kAtomBytes, &tm_dy, &full[s], o + 64, t.begin + k0, 0);
             } else {
               mbar_arrive_expect_tx(&full[s], kCodeBytes + kExpBytes);
               tma_load_2d(sm_codes + s * kCodeBytes, &tm_codes, &full[s], i, t.begin + k0);
@@ -657,14 +679,14 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
             tc_fence_after();
             const uint32_t b_addr = smem_u32(sm_x + b * kSlotBytes);
 #pragma unroll
-            for (int p = C::kPlanes - 1; p >= 0; --p) {
-              const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kDyBytes);
+            for (int p = PLANES - 1; p >= 0; --p) {
+              const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kAtomBytes);
 #pragma unroll
               for (int ks = 0; ks < kBK / 16; ++ks)
                 tc_mma_bf16_pair(d + (p > 0 ? 256u : 0u),
-                                 smem_desc_sw128(a_addr + ks * 2048, kAtomBytes, 1024),
+                                 smem_desc_sw128(a_addr + ks * 2048, PLANES * kAtomBytes, 1024),
                                  smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
-                                 k0 == 0 && (p == 0 || p == C::kPlanes - 1) && ks == 0 ? 0u : 1u);
+                                 k0 == 0 && (p == 0 || p == PLANES - 1) && ks == 0 ? 0u : 1u);
             }
             tc_commit_pair_multicast(&dy_empty[s], 0x3);
             if (++s == kDyStages) s = 0;
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
         if (end) break;
       }
     }
-  } else if (warp < C::kLoad0) {
+  } else if (warp < C::kEpi0) {
     // ---------------------------------------------------------- converters
     // Group g decodes the blocks c = g, g + kSlots, ... into slot g, so that the
     // latencies of one block's chain (wait, read, decode, write, fence, arrive)
@@ -770,15 +792,17 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ (b << 4)),
                        "r"(v[b][0]), "r"(v[b][1]), "r"(v[b][2]), "r"(v[b][3])
                        : "memory");
-        if constexpr (MODE == kTma) {
-          const uint32_t ds = c % kDyStages;
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_full[ds], c / kDyStages & 1u, abort_flag,
-                                                         a.status, a.timeout_ns));
-          if (!ok) break;
-          if (out) {   // its dy too, this thread's half of the row
-            uint4* p = reinterpret_cast<uint4*>(sm_dy + ds * kDyBytes + j * kAtomBytes + r * 128);
+        const uint32_t ds = c % kDyStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_full[ds], c / kDyStages & 1u, abort_flag,
+                                                       a.status, a.timeout_ns));
+        if (!ok) break;
+        if (out) {   // its dy too, this thread's half of the row
 #pragma unroll
-            for (int z = 0; z < 8; ++z) p[z] = make_uint4(0, 0, 0, 0);
+          for (int p = 0; p < PLANES; ++p) {
+            uint4* y = reinterpret_cast<uint4*>(sm_dy + ds * C::kStageBytes +
+                                                (j * PLANES + p) * kAtomBytes + r * 128);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) y[z] = make_uint4(0, 0, 0, 0);
           }
         }
         // The readers are the tensor cores, which see this CTA's shared memory as
@@ -790,149 +814,9 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       }
       c0 += blocks;
     }
-  } else if (warp < C::kEpi0) {
-    // ------------------------------------------------------------- loaders
-    // dy through registers, written where TMA puts a bf16 tile.  Rows of the next
-    // expert and columns past the end are zeros.
-    if constexpr (MODE == kLoad16) {
-      // Two groups of four warps take the blocks in turn.  A thread takes 16 columns
-      // of every 16th row: the 16-byte pieces that hold them, its next block's
-      // fetched ahead, shifted into place (8192 tokens, 4097 x 4096: 417 us, 500 with
-      // one group; 199 for the 4096 that TMA fetches).
-      static_assert(kDyStages == 2 && kSlots == 2, "a stage and a slot for each group");
-      constexpr int kRows = 4;   // of a thread
-      const int tid = threadIdx.x - 32 * C::kLoad0;
-      const int lg = tid >> 7, tr = (tid & 127) >> 3, j = tid & 7;
-      const uint32_t ready_g = mapa_shared(&ready[lg], 0);
-      uint32_t c0 = 0;   // blocks before this unit
-      bool ok = true;
-      Unit t;
-      while (ok && take(t, true)) {
-        const int o = t.o0 + static_cast<int>(rank) * 128 + 16 * j;
-        const int cols = min(a.out - o, kCols);
-        uint32_t w[kRows][12];   // 16 columns at any alignment
-        uint32_t by[kRows];
-        const auto fetch = [&](uint32_t k) {   // block k of the unit
-#pragma unroll
-          for (int q = 0; q < kRows; ++q) {
-            const int r = static_cast<int>(k) * kBK + tr + 16 * q;
-            const uintptr_t p = reinterpret_cast<uintptr_t>(a.dy) +
-                                2 * (static_cast<int64_t>(t.begin + r) * a.dy_stride + o);
-            const int n = r < t.n ? cols : 0;
-            by[q] = static_cast<uint32_t>(p) & 15u;
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-              uint4 u = make_uint4(0, 0, 0, 0);
-              if (n > 0 && 16 * x < static_cast<int>(by[q]) + 2 * n)
-                u = reinterpret_cast<const uint4*>(p - by[q])[x];
-              w[q][4 * x] = u.x; w[q][4 * x + 1] = u.y; w[q][4 * x + 2] = u.z; w[q][4 * x + 3] = u.w;
-            }
-          }
-        };
-        const uint32_t blocks = static_cast<uint32_t>((t.n + kBK - 1) / kBK);
-        uint32_t k = (lg - c0) % 2u;
-        if (k < blocks) fetch(k);
-        for (; k < blocks; k += 2) {
-          const uint32_t turn = (c0 + k) / 2;   // this group's blocks before
-#pragma unroll
-          for (int q = 0; q < kRows; ++q) {
-            shift_words<__nv_bfloat16, 8>(w[q], by[q]);
-            if (cols < kCols) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                w[q][x] = 2 * x + 1 < cols ? w[q][x] : 2 * x < cols ? w[q][x] & 0xFFFFu : 0u;
-            }
-          }
-          if (turn > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&dy_empty[lg], (turn & 1u) ^ 1u, abort_flag,
-                                                           a.status, a.timeout_ns));
-            if (!ok) break;
-          }
-#pragma unroll
-          for (int q = 0; q < kRows; ++q) {
-            const int r = tr + 16 * q;
-            uint8_t* at = sm_dy + lg * C::kStageBytes + (j >> 2) * kAtomBytes + r * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<uint4*>(at + (((2 * (j & 3) + h) ^ (r & 7)) << 4)) =
-                  make_uint4(w[q][4 * h], w[q][4 * h + 1], w[q][4 * h + 2], w[q][4 * h + 3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(ready_g);
-          if (k + 2 < blocks) fetch(k + 2);
-        }
-        c0 += blocks;
-      }
-    } else if constexpr (MODE != kTma) {
-      // fp32: a warp takes a row of 128 columns, four a thread, from memory (a block
-      // ahead) or from TMA's tile, and writes them as planes.
-      const int lw = warp - C::kLoad0;
-      const int col4 = 4 * lane;   // within the CTA's 128 columns
-      const uint32_t ready0 = mapa_shared(&ready[0], 0);
-      uint32_t c = 0;
-      bool ok = true;
-      Unit t;
-      while (ok && take(t, true)) {
-        const int o = t.o0 + static_cast<int>(rank) * 128 + col4;
-        float v[8][4];
-        const auto fetch = [&](int k0) {   // from memory
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = q * C::kLoadWarps + lw;
-            const float* row =
-                static_cast<const float*>(a.dy) + static_cast<int64_t>(t.begin + k0 + r) * a.dy_stride;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[q][k] = k0 + r < t.n && o + k < a.out ? row[o + k] : 0.f;
-          }
-        };
-        if (MODE != kTma32 && t.n > 0) fetch(0);
-        for (int k0 = 0; k0 < t.n; k0 += kBK, ++c) {
-          const uint32_t s = c % kDyStages;
-          uint2 w[8][C::kPlanes];   // split before the stage is free
-          if constexpr (MODE == kTma32) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars.raw_full[c % 2], c / 2 & 1u, abort_flag,
-                                                           a.status, a.timeout_ns));
-            if (!ok) break;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int r = q * C::kLoadWarps + lw;
-              const float4 x = *reinterpret_cast<const float4*>(sm_raw + c % 2 * kRawBytes + r * 512 +
-                                                                lane * 16);
-              const bool in = k0 + r < t.n;
-              const float y[4] = {in ? x.x : 0.f, in ? x.y : 0.f, in ? x.z : 0.f, in ? x.w : 0.f};
-              split4(y, w[q]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.raw_empty[c % 2]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) split4(v[q], w[q]);
-          }
-          if (c >= kDyStages) {
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded(&dy_empty[s], (c / kDyStages & 1u) ^ 1u, abort_flag,
-                                              a.status, a.timeout_ns));
-            if (!ok) break;
-          }
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = q * C::kLoadWarps + lw;
-            uint8_t* at = sm_dy + s * C::kStageBytes + (lane >> 4) * kAtomBytes + r * 128 +
-                          ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
-#pragma unroll
-            for (int p = 0; p < C::kPlanes; ++p) *reinterpret_cast<uint2*>(at + p * kDyBytes) = w[q][p];
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(ready0 + c % kSlots * 8u);
-          if (MODE != kTma32 && k0 + kBK < t.n) fetch(k0 + kBK);
-        }
-      }
-    }
   } else {
     // ------------------------------------------------------------ epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if constexpr (PLANES == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // A warp drains 32 rows x 128 columns in four pieces of 16 x 64: a thread
     // gets 16 consecutive columns of two rows, four threads 64 columns, so that
     // a store of the warp fills eight whole 128-byte lines.
@@ -964,11 +848,11 @@ __global__ void __launch_bounds__(Cfg<MODE>::kThreads, 1)
       if (a.g.ptrs != nullptr && reinterpret_cast<uintptr_t>(g) % 16 != 0) {
         if (lane == 0) atomicOr(a.status, kFlagMisaligned);   // left untouched
       } else if (inside && bits % 32 == 0) {
-        drain_inside<C::kPlanes, true>(src, a.g, p, row_bytes, t.n == 0, add);
+        drain_inside<PLANES, true>(src, a.g, p, row_bytes, t.n == 0, add);
       } else if (inside && (!EDGE || bits % 16 == 0)) {
-        drain_inside<C::kPlanes, false>(src, a.g, p, row_bytes, t.n == 0, add);
+        drain_inside<PLANES, false>(src, a.g, p, row_bytes, t.n == 0, add);
       } else if constexpr (EDGE) {
-        drain_any<C::kPlanes>(src, g + o * row_bytes + static_cast<int64_t>(i) * esz, a.g.stride,
+        drain_any<PLANES>(src, g + o * row_bytes + static_cast<int64_t>(i) * esz, a.g.stride,
                               a.g.rows - o, a.g.cols - i, a.g.dtype == MUON_F32, t.n == 0, add);
       }
       if (t.n == 0) continue;
@@ -1041,21 +925,35 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A [rows][cols] operand of element size esz, boxes of box_cols x kBK rows.
-// Columns and rows past the operand's read as 0.
-bool map_rows(CUtensorMap* m, CUtensorMapDataType type, int esz, const void* base, int64_t rows,
-              int64_t cols, int64_t stride, int box_cols, CUtensorMapSwizzle swizzle) {
+// The codes or the exponents of `rows` rows, boxes of kBK rows.  What lies past
+// an operand's columns and rows reads as 0.
+bool map_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_cols,
+               CUtensorMapSwizzle swizzle) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * esz};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), kBK};
   const cuuint32_t es[2] = {1, 1};
-  return encode_fn()(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Planes of dy, boxes of 64 columns x kBK rows of all planes.
+bool map_dy(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t stride, int planes,
+            int64_t plane) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride) * 2,
+                                 static_cast<cuuint64_t>(planes == 1 ? stride : plane) * 2};
+  const cuuint32_t box[3] = {64, kBK, static_cast<cuuint32_t>(planes)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // CTA pairs that fit the current device at once (asked once per device).
-template <DyMode MODE, bool EDGE>
+template <int PLANES, bool EDGE>
 cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];
@@ -1065,7 +963,7 @@ cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   if (dev < kDevices && (*out = known[dev].load()) > 0) return cudaSuccess;
   cfg.gridDim = dim3(2);
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad<MODE, EDGE>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, k_wgrad<PLANES, EDGE>, &cfg);
   if (e != cudaSuccess) return e;
   if (n < 1) return cudaErrorInvalidConfiguration;
   if (dev < kDevices) known[dev].store(n);
@@ -1073,52 +971,58 @@ cudaError_t resident_pairs(cudaLaunchConfig_t& cfg, int* out) {
   return cudaSuccess;
 }
 
-template <DyMode MODE, bool EDGE>
-cudaError_t launch_mode(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
-  using C = Cfg<MODE>;
-  cudaError_t e = cudaFuncSetAttribute(k_wgrad<MODE, EDGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+// dy: planes of bf16, rows on 16-byte boundaries.  staged: k_wgrad_dy, just
+// launched, writes them; the kernel's start overlaps it.
+struct Planes {
+  const void* base;
+  int64_t stride, plane;
+  bool staged;
+};
+
+template <int PLANES, bool EDGE>
+cudaError_t launch_edge(const WgradArgs& a, const Planes& y, const muon_act8_t& x, cudaStream_t st) {
+  using C = Cfg<PLANES>;
+  cudaError_t e = cudaFuncSetAttribute(k_wgrad<PLANES, EDGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
   int pairs = 0;
-  e = resident_pairs<MODE, EDGE>(cfg, &pairs);
+  e = resident_pairs<PLANES, EDGE>(cfg, &pairs);
   if (e != cudaSuccess) return e;
   CUtensorMap dy{}, codes{}, exps{};
   if (a.rows > 0) {
     if (encode_fn() == nullptr) return cudaErrorNotSupported;
     const int64_t blocks = (static_cast<int64_t>(a.in) + 31) / 32;
-    if ((MODE == kTma && !map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.dy, a.rows, a.out,
-                                   a.dy_stride, 64, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        (MODE == kTma32 && !map_rows(&dy, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.dy, a.rows, a.out,
-                                     a.dy_stride, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) ||
-        !map_rows(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, a.rows, a.in, x.code_stride, 128,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_rows(&exps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.exps, a.rows, blocks, x.exp_stride, 16,
-                  CU_TENSOR_MAP_SWIZZLE_NONE))
+    if (!map_dy(&dy, y.base, a.rows, a.out, y.stride, PLANES, y.plane) ||
+        !map_bytes(&codes, x.codes, a.rows, a.in, x.code_stride, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_bytes(&exps, x.exps, a.rows, blocks, x.exp_stride, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
       return cudaErrorInvalidValue;
   }
+  cfg.numAttrs = y.staged ? 2 : 1;
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min(a.units, pairs)));
-  return cudaLaunchKernelEx(&cfg, k_wgrad<MODE, EDGE>, dy, codes, exps, a);
+  return cudaLaunchKernelEx(&cfg, k_wgrad<PLANES, EDGE>, dy, codes, exps, a);
 }
 
-template <DyMode MODE>
-cudaError_t launch(const WgradArgs& a, const muon_act8_t& x, cudaStream_t st) {
+template <int PLANES>
+cudaError_t launch(const WgradArgs& a, const Planes& y, const muon_act8_t& x, cudaStream_t st) {
   // pointers in a device array are on 16-byte boundaries, or their matrix is left alone
   const int esz = a.g.dtype == MUON_F32 ? 4 : 2;
   const uint64_t bits = reinterpret_cast<uintptr_t>(a.g.base) |
                         static_cast<uint64_t>((a.g.ptrs != nullptr ? 0 : a.g.batch_stride) * esz) |
                         static_cast<uint64_t>(a.g.stride * esz);
   const bool edge = a.g.rows % 32 != 0 || a.g.cols % 128 != 0 || bits % 16 != 0;
-  return edge ? launch_mode<MODE, true>(a, x, st) : launch_mode<MODE, false>(a, x, st);
+  return edge ? launch_edge<PLANES, true>(a, y, x, st) : launch_edge<PLANES, false>(a, y, x, st);
 }
 
 muon_status_t check_sizes(const muon_weight_grad_t* d) {
@@ -1171,7 +1075,8 @@ int chunks_of(int64_t rows, int experts, int slices, int dy_dtype) {
 
 struct Plan {
   int tiles_o, tiles_i, slices, chunks;
-  size_t part_bytes;
+  int pitch;               // of dy's planes in the workspace
+  size_t part_bytes, plane_bytes;   // partial sums; dy's planes behind them
 };
 
 Plan plan_of(const muon_weight_grad_t* d) {
@@ -1182,6 +1087,8 @@ Plan plan_of(const muon_weight_grad_t* d) {
   p.slices = slices_of(tiles, d->rows, d->experts);
   p.chunks = p.slices > 1 || d->g_dtype == MUON_F32 ? chunks_of(d->rows, d->experts, p.slices, d->dy_dtype)
                                                           : 1;
+  p.pitch = (d->out + kCols - 1) / kCols * kCols;
+  p.plane_bytes = static_cast<size_t>(d->rows) * p.pitch * 2 * (d->dy_dtype == MUON_F32 ? 3 : 1);
   p.part_bytes = p.slices > 1 ? static_cast<size_t>(tiles) * p.slices * 256 * 256 * 4 : 0;
   return p;
 }
@@ -1197,7 +1104,8 @@ muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, 
   if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
   const muon_status_t s = check_sizes(d);
   if (s != MUON_OK) return s;
-  *bytes = kHeader + plan_of(d).part_bytes;
+  const Plan p = plan_of(d);
+  *bytes = kHeader + p.part_bytes + p.plane_bytes;
   return MUON_OK;
 }
 
@@ -1222,10 +1130,9 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
       !at_multiple(d->g_base, esize(d->g_dtype)) || !at_multiple(workspace, 256))
     return MUON_ERR_MISALIGNED;
   const Plan p = plan_of(d);
-  if (workspace_bytes < kHeader + p.part_bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < kHeader + p.part_bytes + p.plane_bytes) return MUON_ERR_WORKSPACE_TOO_SMALL;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st) != cudaSuccess) return MUON_ERR_CUDA;
   const Matrices g{d->g_ptrs, d->g_base, d->g_batch_stride, d->g_stride, d->out, x.cols, d->g_dtype,
                    d->accumulate};
   WgradArgs a{};
@@ -1233,8 +1140,6 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
   a.out = d->out;
   a.in = x.cols;
   a.experts = d->experts;
-  a.dy = d->dy;
-  a.dy_stride = d->dy_stride;
   a.offsets = d->offsets;
   a.g = g;
   a.tiles_o = p.tiles_o;
@@ -1251,16 +1156,30 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
     a.g = Matrices{nullptr, parts, part_matrix, part_stride, p.tiles_o * 256, p.tiles_i * 256,
                    MUON_F32, 0};
   const double rows = static_cast<double>(d->rows);
-  prof_begin(kKindWeightGrad, st);
-  cudaError_t e;
-  if (d->dy_dtype == MUON_F32) {
-    e = at_multiple(d->dy, 16) && d->dy_stride % 4 == 0 ? launch<kTma32>(a, x, st)
-                                                        : launch<kLoad32>(a, x, st);
-  } else if (at_multiple(d->dy, 16) && d->dy_stride % 8 == 0) {
-    e = launch<kTma>(a, x, st);
-  } else {
-    e = launch<kLoad16>(a, x, st);
+  const bool f32 = d->dy_dtype == MUON_F32;
+  Planes y{d->dy, d->dy_stride, 0, d->rows > 0 && (f32 || !at_multiple(d->dy, 16) || d->dy_stride % 8 != 0)};
+  if (y.staged) {
+    auto* to = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + kHeader + p.part_bytes);
+    y.base = to;
+    y.stride = p.pitch;
+    y.plane = d->rows * p.pitch;
+    const int64_t items = d->rows * (p.pitch / kCols);
+    if (items > int64_t{0x7FFFFFFF} * 256) return MUON_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>((items + 255) / 256);
+    prof_begin(kKindWeightGrad, st);
+    if (f32)
+      k_wgrad_dy<<<grid, 256, 0, st>>>(static_cast<const float*>(d->dy), d->dy_stride, items, d->out, to,
+                                       p.pitch, y.plane, a.status);
+    else
+      k_wgrad_dy<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(d->dy), d->dy_stride, items, d->out,
+                                       to, p.pitch, y.plane, a.status);
+    prof_end(kKindWeightGrad, st, 0.0, 0.0);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  } else if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st) != cudaSuccess) {
+    return MUON_ERR_CUDA;
   }
+  prof_begin(kKindWeightGrad, st);
+  const cudaError_t e = f32 ? launch<3>(a, y, x, st) : launch<1>(a, y, x, st);
   prof_end(kKindWeightGrad, st, 2.0 * rows * d->out * x.cols,
            rows * (d->out * esize(d->dy_dtype) + x.cols * (1.0 + 1.0 / 32)) +
                static_cast<double>(d->experts) * d->out * x.cols * esize(d->g_dtype) *
