@@ -600,6 +600,35 @@ def test_weight_grad_pointer_array_alignment():
                 within(f64(mats[e]), want[e], wgrad_bound(size, want, offsets, HALF["bf16"])[e])
 
 
+def test_weight_grad_workspace_reused():
+    """One workspace for calls that keep a copy of dy in it (fp32, rows off
+    16-byte boundaries) and calls that do not, back to back on a side stream:
+    each call's status is its own, each result that of a fresh workspace."""
+    offsets, rows, out, inp = [0, 40, 40, 171], 171, 72, 128
+    cases = []
+    for k, (dy, how) in enumerate([("f32", "dense"), ("bf16", "shifted"), ("bf16", "padded"), ("f32", "shifted")]):
+        d, x8, off, _, _ = wgrad_case(20 + k, offsets, rows, out, inp, dy, how)
+        alone = torch.empty(3, out, inp, device=DEV)
+        assert run_wgrad(d, x8, alone, off) == 0
+        cases.append((d, x8, off, alone))
+    ws = m.workspace(m.muon_act8_weight_grad_workspace_size(rows, out, inp, 3, torch.float32, torch.float32))
+    ws.fill_(255)
+    buf = torch.empty(3 * out * inp + 8, device=DEV)
+    bad = [buf[e * out * inp + (e == 1):][: out * inp].view(out, inp) for e in range(3)]   # the second off its step
+    group = m.Group(bad, bad, bad)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for d, x8, off, alone in cases * 3:
+            G = torch.full((3, out, inp), 3.0, device=DEV)
+            m.muon_act8_weight_grad(d, x8, G, ws, offsets=off)
+            assert m.muon_get_status(ws) == (m.MUON_OK, 0)
+            assert torch.equal(G, alone)
+            m.muon_act8_weight_grad(d, x8, group, ws, offsets=off)
+            assert m.muon_get_status(ws) == (m.MUON_OK, m.MUON_FLAG_MISALIGNED)
+    torch.cuda.current_stream().wait_stream(side)
+
+
 def test_step_from_router_to_muon():
     """The operators in one step: counts -> offsets -> expert gradients into a
     group's G, which the optimizer step takes; the dense form in fp32 agrees."""
