@@ -31,11 +31,12 @@ constexpr int kFinThreads = 1024;   // finalize: 32 experts x 32 partial rows at
 constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks
 
 // Tokens of a chunk.  Chunks and the cuts at sequence bounds together make up
-// to 608 blocks, four on each of 152 SMs at once (one block more would be a
-// second wave); with many sequences there are up to 304 beside their cuts.  A
+// to 760 blocks, five on each of 152 SMs at once (one block more would be a
+// second wave; with four on each 131072 x 256 bf16 in 32 sequences take 47 us, so
+// 44); with many sequences there are up to 380 beside their cuts.  A
 // function of the sizes alone, as the order of the sums follows it.
 int chunk_tokens(int64_t tokens, int sequences) {
-  const int64_t most = 608 - (sequences < 304 ? sequences : 304);
+  const int64_t most = 760 - (sequences < 380 ? sequences : 380);
   const int64_t c = tokens / most + 1;
   return static_cast<int>(c < 32 ? 32 : c);
 }
@@ -221,7 +222,7 @@ __device__ __forceinline__ float row_scores(int sigmoid, float (&x)[VPT]) {
 // One chunk of tokens of one sequence per block: sum_t p_te, c_e and the
 // number of valid tokens.
 template <int LANES, int VPT, bool FULL>
-__global__ void __launch_bounds__(kThreads, VPT <= 16 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, VPT <= 16 ? 5 : 2)
     k_balance_forward(const __grid_constant__ BalanceArgs a) {
   constexpr int kGroups = kThreads / LANES;
   constexpr int kCols = LANES * VPT;
