@@ -882,9 +882,14 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
 // [rows][stride] fp32.  Four columns of a row per thread.
 __global__ void __launch_bounds__(256)
     k_wgrad_join(const float* parts, int slices, int64_t slice_stride, int64_t matrix_stride,
-                 int64_t stride, const __grid_constant__ Matrices g) {
+                 int64_t stride, const __grid_constant__ Matrices g, uint32_t* status) {
   const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int o = blockIdx.y, e = blockIdx.z;
+  char* m = matrix_of(g, e);
+  if (g.ptrs != nullptr && reinterpret_cast<uintptr_t>(m) % 16 != 0) {   // left untouched
+    if (threadIdx.x == 0) atomicOr(status, kFlagMisaligned);
+    return;
+  }
   if (i >= g.cols) return;
   const float* p = parts + e * matrix_stride + o * stride + i;
   float v[4] = {};
@@ -892,7 +897,6 @@ __global__ void __launch_bounds__(256)
     const float4 w = *reinterpret_cast<const float4*>(p + s * slice_stride);
     v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
   }
-  char* m = matrix_of(g, e);
   const int64_t at = o * g.stride + i;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -1189,7 +1193,7 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
     prof_begin(kKindWeightGrad, st);
     const dim3 grid((x.cols + 1023) / 1024, d->out, d->experts);
     k_wgrad_join<<<grid, 256, 0, st>>>(parts, p.slices, part_matrix * d->experts, part_matrix,
-                                       part_stride, g);
+                                       part_stride, g, a.status);
     prof_end(kKindWeightGrad, st, 0.0, 0.0);
     if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
   }

@@ -600,6 +600,26 @@ def test_weight_grad_pointer_array_alignment():
                 within(f64(mats[e]), want[e], wgrad_bound(size, want, offsets, HALF["bf16"])[e])
 
 
+def test_weight_grad_pointer_array_alignment_in_slices():
+    """The same where the tokens of a tile are cut into slices."""
+    rows, out, inp = 4096, 64, 128
+    d, x8, off, ds, xs = wgrad_case(9, [0, rows], rows, out, inp, "bf16", "dense")
+    want, size = R.weight_grads(ds, xs, [0, rows])
+    need = m.muon_act8_weight_grad_workspace_size(rows, out, inp, 1)
+    assert need > 4 * 256 * 256 * 4   # slices leave partial sums
+    buf = torch.empty(out * inp + 16, dtype=torch.bfloat16, device=DEV)
+    for lead, flag in ((8, 0), (1, m.MUON_FLAG_MISALIGNED)):
+        buf.fill_(7.0)
+        mats = [buf[lead:][: out * inp].view(out, inp)]
+        ws = m.workspace(need)
+        m.muon_act8_weight_grad(d, x8, m.Group(mats, mats, mats), ws, offsets=off)
+        assert m.muon_get_status(ws) == (m.MUON_OK, flag)
+        if flag:
+            assert (buf == 7.0).all()
+        else:
+            within(f64(mats[0]), want[0], wgrad_bound(size, want, [0, rows], HALF["bf16"])[0])
+
+
 def test_weight_grad_workspace_reused():
     """One workspace for calls that keep a copy of dy in it (fp32, rows off
     16-byte boundaries) and calls that do not, back to back on a side stream:
