@@ -584,6 +584,8 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  griddep_launch_dependents();   // k_wgrad_join, which waits for this grid's end
+
   // One warp works out the units, a batch at a time, ahead of the other roles,
   // which take them in the same order and number the blocks of 64 tokens c = 0,
   // 1, ... since the start.
@@ -885,6 +887,7 @@ __global__ void __launch_bounds__(256)
                  int64_t stride, const __grid_constant__ Matrices g, uint32_t* status) {
   const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int o = blockIdx.y, e = blockIdx.z;
+  griddep_wait();   // k_wgrad's end
   char* m = matrix_of(g, e);
   if (g.ptrs != nullptr && reinterpret_cast<uintptr_t>(m) % 16 != 0) {   // left untouched
     if (threadIdx.x == 0) atomicOr(status, kFlagMisaligned);
@@ -893,6 +896,7 @@ __global__ void __launch_bounds__(256)
   if (i >= g.cols) return;
   const float* p = parts + e * matrix_stride + o * stride + i;
   float v[4] = {};
+#pragma unroll 4
   for (int s = 0; s < slices; ++s) {
     const float4 w = *reinterpret_cast<const float4*>(p + s * slice_stride);
     v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
@@ -1192,10 +1196,19 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
   if (p.slices > 1) {
     prof_begin(kKindWeightGrad, st);
     const dim3 grid((x.cols + 1023) / 1024, d->out, d->experts);
-    k_wgrad_join<<<grid, 256, 0, st>>>(parts, p.slices, part_matrix * d->experts, part_matrix,
-                                       part_stride, g, a.status);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_wgrad_join, static_cast<const float*>(parts), p.slices,
+                                             part_matrix * d->experts, part_matrix, part_stride, g, a.status);
     prof_end(kKindWeightGrad, st, 0.0, 0.0);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    if (e != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
 }
