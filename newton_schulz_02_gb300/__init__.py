@@ -510,18 +510,24 @@ def _rows2d(t: torch.Tensor, what: str, shape=None) -> int:
         raise ValueError(f"{what} needs the shape {tuple(shape)}, not {tuple(got)}")
     if len(got) != 2:
         raise ValueError(f"{what} needs two dimensions")
-    if got[0] <= 1 and (got[1] <= 1 or got[0] == 0 or t.stride(1) == 1):
-        return got[1]   # the stride of no row or of the only one is never used; it may be anything
-    rs, cs = t.stride()
-    if cs != 1 and got[1] > 1:
+    return _row_stride(*got, *t.stride(), what)
+
+
+def _row_stride(rows: int, cols: int, rs: int, cs: int, what: str) -> int:
+    if cs == 1 and rows > 1:
+        return rs
+    if rows <= 1 and (cols <= 1 or rows == 0 or cs == 1):
+        return cols   # the stride of no row or of the only one is never used; it may be anything
+    if cs != 1 and cols > 1:
         raise ValueError(f"{what} needs unit column stride")
     return rs
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in _DT:
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{what} must be bfloat16 or float32, not {t.dtype}")
-    return _DT[t.dtype]
+    return dt
 
 
 def _vector(t: torch.Tensor, what: str, dtype: torch.dtype, numel: int) -> int:
@@ -620,8 +626,9 @@ class Act8:
         self = cls.__new__(cls)
         blocks = (cols + 31) // 32
         cs, es = blocks * 32, (blocks + 15) // 16 * 16
-        # one piece of memory; every exponent row starts on a 16-byte boundary
-        self._memory = torch.empty(rows * (cs + es), dtype=torch.int8, device=device)
+        # one piece of memory, without a tensor around it (half the time of a call);
+        # every exponent row starts on a 16-byte boundary
+        self._memory = torch.UntypedStorage(rows * (cs + es), device=device)
         self._codes = self._exps = None
         self.shape = (rows, int(cols))
         base = self._memory.data_ptr()
@@ -632,16 +639,18 @@ class Act8:
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            n = self.shape[0] * self.c.code_stride
-            self._codes = self._memory[:n].view(self.shape[0], self.c.code_stride)
+            self._codes = self._view(torch.int8, 0, self.c.code_stride)
         return self._codes
 
     @property
     def exps(self) -> torch.Tensor:
         if self._exps is None:
-            n = self.shape[0] * self.c.code_stride
-            self._exps = self._memory[n:].view(torch.uint8).view(self.shape[0], self.c.exp_stride)
+            self._exps = self._view(torch.uint8, self.shape[0] * self.c.code_stride, self.c.exp_stride)
         return self._exps
+
+    def _view(self, dtype: torch.dtype, offset: int, stride: int) -> torch.Tensor:
+        t = torch.empty(0, dtype=dtype, device=self._memory.device)
+        return t.set_(self._memory, offset, (self.shape[0], stride), (stride, 1))
 
 
 act8_empty = Act8.empty
@@ -660,8 +669,8 @@ def muon_act8_unpack(a: Act8, out: torch.Tensor, stream=None) -> None:
            "muon_act8_unpack")
 
 
-def _one_dtype(first: torch.Tensor, *others: torch.Tensor) -> int:
-    if any(t.dtype != first.dtype for t in others):
+def _one_dtype(first: torch.Tensor, second: torch.Tensor, third: torch.Tensor) -> int:
+    if second.dtype != first.dtype or third.dtype != first.dtype:
         raise ValueError("the tensors need one dtype")
     return _dtype(first, "the tensors")
 
@@ -714,10 +723,12 @@ def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
         experts, shape, gs, gdt = G.c.batch, (v.rows, v.cols), v.row_stride, G.c.g_dtype
         ptrs, base, bs = G.c.g_ptrs, None, 0
     else:
-        g3 = G if G.dim() == 3 else G.unsqueeze(0)
-        experts, shape, gdt = g3.shape[0], tuple(g3.shape[1:]), _dtype(G, "G")
-        gs = _rows2d(g3[0], "G")
-        ptrs, base, bs = None, G.data_ptr(), g3.stride(0)
+        if G.dim() not in (2, 3):
+            raise ValueError("G needs two or three dimensions")
+        experts, bs = (G.shape[0], G.stride(0)) if G.dim() == 3 else (1, 0)
+        shape, gdt = tuple(G.shape[-2:]), _dtype(G, "G")
+        gs = _row_stride(*shape, *G.stride()[-2:], "G")
+        ptrs, base = None, G.data_ptr()
     if shape != (out, inp):
         raise ValueError(f"G needs matrices of {out} x {inp}, not {shape[0]} x {shape[1]}")
     op = None if offsets is None else _vector(offsets, "offsets", torch.int32, experts + 1)
