@@ -510,12 +510,13 @@ def _rows2d(t: torch.Tensor, what: str, shape=None) -> int:
         raise ValueError(f"{what} needs the shape {tuple(shape)}, not {tuple(got)}")
     if len(got) != 2:
         raise ValueError(f"{what} needs two dimensions")
-    return _row_stride(*got, *t.stride(), what)
+    rs, cs = t.stride()
+    if cs == 1 and got[0] > 1:
+        return rs
+    return _row_stride(got[0], got[1], rs, cs, what)
 
 
 def _row_stride(rows: int, cols: int, rs: int, cs: int, what: str) -> int:
-    if cs == 1 and rows > 1:
-        return rs
     if rows <= 1 and (cols <= 1 or rows == 0 or cs == 1):
         return cols   # the stride of no row or of the only one is never used; it may be anything
     if cs != 1 and cols > 1:
