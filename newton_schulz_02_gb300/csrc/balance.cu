@@ -27,8 +27,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxExperts = 1024;
-constexpr int kFinThreads = 1024;   // finalize: 32 experts x 32 partial rows at a time
-constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks
+constexpr int kFinWide = 1024, kFinNarrow = 256;   // threads of a finalize block
+constexpr int kTotalThreads = 1024;
+constexpr int kTotalItems = 4096;   // more chunks than these are counted once, not by every block
+constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks, counts of the batch
 
 // Tokens of a chunk.  Chunks and the cuts at sequence bounds together make up
 // to 760 blocks, five on each of 152 SMs at once (one block more would be a
@@ -70,6 +72,8 @@ struct BalanceArgs {
   float* lossp;               // [sequences * expert blocks]
   uint32_t* status;
   int* ticket;
+  int* bounds;                // whether the sequence bounds were out of order
+  int* total;                 // valid tokens of the batch, conditions seen; nullptr: finalize adds pval
   float* loss;
   int32_t* counts;
   float* load;
@@ -309,37 +313,75 @@ __global__ void __launch_bounds__(kThreads, VPT <= 16 ? 5 : 2)
   }
 }
 
+// Valid tokens of the batch and the conditions seen, from every chunk's: with
+// 65536 sequences the pass as a whole takes 0.9 ms, 5.1 where every block of the
+// next kernel adds them up.
+__global__ void __launch_bounds__(kTotalThreads) k_balance_total(const __grid_constant__ BalanceArgs a) {
+  __shared__ int s_n[kTotalThreads / 32], s_bad[kTotalThreads / 32];
+  int n = 0, bad = 0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < a.items; i += kTotalThreads) {
+    n += a.pval[i];
+    bad |= a.pflag[i];
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  bad = __any_sync(0xffffffffu, bad);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+    s_n[warp] = n;
+    s_bad[warp] = bad;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+    bad = __any_sync(0xffffffffu, s_bad[lane]);
+    if (lane == 0) {
+      a.total[0] = n;
+      a.total[1] = bad;
+    }
+  }
+}
+
 // One block per (sequence, 32 experts): adds the chunks' partial rows, writes
-// the load, adds the counts; the last block to finish adds the loss.
-__global__ void __launch_bounds__(kFinThreads) k_balance_finalize(const __grid_constant__ BalanceArgs a) {
-  __shared__ float s_f[32][33];
-  __shared__ int s_i[32][33];
-  __shared__ int s_all[32], s_mine[32], s_bad[32];
+// the load, adds the counts; the last block to finish adds the loss.  Its time
+// is that of a few dependent trips to L2.
+__global__ void __launch_bounds__(kFinWide) k_balance_finalize(const __grid_constant__ BalanceArgs a) {
+  __shared__ float s_f[kFinWide / 32][32];
+  __shared__ int s_i[kFinWide / 32][32];
+  __shared__ int s_all[kFinWide / 32], s_mine[kFinWide / 32], s_bad[kFinWide / 32];
   __shared__ int s_last;
+  const int threads = blockDim.x, warps = threads / 32;
   const int eblocks = (a.experts + 31) / 32;
   const int s = blockIdx.x / eblocks, eb = blockIdx.x % eblocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = seq_at(a, s), end = seq_at(a, s + 1);
   const int i0 = b / a.chunk + s, i1 = b < end ? min((end - 1) / a.chunk + s, a.items - 1) : i0 - 1;
+  int misplaced = 0;   // bounds that do not ascend within [0, tokens]
+  if (blockIdx.x == 0 && a.seq_begin != nullptr)
+    for (int i = threadIdx.x; i <= a.sequences; i += threads) {
+      const int at = a.seq_begin[i];
+      if (at < 0 || at > a.tokens || (i > 0 && at < a.seq_begin[i - 1])) misplaced = 1;
+    }
   griddep_wait();
-  // partial rows: warp w takes every 32nd, a lane one expert
+  // partial rows: warp w takes every `warps`th, a lane one expert
   float p = 0.f;
   int c = 0;
   if (eb * 32 + lane < a.experts) {
     const int64_t at = static_cast<int64_t>(eb) * 32 + lane;
-    for (int i = i0 + warp; i <= i1; i += 32) {
+#pragma unroll 4
+    for (int i = i0 + warp; i <= i1; i += warps) {
       p += a.psum[i * static_cast<int64_t>(a.experts) + at];
       c += a.pcnt[i * static_cast<int64_t>(a.experts) + at];
     }
   }
   // valid tokens of the batch and of this sequence, device conditions
   int all = 0, mine = 0, bad = 0;
-  for (int i = threadIdx.x; i < a.items; i += kFinThreads) {
-    const int n = a.pval[i];
-    all += n;
-    if (i >= i0 && i <= i1) mine += n;
+#pragma unroll 4
+  for (int i = a.total == nullptr ? threadIdx.x : a.items; i < a.items; i += threads) {
+    all += a.pval[i];
     bad |= a.pflag[i];
   }
+  for (int i = i0 + threadIdx.x; i <= i1; i += threads) mine += a.pval[i];
   all = __reduce_add_sync(0xffffffffu, all);
   mine = __reduce_add_sync(0xffffffffu, mine);
   bad = __any_sync(0xffffffffu, bad);
@@ -350,62 +392,59 @@ __global__ void __launch_bounds__(kFinThreads) k_balance_finalize(const __grid_c
     s_mine[warp] = mine;
     s_bad[warp] = bad;
   }
-  __syncthreads();
-  // warp w: expert 32 eb + w
-  const int e = eb * 32 + warp;
-  p = group_sum<32>(s_f[lane][warp]);
-  c = __reduce_add_sync(0xffffffffu, s_i[lane][warp]);
-  all = __reduce_add_sync(0xffffffffu, s_all[lane]);
-  mine = __reduce_add_sync(0xffffffffu, s_mine[lane]);
-  bad = __any_sync(0xffffffffu, s_bad[lane]);
-  float contrib = 0.f;
-  if (e < a.experts) {
-    const float scale = mine == 0 ? 0.f
-                                  : a.coef / static_cast<float>(all) *
-                                        (static_cast<float>(a.experts) /
-                                         (static_cast<float>(a.topk) * static_cast<float>(mine)));
-    const float f = scale * static_cast<float>(c);
-    contrib = f * p;
-    if (lane == 0) {
+  misplaced = __syncthreads_or(misplaced);
+  if (warp == 0) {
+    p = 0.f;
+    c = 0;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
+      p += s_f[w][lane];
+      c += s_i[w][lane];
+    }
+    all = __reduce_add_sync(0xffffffffu, lane < warps ? s_all[lane] : 0);
+    mine = __reduce_add_sync(0xffffffffu, lane < warps ? s_mine[lane] : 0);
+    bad = __any_sync(0xffffffffu, lane < warps ? s_bad[lane] : 0);
+    if (a.total != nullptr) {
+      all = a.total[0];
+      bad = a.total[1];
+    }
+    const int e = eb * 32 + lane;
+    float contrib = 0.f;
+    if (e < a.experts) {
+      const float scale = mine == 0 ? 0.f
+                                    : a.coef / static_cast<float>(all) *
+                                          (static_cast<float>(a.experts) /
+                                           (static_cast<float>(a.topk) * static_cast<float>(mine)));
+      const float f = scale * static_cast<float>(c);
+      contrib = f * p;
       a.load[static_cast<int64_t>(s) * a.experts + e] = f;
       if (c) atomicAdd(a.counts + e, c);
     }
-  }
-  __syncthreads();
-  if (lane == 0) s_f[0][warp] = contrib;
-  __syncthreads();
-  if (warp != 0) {
-    if (gridDim.x == 1) return;
-  } else {
-    contrib = group_sum<32>(s_f[0][lane]);
-  }
-  if (gridDim.x > 1) {
-    if (threadIdx.x == 0) {
+    contrib = group_sum<32>(contrib);
+    if (lane == 0 && gridDim.x == 1) {
+      *a.loss = contrib;
+      *a.status = bad || misplaced ? MUON_FLAG_INDEX : 0u;
+    } else if (lane == 0) {
       a.lossp[blockIdx.x] = contrib;
+      if (blockIdx.x == 0) *a.bounds = misplaced;
       __threadfence();
       s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
     }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    float v = 0.f;
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinThreads) v += __ldcg(a.lossp + i);
-    v = group_sum<32>(v);
-    if (lane == 0) s_f[1][warp] = v;
-    __syncthreads();
-    if (warp != 0) return;
-    contrib = group_sum<32>(s_f[1][lane]);
   }
-  // bounds that do not ascend within [0, tokens]
-  if (a.seq_begin != nullptr)
-    for (int i = lane; i <= a.sequences; i += 32) {
-      const int at = a.seq_begin[i];
-      if (at < 0 || at > a.tokens || (i > 0 && at < a.seq_begin[i - 1])) bad = 1;
-    }
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    *a.loss = contrib;
-    *a.status = bad ? MUON_FLAG_INDEX : 0u;
+  if (gridDim.x == 1) return;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  float v = 0.f;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += threads) v += __ldcg(a.lossp + i);
+  v = group_sum<32>(v);
+  if (lane == 0) s_f[0][warp] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.f;
+    for (int w = 0; w < warps; ++w) v += s_f[0][w];
+    *a.loss = v;
+    *a.status = bad || __ldcg(a.bounds) ? MUON_FLAG_INDEX : 0u;
   }
 }
 
@@ -678,6 +717,8 @@ muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t
   a.lossp = reinterpret_cast<float*>(ws + l.lossp);
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.ticket = reinterpret_cast<int*>(ws) + 1;
+  a.bounds = reinterpret_cast<int*>(ws) + 2;
+  a.total = a.items > kTotalItems ? reinterpret_cast<int*>(ws) + 3 : nullptr;
   a.loss = loss;
   a.counts = counts;
   a.load = load;
@@ -687,13 +728,23 @@ muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t
   prof_end(kKindBalance, st, 0.0,
            rows * (b->experts * esize(b->dtype) + b->topk * b->chosen_bytes));
   if (e != cudaSuccess) return MUON_ERR_CUDA;
-  // a programmatic dependent of the first kernel (it waits for the partial rows)
+  if (a.total != nullptr) {
+    prof_begin(kKindBalance, st);
+    k_balance_total<<<1, kTotalThreads, 0, st>>>(a);
+    prof_end(kKindBalance, st, 0.0, 0.0);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  // a programmatic dependent of the kernel before (it waits for the partial rows)
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(b->sequences) * ((b->experts + 31) / 32));
-  cfg.blockDim = dim3(kFinThreads);
+  // A block with few partial rows is small, so that more of them run beside each
+  // other: 131072 x 64 in 1000 sequences 74 -> 44 us, in 32 sequences 44 -> 42.  A
+  // sequence of many rows wants a warp for each of them: one sequence takes 27 us,
+  // 35 with the small block.
+  cfg.blockDim = dim3(a.items > 64 * b->sequences ? kFinWide : kFinNarrow);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -128,6 +128,21 @@ def test_balance(score, dtype, T, E, K, S, padding, how):
     assert untouched(buf, dl)
 
 
+@pytest.mark.parametrize("T,E,S", [(9000, 20, 5000), (300, 40, 6000), (40000, 8, 64)])
+def test_balance_many_sequences(T, E, S):
+    """Thousands of sequences, most of one token or none; bounds out of order
+    are flagged there too."""
+    x, xs, chosen, begin, mask = balance_case(T, T, E, 3, S, torch.float32, True, "dense")
+    loss, counts, load, dl, flags = run_balance(x, chosen, begin, mask, "softmax", 0.25)
+    ref = R.balance(xs, chosen, begin, mask, "softmax", np.float32(0.25))
+    assert flags == 0 and counts.cpu().numpy().tolist() == ref["counts"].tolist()
+    assert abs(loss.item() - ref["loss"]) <= 512 * U * ref["loss"] + 1e-30
+    within(f64(load), ref["load"], 8 * U * ref["load"])
+    within(f64(dl), ref["grad"], grad_bound(ref, xs, U))
+    begin[S // 2] = T + 7
+    assert run_balance(x, chosen, begin, mask, "softmax", 0.25)[4] == m.MUON_FLAG_INDEX
+
+
 def test_balance_one_sequence_without_bounds_equals_with():
     x, xs, chosen, _, _ = balance_case(3, 500, 48, 4, 1, torch.float32, False, "dense")
     a = run_balance(x, chosen, None, None, "softmax", 0.1)
