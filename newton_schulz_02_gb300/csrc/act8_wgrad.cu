@@ -463,6 +463,23 @@ __device__ __forceinline__ char* matrix_of(const Matrices& g, int m) {
                                       m * g.batch_stride * (g.dtype == MUON_F32 ? 4 : 2));
 }
 
+// 32 rows from o, 128 columns from i of the matrix at g.  p: this lane's first 16
+// columns.  PLANES > 1: both accumulators' sum.
+template <int PLANES, bool EDGE>
+__device__ __forceinline__ void drain_unit(uint32_t src, const Matrices& m, char* g, char* p, int64_t row_bytes,
+                                           int o, int i, bool empty, bool add) {
+  const uint64_t bits = reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes);
+  const bool inside = o + 32 <= m.rows && i + 128 <= m.cols;
+  const int esz = m.dtype == MUON_F32 ? 4 : 2;
+  if (inside && bits % 32 == 0)
+    drain_inside<PLANES, true>(src, m, p, row_bytes, empty, add);
+  else if (inside && (!EDGE || bits % 16 == 0))
+    drain_inside<PLANES, false>(src, m, p, row_bytes, empty, add);
+  else if constexpr (EDGE)
+    drain_any<PLANES>(src, g + o * row_bytes + static_cast<int64_t>(i) * esz, m.stride, m.rows - o, m.cols - i,
+                      m.dtype == MUON_F32, empty, add);
+}
+
 // dy [rows][out] as planes of bf16 [rows][pitch] at `to`, `plane` values apart
 // (pitch: out rounded up to 16; columns past out are 0).  bf16: one plane, the
 // values themselves.  fp32: three, the upper 8 significant bits, the next 8 and
@@ -530,11 +547,12 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   using C = Cfg<PLANES>;
   constexpr int kDyStages = C::kDyStages, kSlots = C::kSlots;
-  // Two accumulators take turns; with three planes one takes the sums of the
-  // upper parts and the other those of the rest.  The tensor core's additions
-  // truncate: apart, the long sum is added to a third as often, and the error of
-  // 32 blocks against 64 bits falls from 6e-6 to 2e-6.
-  constexpr uint32_t kAccs = PLANES == 1 ? 2 : 1;
+  // Two accumulators take turns.  The tensor core's additions truncate, so with
+  // three planes a sum of more than 256 tokens has both: one for the upper parts
+  // and one for the rest.  Apart, the long sum is added to a third as often, and
+  // the error of 32 blocks against 64 bits falls from 6e-6 to 2e-6.  (Few tokens
+  // need that less than the overlap: 16 experts of 50, 6752 x 3760 344 -> 285 us.)
+  const auto both = [](const Unit& t) { return PLANES > 1 && t.n > 256; };
   uint8_t* sm_dy = smem;                                    // swizzled: 1024-byte boundaries
   uint8_t* sm_x = sm_dy + kDyStages * C::kStageBytes;       // decoded, swizzled
   uint8_t* sm_codes = sm_x + kSlots * kSlotBytes;           // swizzled
@@ -661,14 +679,18 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0 && rank == 0) {
         // -------------------------------------------------------- MMA issuer
-        uint32_t c = 0, s = 0, tile = 0;
+        uint32_t c = 0, s = 0;
+        uint32_t turn = 0, phase = 0;   // the next accumulator; whose turn's parity is odd
         bool ok = true;
         Unit t;
         while (ok && take(t, false)) {
           if (t.n == 0) continue;
-          const uint32_t acc = tile % kAccs;
-          if (!mbar_wait_bounded(&tempty[acc], (tile / kAccs & 1u) ^ 1u, abort_flag, a.status,
-                                 a.timeout_ns))
+          const bool two = both(t);
+          const uint32_t acc = two ? 0 : turn;
+          if (!mbar_wait_bounded(&tempty[acc], (phase >> acc & 1u) ^ 1u, abort_flag, a.status,
+                                 a.timeout_ns) ||
+              (two && !mbar_wait_bounded(&tempty[1], (phase >> 1 & 1u) ^ 1u, abort_flag, a.status,
+                                         a.timeout_ns)))
             break;
           tc_fence_after();
           const uint32_t d = tmem_base + acc * 256u;
@@ -685,17 +707,19 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
               const uint32_t a_addr = smem_u32(sm_dy + s * C::kStageBytes + p * kAtomBytes);
 #pragma unroll
               for (int ks = 0; ks < kBK / 16; ++ks)
-                tc_mma_bf16_pair(d + (p > 0 ? 256u : 0u),
+                tc_mma_bf16_pair(d + (p > 0 && two ? 256u : 0u),
                                  smem_desc_sw128(a_addr + ks * 2048, PLANES * kAtomBytes, 1024),
                                  smem_desc_sw128(b_addr + ks * 2048, kAtomBytes, 1024), kIdesc,
-                                 k0 == 0 && (p == 0 || p == PLANES - 1) && ks == 0 ? 0u : 1u);
+                                 k0 == 0 && ((p == 0 && two) || p == PLANES - 1) && ks == 0 ? 0u : 1u);
             }
             tc_commit_pair_multicast(&dy_empty[s], 0x3);
             if (++s == kDyStages) s = 0;
           }
           if (!ok) break;
           tc_commit_pair_multicast(&tfull[acc], 0x3);
-          ++tile;
+          if (two) tc_commit_pair_multicast(&tfull[1], 0x3);
+          phase ^= two ? 3u : 1u << acc;
+          turn ^= two ? 0u : 1u;
         }
         tc_commit_pair_multicast(drain, 0x1);
         wait_drain(drain, 0, a.status, a.timeout_ns);
@@ -825,16 +849,17 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     const int q = warp & 3;                    // tensor-memory lanes 32 q ..
     const int half = (warp - C::kEpi0) >> 2;      // columns 128 half ..
     const uint32_t tempty0 = mapa_shared(&tempty[0], 0);
-    uint32_t tile = 0;
+    uint32_t turn = 0, phase = 0;
     Unit t;
     while (take(t, true)) {
+      const bool two = both(t);
       const bool add = a.g.accumulate || t.add;
       if (t.n == 0 && add) continue;
-      const uint32_t acc = tile % kAccs;
+      const uint32_t acc = two ? 0 : turn;
       if (t.n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tile / kAccs & 1u, abort_flag,
-                                                       a.status, a.timeout_ns)))
-          break;
+        bool ok = mbar_wait_bounded(&tfull[acc], phase >> acc & 1u, abort_flag, a.status, a.timeout_ns);
+        if (two) ok &= mbar_wait_bounded(&tfull[1], phase >> 1 & 1u, abort_flag, a.status, a.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       }
       char* g = matrix_of(a.g, t.m);
@@ -843,25 +868,24 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
       const int o = t.o0 + static_cast<int>(rank) * 128 + q * 32;
       const int i = t.i0 + half * 128;
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q) << 21) + acc * 256u + half * 128u;
-      const uint64_t bits = reinterpret_cast<uintptr_t>(g) | static_cast<uint64_t>(row_bytes);
-      const bool inside = o + 32 <= a.g.rows && i + 128 <= a.g.cols;
       char* p = g + (o + (lane >> 2)) * row_bytes + (i + 16 * (lane & 3)) * esz;
       __syncwarp();   // tcgen05.ld takes the warp together
       if (a.g.ptrs != nullptr && reinterpret_cast<uintptr_t>(g) % 16 != 0) {
         if (lane == 0) atomicOr(a.status, kFlagMisaligned);   // left untouched
-      } else if (inside && bits % 32 == 0) {
-        drain_inside<PLANES, true>(src, a.g, p, row_bytes, t.n == 0, add);
-      } else if (inside && (!EDGE || bits % 16 == 0)) {
-        drain_inside<PLANES, false>(src, a.g, p, row_bytes, t.n == 0, add);
-      } else if constexpr (EDGE) {
-        drain_any<PLANES>(src, g + o * row_bytes + static_cast<int64_t>(i) * esz, a.g.stride,
-                              a.g.rows - o, a.g.cols - i, a.g.dtype == MUON_F32, t.n == 0, add);
+      } else if (two) {
+        drain_unit<PLANES, EDGE>(src, a.g, g, p, row_bytes, o, i, false, add);
+      } else {
+        drain_unit<1, EDGE>(src, a.g, g, p, row_bytes, o, i, t.n == 0, add);
       }
       if (t.n == 0) continue;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8u);
-      ++tile;
+      if (lane == 0) {
+        mbar_arrive_cluster(tempty0 + acc * 8u);
+        if (two) mbar_arrive_cluster(tempty0 + 8u);
+      }
+      phase ^= two ? 3u : 1u << acc;
+      turn ^= two ? 0u : 1u;
     }
   }
 
