@@ -143,6 +143,21 @@ def test_balance_many_sequences(T, E, S):
     assert run_balance(x, chosen, begin, mask, "softmax", 0.25)[4] == m.MUON_FLAG_INDEX
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,K,off", [(352, 4, 2, 2), (1000, 8, 6, 2), (64, 8, 8, 0), (300, 33, 31, 2)])
+def test_balance_every_enabled_expert_taken(score, T, E, K, off):
+    """Tokens that take all experts with a probability: they cannot change the
+    loss, and the gradient is 0, not what is left of a difference."""
+    x = torch.randn(T, E, device=DEV) * 3
+    if off:
+        x[:, 1] = x[:, E - 1] = float("-inf")
+    chosen = torch.topk(x, K).indices.cpu().numpy()
+    loss, counts, load, dl, flags = run_balance(x, chosen, [0, T // 3, T], None, score, 1.0)
+    assert flags == 0 and not dl.any()
+    ref = R.balance(f64(x), chosen, [0, T // 3, T], None, score, 1.0)
+    assert abs(loss.item() - ref["loss"]) <= 512 * U * ref["loss"]
+
+
 def test_balance_one_sequence_without_bounds_equals_with():
     x, xs, chosen, _, _ = balance_case(3, 500, 48, 4, 1, torch.float32, False, "dense")
     a = run_balance(x, chosen, None, None, "softmax", 0.1)
