@@ -679,6 +679,54 @@ def test_weight_grad_workspace_reused():
     torch.cuda.current_stream().wait_stream(side)
 
 
+def test_calls_in_a_graph():
+    """Every operator captured once and replayed on other inputs."""
+    T, E, D, F = 300, 6, 96, 136
+    g = torch.Generator(device=DEV).manual_seed(11)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    logits, x, gate, up, dh = rand(T, E), rand(T, D), rand(T, F), rand(T, F), rand(T, F)
+    chosen = torch.topk(logits, 2).indices
+    begin = torch.tensor([0, 100, T], dtype=torch.int32, device=DEV)
+    offsets = torch.tensor([0, 40, 40, 130, 200, 260, T], dtype=torch.int32, device=DEV)
+    loss, counts, load = rand(1), torch.empty(E, dtype=torch.int32, device=DEV), rand(2, E)
+    outs = [loss, counts, load, rand(T, E), rand(T, F), rand(T, F), rand(T, F), rand(T, D), rand(E, F, D),
+            rand(1, E, D)]
+    x8, g8, u8 = (m.act8_empty(T, n) for n in (D, F, F))
+    wb = m.workspace(m.muon_balance_workspace_size(T, E, 2))
+    size = m.muon_act8_weight_grad_workspace_size
+    wg = m.workspace(size(T, F, D, E, torch.float32, torch.float32))
+    wr = m.workspace(size(T, E, D, 1, torch.float32, torch.float32))
+
+    def calls():
+        b = m.Balance(logits, chosen, begin)
+        m.muon_balance_forward(b, loss, counts, load, wb)
+        m.muon_balance_backward(b, load, outs[3])
+        m.muon_act8_pack(x, x8)
+        m.muon_act8_unpack(x8, outs[7])
+        m.muon_act8_swiglu_forward(gate, up, outs[4], g8, u8)
+        m.muon_act8_swiglu_backward(dh, g8, u8, outs[5], outs[6])
+        m.muon_act8_weight_grad(outs[5], x8, outs[8], wg, offsets=offsets)
+        m.muon_act8_weight_grad(outs[3], x8, outs[9], wr)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(3):
+        for t in (logits, x, gate, up, dh):
+            t.copy_(rand(*t.shape))
+        chosen.copy_(torch.topk(logits, 2).indices)
+        calls()
+        want = [o.clone() for o in outs]
+        for o in outs:
+            o.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert m.muon_get_status(wg) == (m.MUON_OK, 0)
+
+
 def test_step_from_router_to_muon():
     """The operators in one step: counts -> offsets -> expert gradients into a
     group's G, which the optimizer step takes; the dense form in fp32 agrees."""
