@@ -528,13 +528,23 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     dt = _DT.get(t.dtype)
     if dt is None:
         raise ValueError(f"{what} must be bfloat16 or float32, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
     return dt
 
 
 def _vector(t: torch.Tensor, what: str, dtype: torch.dtype, numel: int) -> int:
     if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{what} must be {numel} contiguous {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
     return t.data_ptr()
+
+
+def _memory_of(ws: torch.Tensor) -> int:
+    if not ws.is_cuda:
+        raise ValueError("the workspace must be on the GPU")
+    return ws.data_ptr()
 
 
 class Balance:
@@ -552,6 +562,8 @@ class Balance:
             raise ValueError("chosen must be int32 or int64")
         if chosen.dim() != 2 or chosen.shape[0] != tokens:
             raise ValueError("chosen needs one row of expert numbers for each token")
+        if not chosen.is_cuda:
+            raise ValueError("chosen must be on the GPU")
         topk = chosen.shape[1]
         cs = _rows2d(chosen, "chosen")
         sequences, seq = 1, None
@@ -586,7 +598,7 @@ def muon_balance_forward(b: Balance, loss: torch.Tensor, counts: torch.Tensor,
     _check(load_library().muon_balance_forward(
         ctypes.byref(b.c), _vector(loss, "loss", torch.float32, 1),
         _vector(counts, "counts", torch.int32, experts),
-        _vector(load, "load", torch.float32, b.sequences * experts), ws.data_ptr(), ws.numel(),
+        _vector(load, "load", torch.float32, b.sequences * experts), _memory_of(ws), ws.numel(),
         _stream(stream)), "muon_balance_forward")
 
 
@@ -619,7 +631,7 @@ class Act8:
         self._codes, self._exps, self._memory = codes, exps, None
         self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), _rows2d(codes, "codes"),
                              exps.data_ptr(), _rows2d(exps, "exps"))
-        self.ref = ctypes.byref(self.c)
+        self.ref = ctypes.byref(self.c) if codes.is_cuda and exps.is_cuda else None   # refused by every call
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Act8":
@@ -634,7 +646,8 @@ class Act8:
         self.shape = (rows, int(cols))
         base = self._memory.data_ptr()
         self.c = muon_act8_t(rows, int(cols), base, cs, base + rows * cs, es)
-        self.ref = ctypes.byref(self.c)
+        kind = device.type if isinstance(device, torch.device) else torch.device(device).type
+        self.ref = ctypes.byref(self.c) if kind == "cuda" else None
         return self
 
     @property
@@ -690,6 +703,8 @@ def muon_act8_swiglu_backward(dh: torch.Tensor, gate8: Act8, up8: Act8, dgate: t
                               dup: torch.Tensor, h8: Optional[Act8] = None, stream=None) -> None:
     """Gradients of gate and up; h8, if given, receives silu(gate) * up."""
     dt, s = _one_dtype(dh, dgate, dup), gate8.shape
+    if h8 is not None and h8.ref is None:
+        raise ValueError("h8 must be on the GPU")
     _check(load_library().muon_act8_swiglu_backward(
         dh.data_ptr(), _rows2d(dh, "dh", s), dt, gate8.ref, up8.ref,
         dgate.data_ptr(), _rows2d(dgate, "dgate", s), dup.data_ptr(), _rows2d(dup, "dup", s),
@@ -717,6 +732,8 @@ def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
     matrices receive the gradients.  offsets: int32 [experts + 1] on the
     device; None = all rows belong to the one expert."""
     rows, inp = x8.shape
+    if x8.ref is None:
+        raise ValueError("the checkpoint must be on the GPU")
     out = dy.shape[1] if dy.dim() == 2 else 0
     ds = _rows2d(dy, "dy", (rows, out))
     if isinstance(G, Group):
@@ -735,5 +752,5 @@ def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
     op = None if offsets is None else _vector(offsets, "offsets", torch.int32, experts + 1)
     d = muon_weight_grad_t(rows, out, experts, dy.data_ptr(), _dtype(dy, "dy"), ds, x8.c, op, ptrs,
                            base, bs, gs, gdt, int(bool(accumulate)))
-    _check(load_library().muon_act8_weight_grad(ctypes.byref(d), ws.data_ptr(), ws.numel(),
+    _check(load_library().muon_act8_weight_grad(ctypes.byref(d), _memory_of(ws), ws.numel(),
                                                 _stream(stream)), "muon_act8_weight_grad")

@@ -188,3 +188,20 @@ def test_binding_refusals(lib):
     with pytest.raises(ValueError):
         m.muon_act8_weight_grad(z(4, 8), a, z(2, 8, 70), ws, stream=0,
                                 offsets=z(2, dtype=torch.int32))
+
+
+def test_binding_refuses_host_memory(lib):
+    """Tensors of the CPU, right in everything else (nothing is enqueued)."""
+    z = torch.zeros
+    with pytest.raises(ValueError, match="GPU"):
+        m.Balance(z(4, 8), z(4, 2, dtype=torch.int64))
+    a = m.act8_empty(4, 70, device="cpu")
+    with pytest.raises(ValueError, match="GPU"):
+        m.muon_act8_pack(z(4, 70), a, stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        m.muon_act8_unpack(a, z(4, 70), stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        m.muon_act8_swiglu_forward(z(4, 70), z(4, 70), z(4, 70), a, a, stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        m.muon_act8_weight_grad(z(4, 8), a, z(1, 8, 70), z(512, dtype=torch.uint8), stream=0)
+    assert a.ref is None and m.Act8(a.codes, a.exps, 70).ref is None   # a call takes it as a missing argument
