@@ -104,12 +104,13 @@ struct Cfg {
   struct Shared {
     uint64_t dy_full[kDyStages], dy_empty[kDyStages];     // loads landed; MMAs on the stage done
     uint64_t code_full[kSlots], code_empty[kSlots];       // loads landed; read into registers
-    uint64_t ready[kSlots];                               // both operands of a block in place
+    uint64_t ready[kSlots];                               // both operands of a block in place, in both CTAs
     uint64_t unit_full[2], unit_empty[2];                 // a batch of units announced; taken
     uint64_t tfull[2], tempty[2];                         // accumulator summed; drained
     uint64_t drain;
     uint32_t tmem_slot;
     int abort;
+    uint32_t notes[kSlots][kConvWarps];                   // what the odd CTA's notices store; not read
     alignas(16) int units[2 * kUnits][8];
   };
   static constexpr size_t kSmem = kDyStages * kStageBytes +
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&code_full[s], 1);
       mbar_init(&code_empty[s], kConvWarps);    // read into registers
-      mbar_init(&ready[s], 2 * kConvWarps);     // both CTAs' warps
+      mbar_init(&ready[s], kConvWarps);         // the even CTA's warps, beside the odd CTA's bytes
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     // leave the whole time to G's stores, and those get slower the closer together
     // they come: 256 experts of 16 tokens 1222 -> 1310 us, so those stay as they are.
     const int turn = PLANES > 1 || a.rows / a.experts > kBK ? r & 7 : 0;
-    const uint32_t ready_g = mapa_shared(&ready[g], 0);
+    const uint32_t ready_g = mapa_shared(&ready[g], 0), note = mapa_shared(&bars.notes[g][wi], 0);
     const uint32_t dst = smem_u32(sm_x) + g * kSlotBytes + j * kAtomBytes + r * 128 + ((r & 7) << 4);
     const uint32_t src = smem_u32(sm_codes) + r * 128 + ((j * 4 ^ (r & 7)) << 4);
     uint32_t c0 = 0;   // blocks before this unit
@@ -836,12 +837,24 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
             for (int z = 0; z < 8; ++z) y[z ^ turn] = make_uint4(0, 0, 0, 0);
           }
         }
-        // The readers are the tensor cores, which see this CTA's shared memory as
-        // the proxy fence left it; a cluster-scope release on the arrival adds
-        // nothing to that and costs the chain of a slot a quarter of its time.
+        // The readers are the tensor cores, by MMAs that the even CTA issues: each
+        // writer's proxy fence, then an arrival that pairs with the issuer's acquire.
+        // From the odd CTA that has to release at cluster scope.  An asynchronous store
+        // comes after what its thread did before it, and its completion on the barrier
+        // is such a release, for which nobody waits.  (An arrival that releases at
+        // cluster scope does make its warp wait: 14336 x 4096 over 8192 tokens 835 us
+        // against 641, 64 experts of 256 tokens 595 against 509; one thread that does
+        // so for the others, 1305 and 858.)
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(ready_g);
+        if (lane == 0) {
+          if (rank != 0)
+            st_async_cluster(note, 0u, ready_g);
+          else if (wi == 0)
+            mbar_arrive_expect_tx(&ready[g], kConvWarps * sizeof(uint32_t));
+          else
+            mbar_arrive(&ready[g]);
+        }
       }
       c0 += blocks;
     }
@@ -901,6 +914,13 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+  // Every notice of the odd CTA has been waited for, unless a role gave up: then one may
+  // still be on its way into this CTA's shared memory, and takes about 1 us.
+  if (rank == 0 && *abort_flag) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000) {
+    }
   }
   // offsets that do not ascend within [0, rows]
   if (a.offsets != nullptr && blockIdx.x == 0)

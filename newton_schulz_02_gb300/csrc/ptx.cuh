@@ -283,6 +283,18 @@ __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar_cluster
                : "memory");
 }
 
+// Store a word into another CTA's shared memory asynchronously, completing 4
+// bytes on an mbarrier of that CTA.  The store comes after what this thread did
+// before it, and the completion is a release at cluster scope: a cluster-scope
+// acquire wait on the barrier sees all of that.  The thread does not wait.
+__device__ __forceinline__ void st_async_cluster(uint32_t cluster_addr, uint32_t v,
+                                                 uint32_t bar_cluster_addr) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   cluster_addr),
+               "r"(v), "r"(bar_cluster_addr)
+               : "memory");
+}
+
 // Same address mapping for a shared::cta address given as a number.
 __device__ __forceinline__ uint32_t mapa_shared_u32(uint32_t saddr, uint32_t rank) {
   uint32_t r;

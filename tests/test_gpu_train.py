@@ -511,6 +511,30 @@ def test_weight_grad_other_experts_rows_do_not_leak(dy):
 
 
 @pytest.mark.parametrize("dy", ["bf16", "f32"])
+def test_weight_grad_both_ctas_operands_arrive(dy):
+    """Many short spans side by side with experts of NaN, on all pairs at once and
+    again and again: each CTA of a pair zeroes its own half of the neighbours' rows
+    and the pair's products read both."""
+    rng = np.random.default_rng(12)
+    offsets = np.concatenate([[0], np.cumsum(rng.integers(1, 130, size=64))]).tolist()
+    rows, out, inp = offsets[-1], 512, 512
+    d, x8, off, ds, xs = wgrad_case(12, offsets, rows, out, inp, dy, "dense")
+    want, size = R.weight_grads(ds, xs, offsets)
+    bound = wgrad_bound(size, want, offsets, U)
+    for e in range(1, 64, 2):
+        d[offsets[e]:offsets[e + 1]] = float("nan")
+        x8.exps[offsets[e]:offsets[e + 1]] = 255
+    first = torch.empty(64, out, inp, device=DEV)
+    assert run_wgrad(d, x8, first, off) == 0
+    within(f64(first[::2]), want[::2], bound[::2])
+    assert torch.isnan(first[1::2]).all()
+    for _ in range(20):
+        G = torch.full_like(first, 3.0)
+        assert run_wgrad(d, x8, G, off) == 0
+        assert torch.equal(G[::2], first[::2])
+
+
+@pytest.mark.parametrize("dy", ["bf16", "f32"])
 def test_weight_grad_nan_block_reaches_its_columns_only(dy):
     offsets, rows, out, inp = [0, 70], 70, 64, 160
     d, x8, off, ds, xs = wgrad_case(2, offsets, rows, out, inp, dy, "dense")

@@ -3,6 +3,7 @@ entry points, struct layouts and workspace sizes (no GPU: every case returns
 before the library touches CUDA)."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -205,3 +206,17 @@ def test_binding_refuses_host_memory(lib):
     with pytest.raises(ValueError, match="GPU"):
         m.muon_act8_weight_grad(z(4, 8), a, z(1, 8, 70), z(512, dtype=torch.uint8), stream=0)
     assert a.ref is None and m.Act8(a.codes, a.exps, 70).ref is None   # a call takes it as a missing argument
+
+
+def test_operands_of_the_other_cta_are_released_at_cluster_scope():
+    """The MMAs that one CTA of a pair issues read the other's shared memory: what
+    tells the issuer's barrier of it has to release at cluster scope (a CTA-scope
+    release does not pair with the issuer's cluster-scope acquire), as an arrival
+    that says so or as the completion of an asynchronous store."""
+    with open(os.path.join(nbuild.CSRC, "act8_wgrad.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    remote = re.findall(r"(\w+)\s*=\s*mapa_shared\(&ready\b", code) + [r"mapa_shared\(&ready"]
+    names = "(?:" + "|".join(remote) + ")"
+    assert not re.search(rf"mbar_arrive_cluster\(\s*{names}", code)
+    assert re.search(rf"(mbar_arrive_release_cluster\(|st_async_cluster\([^;]*,)\s*{names}", code)
+    assert re.search(r"wait_cluster\(&ready\b", code)
