@@ -58,7 +58,7 @@ struct WgradArgs {
   Matrices g;
   int tiles_o, tiles_i;   // 256 x 256 tiles of a matrix
   int slices;             // of a tile's tokens; slice s of expert e goes to matrix s * experts + e
-  int chunks;             // of a slice, one after the other, added up in G
+  int cut;                // sums are cut into chunks, one after the other, added up in G
   int units;              // tiles x slices of all experts
   uint32_t* status;
   uint64_t timeout_ns;
@@ -134,7 +134,7 @@ struct Unit {
   int add;   // to what earlier chunks left there
 };
 
-__device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u, int chunk) {
+__device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u) {
   const int slice = u % a.slices;
   u /= a.slices;
   const int per = a.tiles_o * a.tiles_i;
@@ -148,17 +148,33 @@ __device__ __forceinline__ Unit unit_of(const WgradArgs& a, int u, int chunk) {
   t.i0 = (q / rows) * 256;
   span_of(a, t.e, t.begin, t.n);
   t.m = slice * a.experts + t.e;
-  t.add = chunk > 0;
-  const int parts = a.slices * a.chunks;
-  if (parts > 1) {   // whole blocks, as even as can be
-    const int part = slice * a.chunks + chunk;
+  t.add = 0;
+  if (a.slices > 1) {   // whole blocks, as even as can be
     const int blocks = (t.n + kBK - 1) / kBK;
-    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * part / parts);
-    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / parts);
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * slice / a.slices);
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (slice + 1) / a.slices);
     t.n = min(t.n, b1 * kBK) - b0 * kBK;
     t.begin += b0 * kBK;
   }
   return t;
+}
+
+// Tokens of a chunk of a unit of n tokens whose sums are kept in fp32.  The tensor
+// core's additions truncate, and the error grows with their number (6e-6 of the
+// result for 384); so after 32 blocks (128 additions) at most the accumulator is
+// drained and added, with rounding, to what G holds, which the same pair finds in
+// L2.  The drain runs beside the next chunk.  A matter of each unit's own tokens, as
+// one expert may have most of them (16000 of 16384 on one of 64: 1.9e-5 in one
+// piece, 2.4e-6 cut).  Units of 17 to 32 blocks are cut in two where the drain does
+// run beside the next one (one plane): fp32 sums of so few products are themselves
+// good to 5e-7.  (14336 x 4096 over 8192 tokens: 665 us with fp32 G; bf16
+// G, in one piece, 640.)
+template <int PLANES>
+__device__ __forceinline__ int chunk_of(const WgradArgs& a, int n) {
+  const int blocks = (n + kBK - 1) / kBK;
+  int chunks = 1;
+  if (a.cut) chunks = blocks > 32 ? (blocks + 31) / 32 : blocks > 16 && PLANES == 1 ? 2 : 1;
+  return max((blocks + chunks - 1) / chunks, 1) * kBK;
 }
 
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
@@ -728,11 +744,39 @@ __global__ void __launch_bounds__(Cfg<PLANES>::kThreads, 1)
     } else if (warp == 3) {
       // ------------------------------------------------------------- walker
       const int step = static_cast<int>(gridDim.x >> 1);
-      int local = lane;   // of this pair's chunks
-      for (uint32_t k = 0;; ++k, local += kUnits) {
-        const int64_t u = (blockIdx.x >> 1) + static_cast<int64_t>(local / a.chunks) * step;
+      // Entry j of a batch (lane j's) is a chunk of one of the next 32 units, found in
+      // the running sum of their numbers of chunks; lane kUnits finds where the next
+      // batch starts.  Past the last unit there is an entry without an expert.
+      int first = 0, chunk0 = 0;   // the pair's next unit, and its next chunk
+      for (uint32_t k = 0;; ++k) {
+        const int64_t u = (blockIdx.x >> 1) + static_cast<int64_t>(first + lane) * step;
         Unit t{-1, 0, 0, 0, 0, 0, 0};
-        if (lane < kUnits && u < a.units) t = unit_of(a, static_cast<int>(u), local % a.chunks);
+        if (u < a.units) t = unit_of(a, static_cast<int>(u));
+        int per = chunk_of<PLANES>(a, t.n);
+        int upto = max((t.n + per - 1) / per, 1) - (lane == 0 ? chunk0 : 0);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += v;
+        }
+        int from = 0;   // units whose chunks all come before this entry (at most lane of them)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          const int v = __shfl_sync(0xffffffffu, upto, from + d - 1);
+          if (v <= lane) from += d;
+        }
+        const int before = __shfl_sync(0xffffffffu, upto, max(from - 1, 0));
+        const int chunk = from == 0 ? lane + chunk0 : lane - before;
+        per = __shfl_sync(0xffffffffu, per, from);
+        t.e = __shfl_sync(0xffffffffu, t.e, from);
+        t.o0 = __shfl_sync(0xffffffffu, t.o0, from);
+        t.i0 = __shfl_sync(0xffffffffu, t.i0, from);
+        t.m = __shfl_sync(0xffffffffu, t.m, from);
+        t.begin = __shfl_sync(0xffffffffu, t.begin, from) + chunk * per;
+        t.n = min(__shfl_sync(0xffffffffu, t.n, from) - chunk * per, per);
+        t.add = chunk > 0;
+        first += __shfl_sync(0xffffffffu, from, kUnits);
+        chunk0 = __shfl_sync(0xffffffffu, chunk, kUnits);
         const bool end = __any_sync(0xffffffffu, lane < kUnits && t.e < 0);
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&unit_empty[k % 2], (k / 2 & 1u) ^ 1u, abort_flag,
                                                        a.status, a.timeout_ns)))
@@ -1117,21 +1161,9 @@ int slices_of(int64_t tiles, int64_t rows, int experts) {
   return best;
 }
 
-// Chunks of a slice whose sums are kept in fp32.  The tensor core's additions
-// truncate, and the error grows with their number (6e-6 of the result for 384);
-// so every 32 blocks (128 additions) the accumulator is drained and added, with
-// rounding, to what G holds, which the same pair finds in L2.  The drain runs
-// beside the next chunk.  Sums of 17 to 32 blocks are cut in two where that is
-// so (one plane): fp32 sums of so few products are themselves good to 5e-7.
-// (14336 x 4096 over 8192 tokens: 716 us against 640 us in one piece.)
-int chunks_of(int64_t rows, int experts, int slices, int dy_dtype) {
-  const int64_t blocks = (rows / experts + kBK - 1) / kBK / slices;
-  if (blocks > 32) return static_cast<int>((blocks + 31) / 32);
-  return blocks > 16 && dy_dtype == MUON_BF16 ? 2 : 1;
-}
-
 struct Plan {
-  int tiles_o, tiles_i, slices, chunks;
+  int tiles_o, tiles_i, slices;
+  bool cut;                // fp32 sums, see chunk_of
   int pitch;               // of dy's planes in the workspace
   size_t part_bytes, plane_bytes;   // partial sums; dy's planes behind them
 };
@@ -1142,8 +1174,7 @@ Plan plan_of(const muon_weight_grad_t* d) {
   p.tiles_i = (d->x.cols + 255) / 256;
   const int64_t tiles = static_cast<int64_t>(p.tiles_o) * p.tiles_i * d->experts;
   p.slices = slices_of(tiles, d->rows, d->experts);
-  p.chunks = p.slices > 1 || d->g_dtype == MUON_F32 ? chunks_of(d->rows, d->experts, p.slices, d->dy_dtype)
-                                                          : 1;
+  p.cut = p.slices > 1 || d->g_dtype == MUON_F32;
   p.pitch = (d->out + kCols - 1) / kCols * kCols;
   p.plane_bytes = static_cast<size_t>(d->rows) * p.pitch * 2 * (d->dy_dtype == MUON_F32 ? 3 : 1);
   p.part_bytes = p.slices > 1 ? static_cast<size_t>(tiles) * p.slices * 256 * 256 * 4 : 0;
@@ -1202,7 +1233,7 @@ muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace
   a.tiles_o = p.tiles_o;
   a.tiles_i = p.tiles_i;
   a.slices = p.slices;
-  a.chunks = p.chunks;
+  a.cut = p.cut;
   a.units = p.tiles_o * p.tiles_i * d->experts * p.slices;
   a.status = static_cast<uint32_t*>(workspace);
   a.timeout_ns = wait_timeout_ns();

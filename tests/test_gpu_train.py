@@ -631,6 +631,24 @@ def test_weight_grad_long_fp32_sums_stay_exact():
     assert np.linalg.norm(f64(G)[0] - want) <= 3e-6 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("dy", ["bf16", "f32"])
+@pytest.mark.parametrize("E,out,inp,slices", [(64, 256, 256, False), (6, 256, 512, True)])
+def test_weight_grad_long_fp32_sums_of_one_hot_expert(E, out, inp, slices, dy):
+    """One expert with nearly all of 16384 tokens: the bound on the error's norm is
+    that of one expert alone, whatever the average is; with and without slices."""
+    rows, hot = 16384, E // 2
+    offsets = [0] + np.cumsum([rows - 6 * (E - 1) if e == hot else 6 for e in range(E)]).tolist()
+    d, x8, off, ds, xs = wgrad_case(13, offsets, rows, out, inp, dy, "dense")
+    need = m.muon_act8_weight_grad_workspace_size(rows, out, inp, E, d.dtype, torch.float32)
+    assert (need > rows * out * (6 if dy == "f32" else 2) + 256) == slices
+    G = torch.empty(E, out, inp, device=DEV)
+    assert run_wgrad(d, x8, G, off) == 0
+    want, _ = R.weight_grads(ds, xs, offsets)
+    for e in range(E):
+        err = np.linalg.norm(f64(G[e]) - want[e]) / np.linalg.norm(want[e])
+        assert err <= 3e-6, (e, err)
+
+
 def test_weight_grad_pointer_array_alignment():
     """Pointers of a device array: 16-byte steps are written, others flagged and
     their matrices left alone."""
