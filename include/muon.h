@@ -364,7 +364,8 @@ typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score_t;
  * seq_begin: device [sequences + 1], ascending; sequence s holds the tokens
  * seq_begin[s] .. seq_begin[s+1] - 1, tokens outside every sequence are not
  * valid.  NULL = one sequence of all tokens (sequences must be 1).  Values
- * outside [0, tokens] or out of order set MUON_FLAG_INDEX.
+ * outside [0, tokens] or out of order set MUON_FLAG_INDEX; the outputs then depend
+ * on the inputs alone, but which sequence a token is counted in is unspecified.
  * token_mask: device [tokens] of 0/1 (0 = padding: not read, not counted, no
  * gradient); NULL = all valid.
  * experts <= 1024; tokens < 2^31. */

@@ -364,15 +364,20 @@ __global__ void __launch_bounds__(kFinWide) k_balance_finalize(const __grid_cons
       if (at < 0 || at > a.tokens || (i > 0 && at < a.seq_begin[i - 1])) misplaced = 1;
     }
   griddep_wait();
-  // partial rows: warp w takes every `warps`th, a lane one expert
+  // Partial rows: warp w takes every `warps`th, a lane one expert.  Where bounds are
+  // out of order a sequence may span chunks that no sequence had in the first pass:
+  // they have no valid token, and their rows were not written.
   float p = 0.f;
   int c = 0;
   if (eb * 32 + lane < a.experts) {
     const int64_t at = static_cast<int64_t>(eb) * 32 + lane;
 #pragma unroll 4
     for (int i = i0 + warp; i <= i1; i += warps) {
-      p += a.psum[i * static_cast<int64_t>(a.experts) + at];
-      c += a.pcnt[i * static_cast<int64_t>(a.experts) + at];
+      const bool written = a.pval[i] != 0;
+      const float pi = a.psum[i * static_cast<int64_t>(a.experts) + at];
+      const int ci = a.pcnt[i * static_cast<int64_t>(a.experts) + at];
+      p += written ? pi : 0.f;
+      c += written ? ci : 0;
     }
   }
   // valid tokens of the batch and of this sequence, device conditions

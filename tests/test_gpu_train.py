@@ -215,6 +215,25 @@ def test_balance_nan_propagates_and_bad_indices_are_flagged():
     assert torch.isnan(n[0]).all() and torch.isnan(n[3][5]).all() and not torch.isnan(n[3][6]).any()
 
 
+@pytest.mark.parametrize("begin", [[0, 64, 0, 64], [0, 40, 20, 64], [64, 0], [0, 200, -3, 64, 10], [50, 10, 64, 0]])
+def test_balance_bounds_out_of_order_do_not_read_the_workspace(begin):
+    """What the workspace held before shows in no output, whatever the bounds."""
+    x = torch.randn(64, 16, device=DEV)
+    b = m.Balance(x, torch.topk(x, 2).indices, torch.tensor(begin, dtype=torch.int32, device=DEV))
+    seqs, first = len(begin) - 1, None
+    for fill in (0, 1, 255):
+        loss, counts = torch.empty(1, device=DEV), torch.empty(16, dtype=torch.int32, device=DEV)
+        load, dl = torch.empty(seqs, 16, device=DEV), torch.empty(64, 16, device=DEV)
+        ws = m.workspace(m.muon_balance_workspace_size(64, 16, seqs))
+        ws.fill_(fill)
+        m.muon_balance_forward(b, loss, counts, load, ws)
+        m.muon_balance_backward(b, load, dl)
+        assert m.muon_get_status(ws) == (m.MUON_OK, m.MUON_FLAG_INDEX)
+        got = [loss, counts, load, dl]
+        first = first or got
+        assert all(torch.isfinite(t).all() and torch.equal(t, f) for t, f in zip(got, first))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_balance_accumulate_scale_and_in_place(dtype):
     x, xs, chosen, begin, mask = balance_case(4, 210, 40, 4, 3, DT[dtype], True, "dense")
