@@ -402,7 +402,10 @@ muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t
  * written (0 for tokens that are not valid), or added to when accumulate is 1.
  * load: as muon_balance_forward left it.  dloss: device, 1 fp32, the gradient
  * of the loss itself; NULL = 1.  Reads neither b->chosen nor b->coef; needs
- * no workspace.  dlogits may be the logits themselves (same stride and type). */
+ * no workspace.  dlogits may be the logits themselves (same stride and type).
+ * Where every token takes every expert with a probability the gradient is 0.  With
+ * up to 64 experts and 4 * topk >= experts it comes out as 0; elsewhere it is what
+ * rounding leaves of f_se - sum_j f_sj p_tj, within 2^-17 of either term. */
 muon_status_t muon_balance_backward(const muon_balance_t* b, const float* load,
                                     const float* dloss, void* dlogits, muon_dtype_t ddt,
                                     int64_t dlogits_stride, int accumulate,

@@ -824,8 +824,11 @@ muon_status_t muon_balance_backward(const muon_balance_t* b, const float* load,
   a.lvec = vectorised(load, MUON_F32, b->experts, b->experts);
   a.dvec = vectorised(dlogits, ddt, dlogits_stride, b->experts);
   a.accumulate = accumulate;
-  // Tokens that take a good part of a few experts may take all that are enabled;
-  // elsewhere the search is left out (131072 x 256 fp32: 56 us with it, 52 without).
+  // Tokens that take a good part of a few experts may take all that are enabled, and
+  // get their exact 0.  Elsewhere the search is left out, and a rounding remainder
+  // left: looking for such sequences at every width, by the loads themselves, costs
+  // every batch (131072 x 256: fp32 47.8 -> 49.8 us, bf16 36.9 -> 40.9; 200 experts
+  // bf16 39.3 -> 45.2).
   a.levels = 4 * static_cast<int64_t>(b->topk) >= b->experts;
   prof_begin(kKindBalance, st);
   const cudaError_t e = by_width<Backward>(a, st);

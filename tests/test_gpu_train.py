@@ -158,6 +158,30 @@ def test_balance_every_enabled_expert_taken(score, T, E, K, off):
     assert abs(loss.item() - ref["loss"]) <= 512 * U * ref["loss"]
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,K,on", [(300, 64, 8, 8), (300, 128, 8, 8), (500, 256, 8, 8), (77, 40, 1, 1), (60, 64, 16, 16),
+                                      (200, 257, 3, 3), (90, 512, 300, 300), (41, 1024, 2, 2), (50, 33, 9, 9)])
+def test_balance_every_enabled_expert_taken_among_disabled_ones(score, T, E, K, on):
+    """The same routing among many disabled experts: 0 where the header says so,
+    else what rounding leaves of two equal terms; a sequence beside it that does
+    choose has its gradient."""
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    x = torch.full((T, E), float("-inf"), device=DEV)
+    cols = torch.randperm(E, generator=g, device=DEV)[:on]
+    x[:, cols] = torch.randn(T, on, generator=g, device=DEV) * 3
+    half = T // 2
+    for rest in (x[half:], torch.randn(T - half, E, generator=g, device=DEV) * 3):
+        x[half:] = rest
+        chosen = torch.topk(x, K).indices.cpu().numpy()
+        loss, counts, load, dl, flags = run_balance(x, chosen, [0, half, T], None, score, 1.0)
+        ref = R.balance(f64(x), chosen, [0, half, T], None, score, 1.0)
+        assert flags == 0
+        within(f64(dl), ref["grad"], grad_bound(ref, f64(x), U))
+        assert np.all(np.abs(f64(dl[:half])) <= 2.0 ** -17 * ref["mass"][:half])
+        if E <= 64 and 4 * K >= E:
+            assert not dl[:half].any()
+
+
 def test_balance_one_sequence_without_bounds_equals_with():
     x, xs, chosen, _, _ = balance_case(3, 500, 48, 4, 1, torch.float32, False, "dense")
     a = run_balance(x, chosen, None, None, "softmax", 0.1)
