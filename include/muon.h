@@ -353,7 +353,8 @@ muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
  * constant of the gradient:
  *   dloss/dl_te = coef / N * p_te (f_se - sum_j f_sj p_tj)   [* (1 - sigma(l_te))].
  * A logit of -inf (a disabled expert) has probability 0; a row of them alone
- * has probability 0 everywhere and no gradient. */
+ * has probability 0 everywhere and no gradient, and under sigmoid so has a row
+ * whose largest logit is below -700. */
 typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score_t;
 
 /* logits: device [tokens][experts], row stride logits_stride >= experts.

@@ -224,6 +224,33 @@ def test_balance_rows_without_an_expert(score):
     within(f64(dl), ref["grad"], grad_bound(ref, xs, U))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E,K", [(10, 2), (60, 6), (200, 8), (256, 8), (600, 4)])
+def test_balance_sigmoid_rows_far_below_zero(E, K, dtype):
+    """sigma / sum sigma of rows whose logits are all so low that fp32 has no sigmoid
+    for them, beside ordinary rows, with disabled experts, in place and added."""
+    g = torch.Generator(device=DEV).manual_seed(E)
+    x = torch.randn(120, E, generator=g, device=DEV) * 2
+    for r, shift in ((3, -25.0), (7, -60.0), (8, -90.0), (31, -150.0), (64, -500.0), (65, -690.0), (100, -100.0)):
+        x[r] += shift
+    x[8, 1::2] = float("-inf")
+    x[9] = float("-inf")
+    x[100, 0] = 5.0            # one ordinary logit among low ones
+    x = x.to(DT[dtype])
+    chosen = torch.topk(x.float(), K).indices.cpu().numpy()
+    loss, counts, load, dl, flags = run_balance(x, chosen, [0, 50, 120], None, "sigmoid", 1.0)
+    ref = R.balance(f64(x), chosen, [0, 50, 120], None, "sigmoid", 1.0)
+    assert flags == 0 and abs(loss.item() - ref["loss"]) <= 512 * U * ref["loss"]
+    within(f64(dl), ref["grad"], grad_bound(ref, f64(x), HALF[dtype]))
+    assert (dl[[7, 8, 31, 64, 65]] != 0).any(dim=1).all() and not dl[9].any()
+    mine = x.clone()
+    assert torch.equal(run_balance(mine, chosen, [0, 50, 120], None, "sigmoid", 1.0, dl=mine)[3], dl)
+    start = torch.randn(120, E, generator=g, device=DEV)
+    got = run_balance(x, chosen, [0, 50, 120], None, "sigmoid", 1.0, dl=start.clone(), acc=True)[3]
+    total = f64(start) + ref["grad"]
+    within(f64(got), total, grad_bound(ref, f64(x), U) + U * np.abs(total) * 1.01)
+
+
 def test_balance_nan_propagates_and_bad_indices_are_flagged():
     x = torch.randn(64, 16, device=DEV)
     chosen = torch.topk(x, 2).indices.cpu().numpy()
