@@ -614,9 +614,10 @@ def muon_balance_backward(b: Balance, load: torch.Tensor, dlogits: torch.Tensor,
 
 
 class Act8:
-    """An activation [rows, cols] held in 8 bits: codes (int8, [rows, >= cols],
-    row stride a multiple of 32) and exps (uint8, one biased exponent for each
-    32 columns of a row, row stride a multiple of 16)."""
+    """An activation [rows, cols] held in 8 bits: codes (int8, [rows, cols rounded
+    up to 32 or more], row stride a multiple of 32; whole blocks are written) and
+    exps (uint8, one biased exponent for each 32 columns of a row, row stride a
+    multiple of 16)."""
 
     __slots__ = ("shape", "c", "ref", "_codes", "_exps", "_memory")
 
@@ -624,9 +625,11 @@ class Act8:
         if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
             raise ValueError("codes are int8, exps uint8")
         rows = codes.shape[0]
+        blocks = (int(cols) + 31) // 32
         if codes.dim() != 2 or exps.dim() != 2 or exps.shape[0] != rows or \
-                codes.shape[1] < cols or exps.shape[1] * 32 < cols:
-            raise ValueError("codes [rows, >= cols] and exps [rows, >= cols / 32] are needed")
+                codes.shape[1] < 32 * blocks or exps.shape[1] < blocks:
+            raise ValueError(f"codes [rows, >= {32 * blocks}] (whole blocks of 32 columns) and exps "
+                             f"[rows, >= {blocks}] are needed")
         self.shape = (rows, int(cols))
         self._codes, self._exps, self._memory = codes, exps, None
         self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), _rows2d(codes, "codes"),

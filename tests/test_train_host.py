@@ -191,6 +191,19 @@ def test_binding_refusals(lib):
                                 offsets=z(2, dtype=torch.int32))
 
 
+def test_checkpoint_needs_whole_blocks(lib):
+    """A pass writes whole blocks of 32 codes: a view that ends inside one would have
+    its neighbours overwritten, or what lies behind its tensor."""
+    big, exps = torch.zeros(4, 192, dtype=torch.int8), torch.zeros(4, 16, dtype=torch.uint8)
+    for width, cols in ((70, 70), (95, 70), (31, 1), (33, 33)):
+        with pytest.raises(ValueError, match="whole blocks"):
+            m.Act8(big[:, :width], exps, cols)
+    with pytest.raises(ValueError):
+        m.Act8(big[:, :96], exps[:, :2], 70)
+    for width, cols in ((96, 70), (32, 1), (64, 33), (192, 192)):
+        assert m.Act8(big[:, :width], exps[:, :(cols + 31) // 32], cols).c.code_stride == 192
+
+
 def test_binding_refuses_host_memory(lib):
     """Tensors of the CPU, right in everything else (nothing is enqueued)."""
     z = torch.zeros
