@@ -632,8 +632,10 @@ class Act8:
                              f"[rows, >= {blocks}] are needed")
         self.shape = (rows, int(cols))
         self._codes, self._exps, self._memory = codes, exps, None
-        self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), _rows2d(codes, "codes"),
-                             exps.data_ptr(), _rows2d(exps, "exps"))
+        cs, es = _rows2d(codes, "codes"), _rows2d(exps, "exps")
+        if rows <= 1:   # never used: any that the library takes
+            cs, es = 32 * blocks, (blocks + 15) // 16 * 16
+        self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), cs, exps.data_ptr(), es)
         self.ref = ctypes.byref(self.c) if codes.is_cuda and exps.is_cuda else None   # refused by every call
 
     @classmethod

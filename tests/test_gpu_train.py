@@ -380,6 +380,27 @@ def test_act8_not_finite_and_extreme():
         assert not torch.isinf(back).any()
 
 
+def test_act8_one_row_of_many():
+    """Single rows of a checkpoint as checkpoints of their own, in every pass."""
+    rows, cols = 6, 200
+    x = torch.randn(rows, cols, device=DEV)
+    codes = torch.full((rows, 256), 55, dtype=torch.int8, device=DEV)
+    exps = torch.full((rows, 16), 77, dtype=torch.uint8, device=DEV)
+    for r in range(rows):
+        m.muon_act8_pack(x[r:r + 1], m.Act8(codes[r:r + 1, :224], exps[r:r + 1, :7], cols))
+    want, we = R.act8_encode(f64(x))
+    assert np.array_equal(codes[:, :224].cpu().numpy(), want) and (codes[:, 224:] == 55).all()
+    assert np.array_equal(exps[:, :7].cpu().numpy(), we) and (exps[:, 7:] == 77).all()
+    back = torch.empty(1, cols, device=DEV)
+    one = m.Act8(codes[4:5, :224], exps[4:5, :7], cols)
+    m.muon_act8_unpack(one, back)
+    assert np.array_equal(f64(back), R.act8_decode(want[4:5], we[4:5], cols))
+    dy, G = torch.randn(1, 40, device=DEV), torch.empty(1, 40, cols, device=DEV)
+    assert run_wgrad(dy, one, G, torch.tensor([0, 1], dtype=torch.int32, device=DEV)) == 0
+    full, size = R.weight_grads(f64(dy), f64(back), [0, 1])
+    within(f64(G), full, wgrad_bound(size, full, [0, 1], U))
+
+
 def test_act8_offsets_past_32_bits():
     """70000 rows of 32768 columns: elements past 2^31 in the source and the codes."""
     rows, cols = 70000, 32768

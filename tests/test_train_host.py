@@ -204,6 +204,18 @@ def test_checkpoint_needs_whole_blocks(lib):
         assert m.Act8(big[:, :width], exps[:, :(cols + 31) // 32], cols).c.code_stride == 192
 
 
+def test_checkpoint_of_one_row(lib):
+    """One row cut out of a checkpoint is as good as several: the stride between rows
+    that are not there does not matter."""
+    codes, exps = torch.zeros(8, 192, dtype=torch.int8), torch.zeros(8, 16, dtype=torch.uint8)
+    for n in (0, 1, 2):
+        c = m.Act8(codes[3:3 + n, :72 + 24], exps[3:3 + n, :3], 72).c
+        assert c.code_stride % 32 == 0 and c.code_stride >= 96 and c.exp_stride % 16 == 0
+        assert c.codes == codes.data_ptr() + 3 * 192 or n == 0
+    one = m.Act8(torch.zeros(1, 100, dtype=torch.int8), torch.zeros(1, 3, dtype=torch.uint8), 72).c
+    assert (one.code_stride, one.exp_stride) == (96, 16)
+
+
 def test_binding_refuses_host_memory(lib):
     """Tensors of the CPU, right in everything else (nothing is enqueued)."""
     z = torch.zeros
