@@ -524,27 +524,44 @@ def _row_stride(rows: int, cols: int, rs: int, cs: int, what: str) -> int:
     return rs
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
+def _elsewhere(what: str, dev: int) -> ValueError:
+    return ValueError(f"{what} must be on the GPU" + (f" {dev} of the others" if dev >= 0 else ""))
+
+
+def _dtype(t: torch.Tensor, what: str, dev: int) -> int:
+    """dev: the GPU of the call's operands (-1: the first one is not on any)."""
     dt = _DT.get(t.dtype)
     if dt is None:
         raise ValueError(f"{what} must be bfloat16 or float32, not {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
+    if t.get_device() != dev or dev < 0:
+        raise _elsewhere(what, dev)
     return dt
 
 
-def _vector(t: torch.Tensor, what: str, dtype: torch.dtype, numel: int) -> int:
+def _vector(t: torch.Tensor, what: str, dtype: torch.dtype, numel: int, dev: int) -> int:
     if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{what} must be {numel} contiguous {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
+    if t.get_device() != dev:
+        raise _elsewhere(what, dev)
     return t.data_ptr()
 
 
-def _memory_of(ws: torch.Tensor) -> int:
-    if not ws.is_cuda:
-        raise ValueError("the workspace must be on the GPU")
+def _memory_of(ws: torch.Tensor, dev: int) -> int:
+    if ws.get_device() != dev:
+        raise _elsewhere("the workspace", dev)
     return ws.data_ptr()
+
+
+def _stream_of(stream, dev: int) -> int:
+    """The stream's handle; the call has to run on `dev`, the GPU of its operands."""
+    here = torch._C._cuda_getDevice()   # CUDA is up: there are tensors on it
+    if here == dev:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(dev)
+        if getattr(stream, "device_index", dev) == dev:
+            return _stream(stream)
+    raise ValueError(f"the tensors are on GPU {dev}: it has to be the current device (it is {here}) "
+                     "and the stream's")
 
 
 class Balance:
@@ -562,25 +579,27 @@ class Balance:
             raise ValueError("chosen must be int32 or int64")
         if chosen.dim() != 2 or chosen.shape[0] != tokens:
             raise ValueError("chosen needs one row of expert numbers for each token")
-        if not chosen.is_cuda:
-            raise ValueError("chosen must be on the GPU")
-        topk = chosen.shape[1]
+        topk, dev = chosen.shape[1], logits.get_device()
         cs = _rows2d(chosen, "chosen")
         sequences, seq = 1, None
         if seq_begin is not None:
             sequences = seq_begin.numel() - 1
-            seq = _vector(seq_begin, "seq_begin", torch.int32, sequences + 1)
+            seq = _vector(seq_begin, "seq_begin", torch.int32, sequences + 1, dev)
         mp = None
         if mask is not None:
             if mask.dtype not in (torch.bool, torch.uint8):
                 raise ValueError("mask must be bool or uint8")
-            mp = _vector(mask, "mask", mask.dtype, tokens)
+            mp = _vector(mask, "mask", mask.dtype, tokens, dev)
+        dt = _dtype(logits, "logits", dev)
+        if chosen.get_device() != dev:
+            raise _elsewhere("chosen", dev)
         self.tensors = (logits, chosen, seq_begin, mask)
+        self.device = dev
         self.shape = (tokens, experts)
         self.sequences = sequences
-        self.c = muon_balance_t(tokens, experts, topk, logits.data_ptr(), _dtype(logits, "logits"),
-                                ls, chosen.data_ptr(), chosen.element_size(), cs, sequences, seq,
-                                mp, _SCORE[score], float(coef))
+        self.c = muon_balance_t(tokens, experts, topk, logits.data_ptr(), dt, ls, chosen.data_ptr(),
+                                chosen.element_size(), cs, sequences, seq, mp, _SCORE[score],
+                                float(coef))
 
 
 def muon_balance_workspace_size(tokens: int, experts: int, sequences: int = 1) -> int:
@@ -594,23 +613,24 @@ def muon_balance_workspace_size(tokens: int, experts: int, sequences: int = 1) -
 def muon_balance_forward(b: Balance, loss: torch.Tensor, counts: torch.Tensor,
                          load: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """loss: fp32, one element; counts: int32 [experts]; load: fp32 [sequences, experts]."""
-    experts = b.shape[1]
+    experts, dev = b.shape[1], b.device
     _check(load_library().muon_balance_forward(
-        ctypes.byref(b.c), _vector(loss, "loss", torch.float32, 1),
-        _vector(counts, "counts", torch.int32, experts),
-        _vector(load, "load", torch.float32, b.sequences * experts), _memory_of(ws), ws.numel(),
-        _stream(stream)), "muon_balance_forward")
+        ctypes.byref(b.c), _vector(loss, "loss", torch.float32, 1, dev),
+        _vector(counts, "counts", torch.int32, experts, dev),
+        _vector(load, "load", torch.float32, b.sequences * experts, dev), _memory_of(ws, dev),
+        ws.numel(), _stream_of(stream, dev)), "muon_balance_forward")
 
 
 def muon_balance_backward(b: Balance, load: torch.Tensor, dlogits: torch.Tensor,
                           dloss: Optional[torch.Tensor] = None, accumulate: bool = False,
                           stream=None) -> None:
     """dlogits [tokens, experts] is written, or added to with accumulate."""
+    dev = b.device
     _check(load_library().muon_balance_backward(
-        ctypes.byref(b.c), _vector(load, "load", torch.float32, b.sequences * b.shape[1]),
-        None if dloss is None else _vector(dloss, "dloss", torch.float32, 1),
-        dlogits.data_ptr(), _dtype(dlogits, "dlogits"), _rows2d(dlogits, "dlogits", b.shape),
-        int(bool(accumulate)), _stream(stream)), "muon_balance_backward")
+        ctypes.byref(b.c), _vector(load, "load", torch.float32, b.sequences * b.shape[1], dev),
+        None if dloss is None else _vector(dloss, "dloss", torch.float32, 1, dev),
+        dlogits.data_ptr(), _dtype(dlogits, "dlogits", dev), _rows2d(dlogits, "dlogits", b.shape),
+        int(bool(accumulate)), _stream_of(stream, dev)), "muon_balance_backward")
 
 
 class Act8:
@@ -619,7 +639,7 @@ class Act8:
     exps (uint8, one biased exponent for each 32 columns of a row, row stride a
     multiple of 16)."""
 
-    __slots__ = ("shape", "c", "ref", "_codes", "_exps", "_memory")
+    __slots__ = ("shape", "device", "c", "ref", "_codes", "_exps", "_memory")
 
     def __init__(self, codes: torch.Tensor, exps: torch.Tensor, cols: int):
         if codes.dtype != torch.int8 or exps.dtype != torch.uint8:
@@ -636,7 +656,9 @@ class Act8:
         if rows <= 1:   # never used: any that the library takes
             cs, es = 32 * blocks, (blocks + 15) // 16 * 16
         self.c = muon_act8_t(rows, int(cols), codes.data_ptr(), cs, exps.data_ptr(), es)
-        self.ref = ctypes.byref(self.c) if codes.is_cuda and exps.is_cuda else None   # refused by every call
+        dev = codes.get_device()
+        self.device = dev if dev == exps.get_device() else -1   # -1: refused by every call
+        self.ref = ctypes.byref(self.c) if self.device >= 0 else None
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Act8":
@@ -651,8 +673,12 @@ class Act8:
         self.shape = (rows, int(cols))
         base = self._memory.data_ptr()
         self.c = muon_act8_t(rows, int(cols), base, cs, base + rows * cs, es)
-        kind = device.type if isinstance(device, torch.device) else torch.device(device).type
-        self.ref = ctypes.byref(self.c) if kind == "cuda" else None
+        where = device if isinstance(device, torch.device) else torch.device(device)
+        if where.type != "cuda":
+            self.device, self.ref = -1, None
+        else:
+            self.device = torch.cuda.current_device() if where.index is None else where.index
+            self.ref = ctypes.byref(self.c)
         return self
 
     @property
@@ -677,43 +703,52 @@ act8_empty = Act8.empty
 
 def muon_act8_pack(x: torch.Tensor, out: Act8, stream=None) -> None:
     """Write x [rows, cols] (bf16 or fp32) into the checkpoint."""
-    _check(load_library().muon_act8_pack(x.data_ptr(), _dtype(x, "x"), _rows2d(x, "x", out.shape),
-                                         out.ref, _stream(stream)), "muon_act8_pack")
+    dev = out.device
+    _check(load_library().muon_act8_pack(x.data_ptr(), _dtype(x, "x", dev),
+                                         _rows2d(x, "x", out.shape), out.ref,
+                                         _stream_of(stream, dev)), "muon_act8_pack")
 
 
 def muon_act8_unpack(a: Act8, out: torch.Tensor, stream=None) -> None:
     """Read a checkpoint back into out [rows, cols] (bf16 or fp32)."""
-    _check(load_library().muon_act8_unpack(a.ref, out.data_ptr(), _dtype(out, "out"),
-                                           _rows2d(out, "out", a.shape), _stream(stream)),
+    dev = a.device
+    _check(load_library().muon_act8_unpack(a.ref, out.data_ptr(), _dtype(out, "out", dev),
+                                           _rows2d(out, "out", a.shape), _stream_of(stream, dev)),
            "muon_act8_unpack")
 
 
-def _one_dtype(first: torch.Tensor, second: torch.Tensor, third: torch.Tensor) -> int:
+def _one_dtype(first: torch.Tensor, second: torch.Tensor, third: torch.Tensor, dev: int) -> int:
     if second.dtype != first.dtype or third.dtype != first.dtype:
         raise ValueError("the tensors need one dtype")
-    return _dtype(first, "the tensors")
+    if second.get_device() != dev or third.get_device() != dev:
+        raise _elsewhere("the tensors", dev)
+    return _dtype(first, "the tensors", dev)
 
 
 def muon_act8_swiglu_forward(gate: torch.Tensor, up: torch.Tensor, h: torch.Tensor, gate8: Act8,
                              up8: Act8, stream=None) -> None:
     """h = silu(gate) * up; gate8 and up8 keep gate and up for the backward pass."""
-    dt, s = _one_dtype(gate, up, h), gate8.shape
+    dev, s = gate8.device, gate8.shape
+    dt = _one_dtype(gate, up, h, dev)
+    if up8.device != dev:
+        raise _elsewhere("up8", dev)
     _check(load_library().muon_act8_swiglu_forward(
         gate.data_ptr(), _rows2d(gate, "gate", s), up.data_ptr(), _rows2d(up, "up", s), dt,
         h.data_ptr(), _rows2d(h, "h", s), gate8.ref, up8.ref,
-        _stream(stream)), "muon_act8_swiglu_forward")
+        _stream_of(stream, dev)), "muon_act8_swiglu_forward")
 
 
 def muon_act8_swiglu_backward(dh: torch.Tensor, gate8: Act8, up8: Act8, dgate: torch.Tensor,
                               dup: torch.Tensor, h8: Optional[Act8] = None, stream=None) -> None:
     """Gradients of gate and up; h8, if given, receives silu(gate) * up."""
-    dt, s = _one_dtype(dh, dgate, dup), gate8.shape
-    if h8 is not None and h8.ref is None:
-        raise ValueError("h8 must be on the GPU")
+    dev, s = gate8.device, gate8.shape
+    dt = _one_dtype(dh, dgate, dup, dev)
+    if up8.device != dev or (h8 is not None and h8.device != dev):
+        raise _elsewhere("up8 and h8", dev)
     _check(load_library().muon_act8_swiglu_backward(
         dh.data_ptr(), _rows2d(dh, "dh", s), dt, gate8.ref, up8.ref,
         dgate.data_ptr(), _rows2d(dgate, "dgate", s), dup.data_ptr(), _rows2d(dup, "dup", s),
-        None if h8 is None else h8.ref, _stream(stream)), "muon_act8_swiglu_backward")
+        None if h8 is None else h8.ref, _stream_of(stream, dev)), "muon_act8_swiglu_backward")
 
 
 def muon_act8_weight_grad_workspace_size(rows: int, out: int, inp: int, experts: int = 1,
@@ -736,26 +771,28 @@ def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
     G: a tensor [experts, out, in] (or [out, in] for one), or a Group whose G
     matrices receive the gradients.  offsets: int32 [experts + 1] on the
     device; None = all rows belong to the one expert."""
-    rows, inp = x8.shape
-    if x8.ref is None:
-        raise ValueError("the checkpoint must be on the GPU")
+    (rows, inp), dev = x8.shape, x8.device
+    if dev < 0:
+        raise _elsewhere("the checkpoint", dev)
     out = dy.shape[1] if dy.dim() == 2 else 0
     ds = _rows2d(dy, "dy", (rows, out))
     if isinstance(G, Group):
         v = G.c.view
         experts, shape, gs, gdt = G.c.batch, (v.rows, v.cols), v.row_stride, G.c.g_dtype
         ptrs, base, bs = G.c.g_ptrs, None, 0
+        if G.ptrs.get_device() != dev:
+            raise _elsewhere("the group", dev)
     else:
         if G.dim() not in (2, 3):
             raise ValueError("G needs two or three dimensions")
         experts, bs = (G.shape[0], G.stride(0)) if G.dim() == 3 else (1, 0)
-        shape, gdt = tuple(G.shape[-2:]), _dtype(G, "G")
+        shape, gdt = tuple(G.shape[-2:]), _dtype(G, "G", dev)
         gs = _row_stride(*shape, *G.stride()[-2:], "G")
         ptrs, base = None, G.data_ptr()
     if shape != (out, inp):
         raise ValueError(f"G needs matrices of {out} x {inp}, not {shape[0]} x {shape[1]}")
-    op = None if offsets is None else _vector(offsets, "offsets", torch.int32, experts + 1)
-    d = muon_weight_grad_t(rows, out, experts, dy.data_ptr(), _dtype(dy, "dy"), ds, x8.c, op, ptrs,
-                           base, bs, gs, gdt, int(bool(accumulate)))
-    _check(load_library().muon_act8_weight_grad(ctypes.byref(d), _memory_of(ws), ws.numel(),
-                                                _stream(stream)), "muon_act8_weight_grad")
+    op = None if offsets is None else _vector(offsets, "offsets", torch.int32, experts + 1, dev)
+    d = muon_weight_grad_t(rows, out, experts, dy.data_ptr(), _dtype(dy, "dy", dev), ds, x8.c, op,
+                           ptrs, base, bs, gs, gdt, int(bool(accumulate)))
+    _check(load_library().muon_act8_weight_grad(ctypes.byref(d), _memory_of(ws, dev), ws.numel(),
+                                                _stream_of(stream, dev)), "muon_act8_weight_grad")

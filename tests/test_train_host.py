@@ -216,6 +216,70 @@ def test_checkpoint_of_one_row(lib):
     assert (one.code_stride, one.exp_stride) == (96, 16)
 
 
+class Placed(torch.Tensor):
+    """A CPU tensor that says it is on a GPU."""
+
+    def get_device(self):
+        return self.gpu
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def placed(gpu, *shape, dtype=torch.float32):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(Placed)
+    t.gpu = gpu
+    return t
+
+
+def test_binding_refuses_operands_of_several_gpus(lib, monkeypatch):
+    """Every operand on the first one's GPU, and that the current one (no call gets
+    as far as the library: there is no GPU here)."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    P, i32, i64, u8 = placed, torch.int32, torch.int64, torch.uint8
+
+    def act8(gpu):
+        return m.Act8(P(gpu, 4, 96, dtype=torch.int8), P(gpu, 4, 16, dtype=u8), 70)
+
+    def bal(a=0, b=0, c=0, d=0):
+        return m.Balance(P(a, 4, 8), P(b, 4, 2, dtype=i64), P(c, 2, dtype=i32), P(d, 4, dtype=u8))
+
+    def fwd(b=0, loss=0, counts=0, load=0, ws=0):
+        m.muon_balance_forward(bal(b, b, b, b), P(loss, 1), P(counts, 8, dtype=i32), P(load, 1, 8),
+                               P(ws, 4096, dtype=u8), stream=0)
+
+    def bwd(b=0, load=0, dl=0, dloss=0):
+        m.muon_balance_backward(bal(b, b, b, b), P(load, 1, 8), P(dl, 4, 8), P(dloss, 1), stream=0)
+
+    def swf(x=0, y=0, z=0, g=0, u=0):
+        m.muon_act8_swiglu_forward(P(x, 4, 70), P(y, 4, 70), P(z, 4, 70), act8(g), act8(u), stream=0)
+
+    def swb(x=0, y=0, z=0, g=0, u=0, h=0):
+        m.muon_act8_swiglu_backward(P(x, 4, 70), act8(g), act8(u), P(y, 4, 70), P(z, 4, 70), act8(h), stream=0)
+
+    def wg(dy=0, x=0, G=0, ws=0, off=0):
+        m.muon_act8_weight_grad(P(dy, 4, 8), act8(x), P(G, 2, 8, 70), P(ws, 1 << 16, dtype=u8),
+                                offsets=P(off, 3, dtype=i32), stream=0)
+
+    def pack(x=0, a=0):
+        m.muon_act8_pack(P(x, 4, 70), act8(a), stream=0)
+
+    def unpack(x=0, a=0):
+        m.muon_act8_unpack(act8(a), P(x, 4, 70), stream=0)
+
+    for call in (bal, fwd, bwd, swf, swb, wg, pack, unpack):
+        names = call.__code__.co_varnames[:call.__code__.co_argcount]
+        for n in names:
+            with pytest.raises(ValueError, match="GPU"):
+                call(**{n: 1})
+        if call is not bal:   # all on a GPU that is not the current one
+            with pytest.raises(ValueError, match="current device"):
+                call(**{n: 1 for n in names})
+    assert m.Act8(P(0, 4, 96, dtype=torch.int8), P(1, 4, 16, dtype=u8), 70).ref is None
+    bal()
+
+
 def test_binding_refuses_host_memory(lib):
     """Tensors of the CPU, right in everything else (nothing is enqueued)."""
     z = torch.zeros
