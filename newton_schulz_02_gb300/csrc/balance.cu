@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -32,13 +33,20 @@ constexpr int kTotalThreads = 1024;
 constexpr int kTotalItems = 4096;   // more chunks than these are counted once, not by every block
 constexpr size_t kHeader = 256;     // status word, ticket of the finalize blocks, counts of the batch
 
+// Blocks of the forward pass that an SM holds at once.  Up to 512 experts five, by
+// 48 registers: with four, 100 experts and more take 7 to 36% longer (131072 x 256
+// bf16 48.8 us for 35.9), also at the widths whose bound checks then cost a few
+// spilled registers (131072 x 200 bf16 49.1 for 40.8), and fewer experts as long or
+// longer.  More than 512 experts need the registers, and two fit.
+constexpr int blocks_per_sm(int experts) { return experts <= 512 ? 5 : 2; }
+
 // Tokens of a chunk.  Chunks and the cuts at sequence bounds together make up
-// to 760 blocks, five on each of 152 SMs at once (one block more would be a
-// second wave; with four on each 131072 x 256 bf16 in 32 sequences take 47 us, so
-// 44); with many sequences there are up to 380 beside their cuts.  A
+// to one wave of blocks on 152 SMs (65536 x 1024 fp32 63 us, in two waves 65, in two and a
+// half 74); with many sequences there are up to half a wave beside their cuts.  A
 // function of the sizes alone, as the order of the sums follows it.
-int chunk_tokens(int64_t tokens, int sequences) {
-  const int64_t most = 760 - (sequences < 380 ? sequences : 380);
+int chunk_tokens(int64_t tokens, int experts, int sequences) {
+  const int wave = 152 * blocks_per_sm(experts);
+  const int64_t most = wave - std::min(sequences, wave / 2);
   const int64_t c = tokens / most + 1;
   return static_cast<int>(c < 32 ? 32 : c);
 }
@@ -47,8 +55,8 @@ int chunk_tokens(int64_t tokens, int sequences) {
 // bounds.  Sequence s that starts at token b owns the chunks b/C + s ...
 // (e-1)/C + s: one number for each (chunk, sequence) pair, ascending, without
 // knowing the bounds on the host.
-int64_t chunk_items(int64_t tokens, int sequences) {
-  return tokens / chunk_tokens(tokens, sequences) + sequences;
+int64_t chunk_items(int64_t tokens, int experts, int sequences) {
+  return tokens / chunk_tokens(tokens, experts, sequences) + sequences;
 }
 
 struct BalanceArgs {
@@ -264,7 +272,7 @@ struct LowRow {
 // One chunk of tokens of one sequence per block: sum_t p_te, c_e and the
 // number of valid tokens.
 template <int LANES, int VPT, bool FULL, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads, VPT <= 16 ? 5 : 2)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(LANES * VPT))
     k_balance_forward(const __grid_constant__ BalanceArgs a) {
   constexpr int kGroups = kThreads / LANES;
   constexpr int kCols = LANES * VPT;
@@ -747,7 +755,7 @@ struct Layout {
 };
 
 Layout layout(int64_t tokens, int experts, int sequences) {
-  const size_t items = static_cast<size_t>(chunk_items(tokens, sequences));
+  const size_t items = static_cast<size_t>(chunk_items(tokens, experts, sequences));
   Layout l;
   l.psum = kHeader;
   l.pcnt = l.psum + align256(items * experts * 4);
@@ -794,8 +802,8 @@ BalanceArgs base_args(const muon_balance_t* b) {
   a.experts = b->experts;
   a.topk = b->topk;
   a.sequences = b->sequences;
-  a.chunk = chunk_tokens(b->tokens, b->sequences);
-  a.items = static_cast<int>(chunk_items(b->tokens, b->sequences));
+  a.chunk = chunk_tokens(b->tokens, b->experts, b->sequences);
+  a.items = static_cast<int>(chunk_items(b->tokens, b->experts, b->sequences));
   a.logits = b->logits;
   a.dtype = b->dtype;
   a.logits_stride = b->logits_stride;

@@ -216,6 +216,19 @@ def test_checkpoint_of_one_row(lib):
     assert (one.code_stride, one.exp_stride) == (96, 16)
 
 
+@pytest.mark.parametrize("experts,blocks", [(8, 5), (64, 5), (200, 5), (512, 5), (513, 2), (1024, 2)])
+@pytest.mark.parametrize("sequences", [1, 32, 300])
+def test_balance_chunks_fill_one_wave(lib, experts, blocks, sequences):
+    """A chunk leaves one row of partial sums and one of counts: as many as one wave
+    of blocks on 152 SMs, or half of one beside the sequences' own."""
+    size = m.muon_balance_workspace_size(1 << 20, experts, sequences)
+    chunks = (size - 4 * sequences * ((experts + 31) // 32)) / (8 * experts + 8)
+    padding = 6 * 256 / (8 * experts + 8) + 1
+    wave = 152 * blocks
+    assert chunks <= max(wave, wave // 2 + sequences) + padding
+    assert chunks >= 0.97 * min(wave, wave // 2 + sequences) - padding
+
+
 class Placed(torch.Tensor):
     """A CPU tensor that says it is on a GPU."""
 
