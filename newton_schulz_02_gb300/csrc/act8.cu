@@ -275,10 +275,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_act8_swiglu_backward(const __gr
 }
 
 // ---- host ------------------------------------------------------------------
-int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
-
-bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 int64_t blocks_of(int cols) { return (static_cast<int64_t>(cols) + kBlock - 1) / kBlock; }
 
 muon_status_t check_act8(const muon_act8_t* a) {

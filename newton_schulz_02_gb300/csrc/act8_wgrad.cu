@@ -229,15 +229,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int32_t x,
-                                            int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // Codes 0 and 2 of the four int8 in p as a pair of bf16 (with p >> 8: codes 1
 // and 3).  0x4300 is 128 in bf16 and its 7 mantissa bits count units, so
 // 0x4300 | (c & 127) is 128 + (c & 127); what is subtracted is 128 for c >= 0
@@ -1007,10 +998,6 @@ __global__ void __launch_bounds__(256)
     }
   }
 }
-
-int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
-
-bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -766,10 +766,6 @@ Layout layout(int64_t tokens, int experts, int sequences) {
   return l;
 }
 
-int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
-
-bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 // Rows that may be read (or written) four values at a time.
 int vectorised(const void* p, int dtype, int64_t stride, int n) {
   return n % 4 == 0 && stride % 4 == 0 && at_multiple(p, 4 * esize(dtype));

@@ -23,6 +23,10 @@ constexpr int kPad = 128;
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// Bytes of a value of a muon_dtype_t; whether an address is a multiple of n.
+inline int esize(int dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+inline bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 enum PrepMode : int { kPrepMomentumSgd = 0, kPrepMomentumEma = 1, kPrepLoad = 2 };
 
 // The Newton–Schulz iterate is kept as two bf16 planes, X = hi + lo, with
