@@ -337,9 +337,12 @@ muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
  * gradients.  The pages describe the optimizer alone and have no counterpart.
  *
  * Unlike the matrices of the step, their inputs need no alignment beyond
- * their element size and no particular width unless an argument says so:
- * where every row starts on a 16-byte boundary the kernels use wide accesses,
- * elsewhere they take element-wise ones.  Strides are in elements. */
+ * their element size and no particular width unless an argument says so.  Rows
+ * are fastest on 32-byte boundaries (checkpoints, activation, G) or 16-byte ones
+ * (dy); elsewhere they are read and written in shifted 16-byte pieces, and dy is
+ * copied first.  Logits are read four at a time where width and stride are
+ * multiples of four and the base is aligned to four values, else one by one.
+ * Strides are in elements. */
 
 /* Router balance loss.  Token t of a sequence s (of n_s valid tokens, N valid
  * tokens in all) with logits l has the probabilities
@@ -394,7 +397,9 @@ muon_status_t muon_balance_workspace_size(int64_t tokens, int experts, int seque
  * expert by the valid tokens of all sequences.  load: device
  * [sequences][experts] fp32, coef / N * f_se, which the backward pass takes.
  * Status word in the workspace (muon_get_status).  Sums are fp32 in an order
- * fixed by the sizes: the same inputs give the same bits. */
+ * fixed by the sizes: the same inputs give the same bits.  Exponentials are the
+ * fast ones: a probability is off by up to about 16 + |l - largest l| units in the
+ * last place of fp32 (sigmoid: 16 + |l|). */
 muon_status_t muon_balance_forward(const muon_balance_t* b, float* loss, int32_t* counts,
                                    float* load, void* workspace, size_t workspace_bytes,
                                    muon_stream_t stream);
@@ -445,7 +450,9 @@ muon_status_t muon_act8_unpack(const muon_act8_t* a, void* x, muon_dtype_t xdt, 
 
 /* h = silu(gate) * up with silu(g) = g * sigma(g), in fp32, rounded once to
  * dt; gate8 and up8 receive gate and up (one pass over the data).  gate, up
- * and h: rows x cols of dt with row strides; rows and cols are gate8's. */
+ * and h: rows x cols of dt with row strides; rows and cols are gate8's.  sigma is
+ * taken with the fast exponential, here and in the backward pass: a few units in
+ * the last place of fp32 for gates above 0, about |g| more below (20 at g = -20). */
 muon_status_t muon_act8_swiglu_forward(const void* gate, int64_t gate_stride, const void* up,
                                        int64_t up_stride, muon_dtype_t dt, void* h,
                                        int64_t h_stride, const muon_act8_t* gate8,
@@ -493,7 +500,9 @@ typedef struct {
 /* Bytes of workspace muon_act8_weight_grad needs (pointers are not looked at):
  * a header, partial sums where the tokens are cut into slices, and room for a
  * copy of dy, which is made where dy's rows do not start on 16-byte boundaries
- * (2 bytes a value) or are fp32 (three bf16 a value).  Host only. */
+ * (2 bytes a value) or are fp32 (three bf16 a value).  Whether a bf16 dy will be on
+ * such boundaries is known only with its pointer, so the room is always there.
+ * Host only. */
 muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, size_t* bytes);
 
 muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace,

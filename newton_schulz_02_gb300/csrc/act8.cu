@@ -18,10 +18,14 @@
 // took 3 to 6 times as long.  Measured at 16384 rows, in us (and the share of
 // the copy rate):
 //                       pack        unpack      forward     backward with h8
-//   7168 bf16           57 (92%)    55 (96%)    155 (90%)   165 (96%)
-//   7001 bf16           63 (82%)    69 (75%)    174 (78%)   209 (74%)
-//   7168 fp32           86 (102%)   89 (98%)    235 (103%)  255 (102%)
-//   7001 fp32           86 (98%)    116 (73%)   249 (95%)   292 (87%)
+//   7168 bf16           56 (94%)    54 (98%)    153 (91%)   164 (96%)
+//   7001 bf16           62 (83%)    66 (78%)    177 (77%)   201 (76%)
+//   7168 fp32           84 (103%)   88 (99%)    234 (104%)  254 (103%)
+//   7001 fp32           86 (99%)    117 (73%)   248 (96%)   294 (87%)
+// The shifted rows are not bound by HBM (42 to 59% busy where 7168 columns have it
+// 60 to 74%, 8192 rows bf16): shifting is half as many instructions again (issue 65 to
+// 77% busy), and a sector goes out in two pieces (10.7 against 5.5 million sector
+// writes at L2 for unpack, L1 78% busy).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -230,7 +234,8 @@ __global__ void __launch_bounds__(kThreads) k_act8_unpack(const __grid_constant_
 }
 
 // 1 / (1 + e^-g) with the fast exponential and reciprocal: an error of a few
-// units plus (1 - sigma) |g| units in the last place.
+// units plus (1 - sigma) |g| units in the last place.  (With expf and a division
+// fp32 rows of 7001 columns take 266 us forward and 333 backward instead of 248 and 294.)
 __device__ __forceinline__ float sigma(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // x = gate, y = up, z = h; a, b = the checkpoints of gate and up.
