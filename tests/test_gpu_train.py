@@ -740,6 +740,28 @@ def test_weight_grad_long_fp32_sums_of_one_hot_expert(E, out, inp, slices, dy):
         assert err <= 3e-6, (e, err)
 
 
+@pytest.mark.parametrize("dy", ["bf16", "f32"])
+def test_weight_grad_hot_expert_of_many_chunks(dy):
+    """70000 tokens, all but a few on one of 40 experts: more chunks of one tile than
+    are announced at a time, between experts of one chunk and of none."""
+    rows, E, out, inp, hot = 70000, 40, 40, 96, 17
+    sizes = [3 if e % 3 else 0 for e in range(E)]
+    sizes[hot] = rows - sum(sizes) + sizes[hot]
+    offsets = [0] + np.cumsum(sizes).tolist()
+    d, x8, off, ds, xs = wgrad_case(14, offsets, rows, out, inp, dy, "dense")
+    want, size = R.weight_grads(ds, xs, offsets)
+    start = torch.randn(E, out, inp, device=DEV)
+    for acc in (False, True):
+        G = start.clone()
+        assert run_wgrad(d, x8, G, off, acc=acc) == 0
+        total = want + f64(start) if acc else want
+        for e in range(E):
+            if sizes[e] == 0:
+                assert torch.equal(G[e], start[e] if acc else torch.zeros_like(G[e]))
+                continue
+            assert np.linalg.norm(f64(G[e]) - total[e]) <= 3e-6 * (np.linalg.norm(want[e]) + np.linalg.norm(total[e])), e
+
+
 def test_weight_grad_pointer_array_alignment():
     """Pointers of a device array: 16-byte steps are written, others flagged and
     their matrices left alone."""
