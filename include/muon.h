@@ -205,6 +205,17 @@ muon_status_t muon_step_batched(const muon_group_t* groups, int n_groups,
                                 const muon_ns_schedule_t* schedule, void* workspace,
                                 size_t workspace_bytes, muon_stream_t stream);
 
+/* muon_step_batched with every gradient multiplied by *grad_scale (device, 1
+ * fp32, read when the kernels run; NULL = 1) where it is read: G * scale is
+ * rounded to fp32 once, and G itself stays as it is.  muon_grad_norm leaves the
+ * factor that clips the gradients.  Where *grad_scale is not finite the step
+ * changes no W and no M, and sets MUON_FLAG_NONFINITE. */
+muon_status_t muon_step_batched_scaled(const muon_group_t* groups, int n_groups,
+                                       const muon_hparams_t* hparams,
+                                       const muon_ns_schedule_t* schedule,
+                                       const float* grad_scale, void* workspace,
+                                       size_t workspace_bytes, muon_stream_t stream);
+
 /* Bytes of workspace newton_schulz_batched needs.  Host only. */
 muon_status_t newton_schulz_workspace_size(const muon_view_t* view, int batch,
                                            const muon_ns_schedule_t* schedule, size_t* bytes);
@@ -328,6 +339,45 @@ typedef struct {
 muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
                               const muon_adamw_hparams_t* hparams, uint32_t* device_flags,
                               muon_stream_t stream);
+
+/* muon_adamw_step with every gradient multiplied by *grad_scale where it is read, as
+ * muon_step_batched_scaled does; where that is not finite nothing is updated and
+ * MUON_FLAG_NONFINITE is ORed into *device_flags. */
+muon_status_t muon_adamw_step_scaled(const muon_adamw_group_t* groups, int n_groups,
+                                     const muon_adamw_hparams_t* hparams, const float* grad_scale,
+                                     uint32_t* device_flags, muon_stream_t stream);
+
+/* ---- Norm of all gradients, and clipping ------------------------------------
+ *   norm  = sqrt(sum over all tensors of g^2)
+ *   scale = min(1, max_norm / (norm + 1e-6)),  NaN where norm is not finite
+ * The gradients are only read: the optimizer steps above take `scale` and
+ * multiply where they read G, so that clipping costs no pass of its own. */
+
+/* `count` tensors of rows x cols (any shape: rows = 1, cols = its values, for a
+ * contiguous one).  ptrs: DEVICE array of `count` DEVICE pointers, each 16-byte
+ * aligned (else MUON_FLAG_MISALIGNED, and that tensor is left out); a group's
+ * g_ptrs.  row_stride: elements between rows, >= cols (ignored for one row); cols
+ * and row_stride are multiples of 8 where they differ. */
+typedef struct {
+  int count;
+  int64_t rows, cols;
+  int64_t row_stride;
+  muon_dtype_t dtype;
+  const void* const* ptrs;
+} muon_grads_t;
+
+/* Bytes of workspace muon_grad_norm needs.  Host only. */
+muon_status_t muon_grad_norm_workspace_size(const muon_grads_t* groups, int n_groups,
+                                            size_t* bytes);
+
+/* groups: host array [n_groups] (a tensor that is in two counts twice; no tensors:
+ * norm 0).  max_norm: >= 0 (infinity: only the norm; scale is 1).  norm, scale: device, 1 fp32 each.
+ * The sum holds 48 bits or more, whatever the gradients' size: squares do not
+ * overflow or vanish.  Its order is fixed by the sizes and the GPU.  Status word
+ * in the workspace (muon_get_status): MUON_FLAG_NONFINITE, MUON_FLAG_MISALIGNED. */
+muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max_norm, float* norm,
+                             float* scale, void* workspace, size_t workspace_bytes,
+                             muon_stream_t stream);
 
 /* ---- Gradients of a mixture-of-experts training step -----------------------
  * The operators below produce gradients that muon_step_batched and
@@ -507,6 +557,75 @@ muon_status_t muon_act8_weight_grad_workspace_size(const muon_weight_grad_t* d, 
 
 muon_status_t muon_act8_weight_grad(const muon_weight_grad_t* d, void* workspace,
                                     size_t workspace_bytes, muon_stream_t stream);
+
+/* Tokens sorted by expert.  A token t has topk copies, copy t * topk + k for its
+ * choice k.  A copy whose choice is an expert gets a row: rows lie one expert
+ * after the other, an expert's rows in the order of its copies.
+ * rows: of every buffer that is indexed by row below (tokens * topk holds any
+ * batch); copies behind the last of them get no row, which sets MUON_FLAG_INDEX.
+ * offsets: device [experts + 1], first row of each expert and the end of the last
+ * (as muon_weight_grad_t takes them).  order: device [rows], the copy that a row
+ * holds; entries from offsets[experts] on stay as they were.  place: device
+ * [tokens][topk], the row of a copy, -1 = none.  experts, topk <= 1024;
+ * tokens * topk < 2^31.
+ * The passes over activations read place alone (offsets and order may be NULL
+ * there); a place outside [0, rows) is taken as none. */
+typedef struct {
+  int64_t tokens, rows;
+  int experts, topk;
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* place;
+} muon_routing_t;
+
+/* Bytes of workspace muon_moe_sort needs.  Host only. */
+muon_status_t muon_moe_sort_workspace_size(int64_t tokens, int experts, int topk, size_t* bytes);
+
+/* chosen, chosen_bytes, chosen_stride, token_mask: as in muon_balance_t (-1 = not
+ * sent anywhere; any other value outside [0, experts) is taken as that and sets
+ * MUON_FLAG_INDEX; the choices of masked tokens are not read).  Two equal choices
+ * of a token are two copies.  Status word in the workspace. */
+muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen_stride,
+                            const uint8_t* token_mask, const muon_routing_t* routing,
+                            void* workspace, size_t workspace_bytes, muon_stream_t stream);
+
+/* Activations go to the rows and back.  Operands by token have `tokens` rows of
+ * `width` values, operands by row have `rows`; each has its own row stride (in
+ * elements) and may start anywhere; types may differ.  Rows without a copy are
+ * neither read nor written.  Sums are fp32, over k in ascending order, rounded once.
+ * Inputs and outputs may not overlap unless an argument says so.  No workspace. */
+
+/* xs[place[t][k]] = x[t].  x8: NULL, or a checkpoint (rows x width) that receives
+ * the same rows, from x's own values. */
+muon_status_t muon_moe_dispatch(const void* x, muon_dtype_t xdt, int64_t x_stride,
+                                const muon_routing_t* routing, int width, void* xs,
+                                muon_dtype_t xsdt, int64_t xs_stride, const muon_act8_t* x8,
+                                muon_stream_t stream);
+
+/* dx[t] = sum_k dxs[place[t][k]]; accumulate: 1 = added to what dx holds. */
+muon_status_t muon_moe_dispatch_backward(const void* dxs, muon_dtype_t dxsdt, int64_t dxs_stride,
+                                         const muon_routing_t* routing, int width, void* dx,
+                                         muon_dtype_t dxdt, int64_t dx_stride, int accumulate,
+                                         muon_stream_t stream);
+
+/* out[t] = sum_k weights[t][k] * ys[place[t][k]]; accumulate: 1 = added to what out
+ * holds (a residual).  weights: device [tokens][topk] of wdt, row stride w_stride;
+ * those of copies without a row are not read. */
+muon_status_t muon_moe_combine(const void* ys, muon_dtype_t ydt, int64_t y_stride,
+                               const muon_routing_t* routing, const void* weights,
+                               muon_dtype_t wdt, int64_t w_stride, int width, void* out,
+                               muon_dtype_t odt, int64_t out_stride, int accumulate,
+                               muon_stream_t stream);
+
+/* dys[place[t][k]] = weights[t][k] * dout[t] (of ydt; dys may be ys itself, same stride),
+ * dweights[t][k] = sum over the columns of ys[place[t][k]] * dout[t], of wdt; 0 for
+ * copies without a row. */
+muon_status_t muon_moe_combine_backward(const void* dout, muon_dtype_t ddt, int64_t dout_stride,
+                                        const void* ys, muon_dtype_t ydt, int64_t y_stride,
+                                        const muon_routing_t* routing, const void* weights,
+                                        muon_dtype_t wdt, int64_t w_stride, int width, void* dys,
+                                        int64_t dys_stride, void* dweights, int64_t dw_stride,
+                                        muon_stream_t stream);
 
 /* Per-kernel statistics since the last muon_profile_reset.  Launches are
  * always counted.  With profiling on, the library records a CUDA event pair

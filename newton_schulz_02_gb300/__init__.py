@@ -112,6 +112,16 @@ class muon_weight_grad_t(ctypes.Structure):
                 ("accumulate", c_int)]
 
 
+class muon_routing_t(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("rows", c_int64), ("experts", c_int), ("topk", c_int),
+                ("offsets", c_void_p), ("order", c_void_p), ("place", c_void_p)]
+
+
+class muon_grads_t(ctypes.Structure):
+    _fields_ = [("count", c_int), ("rows", c_int64), ("cols", c_int64), ("row_stride", c_int64),
+                ("dtype", c_int), ("ptrs", c_void_p)]
+
+
 # C prototypes: name -> (restype, argtypes)
 PROTOTYPES = {
     "muon_ns_hybrid_schedule": (c_int, [POINTER(muon_ns_schedule_t)]),
@@ -121,6 +131,9 @@ PROTOTYPES = {
                                          POINTER(muon_ns_schedule_t), POINTER(c_size_t)]),
     "muon_step_batched": (c_int, [POINTER(muon_group_t), c_int, POINTER(muon_hparams_t),
                                   POINTER(muon_ns_schedule_t), c_void_p, c_size_t, c_void_p]),
+    "muon_step_batched_scaled": (c_int, [POINTER(muon_group_t), c_int, POINTER(muon_hparams_t),
+                                         POINTER(muon_ns_schedule_t), c_void_p, c_void_p, c_size_t,
+                                         c_void_p]),
     "newton_schulz_workspace_size": (c_int, [POINTER(muon_view_t), c_int,
                                              POINTER(muon_ns_schedule_t), POINTER(c_size_t)]),
     "newton_schulz_batched": (c_int, [c_void_p, c_int, POINTER(muon_view_t), c_int, c_void_p,
@@ -139,6 +152,23 @@ PROTOTYPES = {
     "muon_status_string": (c_char_p, [c_int]),
     "muon_adamw_step": (c_int, [POINTER(muon_adamw_group_t), c_int, POINTER(muon_adamw_hparams_t),
                                 c_void_p, c_void_p]),
+    "muon_adamw_step_scaled": (c_int, [POINTER(muon_adamw_group_t), c_int,
+                                       POINTER(muon_adamw_hparams_t), c_void_p, c_void_p, c_void_p]),
+    "muon_grad_norm_workspace_size": (c_int, [POINTER(muon_grads_t), c_int, POINTER(c_size_t)]),
+    "muon_grad_norm": (c_int, [POINTER(muon_grads_t), c_int, c_float, c_void_p, c_void_p, c_void_p,
+                               c_size_t, c_void_p]),
+    "muon_moe_sort_workspace_size": (c_int, [c_int64, c_int, c_int, POINTER(c_size_t)]),
+    "muon_moe_sort": (c_int, [c_void_p, c_int, c_int64, c_void_p, POINTER(muon_routing_t), c_void_p,
+                              c_size_t, c_void_p]),
+    "muon_moe_dispatch": (c_int, [c_void_p, c_int, c_int64, POINTER(muon_routing_t), c_int, c_void_p,
+                                  c_int, c_int64, POINTER(muon_act8_t), c_void_p]),
+    "muon_moe_dispatch_backward": (c_int, [c_void_p, c_int, c_int64, POINTER(muon_routing_t), c_int,
+                                           c_void_p, c_int, c_int64, c_int, c_void_p]),
+    "muon_moe_combine": (c_int, [c_void_p, c_int, c_int64, POINTER(muon_routing_t), c_void_p, c_int,
+                                 c_int64, c_int, c_void_p, c_int, c_int64, c_int, c_void_p]),
+    "muon_moe_combine_backward": (c_int, [c_void_p, c_int, c_int64, c_void_p, c_int, c_int64,
+                                          POINTER(muon_routing_t), c_void_p, c_int, c_int64, c_int,
+                                          c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
     "muon_balance_workspace_size": (c_int, [c_int64, c_int, c_int, POINTER(c_size_t)]),
     "muon_balance_forward": (c_int, [POINTER(muon_balance_t), c_void_p, c_void_p, c_void_p,
                                      c_void_p, c_size_t, c_void_p]),
@@ -332,9 +362,25 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return ws
 
 
+def _grad_scale(scale: Optional[torch.Tensor], groups) -> Optional[int]:
+    if scale is None:
+        return None
+    dev = groups[0].ptrs.get_device() if len(groups) else scale.get_device()
+    if dev < 0:
+        raise _elsewhere("grad_scale", dev)
+    return _vector(scale, "grad_scale", torch.float32, 1, dev)
+
+
 def muon_step_batched(groups: Sequence[Group], hp: muon_hparams_t, ws: torch.Tensor,
-                      schedule=None, stream=None) -> None:
+                      schedule=None, stream=None, grad_scale: Optional[torch.Tensor] = None) -> None:
+    """grad_scale: fp32, one element, on the device: every gradient counts times it
+    (muon_grad_norm leaves the one that clips); None = 1.  Not finite: nothing changes."""
     arr = _group_array(groups)
+    if grad_scale is not None:
+        _check(load_library().muon_step_batched_scaled(
+            arr, len(groups), ctypes.byref(hp), _sched_ref(schedule), _grad_scale(grad_scale, groups),
+            ws.data_ptr(), ws.numel(), _stream(stream)), "muon_step_batched_scaled")
+        return
     _check(load_library().muon_step_batched(arr, len(groups), ctypes.byref(hp),
                                             _sched_ref(schedule), ws.data_ptr(), ws.numel(),
                                             _stream(stream)), "muon_step_batched")
@@ -425,12 +471,12 @@ def muon_profile_reset() -> None:
 
 def muon_profile_query() -> dict:
     """{kernel kind: dict(launches, total_ms, alg_flops, alg_bytes)} since the last reset."""
-    arr = (muon_kernel_stats_t * 16)()
+    arr = (muon_kernel_stats_t * 32)()
     n = c_int(0)
-    _check(load_library().muon_profile_query(arr, 16, ctypes.byref(n)), "muon_profile_query")
+    _check(load_library().muon_profile_query(arr, 32, ctypes.byref(n)), "muon_profile_query")
     return {arr[i].name.decode(): dict(launches=arr[i].launches, total_ms=arr[i].total_ms,
                                        alg_flops=arr[i].alg_flops, alg_bytes=arr[i].alg_bytes)
-            for i in range(min(n.value, 16))}
+            for i in range(min(n.value, 32))}
 
 
 # ---------------------------------------------------------------------------
@@ -492,9 +538,17 @@ def adamw_hparams(lr=2.7e-4, beta1=0.9, beta2=0.95, eps=1e-20, weight_decay=0.1,
 
 
 def muon_adamw_step(groups: Sequence[AdamWGroup], hp: muon_adamw_hparams_t,
-                    flags: Optional[torch.Tensor] = None, stream=None) -> None:
-    """flags: optional int32 device tensor of one element (MUON_FLAG_* are ORed in)."""
+                    flags: Optional[torch.Tensor] = None, stream=None,
+                    grad_scale: Optional[torch.Tensor] = None) -> None:
+    """flags: optional int32 device tensor of one element (MUON_FLAG_* are ORed in).
+    grad_scale: as for muon_step_batched."""
     arr = (muon_adamw_group_t * max(1, len(groups)))(*[g.c for g in groups])
+    if grad_scale is not None:
+        _check(load_library().muon_adamw_step_scaled(
+            arr, len(groups), ctypes.byref(hp), _grad_scale(grad_scale, groups),
+            flags.data_ptr() if flags is not None else None, _stream(stream)),
+            "muon_adamw_step_scaled")
+        return
     _check(load_library().muon_adamw_step(arr, len(groups), ctypes.byref(hp),
                                           flags.data_ptr() if flags is not None else None,
                                           _stream(stream)), "muon_adamw_step")
@@ -796,3 +850,181 @@ def muon_act8_weight_grad(dy: torch.Tensor, x8: Act8, G, ws: torch.Tensor,
                            ptrs, base, bs, gs, gdt, int(bool(accumulate)))
     _check(load_library().muon_act8_weight_grad(ctypes.byref(d), _memory_of(ws, dev), ws.numel(),
                                                 _stream_of(stream, dev)), "muon_act8_weight_grad")
+
+
+# ---------------------------------------------------------------------------
+# tokens on their way to the experts and back
+# ---------------------------------------------------------------------------
+class Routing:
+    """Where the copies of the tokens are, one expert after the other: offsets
+    (int32 [experts + 1], first row of each expert and the end of the last), order
+    (int32 [rows], copy token * topk + k of a row) and place (int32 [tokens, topk],
+    row of a copy, -1 = none).  Every buffer by row has `rows` rows, order's length:
+    tokens * topk unless fewer will do."""
+
+    __slots__ = ("offsets", "order", "place", "device", "tokens", "topk", "experts", "rows", "c", "ref")
+
+    def __init__(self, offsets: torch.Tensor, order: torch.Tensor, place: torch.Tensor):
+        if place.dim() != 2:
+            raise ValueError("place needs one row for each token")
+        self.tokens, self.topk = place.shape
+        self.experts, self.rows = offsets.numel() - 1, order.numel()
+        self.device = place.get_device()
+        if self.device < 0:
+            raise _elsewhere("place", self.device)
+        self.offsets, self.order, self.place = offsets, order, place
+        self.c = muon_routing_t(
+            self.tokens, self.rows, self.experts, self.topk,
+            _vector(offsets, "offsets", torch.int32, self.experts + 1, self.device),
+            _vector(order, "order", torch.int32, self.rows, self.device),
+            _vector(place, "place", torch.int32, self.tokens * self.topk, self.device))
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, tokens: int, topk: int, experts: int, device="cuda",
+              rows: Optional[int] = None) -> "Routing":
+        """Memory for a batch of `tokens` (its values are set by muon_moe_sort)."""
+        new = lambda *s: torch.empty(*s, dtype=torch.int32, device=device)
+        return cls(new(experts + 1), new(tokens * topk if rows is None else rows), new(tokens, topk))
+
+
+def muon_moe_sort_workspace_size(tokens: int, experts: int, topk: int) -> int:
+    nb = c_size_t(0)
+    _check(load_library().muon_moe_sort_workspace_size(int(tokens), int(experts), int(topk),
+                                                       ctypes.byref(nb)),
+           "muon_moe_sort_workspace_size")
+    return nb.value
+
+
+def muon_moe_sort(chosen: torch.Tensor, routing: Routing, ws: torch.Tensor,
+                  mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Fills `routing` from chosen [tokens, topk] (int32 or int64 expert numbers, -1 =
+    none) and mask (bool or uint8 [tokens]; None = every token is valid)."""
+    dev = routing.device
+    if chosen.dtype not in (torch.int32, torch.int64):
+        raise ValueError("chosen must be int32 or int64")
+    if chosen.get_device() != dev:
+        raise _elsewhere("chosen", dev)
+    mp = None
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be bool or uint8")
+        mp = _vector(mask, "mask", mask.dtype, routing.tokens, dev)
+    _check(load_library().muon_moe_sort(
+        chosen.data_ptr(), chosen.element_size(),
+        _rows2d(chosen, "chosen", (routing.tokens, routing.topk)), mp, routing.ref,
+        _memory_of(ws, dev), ws.numel(), _stream_of(stream, dev)), "muon_moe_sort")
+
+
+def _width(t: torch.Tensor, what: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what} needs two dimensions")
+    return t.shape[1]
+
+
+def muon_moe_dispatch(x: torch.Tensor, routing: Routing, xs: torch.Tensor,
+                      x8: Optional[Act8] = None, stream=None) -> None:
+    """xs[place[t, k]] = x[t]; x8, if given, keeps the same rows in 8 bits.  x [tokens,
+    width], xs [rows, width]; rows without a copy stay as they were."""
+    dev, width = routing.device, _width(x, "x")
+    if x8 is not None and x8.device != dev:
+        raise _elsewhere("x8", dev)
+    _check(load_library().muon_moe_dispatch(
+        x.data_ptr(), _dtype(x, "x", dev), _rows2d(x, "x", (routing.tokens, width)), routing.ref, width,
+        xs.data_ptr(), _dtype(xs, "xs", dev), _rows2d(xs, "xs", (routing.rows, width)),
+        None if x8 is None else x8.ref, _stream_of(stream, dev)), "muon_moe_dispatch")
+
+
+def muon_moe_dispatch_backward(dxs: torch.Tensor, routing: Routing, dx: torch.Tensor,
+                               accumulate: bool = False, stream=None) -> None:
+    """dx[t] (+)= the sum of dxs at the token's rows."""
+    dev, width = routing.device, _width(dx, "dx")
+    _check(load_library().muon_moe_dispatch_backward(
+        dxs.data_ptr(), _dtype(dxs, "dxs", dev), _rows2d(dxs, "dxs", (routing.rows, width)), routing.ref,
+        width, dx.data_ptr(), _dtype(dx, "dx", dev), _rows2d(dx, "dx", (routing.tokens, width)),
+        int(bool(accumulate)), _stream_of(stream, dev)), "muon_moe_dispatch_backward")
+
+
+def muon_moe_combine(ys: torch.Tensor, weights: torch.Tensor, routing: Routing, out: torch.Tensor,
+                     accumulate: bool = False, stream=None) -> None:
+    """out[t] (+)= sum_k weights[t, k] * ys[place[t, k]].  weights [tokens, topk] (bf16 or fp32)."""
+    dev, width = routing.device, _width(out, "out")
+    _check(load_library().muon_moe_combine(
+        ys.data_ptr(), _dtype(ys, "ys", dev), _rows2d(ys, "ys", (routing.rows, width)), routing.ref,
+        weights.data_ptr(), _dtype(weights, "weights", dev),
+        _rows2d(weights, "weights", (routing.tokens, routing.topk)), width, out.data_ptr(),
+        _dtype(out, "out", dev), _rows2d(out, "out", (routing.tokens, width)), int(bool(accumulate)),
+        _stream_of(stream, dev)), "muon_moe_combine")
+
+
+def muon_moe_combine_backward(dout: torch.Tensor, ys: torch.Tensor, weights: torch.Tensor,
+                              routing: Routing, dys: torch.Tensor, dweights: torch.Tensor,
+                              stream=None) -> None:
+    """dys[place[t, k]] = weights[t, k] * dout[t] (dys may be ys); dweights[t, k] = the
+    product of ys[place[t, k]] and dout[t] summed over the columns."""
+    dev, width = routing.device, _width(dout, "dout")
+    if dys.dtype != ys.dtype or dweights.dtype != weights.dtype:
+        raise ValueError("dys needs the dtype of ys, dweights that of weights")
+    _dtype(dys, "dys", dev)
+    _dtype(dweights, "dweights", dev)
+    rows, choices = (routing.rows, width), (routing.tokens, routing.topk)
+    _check(load_library().muon_moe_combine_backward(
+        dout.data_ptr(), _dtype(dout, "dout", dev), _rows2d(dout, "dout", (routing.tokens, width)),
+        ys.data_ptr(), _dtype(ys, "ys", dev), _rows2d(ys, "ys", rows), routing.ref, weights.data_ptr(),
+        _dtype(weights, "weights", dev), _rows2d(weights, "weights", choices), width, dys.data_ptr(),
+        _rows2d(dys, "dys", rows), dweights.data_ptr(), _rows2d(dweights, "dweights", choices),
+        _stream_of(stream, dev)), "muon_moe_combine_backward")
+
+
+# ---------------------------------------------------------------------------
+# the norm of all gradients, and clipping
+# ---------------------------------------------------------------------------
+class Grads:
+    """The gradients of a model: of Groups and AdamWGroups (their G tensors), and
+    tensors that are in no group (contiguous, bf16 or fp32, 16-byte aligned)."""
+
+    def __init__(self, items: Sequence):
+        self.items = list(items)
+        free = [t for t in self.items if isinstance(t, torch.Tensor)]
+        if not self.items:
+            raise ValueError("no gradients")
+        first = self.items[0]
+        self.device = (first if isinstance(first, torch.Tensor) else first.ptrs).get_device()
+        for t in free:
+            _dtype(t, "a gradient", self.device)
+            if not t.is_contiguous():
+                raise ValueError("a gradient outside a group has to be contiguous")
+        self.ptrs = torch.tensor([t.data_ptr() for t in free], dtype=torch.int64).to(
+            free[0].device if free else "cpu")
+        at, descs = self.ptrs.data_ptr(), []
+        for g in self.items:
+            if isinstance(g, torch.Tensor):
+                descs.append(muon_grads_t(1, 1, g.numel(), g.numel(), _DT[g.dtype], at))
+                at += 8
+                continue
+            if g.ptrs.get_device() != self.device or self.device < 0:
+                raise _elsewhere("a group", self.device)
+            if isinstance(g, Group):
+                v = g.c.view
+                descs.append(muon_grads_t(g.c.batch, v.rows, v.cols, v.row_stride, g.c.g_dtype, g.c.g_ptrs))
+            else:
+                descs.append(muon_grads_t(g.c.count, 1, g.c.numel, g.c.numel, g.c.g_dtype, g.c.g_ptrs))
+        self.c = (muon_grads_t * len(descs))(*descs)
+
+
+def muon_grad_norm_workspace_size(grads: Grads) -> int:
+    nb = c_size_t(0)
+    _check(load_library().muon_grad_norm_workspace_size(grads.c, len(grads.c), ctypes.byref(nb)),
+           "muon_grad_norm_workspace_size")
+    return nb.value
+
+
+def muon_grad_norm(grads: Grads, norm: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
+                   max_norm: float = float("inf"), stream=None) -> None:
+    """norm (fp32, one element) = the norm of all gradients together; scale (the same) =
+    min(1, max_norm / (norm + 1e-6)), what the steps take as grad_scale."""
+    dev = grads.device
+    _check(load_library().muon_grad_norm(
+        grads.c, len(grads.c), float(max_norm), _vector(norm, "norm", torch.float32, 1, dev),
+        _vector(scale, "scale", torch.float32, 1, dev), _memory_of(ws, dev), ws.numel(),
+        _stream_of(stream, dev)), "muon_grad_norm")

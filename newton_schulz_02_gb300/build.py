@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libmuon_gb300.so")
 SOURCES = ["muon_api.cu", "elementwise.cu", "ns_gemm.cu", "prof.cu", "noalloc.cu", "adamw.cu",
-           "balance.cu", "act8.cu", "act8_wgrad.cu"]
+           "balance.cu", "act8.cu", "act8_wgrad.cu", "moe.cu", "grad_norm.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "planes.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

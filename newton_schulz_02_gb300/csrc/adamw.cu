@@ -35,6 +35,7 @@ struct AdamWLaunch {
   int64_t item_begin[kAdamWMaxGroups + 1];  // prefix sums of work items per group
   AdamWGroupArgs g[kAdamWMaxGroups];
   float lr, beta1, omb1, beta2, omb2, eps, c1, c2, decay_on;
+  const float* grad_scale;
   uint32_t* flags;
 };
 
@@ -99,6 +100,11 @@ __device__ __forceinline__ bool misaligned16(const void* p) {
 
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamWLaunch p) {
   const int64_t total = p.item_begin[p.n_groups];
+  const float gscale = p.grad_scale == nullptr ? 1.f : *p.grad_scale;
+  if (!isfinite(gscale)) {   // nothing is updated
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags != nullptr) atomicOr(p.flags, MUON_FLAG_NONFINITE);
+    return;
+  }
   for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
     int gi = 0;
     while (gi + 1 < p.n_groups && item >= p.item_begin[gi + 1]) ++gi;
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
       if (full[r]) {
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-          Elem e{W[r][k], Gv[r][k], Mv[r][k], Vv[r][k]};
+          Elem e{W[r][k], Gv[r][k] * gscale, Mv[r][k], Vv[r][k]};
           adamw_elem(p, decay, e);
           W[r][k] = e.w; Mv[r][k] = e.m; Vv[r][k] = e.v;
         }
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
       } else if (idx[r] < G.numel) {
         // ragged tail of the tensor (numel % 8 elements)
         for (int64_t i = idx[r]; i < G.numel; ++i) {
-          Elem e{ld1(w, i, G.w_dtype), ld1(g, i, G.g_dtype), m[i], v[i]};
+          Elem e{ld1(w, i, G.w_dtype), ld1(g, i, G.g_dtype) * gscale, m[i], v[i]};
           adamw_elem(p, decay, e);
           st1(w, i, G.w_dtype, e.w);
           m[i] = e.m;
@@ -196,6 +202,7 @@ cudaError_t launch_adamw(AdamWGroupArgs* groups, int n_groups, const AdamWScalar
     if (items == 0) continue;
     p.lr = s.lr; p.beta1 = s.beta1; p.omb1 = s.omb1; p.beta2 = s.beta2; p.omb2 = s.omb2;
     p.eps = s.eps; p.c1 = s.c1; p.c2 = s.c2; p.decay_on = s.decay_on;
+    p.grad_scale = s.grad_scale;
     p.flags = flags;
     // persistent grid: every resident block (a multiple of the SM count)
     const int grid = static_cast<int>(items < resident ? items : resident);

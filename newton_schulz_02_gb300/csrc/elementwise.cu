@@ -104,9 +104,13 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 // Momentum / look-ahead / load of 8 consecutive elements at `off`.
 __device__ __forceinline__ void prepare8(const PrepareArgs& p, const void* g, float* m,
-                                         int64_t off, float (&x)[8]) {
+                                         float gscale, int64_t off, float (&x)[8]) {
   float gv[8];
   load8(g, off, p.g_dtype, gv);
+  if (p.grad_scale != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) gv[k] *= gscale;
+  }
   if (p.mode == kPrepLoad) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = gv[k];
@@ -137,7 +141,8 @@ __device__ __forceinline__ void prepare8(const PrepareArgs& p, const void* g, fl
 struct MatrixPtrs {
   const void* g;
   float* m;
-  bool skip;
+  float scale;     // of the gradient
+  uint32_t skip;   // why the matrix is left untouched (status bits); 0: it is not
 };
 
 __device__ __forceinline__ MatrixPtrs matrix_ptrs(const PrepareArgs& p, int b) {
@@ -149,7 +154,8 @@ __device__ __forceinline__ MatrixPtrs matrix_ptrs(const PrepareArgs& p, int b) {
   r.m = (p.mode == kPrepLoad) ? nullptr : p.m_ptrs[b];
   bool bad = misaligned16(r.g) || (r.m && misaligned16(r.m));
   if (p.w_ptrs) bad = bad || misaligned16(p.w_ptrs[b]);
-  r.skip = bad;
+  r.scale = p.grad_scale == nullptr ? 1.f : *p.grad_scale;
+  r.skip = (bad ? kFlagMisaligned : 0u) | (isfinite(r.scale) ? 0u : kFlagNonFinite);
   return r;
 }
 
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) k_prepare_wide(PrepareArgs p) {
   const MatrixPtrs mp = matrix_ptrs(p, b);
   if (mp.skip && blockIdx.x == 0 && threadIdx.x == 0) {
     p.skip[b] = 1;
-    atomicOr(p.status, kFlagMisaligned);
+    atomicOr(p.status, mp.skip);
   }
   const int64_t vpr = p.m_pad / 8;
   const int64_t total = static_cast<int64_t>(p.n_pad) * vpr;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_prepare_wide(PrepareArgs p) {
     const int j = static_cast<int>(v - static_cast<int64_t>(i) * vpr) * 8;
     float x[8];
     if (!mp.skip && i < p.rows && j < p.cols) {
-      prepare8(p, mp.g, mp.m, static_cast<int64_t>(i) * p.row_stride + j, x);
+      prepare8(p, mp.g, mp.m, mp.scale, static_cast<int64_t>(i) * p.row_stride + j, x);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc = fmaf(x[k], x[k], acc);
     } else {
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) k_prepare_tall(PrepareArgs p) {
   const MatrixPtrs mp = matrix_ptrs(p, b);
   if (mp.skip && blockIdx.x == 0 && threadIdx.x == 0) {
     p.skip[b] = 1;
-    atomicOr(p.status, kFlagMisaligned);
+    atomicOr(p.status, mp.skip);
   }
   // source tiles: rows (m dimension) x cols (n dimension)
   const int tiles_i = p.m_pad / kTile, tiles_j = p.n_pad / kTile;
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) k_prepare_tall(PrepareArgs p) {
       const int i = i0 + r, j = j0 + c8;
       float x[8];
       if (!mp.skip && i < p.rows && j < p.cols) {
-        prepare8(p, mp.g, mp.m, static_cast<int64_t>(i) * p.row_stride + j, x);
+        prepare8(p, mp.g, mp.m, mp.scale, static_cast<int64_t>(i) * p.row_stride + j, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc = fmaf(x[e], x[e], acc);
       } else {

@@ -1,0 +1,336 @@
+// Norm of all gradients of a model together and the factor that clips it
+// (muon_grad_norm).
+//
+//   n = sqrt(sum over all tensors of g^2),  scale = min(1, max_norm / (n + 1e-6))
+//
+// One pass: every gradient is read once, and nothing else of size is moved (the
+// optimizer steps multiply by the scale where they read the gradient), so HBM's
+// read rate is the bound.  Tensors of any number and size share a launch: a
+// persistent grid strides over fixed pieces of every tensor.
+//
+// A thread adds the squares of 32 values in fp32 and those sums in a pair of
+// fp32 (the rounding error of each addition is kept in the second), which
+// costs 7 additions for 32 values and holds 48 bits; an fp64 addition for each
+// value would take five times as long as the reads.  Squares outside fp32's
+// comfortable range (the sum of 32 below 2^-96 or above 2^90, infinite or NaN)
+// are added up in fp64 instead, value by value.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "planes.cuh"
+#include "ptx.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;                                       // values of a vector
+constexpr int kUnroll = 4;                                    // vectors of a thread in a piece
+constexpr int64_t kPiece = int64_t{kThreads} * kVec * kUnroll;
+constexpr int kMaxGroups = 64;                                // groups of a launch
+constexpr int kFinThreads = 1024;
+constexpr size_t kHeader = 256;
+
+struct NormGroup {
+  const void* const* ptrs;
+  int64_t vecs;              // whole vectors of a tensor
+  int64_t pieces;            // pieces of a tensor
+  int64_t stride;            // vectors between rows; 0: one run of values
+  Divider per_row;           // vectors of a row
+  int tail;                  // values after the last whole vector
+  int dtype;
+};
+
+struct NormArgs {
+  int groups;
+  int64_t begin[kMaxGroups + 1];   // first piece of a group
+  NormGroup g[kMaxGroups];
+  double* sums;                    // [blocks] of this launch
+  uint32_t* flags;                 // [blocks]
+};
+
+struct Sum {
+  float hi, lo;
+  double wide;
+};
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < kVec; ++k)
+    x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+}
+
+// Adds the squares of a thread's values of a piece.
+__device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kVec]) {
+  float part[kUnroll];
+#pragma unroll
+  for (int r = 0; r < kUnroll; ++r) {
+    part[r] = x[r][0] * x[r][0];
+#pragma unroll
+    for (int k = 1; k < kVec; ++k) part[r] = fmaf(x[r][k], x[r][k], part[r]);
+  }
+  const float sq = (part[0] + part[1]) + (part[2] + part[3]);
+  if (sq >= 0x1p-96f && sq <= 0x1p90f) {
+    const float t = s.hi + sq, b = t - s.hi;
+    s.lo += (s.hi - (t - b)) + (sq - b);
+    s.hi = t;
+    return;
+  }
+#pragma unroll 1
+  for (int r = 0; r < kUnroll; ++r)
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const float v = r == 0 ? x[0][k] : r == 1 ? x[1][k] : r == 2 ? x[2][k] : x[3][k];
+      if (v != 0.f) s.wide = fma(static_cast<double>(v), static_cast<double>(v), s.wide);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
+  griddep_launch_dependents();
+  const int64_t total = a.begin[a.groups];
+  Sum s{0.f, 0.f, 0.0};
+  uint32_t flags = 0;
+  int gi = 0;
+  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    while (item >= a.begin[gi + 1]) ++gi;
+    const NormGroup& G = a.g[gi];
+    const int64_t local = item - a.begin[gi];
+    const int64_t tensor = local / G.pieces;
+    const int64_t piece = local - tensor * G.pieces;
+    const char* p = static_cast<const char*>(G.ptrs[tensor]);
+    if (!((reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
+      flags |= MUON_FLAG_MISALIGNED;
+      continue;   // the tensor is left out
+    }
+    const int64_t v0 = piece * (kPiece / kVec);
+    float x[kUnroll][kVec];
+    int64_t at[kUnroll];   // vectors from the tensor's start; -1: none
+    if (G.stride == 0) {
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const int64_t v = v0 + r * kThreads + threadIdx.x;
+        at[r] = v < G.vecs ? v : -1;
+      }
+    } else {
+      const int64_t row0 = v0 / G.per_row.d;
+      const uint32_t col0 = static_cast<uint32_t>(v0 - row0 * G.per_row.d);
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const uint32_t c = col0 + r * kThreads + threadIdx.x;
+        const uint32_t down = quotient(c, G.per_row);
+        at[r] = v0 + r * kThreads + threadIdx.x < G.vecs ? (row0 + down) * G.stride + (c - down * G.per_row.d) : -1;
+      }
+    }
+    if (G.dtype == MUON_BF16) {
+      uint4 u[kUnroll];
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        u[r] = make_uint4(0, 0, 0, 0);
+        if (at[r] >= 0) u[r] = reinterpret_cast<const uint4*>(p)[at[r]];
+      }
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) unpack(u[r], x[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        float4 q[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (at[r] >= 0) {
+          q[0] = reinterpret_cast<const float4*>(p)[2 * at[r]];
+          q[1] = reinterpret_cast<const float4*>(p)[2 * at[r] + 1];
+        }
+        x[r][0] = q[0].x; x[r][1] = q[0].y; x[r][2] = q[0].z; x[r][3] = q[0].w;
+        x[r][4] = q[1].x; x[r][5] = q[1].y; x[r][6] = q[1].z; x[r][7] = q[1].w;
+      }
+    }
+    if (G.tail > 0 && piece == G.pieces - 1 && threadIdx.x < G.tail) {   // fewer than 8 values
+      const int64_t i = G.vecs * kVec + threadIdx.x;
+      const float v = G.dtype == MUON_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
+                                           : reinterpret_cast<const float*>(p)[i];
+      s.wide = fma(static_cast<double>(v), static_cast<double>(v), s.wide);
+    }
+    add_squares(s, x);
+  }
+  // the block's sum, in a fixed order
+  __shared__ double red[kThreads / 32];
+  double d = (static_cast<double>(s.hi) + static_cast<double>(s.lo)) + s.wide;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
+  const int any = __syncthreads_or(flags != 0);
+  if (threadIdx.x == 0) {
+    d = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) d += red[w];
+    a.sums[blockIdx.x] = d;
+    a.flags[blockIdx.x] = any ? MUON_FLAG_MISALIGNED : 0u;
+  }
+}
+
+struct FinishArgs {
+  const double* sums;
+  const uint32_t* flags;
+  int blocks;
+  float max_norm;
+  float* norm;
+  float* scale;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kFinThreads) k_grad_norm_finish(FinishArgs a) {
+  griddep_wait();
+  __shared__ double red[kFinThreads / 32];
+  double d = 0.0;
+  uint32_t f = 0;
+  for (int i = threadIdx.x; i < a.blocks; i += kFinThreads) {
+    d += a.sums[i];
+    f |= a.flags[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
+  const int any = __syncthreads_or(f != 0);
+  if (threadIdx.x == 0) {
+    d = red[0];
+    for (int w = 1; w < kFinThreads / 32; ++w) d += red[w];
+    const double n = sqrt(d);
+    const bool finite = isfinite(n);
+    *a.norm = static_cast<float>(n);
+    *a.scale = finite ? static_cast<float>(fmin(1.0, static_cast<double>(a.max_norm) / (n + 1e-6)))
+                      : __uint_as_float(0x7FC00000u);
+    *a.status = (any ? MUON_FLAG_MISALIGNED : 0u) | (finite ? 0u : MUON_FLAG_NONFINITE);
+  }
+}
+
+// Blocks of a launch: every resident block of the current device, at most one a piece.
+cudaError_t resident_blocks(int* out) {
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_grad_norm, kThreads, 0);
+  if (e != cudaSuccess) return e;
+  *out = sms * (per_sm > 0 ? per_sm : 1);
+  return cudaSuccess;
+}
+
+constexpr int kMaxBlocks = 2048;   // of a launch: SMs x 8 blocks of 256 threads, and more
+
+bool empty(const muon_grads_t& g) { return g.count == 0 || g.rows == 0 || g.cols == 0; }
+
+muon_status_t check_grads(const muon_grads_t* g, int n_groups, int* used) {
+  if (n_groups < 0 || (n_groups > 0 && g == nullptr)) return MUON_ERR_INVALID_ARG;
+  *used = 0;
+  for (int i = 0; i < n_groups; ++i) {
+    if (g[i].count < 0 || g[i].rows < 0 || g[i].cols < 0) return MUON_ERR_INVALID_ARG;
+    if (g[i].dtype != MUON_BF16 && g[i].dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
+    if (empty(g[i])) continue;
+    if (g[i].ptrs == nullptr) return MUON_ERR_INVALID_ARG;
+    if (!at_multiple(g[i].ptrs, 8)) return MUON_ERR_MISALIGNED;
+    if (g[i].rows > 1) {
+      if (g[i].row_stride < g[i].cols) return MUON_ERR_INVALID_ARG;
+      if (g[i].row_stride > g[i].cols) {
+        if (g[i].cols % kVec != 0 || g[i].cols > (int64_t{1} << 32)) return MUON_ERR_UNSUPPORTED;
+        if (g[i].row_stride % kVec != 0) return MUON_ERR_MISALIGNED;
+      }
+      if (g[i].rows > (int64_t{1} << 62) / g[i].row_stride) return MUON_ERR_UNSUPPORTED;
+    }
+    ++*used;
+  }
+  return MUON_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int launches_of(int used) { return (used + kMaxGroups - 1) / kMaxGroups; }
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status_t muon_grad_norm_workspace_size(const muon_grads_t* groups, int n_groups, size_t* bytes) {
+  if (bytes == nullptr) return MUON_ERR_INVALID_ARG;
+  int used = 0;
+  const muon_status_t s = check_grads(groups, n_groups, &used);
+  if (s != MUON_OK) return s;
+  *bytes = kHeader + align256(static_cast<size_t>(launches_of(used)) * kMaxBlocks * 12);
+  return MUON_OK;
+}
+
+muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max_norm, float* norm,
+                             float* scale, void* workspace, size_t workspace_bytes,
+                             muon_stream_t stream) {
+  int used = 0;
+  muon_status_t s = check_grads(groups, n_groups, &used);
+  if (s != MUON_OK) return s;
+  if (!(max_norm >= 0.f) || norm == nullptr || scale == nullptr || workspace == nullptr)
+    return MUON_ERR_INVALID_ARG;
+  if (!at_multiple(norm, 4) || !at_multiple(scale, 4) || !at_multiple(workspace, 256))
+    return MUON_ERR_MISALIGNED;
+  size_t need = 0;
+  s = muon_grad_norm_workspace_size(groups, n_groups, &need);
+  if (s != MUON_OK) return s;
+  if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
+
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  double* sums = reinterpret_cast<double*>(ws + kHeader);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(sums + static_cast<size_t>(launches_of(used)) * kMaxBlocks);
+  int resident = 0;
+  if (resident_blocks(&resident) != cudaSuccess) return MUON_ERR_CUDA;
+  if (resident > kMaxBlocks) resident = kMaxBlocks;
+  int blocks = 0, next = 0;
+  while (next < n_groups) {
+    NormArgs a{};
+    double bytes = 0.0;
+    for (; next < n_groups && a.groups < kMaxGroups; ++next) {
+      const muon_grads_t& src = groups[next];
+      if (empty(src)) continue;
+      NormGroup& g = a.g[a.groups];
+      const int64_t values = src.rows * src.cols;
+      const bool strided = src.rows > 1 && src.row_stride > src.cols;
+      g.ptrs = src.ptrs;
+      g.vecs = values / kVec;
+      g.tail = static_cast<int>(values % kVec);
+      g.pieces = (values + kPiece - 1) / kPiece;
+      g.stride = strided ? src.row_stride / kVec : 0;
+      g.per_row = divider(strided ? static_cast<uint32_t>(src.cols / kVec) : 1);
+      g.dtype = src.dtype;
+      a.begin[a.groups + 1] = a.begin[a.groups] + g.pieces * src.count;
+      bytes += static_cast<double>(values) * src.count * esize(src.dtype);
+      ++a.groups;
+    }
+    const int64_t items = a.begin[a.groups];
+    if (items == 0) break;
+    const int grid = static_cast<int>(items < resident ? items : resident);
+    a.sums = sums + blocks;
+    a.flags = flags + blocks;
+    blocks += grid;
+    prof_begin(kKindGradNorm, st);
+    k_grad_norm<<<grid, kThreads, 0, st>>>(a);
+    prof_end(kKindGradNorm, st, 0.0, bytes);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  FinishArgs f{sums, flags, blocks, max_norm, norm, scale, reinterpret_cast<uint32_t*>(ws)};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kFinThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 0 ? 1 : 0;
+  prof_begin(kKindGradNorm, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_norm_finish, f);
+  prof_end(kKindGradNorm, st, 0.0, 12.0 * blocks);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -51,6 +51,7 @@ struct PrepareArgs {
   float mu;            // sgd: mu; ema: beta
   double ema_omb;      // ema: 1 - beta (exact, from the fp32 beta)
   float c_mom, c_grad;  // ema look-ahead: X = c_mom*buf + c_grad*g
+  const float* grad_scale;  // device: G counts times this, nothing if it is not finite; nullptr = 1
   __nv_bfloat16* X;     // hi plane [batch][n_pad][m_pad]; lo plane at X + x_lo_off
   int64_t x_lo_off;
   int n_pad, m_pad;
@@ -165,6 +166,8 @@ enum KernelKind : int {
   kKindAct8,
   kKindSwiglu,
   kKindWeightGrad,
+  kKindMoe,
+  kKindGradNorm,
   kKindCount
 };
 void prof_begin(KernelKind k, cudaStream_t st);
@@ -195,6 +198,7 @@ struct AdamWScalars {
   float lr, beta1, omb1, beta2, omb2, eps;
   float c1, c2;              // 1/(1 - beta1^t), 1/(1 - beta2^t)
   float decay_on;            // 1 - lr*wd
+  const float* grad_scale;   // device: G counts times this, nothing if it is not finite; nullptr = 1
 };
 
 cudaError_t launch_adamw(AdamWGroupArgs* groups, int n_groups, const AdamWScalars& s,

@@ -381,6 +381,14 @@ muon_status_t muon_step_workspace_size(const muon_group_t* groups, int n_groups,
 muon_status_t muon_step_batched(const muon_group_t* groups, int n_groups,
                                 const muon_hparams_t* hp, const muon_ns_schedule_t* schedule,
                                 void* workspace, size_t workspace_bytes, muon_stream_t stream) {
+  return muon_step_batched_scaled(groups, n_groups, hp, schedule, nullptr, workspace, workspace_bytes,
+                                  stream);
+}
+
+muon_status_t muon_step_batched_scaled(const muon_group_t* groups, int n_groups,
+                                       const muon_hparams_t* hp, const muon_ns_schedule_t* schedule,
+                                       const float* grad_scale, void* workspace,
+                                       size_t workspace_bytes, muon_stream_t stream) {
   if (hp == nullptr || n_groups < 0 || (n_groups > 0 && groups == nullptr))
     return MUON_ERR_INVALID_ARG;
   if (!std::isfinite(hp->mu) || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay) ||
@@ -411,6 +419,7 @@ muon_status_t muon_step_batched(const muon_group_t* groups, int n_groups,
   if (s != MUON_OK) return s;
   s = check_workspace(workspace, workspace_bytes, need);
   if (s != MUON_OK) return s;
+  if (!at_multiple(grad_scale, 4)) return MUON_ERR_MISALIGNED;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
@@ -454,6 +463,7 @@ muon_status_t muon_step_batched(const muon_group_t* groups, int n_groups,
       pa.ema_omb = 1.0 - beta;
       pa.c_mom = static_cast<float>(c_mom);
       pa.c_grad = static_cast<float>(c_grad);
+      pa.grad_scale = grad_scale;
       pa.X = reinterpret_cast<__nv_bfloat16*>(ws + L.x0) + off * L.n_pad * L.m_pad;
       pa.x_lo_off = L.lo_off;
       pa.n_pad = L.n_pad;
@@ -616,6 +626,12 @@ muon_status_t muon_occupy_sms(int blocks, size_t smem_bytes, uint64_t ns, muon_s
 muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
                               const muon_adamw_hparams_t* hp, uint32_t* device_flags,
                               muon_stream_t stream) {
+  return muon_adamw_step_scaled(groups, n_groups, hp, nullptr, device_flags, stream);
+}
+
+muon_status_t muon_adamw_step_scaled(const muon_adamw_group_t* groups, int n_groups,
+                                     const muon_adamw_hparams_t* hp, const float* grad_scale,
+                                     uint32_t* device_flags, muon_stream_t stream) {
   if (hp == nullptr || n_groups < 0 || (n_groups > 0 && groups == nullptr))
     return MUON_ERR_INVALID_ARG;
   if (hp->t < 1 || !(hp->beta1 >= 0.f && hp->beta1 < 1.f) || !(hp->beta2 >= 0.f && hp->beta2 < 1.f))
@@ -623,7 +639,7 @@ muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
   if (!(hp->eps >= 0.f) || !std::isfinite(hp->eps) || !std::isfinite(hp->lr) ||
       !std::isfinite(hp->weight_decay))
     return MUON_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(device_flags) & 3u) != 0) return MUON_ERR_MISALIGNED;
+  if (!at_multiple(device_flags, 4) || !at_multiple(grad_scale, 4)) return MUON_ERR_MISALIGNED;
   std::vector<AdamWGroupArgs> args;
   args.reserve(static_cast<size_t>(n_groups));
   for (int i = 0; i < n_groups; ++i) {
@@ -658,6 +674,7 @@ muon_status_t muon_adamw_step(const muon_adamw_group_t* groups, int n_groups,
   sc.c1 = static_cast<float>(1.0 / (1.0 - std::pow(b1, t)));
   sc.c2 = static_cast<float>(1.0 / (1.0 - std::pow(b2, t)));
   sc.decay_on = static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
+  sc.grad_scale = grad_scale;
   return cuda_status(launch_adamw(args.data(), static_cast<int>(args.size()), sc, device_flags,
                                   reinterpret_cast<cudaStream_t>(stream)));
 }

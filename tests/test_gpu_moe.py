@@ -1,0 +1,412 @@
+"""Tokens sorted by expert, dispatched and combined, with their gradients, on the
+GPU against the float64 oracle (oracle/moe_ref.py).
+
+Numbers of the sort are exact.  Tolerances of the others, U = 2^-24, HALF of a type
+half a step relative to the value (bf16 2^-8, fp32 U):
+  dispatch   a value is rounded to its row's type once: HALF |x|; checkpoints are
+             those that muon_act8_pack writes of the same values, bit for bit.
+  combine    at most K products and additions in a chain, and one more when it
+             accumulates: (K + 2) U times the sum of the terms' magnitudes; HALF.
+  gradients  one product and its rounding: 2 HALF of dys.  dweights: the D products
+             are added up in fp32, in whatever order, by at most D additions:
+             (D + 2) U times the sum of their magnitudes; HALF."""
+import numpy as np
+import pytest
+import torch
+
+import newton_schulz_02_gb300 as m
+from oracle import moe_ref as R
+from tests.gpu_util import f64
+from tests.test_gpu_train import framed, put, untouched, within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+
+
+@pytest.fixture(autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    m.load_library()
+    torch.cuda.set_device(0)
+
+
+def choices(seed, T, E, K, drop=0.0):
+    """Choices of a router that likes some experts more; a token may choose one twice."""
+    rng = np.random.default_rng(seed)
+    p = rng.random(E) ** 3 + 1e-3
+    c = rng.choice(E, size=(T, K), p=p / p.sum())
+    c[rng.random((T, K)) < drop] = -1
+    return c
+
+
+def run_sort(chosen, E, mask=None, rows=None, idx=torch.int64, stride=None):
+    """(routing, flags) with every output set to a mark before."""
+    T, K = chosen.shape
+    c = torch.full((T, stride or K), 10 ** 6, dtype=idx, device=DEV)[:, :K]
+    c.copy_(torch.as_tensor(chosen))
+    r = m.Routing.empty(T, K, E, rows=rows)
+    for t in (r.offsets, r.order, r.place):
+        t.fill_(-77)
+    ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+    ws.fill_(255)
+    mk = None if mask is None else torch.as_tensor(mask).to(DEV)
+    m.muon_moe_sort(c, r, ws, mask=mk)
+    code, flags = m.muon_get_status(ws)
+    assert code == m.MUON_OK
+    return r, flags
+
+
+def check_sort(r, flags, chosen, E, mask=None, rows=None):
+    offsets, order, place, bad = R.sort(chosen, E, mask, rows)
+    assert r.offsets.tolist() == offsets.tolist()
+    got = r.order.cpu().numpy()
+    assert np.array_equal(got[:len(order)], order)
+    assert (got[len(order):] == -77).all()      # rows behind the last stay as they were
+    assert np.array_equal(r.place.cpu().numpy(), place)
+    assert flags == (m.MUON_FLAG_INDEX if bad else 0)
+
+
+@pytest.mark.parametrize("T,E,K", [(0, 4, 2), (1, 1, 1), (1, 8, 8), (33, 8, 2), (100, 7, 3), (511, 60, 6),
+                                   (1024, 16, 1), (1025, 1024, 8), (4097, 257, 2), (9000, 1000, 1),
+                                   (20011, 33, 5)])
+@pytest.mark.parametrize("idx", [torch.int32, torch.int64])
+def test_sort(T, E, K, idx):
+    chosen = choices(T + E, T, E, K, drop=0.1)
+    mask = np.random.default_rng(1).random(T) > 0.2
+    check_sort(*run_sort(chosen, E, idx=idx), chosen, E)
+    check_sort(*run_sort(chosen, E, mask, idx=idx, stride=K + 3), chosen, E, mask)
+
+
+def test_sort_more_copies_than_a_wave_holds():
+    """Blocks of several rounds: 400000 tokens of 4 choices, against a stable sort."""
+    T, E, K = 400000, 200, 4
+    chosen = torch.as_tensor(choices(5, T, E, K, drop=0.05), device=DEV)
+    r = m.Routing.empty(T, K, E)
+    r.order.fill_(-77)
+    ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+    m.muon_moe_sort(chosen, r, ws)
+    key = torch.where(chosen < 0, E, chosen).flatten()
+    want = torch.sort(key, stable=True).indices
+    n = int((key < E).sum())
+    assert r.offsets[-1].item() == n and torch.equal(r.order[:n].long(), want[:n])
+    assert bool((r.order[n:] == -77).all())
+    assert torch.equal(r.offsets.long(), torch.searchsorted(key[want], torch.arange(E + 1, device=DEV)))
+    place = torch.full((T * K,), -1, dtype=torch.int32, device=DEV)
+    place[want[:n]] = torch.arange(n, dtype=torch.int32, device=DEV)
+    assert torch.equal(r.place.flatten(), place)
+    assert m.muon_get_status(ws) == (m.MUON_OK, 0)
+
+
+@pytest.mark.parametrize("T", [300, 30000])
+def test_sort_one_expert_takes_all_and_all_tokens_masked(T):
+    one = np.full((T, 3), 5)
+    check_sort(*run_sort(one, 9), one, 9)
+    none = np.zeros(T, dtype=bool)
+    check_sort(*run_sort(one, 9, none), one, 9, none)
+
+
+@pytest.mark.parametrize("T", [50, 20000])
+def test_sort_bad_numbers_and_too_few_rows_are_flagged(T):
+    chosen = choices(3, T, 12, 2)
+    for bad in (12, -2, 2 ** 31 - 1, -(2 ** 31)):
+        c = chosen.copy()
+        c[T // 2, 1] = bad
+        check_sort(*run_sort(c, 12, idx=torch.int32), c, 12)
+    c = chosen.copy()
+    c[0, 0] = 2 ** 32 + 3      # its low half is an expert
+    check_sort(*run_sort(c, 12), c, 12)
+    for rows in (0, 1, T, 2 * T - 1, 2 * T, 2 * T + 5):
+        check_sort(*run_sort(chosen, 12, rows=rows), chosen, 12, rows=rows)
+    mask = np.ones(T, dtype=bool)
+    mask[T // 2] = False       # the choices of masked tokens are not looked at
+    c = chosen.copy()
+    c[T // 2] = 99
+    r, flags = run_sort(c, 12, mask)
+    assert flags == 0
+
+
+# ---- activations ------------------------------------------------------------
+def routed(seed, T, E, K, drop=0.15, rows=None):
+    chosen = choices(seed, T, E, K, drop)
+    r, _ = run_sort(chosen, E, rows=rows)
+    return r, r.place.cpu().numpy()
+
+
+SIZES = [(1, 1, 1, 1), (1, 3, 8, 16), (5, 4, 2, 31), (70, 8, 2, 512), (33, 60, 6, 1111), (19, 16, 9, 77),
+         (40, 5, 3, 8), (9, 4, 17, 4100), (6, 3, 2, 8193)]
+TYPES = [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")]
+
+
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("how", ["dense", "padded", "shifted"])
+@pytest.mark.parametrize("T,E,K,D", SIZES)
+def test_dispatch(outer, inner, how, T, E, K, D):
+    r, place = routed(T + D, T, E, K)
+    x = put(np.random.default_rng(D).normal(size=(T, D)), DT[outer], how)
+    buf, xs = framed(r.rows, D, DT[inner], how)
+    x8, alone = m.act8_empty(r.rows, D), m.act8_empty(r.rows, D)
+    for a in (x8, alone):
+        a.codes.fill_(99)
+        a.exps.fill_(98)
+    m.muon_moe_dispatch(x, r, xs, x8)
+    want = R.dispatch(f64(x), place, r.rows)
+    held = ~np.isnan(want[:, 0])
+    got = f64(xs)
+    within(got[held], want[held], HALF[inner] * np.abs(want[held]))
+    assert (got[~held] == 7.0).all() and untouched(buf, xs)
+    # the checkpoint: what packing the rows of x writes
+    rows = torch.as_tensor(np.where(held)[0], device=DEV)
+    source = (r.order[rows].long() // K) if len(rows) else rows
+    packed = m.act8_empty(len(rows), D)
+    m.muon_act8_pack(x[source].contiguous(), packed)
+    nb = (D + 31) // 32
+    assert torch.equal(x8.codes[rows], packed.codes) and torch.equal(x8.exps[rows, :nb], packed.exps[:, :nb])
+    rest = torch.as_tensor(np.where(~held)[0], device=DEV)
+    assert torch.equal(x8.codes[rest], alone.codes[rest]) and torch.equal(x8.exps[rest], alone.exps[rest])
+    # without a checkpoint
+    buf2, xs2 = framed(r.rows, D, DT[inner], how)
+    m.muon_moe_dispatch(x, r, xs2)
+    assert torch.equal(buf2, buf)
+
+
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("how", ["dense", "padded", "shifted"])
+@pytest.mark.parametrize("T,E,K,D", SIZES)
+def test_combine_and_dispatch_gradient(outer, inner, how, T, E, K, D):
+    rng = np.random.default_rng(T * D)
+    r, place = routed(T + D + 1, T, E, K)
+    ys = put(rng.normal(size=(r.rows, D)), DT[inner], how)
+    ys[r.offsets[-1]:] = float("nan")     # rows without a copy are not read
+    w = put(rng.random((T, K)), torch.float32, how)
+    w[r.place < 0] = float("nan")         # nor are weights of copies without a row
+    for weights, wd in ((w, None), (w.bfloat16(), None), (None, 1)):
+        buf, out = framed(T, D, DT[outer], how)
+        start = rng.normal(size=(T, D))
+        for acc in (False, True):
+            if acc:
+                out.copy_(torch.as_tensor(start))
+            old = f64(out) if acc else np.zeros((T, D))
+            if weights is None:
+                m.muon_moe_dispatch_backward(ys, r, out, accumulate=acc)
+            else:
+                m.muon_moe_combine(ys, weights, r, out, accumulate=acc)
+            want, mass = R.combine(f64(ys), place, None if weights is None else f64(weights))
+            want = want + old
+            within(f64(out), want, (K + 2) * U * (mass + np.abs(old)) + HALF[outer] * np.abs(want) * (1 + 2.0 ** -7))
+            assert untouched(buf, out)
+
+
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("how", ["dense", "padded", "shifted"])
+@pytest.mark.parametrize("T,E,K,D", SIZES)
+def test_combine_gradient(outer, inner, how, T, E, K, D):
+    rng = np.random.default_rng(T * D + 5)
+    r, place = routed(T + D + 2, T, E, K)
+    dout = put(rng.normal(size=(T, D)), DT[outer], how)
+    y0 = put(rng.normal(size=(r.rows, D)), DT[inner], how)
+    y0[r.offsets[-1]:] = float("nan")
+    for wdt in ("f32", "bf16"):
+        w = put(rng.random((T, K)), DT[wdt], how)
+        w[r.place < 0] = float("nan")
+        want, dw_want, mass = R.combine_grad(f64(dout), f64(y0), f64(w), place)
+        held = ~np.isnan(want[:, 0])
+        for inplace in (False, True):
+            bufy, ys = framed(r.rows, D, DT[inner], how)
+            ys.copy_(y0)
+            buf, dys = framed(r.rows, D, DT[inner], how)
+            if inplace:
+                buf, dys = bufy, ys
+            bufw, dw = framed(T, K, DT[wdt], how)
+            m.muon_moe_combine_backward(dout, ys, w, r, dys, dw)
+            got = f64(dys)
+            within(got[held], want[held], 2 * HALF[inner] * np.abs(want[held]))
+            assert np.isnan(got[~held]).all() if inplace else (got[~held] == 7.0).all()
+            within(f64(dw), dw_want, (D + 2) * U * mass + HALF[wdt] * np.abs(dw_want) * (1 + 2.0 ** -7))
+            assert untouched(buf, dys) and untouched(bufw, dw)
+            if not inplace:
+                assert torch.equal(torch.nan_to_num(ys), torch.nan_to_num(y0))
+
+
+def test_not_finite_values_reach_their_own_columns_only():
+    T, E, K, D = 12, 4, 3, 130
+    r, place = routed(3, T, E, K, drop=0.0)
+    ys = torch.randn(r.rows, D, device=DEV)
+    ys[place[2][0], 17], ys[place[5][1], 129] = float("inf"), float("nan")
+    w = torch.rand(T, K, device=DEV)
+    out = torch.empty(T, D, device=DEV)
+    m.muon_moe_combine(ys, w, r, out)
+    bad = torch.zeros(T, D, dtype=torch.bool, device=DEV)
+    bad[2, 17] = bad[5, 129] = True
+    assert torch.equal(~torch.isfinite(out), bad)
+    dout, dys, dw = torch.randn(T, D, device=DEV), torch.empty_like(ys), torch.empty_like(w)
+    m.muon_moe_combine_backward(dout, ys, w, r, dys, dw)
+    bad = torch.zeros(T, K, dtype=torch.bool, device=DEV)
+    bad[2, 0] = bad[5, 1] = True
+    assert torch.equal(~torch.isfinite(dw), bad) and bool(torch.isfinite(dys).all())
+
+
+def test_places_outside_the_rows_are_taken_as_none():
+    T, K, D, rows = 6, 2, 40, 7
+    r = m.Routing.empty(T, K, 3, rows=rows)
+    place = torch.tensor([[0, 6], [7, 1], [-1, 2], [2 ** 31 - 1, 3], [-2 ** 31, 4], [5, 100]], dtype=torch.int32)
+    r.place.copy_(place)
+    x, xs = torch.randn(T, D, device=DEV), torch.full((rows, D), 7.0, device=DEV)
+    m.muon_moe_dispatch(x, r, xs)
+    want = R.dispatch(f64(x), place.numpy(), rows)
+    assert np.array_equal(f64(xs), want)
+    out = torch.empty(T, D, device=DEV)
+    m.muon_moe_dispatch_backward(xs, r, out)
+    assert torch.equal(out, x * torch.tensor([2., 1, 1, 1, 1, 1], device=DEV)[:, None])
+    dys, dw = torch.empty_like(xs), torch.empty(T, K, device=DEV)
+    m.muon_moe_combine_backward(x, xs, torch.ones(T, K, device=DEV), r, dys, dw)
+    assert torch.equal(dys, xs) and torch.equal((dw != 0).cpu(), (place >= 0) & (place < rows))
+
+
+def test_row_offsets_past_32_bits():
+    """Rows of a buffer of more than 2^32 values; only a few of them are set."""
+    T, K, D, rows = 8, 2, 16384, (1 << 18) + 100
+    r = m.Routing.empty(T, K, 1, rows=rows)
+    at = torch.arange(T * K, dtype=torch.int32).view(T, K)
+    r.place.copy_(rows - 1 - 7 * at)
+    x = torch.randn(T, D, device=DEV).bfloat16()
+    xs = torch.empty(rows, D, dtype=torch.bfloat16, device=DEV)
+    x8 = m.act8_empty(rows, D)
+    m.muon_moe_dispatch(x, r, xs, x8)
+    rowsat = r.place.flatten().long()
+    assert torch.equal(xs[rowsat], x.repeat_interleave(K, 0))
+    packed = m.act8_empty(T, D)
+    m.muon_act8_pack(x, packed)
+    assert torch.equal(x8.codes[rowsat], packed.codes.repeat_interleave(K, 0))
+    w, out = torch.full((T, K), 0.5, device=DEV), torch.empty_like(x)
+    m.muon_moe_combine(xs, w, r, out)
+    assert torch.equal(out, x)
+    dw = torch.empty(T, K, device=DEV)
+    m.muon_moe_combine_backward(x, xs, w, r, xs, dw)
+    assert torch.equal(xs[rowsat], (0.5 * x).repeat_interleave(K, 0))
+
+
+def test_repeats_its_bits_and_runs_on_another_stream():
+    T, E, K, D = 700, 16, 4, 1111
+    chosen = torch.as_tensor(choices(2, T, E, K, 0.1), device=DEV)
+    x = torch.randn(T, D, device=DEV)
+    w, dout = torch.rand(T, K, device=DEV), torch.randn(T, D, device=DEV)
+
+    def once(stream=None):
+        r = m.Routing.empty(T, K, E)
+        r.order.fill_(-1)
+        ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+        xs, dys = (torch.zeros(r.rows, D, device=DEV) for _ in range(2))
+        out, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        m.muon_moe_sort(chosen, r, ws, stream=stream)
+        m.muon_moe_dispatch(x, r, xs, stream=stream)
+        m.muon_moe_combine(xs, w, r, out, stream=stream)
+        m.muon_moe_combine_backward(dout, xs, w, r, dys, dw, stream=stream)
+        m.muon_moe_dispatch_backward(dys, r, dx, stream=stream)
+        torch.cuda.synchronize()
+        return [r.offsets, r.order, r.place, xs, out, dys, dw, dx]
+
+    a, b, c = once(), once(), once(torch.cuda.Stream())
+    for p, q, s in zip(a, b, c):
+        assert torch.equal(p, q) and torch.equal(p, s)
+
+
+def test_calls_in_a_graph():
+    """The whole way captured once and replayed on other choices and values."""
+    T, E, K, D = 300, 12, 3, 264
+    chosen = torch.as_tensor(choices(1, T, E, K, 0.1), device=DEV)
+    x, w, dout = torch.randn(T, D, device=DEV), torch.rand(T, K, device=DEV), torch.randn(T, D, device=DEV)
+    r = m.Routing.empty(T, K, E)
+    ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+    xs, dys = (torch.zeros(r.rows, D, device=DEV) for _ in range(2))
+    out, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+
+    def calls():
+        m.muon_moe_sort(chosen, r, ws)
+        m.muon_moe_dispatch(x, r, xs)
+        m.muon_moe_combine(xs, w, r, out)
+        m.muon_moe_combine_backward(dout, xs, w, r, dys, dw)
+        m.muon_moe_dispatch_backward(dys, r, dx)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for seed in (7, 8):
+        c = choices(seed, T, E, K, 0.2)
+        chosen.copy_(torch.as_tensor(c))
+        x.normal_()
+        dout.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        offsets, order, place, _ = R.sort(c, E)
+        assert r.offsets.tolist() == offsets.tolist() and np.array_equal(r.place.cpu().numpy(), place)
+        got = [t.clone() for t in (out, dx, dw)]
+        calls()
+        torch.cuda.synchronize()
+        for p, q in zip(got, (out, dx, dw)):
+            assert torch.equal(p, q)
+
+
+def test_gradients_against_differences():
+    """<d, out(x, w)> with out = combine(f(dispatch(x))), f(v) = v^2: the operators' own
+    forward passes at x and w moved by h either way, in fp32 with a large h: the sum is a
+    polynomial of degree 2 in x and 1 in w, so central differences are exact, and off by
+    roundings alone: 64 U of the sum of the terms' magnitudes over h."""
+    T, E, K, D, h = 20, 5, 3, 48, 0.5
+    r, place = routed(11, T, E, K)
+    x, w, dout = torch.randn(T, D, device=DEV), torch.rand(T, K, device=DEV), torch.randn(T, D, device=DEV)
+    dirx, dirw = torch.randn(T, D, device=DEV), torch.randn(T, K, device=DEV)
+
+    def loss(x, w):
+        xs, out = torch.zeros(r.rows, D, device=DEV), torch.empty(T, D, device=DEV)
+        m.muon_moe_dispatch(x, r, xs)
+        m.muon_moe_combine(xs * xs, w, r, out)
+        terms = dout.double() * out.double()
+        return terms.sum().item(), terms.abs().sum().item()
+
+    xs = torch.zeros(r.rows, D, device=DEV)
+    m.muon_moe_dispatch(x, r, xs)
+    dys, dw, dx = torch.zeros_like(xs), torch.empty_like(w), torch.empty_like(x)
+    m.muon_moe_combine_backward(dout, xs * xs, w, r, dys, dw)
+    m.muon_moe_dispatch_backward(2 * xs * dys, r, dx)
+    for grad, move in ((dx, lambda s: loss(x + s * dirx, w)), (dw, lambda s: loss(x, w + s * dirw))):
+        (up, mu), (down, md) = move(h), move(-h)
+        want = (grad.double() * (dirx if grad is dx else dirw).double()).sum().item()
+        assert abs((up - down) / (2 * h) - want) <= 64 * U * (mu + md) / h
+
+
+def test_from_the_choice_to_the_weight_gradient():
+    """Sort, dispatch with a checkpoint and the experts' weight gradients together: the
+    offsets and the checkpoint go straight into muon_act8_weight_grad."""
+    T, E, K, D, F = 500, 6, 2, 96, 64
+    chosen = choices(4, T, E, K, 0.1)
+    r, _ = run_sort(chosen, E)
+    x = torch.randn(T, D, device=DEV)
+    xs = torch.zeros(r.rows, D, dtype=torch.bfloat16, device=DEV)
+    x8 = m.act8_empty(r.rows, D)
+    m.muon_moe_dispatch(x, r, xs, x8)
+    dy = torch.randn(r.rows, F, device=DEV).bfloat16()
+    G = torch.empty(E, F, D, device=DEV)
+    ws = m.workspace(m.muon_act8_weight_grad_workspace_size(r.rows, F, D, E, dy.dtype, G.dtype))
+    m.muon_act8_weight_grad(dy, x8, G, ws, offsets=r.offsets)
+    assert m.muon_get_status(ws) == (m.MUON_OK, 0)
+    one = m.act8_empty(T, D)
+    m.muon_act8_pack(x, one)
+    xv = torch.empty(T, D, device=DEV)
+    m.muon_act8_unpack(one, xv)
+    cut, order = r.offsets.tolist(), r.order.long()
+    for e in range(E):
+        a, b = cut[e], cut[e + 1]
+        rows = f64(xv[order[a:b] // K])
+        want, mass = f64(dy[a:b]).T @ rows, np.abs(f64(dy[a:b])).T @ np.abs(rows)
+        within(f64(G[e]), want, (b - a + 64) * U * mass)
