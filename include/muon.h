@@ -583,7 +583,7 @@ muon_status_t muon_moe_sort_workspace_size(int64_t tokens, int experts, int topk
 
 /* chosen, chosen_bytes, chosen_stride, token_mask: as in muon_balance_t (-1 = not
  * sent anywhere; any other value outside [0, experts) is taken as that and sets
- * MUON_FLAG_INDEX; the choices of masked tokens are not read).  Two equal choices
+ * MUON_FLAG_INDEX; the choices of masked tokens do not matter).  Two equal choices
  * of a token are two copies.  Status word in the workspace. */
 muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen_stride,
                             const uint8_t* token_mask, const muon_routing_t* routing,

@@ -81,6 +81,14 @@ __device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kV
     s.hi = t;
     return;
   }
+  if (sq == 0.f) {   // nearly always nothing but zeros: an expert without tokens
+    uint32_t any = 0;
+#pragma unroll
+    for (int r = 0; r < kUnroll; ++r)
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) any |= __float_as_uint(x[r][k]);
+    if ((any & 0x7FFFFFFFu) == 0) return;
+  }
 #pragma unroll 1
   for (int r = 0; r < kUnroll; ++r)
 #pragma unroll

@@ -33,6 +33,9 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxPer = 8;       // copies a thread holds at a time
+// Copies a thread, up to which one block does it: 2048 copies take it 4.7 us, as two
+// kernels would; 4096 take it 7.0, the two kernels 5.7.
+constexpr int64_t kAlonePer = 2;
 constexpr int kSortBlocks = 152;
 constexpr size_t kHeader = 256;
 
@@ -46,21 +49,25 @@ struct SortPlan {
 // as few copies each as that allows, in several rounds when 8 a thread are not
 // enough.  The order does not depend on it.
 SortPlan sort_plan(int64_t copies) {
-  SortPlan p{1, 1, 1};
-  while (p.per < kMaxPer && copies > static_cast<int64_t>(p.per) * kSortThreads) p.per *= 2;
-  if (copies <= static_cast<int64_t>(p.per) * kSortThreads) return p;
-  p.per = 1;
-  while (p.per < kMaxPer && copies > static_cast<int64_t>(p.per) * kSortThreads * kSortBlocks) p.per *= 2;
-  const int64_t round = static_cast<int64_t>(p.per) * kSortThreads;
-  p.rounds = static_cast<int>((copies + round * kSortBlocks - 1) / (round * kSortBlocks));
-  p.blocks = static_cast<int>((copies + round * p.rounds - 1) / (round * p.rounds));
+  if (copies <= kAlonePer * kSortThreads) {
+    const int64_t per = (copies + kSortThreads - 1) / kSortThreads;
+    return {per < 1 ? 1 : static_cast<int>(per), 1, 1};
+  }
+  const int64_t wave = int64_t{kSortThreads} * kSortBlocks;
+  SortPlan p{kMaxPer, 1, 1};
+  if (copies <= kMaxPer * wave) p.per = static_cast<int>((copies + wave - 1) / wave);
+  else p.rounds = static_cast<int>((copies + kMaxPer * wave - 1) / (kMaxPer * wave));
+  const int64_t block = int64_t{kSortThreads} * p.per * p.rounds;
+  p.blocks = static_cast<int>((copies + block - 1) / block);
   return p;
 }
 
 struct SortArgs {
   uint32_t copies, rows;
   int experts, per, rounds, blocks;
-  int group_bits;            // log2 of the threads that hold one row of counts
+  int dense;                 // copy i's choice is chosen[i], and there is no mask
+  int quad_bits;             // log2 of the threads that read one row of counts
+  int stride;                // of the rows of counts, a multiple of 4
   Divider topk;
   const void* chosen;
   int chosen_bytes;
@@ -69,7 +76,7 @@ struct SortArgs {
   int32_t* offsets;
   int32_t* order;
   int32_t* place;
-  int* counts;               // [blocks][experts]
+  int* counts;               // [blocks][stride]
   uint32_t* flags;           // [blocks]
   uint32_t* status;
 };
@@ -77,38 +84,25 @@ struct SortArgs {
 // Expert of copy i, or -1; a number that is neither sets *bad.
 __device__ __forceinline__ int key_of(const SortArgs& a, uint32_t i, bool* bad) {
   if (i >= a.copies) return -1;
-  const uint32_t t = quotient(i, a.topk);
-  if (a.mask != nullptr && a.mask[t] == 0) return -1;
-  const int64_t at = static_cast<int64_t>(t) * a.chosen_stride + (i - t * a.topk.d);
+  uint32_t t = 0;
+  int64_t at = i;
+  if (!a.dense) {   // rows apart from each other, or a mask: the token is needed
+    t = quotient(i, a.topk);
+    at = t * a.chosen_stride + (i - t * a.topk.d);
+  }
   const int64_t e = a.chosen_bytes == 8 ? static_cast<const int64_t*>(a.chosen)[at]
                                         : static_cast<const int32_t*>(a.chosen)[at];
-  if (e >= 0 && e < a.experts) return static_cast<int>(e);
-  if (e != -1) *bad = true;
+  const bool valid = a.mask == nullptr || a.mask[t] != 0;   // read beside e, not before it
+  if (valid && static_cast<uint64_t>(e) < static_cast<uint64_t>(a.experts)) return static_cast<int>(e);
+  if (valid && e != -1) *bad = true;
   return -1;
 }
 
-// First copy of a block; a block's copies are consecutive.
-__device__ __forceinline__ uint64_t block_begin(const SortArgs& a, int block) {
-  return static_cast<uint64_t>(block) * a.rounds * a.per * kSortThreads;
-}
-
-__global__ void __launch_bounds__(kSortThreads) k_moe_count(const __grid_constant__ SortArgs a) {
-  extern __shared__ int sm[];
-  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) sm[e] = 0;
-  griddep_launch_dependents();
-  __syncthreads();
-  bool bad = false;
-  const uint64_t begin = block_begin(a, blockIdx.x);
-  for (int j = 0; j < a.rounds * a.per; ++j) {
-    const uint64_t i = begin + static_cast<uint64_t>(j) * kSortThreads + threadIdx.x;
-    if (i >= a.copies) break;
-    const int e = key_of(a, static_cast<uint32_t>(i), &bad);
-    if (e >= 0) atomicAdd(&sm[e], 1);
-  }
-  const int any = __syncthreads_or(bad);
-  for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
-    a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = sm[e];
-  if (threadIdx.x == 0) a.flags[blockIdx.x] = any ? MUON_FLAG_INDEX : 0u;
+// First of a lane's copies in a round: a block's copies are consecutive, and so
+// are a warp's in each round.  (Below 2^32: copies are fewer than 2^31, and a
+// block's rounds reach at most one block's length past them.)
+__device__ __forceinline__ uint32_t lane_begin(const SortArgs& a, int round) {
+  return ((blockIdx.x * a.rounds + round) * kSortWarps + (threadIdx.x >> 5)) * 32 * a.per + (threadIdx.x & 31);
 }
 
 // Exclusive sum over the block's threads, in thread order; *all gets the total.
@@ -120,137 +114,215 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* all) {
     const int u = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += u;
   }
-  __syncthreads();
   if (lane == 31) warp_sums[w] = s;
   __syncthreads();
-  if (w == 0) {
-    int t = warp_sums[lane];
+  int t = warp_sums[lane];   // every warp sums the warps' totals up for itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += u;
-    }
-    warp_sums[lane] = t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += u;
   }
-  __syncthreads();
-  *all = warp_sums[31];
-  return s - v + (w > 0 ? warp_sums[w - 1] : 0);
+  *all = __shfl_sync(0xffffffffu, t, 31);
+  const int before = __shfl_sync(0xffffffffu, t, w > 0 ? w - 1 : 0);
+  return s - v + (w > 0 ? before : 0);
 }
 
-// Places the copies of one block.  A warp owns consecutive copies, counts them by
-// expert in its own row of `hist`, and after the rows are summed up over the
-// warps walks them once more: a lane's row is its warp's next one of that expert
-// plus the number of lower lanes with the same expert.
-__global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constant__ SortArgs a) {
-  extern __shared__ int sm[];
-  int* hist = sm;                              // [warps][experts], before that two of [threads]
-  int* base = sm + max(kSortWarps * a.experts, 2 * kSortThreads);   // [experts]: next row of this block
-  __shared__ int warp_sums[32];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  bool bad = false;
-  if (a.blocks > 1) {
-    griddep_wait();
-    // the experts' totals, and what the blocks before this one have of them
-    const int e = tid & ((1 << a.group_bits) - 1), g = tid >> a.group_bits;
-    const int groups = kSortThreads >> a.group_bits;
-    int before = 0, total = 0;
-    if (e < a.experts) {
-#pragma unroll 8
-      for (int b = g; b < a.blocks; b += groups) {
-        const int c = a.counts[b * a.experts + e];
-        total += c;
-        before += b < static_cast<int>(blockIdx.x) ? c : 0;
-      }
-    }
-    hist[tid] = total;
-    hist[kSortThreads + tid] = before;
-    __syncthreads();
-    total = before = 0;
-    if (tid < a.experts) {
-      for (int k = 0; k < groups; ++k) {
-        total += hist[(k << a.group_bits) + tid];
-        before += hist[kSortThreads + (k << a.group_bits) + tid];
-      }
-    }
-    int all;
-    const int first = block_scan(total, warp_sums, &all);
-    if (tid < a.experts) base[tid] = first + before;
-    if (blockIdx.x == 0) {
-      if (tid < a.experts) a.offsets[tid] = min(static_cast<uint32_t>(first), a.rows);
-      uint32_t f = tid < a.blocks ? a.flags[tid] : 0u;
-      if (static_cast<uint32_t>(all) > a.rows) f |= MUON_FLAG_INDEX;
-      const int any = __syncthreads_or(f != 0);
-      if (tid == 0) {
-        a.offsets[a.experts] = min(static_cast<uint32_t>(all), a.rows);
-        *a.status = any ? MUON_FLAG_INDEX : 0u;
-      }
-    }
+// offsets[e] of this thread's expert, the end, and the status word.
+__device__ __forceinline__ void write_offsets(const SortArgs& a, int first, int all, bool bad) {
+  if (static_cast<int>(threadIdx.x) < a.experts)
+    a.offsets[threadIdx.x] = static_cast<int32_t>(min(static_cast<uint32_t>(first), a.rows));
+  const int any = __syncthreads_or(bad || static_cast<uint32_t>(all) > a.rows);
+  if (threadIdx.x == 0) {
+    a.offsets[a.experts] = static_cast<int32_t>(min(static_cast<uint32_t>(all), a.rows));
+    *a.status = any ? MUON_FLAG_INDEX : 0u;
   }
-  uint64_t begin = block_begin(a, blockIdx.x) + static_cast<uint64_t>(w) * a.per * 32 + lane;
-  for (int round = 0; round < a.rounds; ++round, begin += static_cast<uint64_t>(a.per) * kSortThreads) {
-    __syncthreads();
-    for (int i = tid; i < kSortWarps * a.experts; i += kSortThreads) hist[i] = 0;
-    int key[kMaxPer];
+}
+
+__device__ __forceinline__ void write_copy(const SortArgs& a, uint32_t i, bool keyed, uint32_t row) {
+  const bool on = keyed && row < a.rows;
+  if (i < a.copies) a.place[i] = on ? static_cast<int32_t>(row) : -1;
+  if (on) a.order[row] = static_cast<int32_t>(i);
+}
+
+// Ranks the copies of a block among those of the same expert.  A warp owns consecutive
+// copies and counts them by itself, 32 at a time: every lane sets its bit in its
+// expert's word of `lanes`, and its rank is the count so far plus the bits below its
+// own; the lowest lane clears the word and moves the count on.  Then the counts are
+// summed up over the warps.  Both kernels for
+// 131072 x 8 of 256 take 13.6 us; finding the lanes of one expert with a match over the
+// warp took 6.3 us more, with a vote for each bit of its number 3.7.
+// ALONE: the block holds all copies, and its ranks become rows at once; else they
+// are left in `place` for k_moe_place, with the block's counts.
+template <bool ALONE>
+__global__ void __launch_bounds__(kSortThreads) k_moe_rank(const __grid_constant__ SortArgs a) {
+  extern __shared__ int sm[];
+  int* base = sm;                                              // [experts]: ALONE: first row
+  uint32_t* lanes = reinterpret_cast<uint32_t*>(sm + a.experts);   // [warps][experts]
+  uint16_t* hist = reinterpret_cast<uint16_t*>(lanes + kSortWarps * a.experts);   // [warps][experts]
+  __shared__ int warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t* my_lanes = lanes + (tid >> 5) * a.experts;
+  uint16_t* mine = hist + (tid >> 5) * a.experts;
+  if (!ALONE) griddep_launch_dependents();
+  bool bad = false;
+  int total = 0;                               // of this thread's expert, over the rounds
+  for (int round = 0; round < a.rounds; ++round) {
+    const uint32_t begin = lane_begin(a, round);
+    int key[kMaxPer], rank[kMaxPer];
 #pragma unroll
-    for (int j = 0; j < kMaxPer; ++j) {
-      const uint64_t i = begin + j * 32;
-      key[j] = j < a.per && i < a.copies ? key_of(a, static_cast<uint32_t>(i), &bad) : -1;
+    for (int j = 0; j < kMaxPer; ++j) key[j] = j < a.per ? key_of(a, begin + 32 * j, &bad) : -1;
+    for (int e = lane; e < a.experts; e += 32) {
+      mine[e] = 0;
+      my_lanes[e] = 0;
     }
-    __syncthreads();
-    int* mine = hist + w * a.experts;
-#pragma unroll
-    for (int j = 0; j < kMaxPer; ++j)
-      if (key[j] >= 0) atomicAdd(&mine[key[j]], 1);
-    __syncthreads();
-    if (a.blocks == 1) {   // the only round: the totals are these counts'
-      int total = 0;
-      if (tid < a.experts)
-        for (int k = 0; k < kSortWarps; ++k) total += hist[k * a.experts + tid];
-      int all;
-      const int first = block_scan(total, warp_sums, &all);
-      if (tid < a.experts) {
-        base[tid] = first;
-        a.offsets[tid] = min(static_cast<uint32_t>(first), a.rows);
-      }
-      const int any = __syncthreads_or(bad || static_cast<uint32_t>(all) > a.rows);
-      if (tid == 0) {
-        a.offsets[a.experts] = min(static_cast<uint32_t>(all), a.rows);
-        *a.status = any ? MUON_FLAG_INDEX : 0u;
-      }
-    }
-    if (tid < a.experts) {
-      int next = base[tid];
-#pragma unroll 8
-      for (int k = 0; k < kSortWarps; ++k) {
-        const int c = hist[k * a.experts + tid];
-        hist[k * a.experts + tid] = next;
-        next += c;
-      }
-      base[tid] = next;
-    }
-    __syncthreads();
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < kMaxPer; ++j) {
       if (j >= a.per) break;   // the same for all threads
-      const uint32_t same = __match_any_sync(0xffffffffu, key[j]);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      const int first = key[j] >= 0 ? mine[key[j]] : 0;
+      const bool on = key[j] >= 0;
+      if (on) atomicOr(&my_lanes[key[j]], 1u << lane);
       __syncwarp();
-      if (key[j] >= 0 && rank == 0) mine[key[j]] = first + __popc(same);
+      const uint32_t same = on ? my_lanes[key[j]] : 0u;
+      const uint32_t lower = same & ((1u << lane) - 1);
+      rank[j] = (on ? mine[key[j]] : 0) + __popc(lower);
       __syncwarp();
-      const uint64_t i = begin + j * 32;
-      const uint32_t row = static_cast<uint32_t>(first + rank);
-      const bool on = key[j] >= 0 && row < a.rows;
-      if (i < a.copies) a.place[i] = on ? static_cast<int32_t>(row) : -1;
-      if (on) a.order[row] = static_cast<int32_t>(i);
+      if (on && lower == 0) {
+        mine[key[j]] = static_cast<uint16_t>(rank[j] + __popc(same));
+        my_lanes[key[j]] = 0;
+      }
+      __syncwarp();
     }
+    __syncthreads();
+    const int rounds_before = total;
+    if (tid < a.experts) {
+      int next = 0;            // at most 8192 in a round
+#pragma unroll 8
+      for (int k = 0; k < kSortWarps; ++k) {
+        const int c = hist[k * a.experts + tid];
+        hist[k * a.experts + tid] = static_cast<uint16_t>(next);
+        next += c;
+      }
+      total += next;
+    }
+    int first = 0, all = 0;
+    if constexpr (ALONE) {
+      first = block_scan(total, warp_sums, &all);
+    }
+    if (tid < a.experts) base[tid] = ALONE ? first : rounds_before;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMaxPer; ++j) {
+      if (j >= a.per) break;
+      const uint32_t i = begin + 32 * j;
+      int r = key[j] >= 0 ? mine[key[j]] + rank[j] : -1;
+      if (key[j] >= 0 && (ALONE || a.rounds > 1)) r += base[key[j]];
+      if constexpr (ALONE)
+        write_copy(a, i, key[j] >= 0, static_cast<uint32_t>(r));
+      else if (i < a.copies)
+        a.place[i] = r;
+    }
+    if constexpr (ALONE) write_offsets(a, first, all, bad);
+    else if (round + 1 < a.rounds) __syncthreads();   // base and hist have been read
+  }
+  if constexpr (!ALONE) {
+    if (tid < a.experts) a.counts[static_cast<int64_t>(blockIdx.x) * a.stride + tid] = total;
+    const int any = __syncthreads_or(bad);
+    if (tid == 0) a.flags[blockIdx.x] = any ? MUON_FLAG_INDEX : 0u;
   }
 }
 
-size_t sort_smem(int experts) {
-  const int words = kSortWarps * experts > 2 * kSortThreads ? kSortWarps * experts : 2 * kSortThreads;
-  return static_cast<size_t>(words + experts) * 4;
+// Ranks to rows: the block's first row of each expert is the expert's plus what the
+// blocks before this one have of it.  The copies of a block that has one round go out
+// sorted, so that runs of `order` are written together: 131072 x 8 of 256 17.2 -> 13.7 us.
+__global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constant__ SortArgs a) {
+  extern __shared__ int sm[];                  // [8 threads]: sums by thread, then the sorted copies
+  int4* part = reinterpret_cast<int4*>(sm);    // totals, then counts of the blocks before
+  int* base = sm + 8 * kSortThreads;           // [experts]
+  int* local = base + a.experts;               // [experts]: first of the expert among the sorted copies
+  __shared__ int warp_sums[32];
+  const int tid = threadIdx.x;
+  const bool sorted = a.rounds == 1;
+  bool bad = false;
+  int key[kMaxPer], rank[kMaxPer];
+#pragma unroll
+  for (int j = 0; j < kMaxPer; ++j)            // on their way during the wait
+    key[j] = j < a.per ? key_of(a, lane_begin(a, 0) + 32 * j, &bad) : -1;
+  griddep_wait();
+#pragma unroll
+  for (int j = 0; j < kMaxPer; ++j) rank[j] = key[j] >= 0 ? a.place[lane_begin(a, 0) + 32 * j] : -1;
+  const bool bad_choice = blockIdx.x == 0 && tid < a.blocks && a.flags[tid] != 0;
+  const int own = tid < a.experts ? a.counts[blockIdx.x * a.stride + tid] : 0;
+  const int quads = 1 << a.quad_bits;          // threads of a row of counts, four experts each
+  const int q = tid & (quads - 1), groups = min(kSortThreads >> a.quad_bits, 32);   // 32: more are slower to join
+  int4 total = make_int4(0, 0, 0, 0), before = total;
+  if (4 * q < a.experts) {
+#pragma unroll 8
+    for (int b = tid >> a.quad_bits; b < a.blocks && (tid >> a.quad_bits) < groups; b += groups) {
+      const int4 c = *reinterpret_cast<const int4*>(a.counts + b * a.stride + 4 * q);
+      const int on = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+      total.x += c.x; total.y += c.y; total.z += c.z; total.w += c.w;
+      before.x += c.x & on; before.y += c.y & on; before.z += c.z & on; before.w += c.w & on;
+    }
+  }
+  part[tid] = total;
+  part[kSortThreads + tid] = before;
+  int held, all;
+  const int first_local = block_scan(own, warp_sums, &held);   // and a barrier
+  int sum = 0, mine = 0;
+  if (tid < a.experts) {
+#pragma unroll 4
+    for (int g = 0; g < groups; ++g) {
+      sum += sm[4 * (g << a.quad_bits) + tid];
+      mine += sm[4 * (kSortThreads + (g << a.quad_bits)) + tid];
+    }
+  }
+  __syncthreads();
+  const int first = block_scan(sum, warp_sums, &all);
+  if (tid < a.experts) {
+    base[tid] = first + mine - (sorted ? first_local : 0);
+    local[tid] = first_local;
+  }
+  __syncthreads();
+  if (sorted) {
+    const uint32_t block_first = blockIdx.x * a.per * kSortThreads;
+    uint32_t* stage = reinterpret_cast<uint32_t*>(sm);   // expert and copy of the block
+#pragma unroll
+    for (int j = 0; j < kMaxPer; ++j) {
+      if (key[j] < 0) continue;
+      const uint32_t i = lane_begin(a, 0) + 32 * j;
+      const int at = local[key[j]] + rank[j];
+      const uint32_t row = static_cast<uint32_t>(base[key[j]] + at);
+      a.place[i] = row < a.rows ? static_cast<int32_t>(row) : -1;
+      stage[at] = static_cast<uint32_t>(key[j]) << 16 | (i - block_first);
+    }
+    __syncthreads();
+    for (int at = tid; at < held; at += kSortThreads) {
+      const uint32_t v = stage[at];
+      const uint32_t row = static_cast<uint32_t>(base[v >> 16] + at);
+      if (row < a.rows) a.order[row] = static_cast<int32_t>(block_first + (v & 0xFFFFu));
+    }
+  } else {
+    for (int round = 0; round < a.rounds; ++round) {
+      const uint32_t begin = lane_begin(a, round);
+      if (round > 0) {
+#pragma unroll
+        for (int j = 0; j < kMaxPer; ++j) key[j] = j < a.per ? key_of(a, begin + 32 * j, &bad) : -1;
+#pragma unroll
+        for (int j = 0; j < kMaxPer; ++j) rank[j] = key[j] >= 0 ? a.place[begin + 32 * j] : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kMaxPer; ++j)
+        if (key[j] >= 0)
+          write_copy(a, begin + 32 * j, true, static_cast<uint32_t>(base[key[j]] + rank[j]));
+    }
+  }
+  if (blockIdx.x == 0)
+    write_offsets(a, first, all, bad_choice);
 }
+
+size_t rank_smem(int experts) { return static_cast<size_t>(6 * kSortWarps + 4) * experts; }
+size_t place_smem(int experts) { return static_cast<size_t>(8 * kSortThreads + 2 * experts) * 4; }
+static_assert(kMaxPer <= 8 && kMaxPer * kSortThreads <= 1 << 16 && kMaxExperts <= kSortThreads);
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -276,13 +348,14 @@ struct Item {
   bool on;
 };
 
+template <int N>
 __device__ __forceinline__ Item item_of(const RowArgs& a) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   Item p;
   p.on = i < a.items;
   const uint32_t at = p.on ? i : a.items - 1;
   p.token = quotient(at, a.per_row);
-  p.col = static_cast<int>(at - p.token * a.per_row.d) * kCols;
+  p.col = static_cast<int>(at - p.token * a.per_row.d) * N;
   p.n = p.on ? a.cols - p.col : 0;
   return p;
 }
@@ -292,13 +365,24 @@ __device__ __forceinline__ float weight_at(const void* w, int wdt, int64_t i) {
                           : static_cast<const float*>(w)[i];
 }
 
+// Columns of a thread of the dispatch.  Where all rows start on 32-byte boundaries 16,
+// which go out as whole sectors.  Elsewhere one 16-byte piece of a row (of bf16,
+// where there is any), so that a warp's pieces lie side by side: with 16 columns
+// a thread most sectors go out in two halves, and 8 rows of 7001 columns a token take
+// 661 us for 356 (8192 tokens, fp32), 467 for 458 (16384, bf16).  The passes that read
+// rows take 16 either way: with one piece a thread their sums took 15% longer and the
+// gradient 50%.
+template <typename TX, typename TY, bool WHOLE>
+constexpr int kColsOf = WHOLE ? kCols : sizeof(TX) + sizeof(TY) == 8 ? 4 : 8;
+
 // A token's values to all of its rows, and their codes to the checkpoint's.
 template <typename TX, typename TY, bool WHOLE, bool CODES>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant__ RowArgs a) {
-  const Item p = item_of(a);
-  float x[kCols];
+  constexpr int N = kColsOf<TX, TY, WHOLE>;
+  const Item p = item_of<N>(a);
+  float x[N];
   load_values<TX, WHOLE>(a.x, p.token, p.col, p.n, x);
-  Codes c;
+  Codes<N> c;
   if constexpr (CODES) c = encode(x);
   const int32_t* at = a.place + static_cast<int64_t>(p.token) * a.topk;
   for (int k = 0; k < a.topk; ++k) {
@@ -312,44 +396,51 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant
 }
 
 // out = sum_k w_k y_k (w_k = 1 without weights), added to what it holds if asked.
-template <typename TY, typename TO, bool WHOLE, bool WEIGHTS>
+template <typename TY, typename TO, bool WHOLE, bool WEIGHTS, int kAhead>
 __global__ void __launch_bounds__(kThreads) k_moe_combine(const __grid_constant__ RowArgs a) {
-  constexpr int kAhead = sizeof(TY) == 2 ? 4 : 2;   // rows in flight
-  const Item p = item_of(a);
-  float acc[kCols];
+  constexpr int N = kCols;
+  const Item p = item_of<N>(a);
+  float acc[N];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+  for (int c = 0; c < N; ++c) acc[c] = 0.f;
   const int32_t* at = a.place + static_cast<int64_t>(p.token) * a.topk;
   for (int k0 = 0; k0 < a.topk; k0 += kAhead) {
-    float y[kAhead][kCols], w[kAhead];
+    Fetched<TY, WHOLE, N> y[kAhead];
+    float w[kAhead];
+    int n[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const uint32_t row = p.on && k0 + j < a.topk ? static_cast<uint32_t>(at[k0 + j]) : a.rows;
       const bool in = row < a.rows;
-      load_values<TY, WHOLE>(a.y, in ? row : 0, p.col, in ? p.n : 0, y[j]);
+      n[j] = in ? p.n : 0;
+      fetch(a.y, in ? row : 0, p.col, n[j], y[j]);
       w[j] = !in ? 0.f : WEIGHTS ? weight_at(a.w, a.wdt, p.token * a.w_stride + k0 + j) : 1.f;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
+    for (int j = 0; j < kAhead; ++j) {
+      float v[N];
+      values_of(y[j], n[j], v);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[c] = fmaf(w[j], y[j][c], acc[c]);
+      for (int c = 0; c < N; ++c) acc[c] = fmaf(w[j], v[c], acc[c]);
+    }
   }
   if (a.accumulate) {
-    float old[kCols];
+    float old[N];
     load_values<TO, WHOLE>(a.x, p.token, p.col, p.n, old);
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] += old[c];
+    for (int c = 0; c < N; ++c) acc[c] += old[c];
     if constexpr (!WHOLE) __syncwarp();   // the warp's reads are over
   }
   store_values<TO, WHOLE>(a.x, p.token, p.col, p.n, acc);
 }
 
-constexpr int kDots = 8;   // choices of a token that a pass over its columns takes
-
-// The sums over the warp's lanes of v[0 .. 7]; lane l gets that of v[l / 4].
-__device__ __forceinline__ float warp_sums8(float (&v)[kDots], int lane) {
+// The sums over the warp's lanes of v[0 .. N-1]; lane l gets that of v[l / (32 / N)].
+// Each step halves the values a lane holds: N + 1 shuffles or so instead of 5 N.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+  int bit = 16;
 #pragma unroll
-  for (int half = 4, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+  for (int half = N / 2; half >= 1; half >>= 1, bit >>= 1) {
     const bool up = lane & bit;
 #pragma unroll
     for (int j = 0; j < half; ++j) {
@@ -358,76 +449,97 @@ __device__ __forceinline__ float warp_sums8(float (&v)[kDots], int lane) {
       v[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
     }
   }
-  float s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
-  return s + __shfl_xor_sync(0xffffffffu, s, 1);
+  float s = v[0];
+#pragma unroll
+  for (; bit >= 1; bit >>= 1) s += __shfl_xor_sync(0xffffffffu, s, bit);
+  return s;
 }
 
-// x = dout, y = ys, z = dys.  `blockDim.x` threads (whole warps) take one token and
-// blockDim.y tokens share a block.
-template <typename TX, typename TY, bool WHOLE>
-__global__ void __launch_bounds__(512) k_moe_combine_backward(const __grid_constant__ RowArgs a) {
-  constexpr int kAhead = sizeof(TY) == 2 ? 4 : 2;   // rows in flight
-  __shared__ float red[16][kDots];
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// x = dout, y = ys, z = dys.  blockDim.x threads take one token (whole warps, or a
+// part of one: SUB) and blockDim.y tokens share a block.  kDots choices are taken in
+// a pass over the columns.
+template <typename TX, typename TY, bool WHOLE, bool SUB, int kDots>
+__global__ void __launch_bounds__(kThreads, kDots > 2 ? 2 : 3)
+    k_moe_combine_backward(const __grid_constant__ RowArgs a) {
+  constexpr int kAhead = kDots > 2 && sizeof(TY) == 2 ? 4 : 2;   // rows in flight
+  constexpr int N = kCols;
+  constexpr int kEach = 32 / kDots;                              // lanes that hold one sum
+  __shared__ float red[kThreads / 32][kDots];
+  const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31, warps = blockDim.x >> 5;
   const int first_warp = threadIdx.y * warps, warp = first_warp + (threadIdx.x >> 5);
   const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
   const bool on = t < a.tokens;
   const uint32_t token = on ? t : a.tokens - 1;
   const int32_t* at = a.place + static_cast<int64_t>(token) * a.topk;
-  const int span = blockDim.x * kCols, width = a.per_row.d * kCols;
+  const int span = blockDim.x * N, width = a.per_row.d * N;
   for (int k0 = 0; k0 < a.topk; k0 += kDots) {
     float dot[kDots];
 #pragma unroll
     for (int j = 0; j < kDots; ++j) dot[j] = 0.f;
     for (int c0 = 0; c0 < width; c0 += span) {   // the same number of times for all threads
-      const int col = c0 + threadIdx.x * kCols;
+      const int col = c0 + threadIdx.x * N;
       const int n = on ? a.cols - col : 0;
-      float d[kCols];
+      float d[N];
       load_values<TX, WHOLE>(a.x, token, col, n, d);
 #pragma unroll
       for (int j0 = 0; j0 < kDots; j0 += kAhead) {
         if (k0 + j0 >= a.topk) break;   // the same for all threads
-        float y[kAhead][kCols], w[kAhead];
+        Fetched<TY, WHOLE, N> y[kAhead];
         uint32_t row[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const int k = k0 + j0 + j;
           row[j] = on && k < a.topk ? static_cast<uint32_t>(at[k]) : a.rows;
           const bool in = row[j] < a.rows;
-          load_values<TY, WHOLE>(a.y, in ? row[j] : 0, col, in ? n : 0, y[j]);
-          w[j] = in ? weight_at(a.w, a.wdt, token * a.w_stride + k) : 0.f;
+          fetch(a.y, in ? row[j] : 0, col, in ? n : 0, y[j]);
         }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) dot[j0 + j] = fmaf(d[c], y[j][c], dot[j0 + j]);
-        if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads are over
+        if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads come first
+        // dys needs nothing of ys: written while that is on its way
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const bool in = row[j] < a.rows;
-          float g[kCols];
+          const float w = in ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
+          float g[N];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) g[c] = w[j] * d[c];
+          for (int c = 0; c < N; ++c) g[c] = w * d[c];
           store_values<TY, WHOLE>(a.z, in ? row[j] : 0, col, in ? n : 0, g);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          float v[N];
+          values_of(y[j], n, v);   // all 0 for a copy without a row
+#pragma unroll
+          for (int c = 0; c < N; ++c) dot[j0 + j] = fmaf(d[c], v[c], dot[j0 + j]);
         }
       }
     }
-    float s = warp_sums8(dot, lane);
-    if (warps > 1) {
-      if ((lane & 3) == 0) red[warp][lane >> 2] = s;
-      __syncthreads();
-      s = 0.f;
-      for (int v = 0; v < warps; ++v) s += red[first_warp + v][lane >> 2];
-      __syncthreads();
-    }
-    const int k = k0 + (lane >> 2);
-    if (on && threadIdx.x < 32 && (lane & 3) == 0 && k < a.topk) {
-      const bool in = static_cast<uint32_t>(at[k]) < a.rows;
+    const auto write = [&](int k, float s) {
+      if (!on || k >= a.topk) return;
+      const float v = static_cast<uint32_t>(at[k]) < a.rows ? s : 0.f;
       const int64_t i = token * a.dw_stride + k;
       if (a.wdt == MUON_BF16)
-        static_cast<__nv_bfloat16*>(a.dw)[i] = __float2bfloat16_rn(in ? s : 0.f);
+        static_cast<__nv_bfloat16*>(a.dw)[i] = __float2bfloat16_rn(v);
       else
-        static_cast<float*>(a.dw)[i] = in ? s : 0.f;
+        static_cast<float*>(a.dw)[i] = v;
+    };
+    if constexpr (SUB) {
+      for (int bit = blockDim.x >> 1; bit > 0; bit >>= 1)
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], bit);
+      if (threadIdx.x == 0) {
+#pragma unroll
+        for (int j = 0; j < kDots; ++j) write(k0 + j, dot[j]);
+      }
+    } else {
+      float s = warp_sums(dot, lane);
+      if (warps > 1) {
+        if (lane % kEach == 0) red[warp][lane / kEach] = s;
+        __syncthreads();
+        s = 0.f;
+        for (int v = 0; v < warps; ++v) s += red[first_warp + v][lane / kEach];
+        if (k0 + kDots < a.topk) __syncthreads();
+      }
+      if (threadIdx.x < 32 && lane % kEach == 0) write(k0 + lane / kEach, s);
     }
   }
 }
@@ -467,13 +579,13 @@ muon_status_t row_args(const muon_routing_t* r, int width, RowArgs* a) {
   a->topk = r->topk;
   a->rows = static_cast<uint32_t>(r->rows);
   a->place = r->place;
-  a->per_row = divider(static_cast<uint32_t>(blocks_of(width) * (kBlock / kCols)));
   return MUON_OK;
 }
 
-// `launch(args, first token)` for every token, in pieces of fewer than 2^30 items.
+// `launch` for every token, `cols` columns an item, in pieces of fewer than 2^30 items.
 template <class F>
-muon_status_t by_tokens(RowArgs a, int64_t tokens, int xdt, F launch) {
+muon_status_t by_tokens(RowArgs a, int64_t tokens, int xdt, int cols, F launch) {
+  a.per_row = divider(static_cast<uint32_t>(blocks_of(a.cols) * (kBlock / cols)));
   int64_t most = (int64_t{1} << 30) / a.per_row.d;
   if (most < 1) most = 1;
   for (int64_t t0 = 0; t0 < tokens; t0 += most) {
@@ -502,27 +614,50 @@ void launch_dispatch(const RowArgs& a, bool whole, bool codes, cudaStream_t st) 
   else k_moe_dispatch<TX, TY, false, false><<<grid, kThreads, 0, st>>>(a);
 }
 
-template <typename TY, typename TO>
-void launch_combine(const RowArgs& a, bool whole, cudaStream_t st) {
+// Rows in flight: two where a token has no more, or where they are fp32, else four.
+template <typename TY, typename TO, int AHEAD>
+void launch_combine_ahead(const RowArgs& a, bool whole, cudaStream_t st) {
   const unsigned grid = grid_of(a);
   const bool weights = a.w != nullptr;
-  if (whole && weights) k_moe_combine<TY, TO, true, true><<<grid, kThreads, 0, st>>>(a);
-  else if (whole) k_moe_combine<TY, TO, true, false><<<grid, kThreads, 0, st>>>(a);
-  else if (weights) k_moe_combine<TY, TO, false, true><<<grid, kThreads, 0, st>>>(a);
-  else k_moe_combine<TY, TO, false, false><<<grid, kThreads, 0, st>>>(a);
+  if (whole && weights) k_moe_combine<TY, TO, true, true, AHEAD><<<grid, kThreads, 0, st>>>(a);
+  else if (whole) k_moe_combine<TY, TO, true, false, AHEAD><<<grid, kThreads, 0, st>>>(a);
+  else if (weights) k_moe_combine<TY, TO, false, true, AHEAD><<<grid, kThreads, 0, st>>>(a);
+  else k_moe_combine<TY, TO, false, false, AHEAD><<<grid, kThreads, 0, st>>>(a);
 }
 
-// Threads of a token: enough for its columns at once, up to 512; narrow tokens
-// share a block of up to 256 threads.
-template <typename TX, typename TY>
-void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
+template <typename TY, typename TO>
+void launch_combine(const RowArgs& a, bool whole, cudaStream_t st) {
+  if constexpr (sizeof(TY) == 2) {
+    if (a.topk > 2) return launch_combine_ahead<TY, TO, 4>(a, whole, st);
+  }
+  launch_combine_ahead<TY, TO, 2>(a, whole, st);
+}
+
+// Threads of a token: up to 256, as many as make the passes over its columns
+// equally long; narrow tokens share a block and, below a warp's columns, a warp.
+template <typename TX, typename TY, int DOTS>
+void launch_combine_backward_of(const RowArgs& a, bool whole, cudaStream_t st) {
   const unsigned items = a.per_row.d;
-  const unsigned threads = items >= 512 ? 512 : (items + 31) / 32 * 32;
-  const unsigned tokens = threads >= 256 ? 1 : 256 / threads;
+  unsigned threads = 2;
+  while (threads < items && threads < 32) threads *= 2;
+  if (items > 32) {
+    const unsigned passes = (items + kThreads - 1) / kThreads;
+    threads = ((items + passes - 1) / passes + 31) / 32 * 32;
+  }
+  const unsigned tokens = kThreads / threads;
   const dim3 block(threads, tokens);
   const unsigned grid = (a.tokens + tokens - 1) / tokens;
-  if (whole) k_moe_combine_backward<TX, TY, true><<<grid, block, 0, st>>>(a);
-  else k_moe_combine_backward<TX, TY, false><<<grid, block, 0, st>>>(a);
+  const bool sub = threads < 32;
+  if (whole && sub) k_moe_combine_backward<TX, TY, true, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (whole) k_moe_combine_backward<TX, TY, true, false, DOTS><<<grid, block, 0, st>>>(a);
+  else if (sub) k_moe_combine_backward<TX, TY, false, true, DOTS><<<grid, block, 0, st>>>(a);
+  else k_moe_combine_backward<TX, TY, false, false, DOTS><<<grid, block, 0, st>>>(a);
+}
+
+template <typename TX, typename TY>
+void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
+  if (a.topk <= 2) launch_combine_backward_of<TX, TY, 2>(a, whole, st);
+  else launch_combine_backward_of<TX, TY, 8>(a, whole, st);
 }
 
 // F<first type, second type> for a pair of types.
@@ -551,7 +686,7 @@ muon_status_t combine(const void* ys, muon_dtype_t ydt, int64_t y_stride, const 
   a.w_stride = w_stride;
   a.accumulate = accumulate;
   const bool whole = rows_aligned(a.x, odt) && rows_aligned(a.y, ydt);
-  return by_tokens(a, r->tokens, odt, [&](const RowArgs& b) {
+  return by_tokens(a, r->tokens, odt, kCols, [&](const RowArgs& b) {
     prof_begin(kKindMoe, st);
     by_types(ydt, odt, [&](auto ty, auto to) { launch_combine<decltype(ty), decltype(to)>(b, whole, st); });
     prof_end(kKindMoe, st, 0.0, static_cast<double>(b.tokens) * width *
@@ -572,7 +707,7 @@ muon_status_t muon_moe_sort_workspace_size(int64_t tokens, int experts, int topk
   if (s != MUON_OK) return s;
   const SortPlan p = sort_plan(tokens * topk);
   *bytes = kHeader + align256(static_cast<size_t>(p.blocks) * 4) +
-           static_cast<size_t>(p.blocks) * experts * 4;
+           static_cast<size_t>(p.blocks) * round_up(experts, 4) * 4;
   return MUON_OK;
 }
 
@@ -603,8 +738,9 @@ muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen
   a.per = plan.per;
   a.rounds = plan.rounds;
   a.blocks = plan.blocks;
-  a.group_bits = 5;
-  while ((1 << a.group_bits) < r->experts) ++a.group_bits;
+  while (4 << a.quad_bits < r->experts) ++a.quad_bits;
+  a.dense = token_mask == nullptr && chosen_stride == r->topk;
+  a.stride = static_cast<int>(round_up(r->experts, 4));
   a.topk = divider(static_cast<uint32_t>(r->topk));
   a.chosen = chosen;
   a.chosen_bytes = chosen_bytes;
@@ -617,31 +753,34 @@ muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen
   a.flags = reinterpret_cast<uint32_t*>(ws + kHeader);
   a.counts = reinterpret_cast<int*>(ws + kHeader + align256(static_cast<size_t>(plan.blocks) * 4));
   const double bytes = static_cast<double>(a.copies) * (chosen_bytes + 8);
-  const size_t smem = sort_smem(r->experts);
-  // per device, and cheap: the attribute is set with every call that needs it
+  const bool alone = plan.blocks == 1;
+  const size_t smem = rank_smem(r->experts);
+  // per device, so with every call that needs it
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k_moe_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sort_smem(kMaxExperts))) != cudaSuccess)
+      cudaFuncSetAttribute(alone ? k_moe_rank<true> : k_moe_rank<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(rank_smem(kMaxExperts))) != cudaSuccess)
     return MUON_ERR_CUDA;
-  if (plan.blocks > 1) {
-    prof_begin(kKindMoe, st);
-    k_moe_count<<<plan.blocks, kSortThreads, r->experts * 4, st>>>(a);
-    prof_end(kKindMoe, st, 0.0, 0.0);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
-  }
+  prof_begin(kKindMoe, st);
+  if (alone) k_moe_rank<true><<<1, kSortThreads, smem, st>>>(a);
+  else k_moe_rank<false><<<plan.blocks, kSortThreads, smem, st>>>(a);
+  prof_end(kKindMoe, st, 0.0, bytes);
+  if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  if (alone) return MUON_OK;
+  // a programmatic dependent of the kernel before (it waits for the ranks)
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(plan.blocks);
   cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = place_smem(r->experts);
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = plan.blocks > 1 ? 1 : 0;   // alone it depends on what was enqueued before the call
+  cfg.numAttrs = 1;
   prof_begin(kKindMoe, st);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_moe_place, a);
-  prof_end(kKindMoe, st, 0.0, bytes);
+  prof_end(kKindMoe, st, 0.0, 0.0);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
@@ -660,7 +799,8 @@ muon_status_t muon_moe_dispatch(const void* x, muon_dtype_t xdt, int64_t x_strid
   if (x8 != nullptr) a.codes = packed(x8);
   const bool whole = rows_aligned(a.x, xdt) && rows_aligned(a.y, xsdt);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return by_tokens(a, r->tokens, xdt, [&](const RowArgs& b) {
+  const int cols = whole ? kCols : xdt == MUON_F32 && xsdt == MUON_F32 ? 4 : 8;   // kColsOf
+  return by_tokens(a, r->tokens, xdt, cols, [&](const RowArgs& b) {
     prof_begin(kKindMoe, st);
     by_types(xdt, xsdt, [&](auto tx, auto ty) {
       launch_dispatch<decltype(tx), decltype(ty)>(b, whole, x8 != nullptr, st);
@@ -711,7 +851,7 @@ muon_status_t muon_moe_combine_backward(const void* dout, muon_dtype_t ddt, int6
   a.dw_stride = dw_stride;
   const bool whole = rows_aligned(a.x, ddt) && rows_aligned(a.y, ydt) && rows_aligned(a.z, ydt);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return by_tokens(a, r->tokens, ddt, [&](const RowArgs& b) {
+  return by_tokens(a, r->tokens, ddt, kCols, [&](const RowArgs& b) {
     prof_begin(kKindMoe, st);
     by_types(ddt, ydt, [&](auto tx, auto ty) {
       launch_combine_backward<decltype(tx), decltype(ty)>(b, whole, st);

@@ -47,11 +47,12 @@ struct Packed {
 };
 
 // ---- 16 values of a row ------------------------------------------------------
-// Columns col .. col + 15 of a row, of which n are in the row (the others are
-// 0).  WHOLE: rows start on 32-byte boundaries.
-template <typename T, bool WHOLE>
+// Columns col .. col + N - 1 of a row, of which n are in the row (the others are
+// 0).  WHOLE: rows start on 32-byte boundaries (N = 16).
+template <typename T, bool WHOLE, int N>
 __device__ __forceinline__ void load_values(const Plane& pl, int64_t row, int col, int n,
-                                            float (&x)[kCols]) {
+                                            float (&x)[N]) {
+  static_assert(!WHOLE || N == kCols);
   constexpr int kWords = kCols * sizeof(T) / 4;
   const T* p = static_cast<const T*>(pl.p) + row * pl.stride + col;
   if constexpr (WHOLE) {
@@ -73,9 +74,9 @@ __device__ __forceinline__ void load_values(const Plane& pl, int64_t row, int co
 }
 
 // The reverse; the whole warp calls it (n <= 0: nothing of this thread's is in the row).
-template <typename T, bool WHOLE>
+template <typename T, bool WHOLE, int N>
 __device__ __forceinline__ void store_values(const Plane& pl, int64_t row, int col, int n,
-                                             const float (&x)[kCols]) {
+                                             const float (&x)[N]) {
   constexpr int kWords = kCols * sizeof(T) / 4;
   T* p = static_cast<T*>(pl.p) + row * pl.stride + col;
   if constexpr (WHOLE) {
@@ -93,7 +94,56 @@ __device__ __forceinline__ void store_values(const Plane& pl, int64_t row, int c
     }
   } else {
     const int lane = threadIdx.x & 31;
-    store_shifted(p, n, lane > 0 && col > 0, lane < 31 ? min(max(n - kCols, 0), kCols) : 0, x);
+    store_shifted(p, n, lane > 0 && col > 0, lane < 31 ? min(max(n - N, 0), N) : 0, x);
+  }
+}
+
+// The same as load_values in two steps, for rows in flight together: fetch issues
+// the loads, values_of waits for them (turning bf16 into floats where they are
+// loaded makes the next row's loads wait: 596 us for 8 rows of 7168 bf16 a token,
+// 16384 tokens, where fp32 of the same bytes took 299).
+template <typename T, bool WHOLE, int N>
+struct Fetched {
+  static constexpr int kWords = N * sizeof(T) / 4;
+  uint32_t w[WHOLE ? kWords : kWords + 4];
+  uint32_t by;   // bytes before the first column
+};
+
+// Where rows start on 32-byte boundaries the sectors that hold one of the n columns
+// are read whole.
+template <typename T, bool WHOLE, int N>
+__device__ __forceinline__ void fetch(const Plane& pl, int64_t row, int col, int n,
+                                      Fetched<T, WHOLE, N>& f) {
+  constexpr int kWords = Fetched<T, WHOLE, N>::kWords;
+  const T* p = static_cast<const T*>(pl.p) + row * pl.stride + col;
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int q = 0; q < kWords; q += 8) {
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (n * static_cast<int>(sizeof(T)) > 4 * q) ld_global_v8(reinterpret_cast<const uint32_t*>(p) + q, a, b);
+      f.w[q] = a.x; f.w[q + 1] = a.y; f.w[q + 2] = a.z; f.w[q + 3] = a.w;
+      f.w[q + 4] = b.x; f.w[q + 5] = b.y; f.w[q + 6] = b.z; f.w[q + 7] = b.w;
+    }
+  } else {
+    f.by = reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - f.by);
+#pragma unroll
+    for (int c = 0; c <= kWords / 4; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (n > 0 && 16 * c < static_cast<int>(f.by) + min(n, N) * static_cast<int>(sizeof(T))) u = q[c];
+      f.w[4 * c] = u.x; f.w[4 * c + 1] = u.y; f.w[4 * c + 2] = u.z; f.w[4 * c + 3] = u.w;
+    }
+  }
+}
+
+// Columns from n on are 0.
+template <typename T, bool WHOLE, int N>
+__device__ __forceinline__ void values_of(Fetched<T, WHOLE, N>& f, int n, float (&x)[N]) {
+  if constexpr (!WHOLE) shift_words<T, Fetched<T, WHOLE, N>::kWords>(f.w, f.by);
+  to_floats<T>(f.w, x);
+  if (n < N) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = k < n ? x[k] : 0.f;
   }
 }
 
@@ -119,51 +169,63 @@ __device__ __forceinline__ float max_magnitude(float a, float b) {
   return m;
 }
 
-// Largest magnitude of a block from its two threads' values; NaN if one is.
-__device__ __forceinline__ float block_amax(const float (&x)[kCols]) {
+// Largest magnitude of a block from the values of its 32 / N threads; NaN if one is.
+template <int N>
+__device__ __forceinline__ float block_amax(const float (&x)[N]) {
   float m = x[0];
 #pragma unroll
-  for (int k = 1; k < kCols; ++k) m = max_magnitude(m, x[k]);
-  return fabsf(max_magnitude(m, __shfl_xor_sync(0xffffffffu, m, 1)));
+  for (int k = 1; k < N; ++k) m = max_magnitude(m, x[k]);
+#pragma unroll
+  for (int o = 1; o < kBlock / N; o *= 2) m = max_magnitude(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return fabsf(m);
 }
 
 // Codes and biased exponent of this thread's values; the whole warp calls it.
 // x / 2^e is exact, and adding 1.5 * 2^23 rounds it to the nearest integer, ties
 // to even, whose two's complement is the sum's low byte.
+template <int N>
 struct Codes {
-  uint4 w;
+  uint32_t w[N / 4];
   int b;
 };
 
-__device__ __forceinline__ Codes encode(const float (&x)[kCols]) {
-  const int b = scale_exponent(block_amax(x));
+template <int N>
+__device__ __forceinline__ Codes<N> encode(const float (&x)[N]) {
+  Codes<N> out;
+  out.b = scale_exponent(block_amax(x));
   // 2^-e: the biased exponent of the reciprocal is 254 - b, in [5, 253]
-  const float inv = b == 255 ? 0.f : exponent_value(254 - b);
-  uint32_t c[kCols];
+  const float inv = out.b == 255 ? 0.f : exponent_value(254 - out.b);
+  uint32_t c[N];
 #pragma unroll
-  for (int k = 0; k < kCols; ++k) c[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
-  if (b == 249) {   // 64 * 2^122 would overflow
+  for (int k = 0; k < N; ++k) c[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
+  if (out.b == 249) {   // 64 * 2^122 would overflow
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
+    for (int k = 0; k < N; ++k)
       c[k] = __float_as_uint(fminf(fmaxf(x[k] * inv, -63.f), 63.f) + 12582912.f);
   }
-  uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    w[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040),
-                       __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040), 0x5410);
-  return {make_uint4(w[0], w[1], w[2], w[3]), b};
+  for (int k = 0; k < N / 4; ++k)
+    out.w[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040),
+                           __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040), 0x5410);
+  return out;
 }
 
-__device__ __forceinline__ void store_codes(const Packed& out, int64_t row, int col, const Codes& c) {
-  *reinterpret_cast<uint4*>(out.codes + row * out.code_stride + col) = c.w;
+template <int N>
+__device__ __forceinline__ void store_codes(const Packed& out, int64_t row, int col, const Codes<N>& c) {
+  int8_t* p = out.codes + row * out.code_stride + col;
+  if constexpr (N == 16)
+    *reinterpret_cast<uint4*>(p) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+  else if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = c.w[0];
   if (col % kBlock == 0) out.exps[row * out.exp_stride + col / kBlock] = static_cast<uint8_t>(c.b);
 }
 
 // Quantises the values of this thread; the whole warp calls it.
 __device__ __forceinline__ void write_codes(const Packed& out, int64_t row, int col,
                                             const float (&x)[kCols], bool on) {
-  const Codes c = encode(x);
+  const Codes<kCols> c = encode(x);
   if (on) store_codes(out, row, col, c);
 }
 

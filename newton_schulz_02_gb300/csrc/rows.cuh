@@ -1,5 +1,5 @@
-// 16 consecutive columns of a row of bf16 or fp32 as a thread's values, read
-// and written in 16-byte pieces wherever the row starts.
+// Consecutive columns of a row of bf16 or fp32 (16, or fewer: N) as a thread's values,
+// read and written in 16-byte pieces wherever the row starts.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,12 +8,12 @@
 
 namespace muon {
 
-constexpr int kCols = 16;   // a thread's columns
+constexpr int kCols = 16;   // a thread's columns, where nothing else is said
 
-template <typename T>
-__device__ __forceinline__ void to_floats(const uint32_t* w, float (&x)[kCols]) {
+template <typename T, int N>
+__device__ __forceinline__ void to_floats(const uint32_t* w, float (&x)[N]) {
 #pragma unroll
-  for (int k = 0; k < kCols; ++k) {
+  for (int k = 0; k < N; ++k) {
     if constexpr (sizeof(T) == 4)
       x[k] = __uint_as_float(w[k]);
     else   // a bf16 is the upper half of an fp32
@@ -21,10 +21,10 @@ __device__ __forceinline__ void to_floats(const uint32_t* w, float (&x)[kCols]) 
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void to_words(const float (&x)[kCols], uint32_t* w) {
+template <typename T, int N>
+__device__ __forceinline__ void to_words(const float (&x)[N], uint32_t* w) {
 #pragma unroll
-  for (int k = 0; k < kCols; k += 4 / sizeof(T)) {
+  for (int k = 0; k < N; k += 4 / sizeof(T)) {
     if constexpr (sizeof(T) == 4) {
       w[k] = __float_as_uint(x[k]);
     } else {
@@ -51,39 +51,39 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t by) {
   }
 }
 
-// Columns p[0 .. 15], of which the first n are in the row (the others are 0):
+// Columns p[0 .. N-1], of which the first n are in the row (the others are 0):
 // the 16-byte pieces that hold a byte of them.  A piece may begin before the
 // row or end after it; those bytes are shifted out or cleared.
-template <typename T>
-__device__ __forceinline__ void load_shifted(const T* p, int n, float (&x)[kCols]) {
-  constexpr int kWords = kCols * sizeof(T) / 4;
+template <typename T, int N>
+__device__ __forceinline__ void load_shifted(const T* p, int n, float (&x)[N]) {
+  constexpr int kWords = N * sizeof(T) / 4;
   const uint32_t by = reinterpret_cast<uintptr_t>(p) & 15u;
   const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - by);
   uint32_t w[kWords + 4];
 #pragma unroll
   for (int c = 0; c <= kWords / 4; ++c) {
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (16 * c < static_cast<int>(by) + min(n, kCols) * static_cast<int>(sizeof(T)) && n > 0) u = q[c];
+    if (16 * c < static_cast<int>(by) + min(n, N) * static_cast<int>(sizeof(T)) && n > 0) u = q[c];
     w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
   }
   shift_words<T, kWords>(w, by);
   to_floats<T>(w, x);
-  if (n < kCols) {
+  if (n < N) {
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) x[k] = k < n ? x[k] : 0.f;
+    for (int k = 0; k < N; ++k) x[k] = k < n ? x[k] : 0.f;
   }
 }
 
 // The reverse; the whole warp calls it.  A chain of lanes holds consecutive
-// columns of a row: `before` says that the lane before this one holds the 16
+// columns of a row: `before` says that the lane before this one holds the N
 // columns before these, `next` how many columns the lane after it goes on with
-// (0 to 16; it counts where n = 16).  n <= 0: nothing of this thread's is in the
+// (0 to N; it counts where n >= N).  n <= 0: nothing of this thread's is in the
 // row.  A thread writes the 16-byte pieces that begin in its columns, with the
 // next lane's first values in the last; a chain's first and last bytes, which
 // fill no piece, go out in 8, 4 and 2 bytes.
-template <typename T>
-__device__ __forceinline__ void store_shifted(T* p, int n, bool before, int next, const float (&x)[kCols]) {
-  constexpr int kWords = kCols * sizeof(T) / 4;
+template <typename T, int N>
+__device__ __forceinline__ void store_shifted(T* p, int n, bool before, int next, const float (&x)[N]) {
+  constexpr int kWords = N * sizeof(T) / 4;
   constexpr int kSize = sizeof(T);
   uint32_t w[kWords + 4];
   {
@@ -95,8 +95,8 @@ __device__ __forceinline__ void store_shifted(T* p, int n, bool before, int next
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[kWords + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
   const int head = static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15u);   // bytes before the first piece
-  const int own = min(n, kCols) * kSize;
-  const int all = n >= kCols ? own + next * kSize : own;
+  const int own = min(n, N) * kSize;
+  const int all = n >= N ? own + next * kSize : own;
   char* at = reinterpret_cast<char*>(p);
   if (head != 0 && !before && own > 0) {
     if (own < head) {   // a row of a few columns
