@@ -365,24 +365,13 @@ __device__ __forceinline__ float weight_at(const void* w, int wdt, int64_t i) {
                           : static_cast<const float*>(w)[i];
 }
 
-// Columns of a thread of the dispatch.  Where all rows start on 32-byte boundaries 16,
-// which go out as whole sectors.  Elsewhere one 16-byte piece of a row (of bf16,
-// where there is any), so that a warp's pieces lie side by side: with 16 columns
-// a thread most sectors go out in two halves, and 8 rows of 7001 columns a token take
-// 661 us for 356 (8192 tokens, fp32), 467 for 458 (16384, bf16).  The passes that read
-// rows take 16 either way: with one piece a thread their sums took 15% longer and the
-// gradient 50%.
-template <typename TX, typename TY, bool WHOLE>
-constexpr int kColsOf = WHOLE ? kCols : sizeof(TX) + sizeof(TY) == 8 ? 4 : 8;
-
 // A token's values to all of its rows, and their codes to the checkpoint's.
 template <typename TX, typename TY, bool WHOLE, bool CODES>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant__ RowArgs a) {
-  constexpr int N = kColsOf<TX, TY, WHOLE>;
-  const Item p = item_of<N>(a);
-  float x[N];
+  const Item p = item_of<kCols>(a);
+  float x[kCols];
   load_values<TX, WHOLE>(a.x, p.token, p.col, p.n, x);
-  Codes<N> c;
+  Codes<kCols> c;
   if constexpr (CODES) c = encode(x);
   const int32_t* at = a.place + static_cast<int64_t>(p.token) * a.topk;
   for (int k = 0; k < a.topk; ++k) {
@@ -391,6 +380,140 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant
     store_values<TY, WHOLE>(a.y, in ? row : 0, p.col, in ? p.n : 0, x);
     if constexpr (CODES) {
       if (in) store_codes(a.codes, row, p.col, c);
+    }
+  }
+}
+
+// The same for rows that start anywhere, and are wide enough for a warp: a warp takes
+// kPieces x 32 pieces of 16 bytes of a token, side by side.  All of a warp's
+// pieces are off a row's 16-byte boundaries by the same amount, so a shift is a choice
+// of registers in a branch that all lanes take together, with the next lane's first words
+// behind the own ones; what is before the first boundary and after the last goes out one
+// value a lane.  8 rows of 7001 columns a token take 313 us (8192 tokens, fp32) and 312
+// (16384, bf16), 97% of the copy rate; with 16 columns a thread, whose sectors go out in
+// two halves, 661 and 467.
+constexpr int kPieces = 4;
+
+// Words Q .. Q + 3 of a lane's four and the next lane's (HALF: from the middle of word
+// Q on); lane 31's next is lane 0 of `after`.
+template <int Q, bool HALF>
+__device__ __forceinline__ uint4 piece_from(const uint32_t (&w)[4], const uint32_t (&after)[4], int lane) {
+  constexpr int kNext = Q + (HALF ? 1 : 0);
+  uint32_t all[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) all[k] = w[k];
+#pragma unroll
+  for (int k = 0; k < kNext; ++k)
+    all[4 + k] = __shfl_sync(0xffffffffu, lane == 0 ? after[k] : w[k], (lane + 1) & 31);
+  uint32_t out[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    out[k] = HALF ? __byte_perm(all[Q + k], all[Q + k + (HALF ? 1 : 0)], 0x5432) : all[Q + k];
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// The 16 bytes from byte `by` (even, below 16, the same for all lanes) of the lane's
+// words on.
+__device__ __forceinline__ uint4 shifted_piece(const uint32_t (&w)[4], const uint32_t (&after)[4], int by,
+                                               int lane) {
+  switch (by >> 1) {
+    case 0: return piece_from<0, false>(w, after, lane);
+    case 2: return piece_from<1, false>(w, after, lane);
+    case 4: return piece_from<2, false>(w, after, lane);
+    case 6: return piece_from<3, false>(w, after, lane);
+    case 1: return piece_from<0, true>(w, after, lane);
+    case 3: return piece_from<1, true>(w, after, lane);
+    case 5: return piece_from<2, true>(w, after, lane);
+    default: return piece_from<3, true>(w, after, lane);
+  }
+}
+
+// Writes a warp's n columns, PIECES x 32 pieces side by side in w, from p on, wherever
+// that is.  `end`: in lane l < 8 the column l, in lane 8 + m the last column but m
+// (their numbers in `edge`).
+template <typename T, int PIECES>
+__device__ __forceinline__ void store_pieces(T* p, int n, const uint32_t (&w)[PIECES + 1][4], int edge,
+                                             float end, int lane) {
+  constexpr int N = 16 / sizeof(T);
+  const int by = static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15u);   // bytes before the boundary
+  const int head = by / static_cast<int>(sizeof(T));
+  const int tail = n > head ? (n - head) % N : 0;
+  if (lane < 8 ? lane < min(head, n) : lane < 8 + tail) store_one(p + edge, end);
+  const int full = (n - head) / N;   // whole pieces (none if negative)
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) {
+    if (j * 32 >= full) break;   // the same for all lanes
+    const uint4 u = shifted_piece(w[j], w[j + 1], by, lane);
+    if (j * 32 + lane < full) q[j * 32 + lane] = u;
+  }
+}
+
+// Column of a warp's n that lane `lane` holds for store_pieces; -1: none.
+__device__ __forceinline__ int edge_column(int n, int lane) {
+  const int e = lane < 8 ? lane : n - 1 - (lane - 8);
+  return lane < 16 && e >= 0 && e < n ? e : -1;
+}
+
+// Piece j of a warp's n columns from p on, of any type: N columns a lane, 0 behind n.
+template <typename T, int N>
+__device__ __forceinline__ void load_piece(const T* p, int n, int j, int lane, float (&x)[N]) {
+  const int first = (j * 32 + lane) * N;
+  if constexpr (N * sizeof(T) >= 16) {
+    load_shifted(p + first, n - first, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = first + k < n ? static_cast<float>(p[first + k]) : 0.f;
+  }
+}
+
+// WEIGHTS: a row gets w times the values (the rows' gradient in combine's).
+template <typename TX, typename TY, bool CODES, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, sizeof(TY) == 4 ? 4 : 3) k_moe_dispatch_wide(const __grid_constant__ RowArgs a) {
+  constexpr int N = 16 / sizeof(TY);        // columns of a piece
+  constexpr int kSpan = 32 * kPieces * N;   // columns of a warp
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (item >= a.items) return;   // whole warps
+  const uint32_t token = quotient(item, a.per_row);
+  const int col = static_cast<int>(item - token * a.per_row.d) * kSpan;
+  const int n = min(a.cols - col, kSpan);   // columns of this warp
+  const TX* x = static_cast<const TX*>(a.x.p) + token * a.x.stride + col;
+  float v[kPieces][N];
+  uint32_t w[kPieces + 1][4];
+  Codes<N> c[CODES ? kPieces : 1];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    load_piece(x, n, j, lane, v[j]);
+    if constexpr (CODES) c[j] = encode(v[j]);
+    if constexpr (!WEIGHTS) to_words<TY>(v[j], w[j]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[kPieces][k] = 0;   // behind the last: never written
+  const int edge = edge_column(n, lane);
+  const float end = edge >= 0 ? static_cast<float>(x[edge]) : 0.f;
+  const int32_t* at = a.place + static_cast<int64_t>(token) * a.topk;
+  for (int k = 0; k < a.topk; ++k) {
+    const uint32_t row = static_cast<uint32_t>(at[k]);
+    if (row >= a.rows) continue;   // the same for all lanes
+    float by = 1.f;
+    if constexpr (WEIGHTS) {
+      by = weight_at(a.w, a.wdt, token * a.w_stride + k);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        float g[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) g[e] = by * v[j][e];
+        to_words<TY>(g, w[j]);
+      }
+    }
+    store_pieces<TY, kPieces>(static_cast<TY*>(a.y.p) + row * a.y.stride + col, n, w, edge, by * end, lane);
+    if constexpr (CODES) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int first = col + (j * 32 + lane) * N;
+        if (first / kBlock * kBlock < a.cols) store_codes(a.codes, row, first, c[j]);
+      }
     }
   }
 }
@@ -457,11 +580,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 
 // x = dout, y = ys, z = dys.  blockDim.x threads take one token (whole warps, or a
 // part of one: SUB) and blockDim.y tokens share a block.  kDots choices are taken in
-// a pass over the columns.
-template <typename TX, typename TY, bool WHOLE, bool SUB, int kDots>
-__global__ void __launch_bounds__(kThreads, kDots > 2 ? 2 : 3)
+// a pass over the columns.  Without ROWS only the weights' gradient is formed.
+template <typename TX, typename TY, bool WHOLE, bool SUB, bool ROWS, int kDots>
+__global__ void __launch_bounds__(kThreads, !ROWS && sizeof(TY) == 2 ? 4 : kDots > 2 && ROWS ? 2 : 3)
     k_moe_combine_backward(const __grid_constant__ RowArgs a) {
-  constexpr int kAhead = kDots > 2 && sizeof(TY) == 2 ? 4 : 2;   // rows in flight
+  constexpr int kAhead = kDots > 2 && ROWS && sizeof(TY) == 2 ? 4 : 2;   // rows in flight
   constexpr int N = kCols;
   constexpr int kEach = 32 / kDots;                              // lanes that hold one sum
   __shared__ float red[kThreads / 32][kDots];
@@ -493,16 +616,18 @@ __global__ void __launch_bounds__(kThreads, kDots > 2 ? 2 : 3)
           const bool in = row[j] < a.rows;
           fetch(a.y, in ? row[j] : 0, col, in ? n : 0, y[j]);
         }
-        if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads come first
-        // dys needs nothing of ys: written while that is on its way
+        if constexpr (ROWS) {
+          if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads come first
+          // dys needs nothing of ys: written while that is on its way
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const bool in = row[j] < a.rows;
-          const float w = in ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
-          float g[N];
+          for (int j = 0; j < kAhead; ++j) {
+            const bool in = row[j] < a.rows;
+            const float w = in ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
+            float g[N];
 #pragma unroll
-          for (int c = 0; c < N; ++c) g[c] = w * d[c];
-          store_values<TY, WHOLE>(a.z, in ? row[j] : 0, col, in ? n : 0, g);
+            for (int c = 0; c < N; ++c) g[c] = w * d[c];
+            store_values<TY, WHOLE>(a.z, in ? row[j] : 0, col, in ? n : 0, g);
+          }
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -585,7 +710,9 @@ muon_status_t row_args(const muon_routing_t* r, int width, RowArgs* a) {
 // `launch` for every token, `cols` columns an item, in pieces of fewer than 2^30 items.
 template <class F>
 muon_status_t by_tokens(RowArgs a, int64_t tokens, int xdt, int cols, F launch) {
-  a.per_row = divider(static_cast<uint32_t>(blocks_of(a.cols) * (kBlock / cols)));
+  // (whole blocks of a checkpoint: 16 columns divide 32, and 32 a warp's)
+  const int64_t padded = blocks_of(a.cols) * kBlock;
+  a.per_row = divider(static_cast<uint32_t>((padded + cols - 1) / cols));
   int64_t most = (int64_t{1} << 30) / a.per_row.d;
   if (most < 1) most = 1;
   for (int64_t t0 = 0; t0 < tokens; t0 += most) {
@@ -605,8 +732,22 @@ muon_status_t by_tokens(RowArgs a, int64_t tokens, int xdt, int cols, F launch) 
 
 unsigned grid_of(const RowArgs& a) { return (a.items + kThreads - 1) / kThreads; }
 
+// Columns of an item of the dispatch: a warp's where rows start anywhere and hold a warp's
+// pieces, else a thread's.  (65536 tokens, 8 rows each: 257 columns of bf16 80 us by
+// warps, 97 by threads; 801 155 and 236; 129 of fp32 64 and 128.)
+int dispatch_cols(int xsdt, bool whole, int width) {
+  const int piece = 16 / esize(xsdt);
+  return whole || width < 32 * piece ? kCols : 32 * kPieces * piece;
+}
+
 template <typename TX, typename TY>
-void launch_dispatch(const RowArgs& a, bool whole, bool codes, cudaStream_t st) {
+void launch_dispatch(const RowArgs& a, bool whole, bool codes, int cols, cudaStream_t st) {
+  if (cols > kCols) {
+    const unsigned grid = (a.items + kThreads / 32 - 1) / (kThreads / 32);
+    if (codes) k_moe_dispatch_wide<TX, TY, true, false><<<grid, kThreads, 0, st>>>(a);
+    else k_moe_dispatch_wide<TX, TY, false, false><<<grid, kThreads, 0, st>>>(a);
+    return;
+  }
   const unsigned grid = grid_of(a);
   if (whole && codes) k_moe_dispatch<TX, TY, true, true><<<grid, kThreads, 0, st>>>(a);
   else if (whole) k_moe_dispatch<TX, TY, true, false><<<grid, kThreads, 0, st>>>(a);
@@ -614,21 +755,23 @@ void launch_dispatch(const RowArgs& a, bool whole, bool codes, cudaStream_t st) 
   else k_moe_dispatch<TX, TY, false, false><<<grid, kThreads, 0, st>>>(a);
 }
 
-// Rows in flight: two where a token has no more, or where they are fp32, else four.
+// Rows in flight: four of bf16 on 32-byte boundaries, else two, so that more blocks fit
+// (8 rows of 7001 bf16, 16384 tokens: 343 us with two, 430 with four; 2 rows of 4096 68
+// and 84).
 template <typename TY, typename TO, int AHEAD>
 void launch_combine_ahead(const RowArgs& a, bool whole, cudaStream_t st) {
   const unsigned grid = grid_of(a);
   const bool weights = a.w != nullptr;
   if (whole && weights) k_moe_combine<TY, TO, true, true, AHEAD><<<grid, kThreads, 0, st>>>(a);
   else if (whole) k_moe_combine<TY, TO, true, false, AHEAD><<<grid, kThreads, 0, st>>>(a);
-  else if (weights) k_moe_combine<TY, TO, false, true, AHEAD><<<grid, kThreads, 0, st>>>(a);
-  else k_moe_combine<TY, TO, false, false, AHEAD><<<grid, kThreads, 0, st>>>(a);
+  else if (weights) k_moe_combine<TY, TO, false, true, 2><<<grid, kThreads, 0, st>>>(a);
+  else k_moe_combine<TY, TO, false, false, 2><<<grid, kThreads, 0, st>>>(a);
 }
 
 template <typename TY, typename TO>
 void launch_combine(const RowArgs& a, bool whole, cudaStream_t st) {
   if constexpr (sizeof(TY) == 2) {
-    if (a.topk > 2) return launch_combine_ahead<TY, TO, 4>(a, whole, st);
+    if (a.topk > 2 && whole) return launch_combine_ahead<TY, TO, 4>(a, whole, st);
   }
   launch_combine_ahead<TY, TO, 2>(a, whole, st);
 }
@@ -636,7 +779,7 @@ void launch_combine(const RowArgs& a, bool whole, cudaStream_t st) {
 // Threads of a token: up to 256, as many as make the passes over its columns
 // equally long; narrow tokens share a block and, below a warp's columns, a warp.
 template <typename TX, typename TY, int DOTS>
-void launch_combine_backward_of(const RowArgs& a, bool whole, cudaStream_t st) {
+void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaStream_t st) {
   const unsigned items = a.per_row.d;
   unsigned threads = 2;
   while (threads < items && threads < 32) threads *= 2;
@@ -648,16 +791,37 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, cudaStream_t st) {
   const dim3 block(threads, tokens);
   const unsigned grid = (a.tokens + tokens - 1) / tokens;
   const bool sub = threads < 32;
-  if (whole && sub) k_moe_combine_backward<TX, TY, true, true, DOTS><<<grid, block, 0, st>>>(a);
-  else if (whole) k_moe_combine_backward<TX, TY, true, false, DOTS><<<grid, block, 0, st>>>(a);
-  else if (sub) k_moe_combine_backward<TX, TY, false, true, DOTS><<<grid, block, 0, st>>>(a);
-  else k_moe_combine_backward<TX, TY, false, false, DOTS><<<grid, block, 0, st>>>(a);
+  if (whole && sub) k_moe_combine_backward<TX, TY, true, true, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (whole) k_moe_combine_backward<TX, TY, true, false, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (narrow) k_moe_combine_backward<TX, TY, false, true, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (sub) k_moe_combine_backward<TX, TY, false, true, false, DOTS><<<grid, block, 0, st>>>(a);
+  else k_moe_combine_backward<TX, TY, false, false, false, DOTS><<<grid, block, 0, st>>>(a);
 }
 
+// Rows that start anywhere and hold a warp's pieces are written by the dispatch, after
+// the weights' gradient has read ys (which may be dys): one more read of dout, and 8
+// rows of 7001 bf16 columns, 16384 tokens, take 722 us
+// for 889 (8192 tokens, fp32: 669 for 748).
 template <typename TX, typename TY>
 void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
-  if (a.topk <= 2) launch_combine_backward_of<TX, TY, 2>(a, whole, st);
-  else launch_combine_backward_of<TX, TY, 8>(a, whole, st);
+  const int cols = dispatch_cols(sizeof(TY) == 2 ? MUON_BF16 : MUON_F32, whole, a.cols);
+  const bool narrow = !whole && cols == kCols;
+  static_assert(32 * 8 <= 16 * kCols, "narrow rows take a part of a warp");
+  const bool rows = whole || narrow;   // by the same kernel
+  const double tokens = static_cast<double>(a.tokens) * a.cols, row = sizeof(TY) * static_cast<double>(a.topk);
+  prof_begin(kKindMoe, st);
+  if (a.topk <= 2) launch_combine_backward_of<TX, TY, 2>(a, whole, narrow, st);
+  else launch_combine_backward_of<TX, TY, 8>(a, whole, narrow, st);
+  prof_end(kKindMoe, st, 0.0, tokens * (sizeof(TX) + (rows ? 2 : 1) * row));
+  if (rows) return;
+  prof_begin(kKindMoe, st);
+  RowArgs b = a;
+  b.y = a.z;
+  b.per_row = divider(static_cast<uint32_t>((a.cols + cols - 1) / cols));
+  b.items = a.tokens * b.per_row.d;
+  k_moe_dispatch_wide<TX, TY, false, true>
+      <<<(b.items + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, st>>>(b);
+  prof_end(kKindMoe, st, 0.0, tokens * row);
 }
 
 // F<first type, second type> for a pair of types.
@@ -799,11 +963,11 @@ muon_status_t muon_moe_dispatch(const void* x, muon_dtype_t xdt, int64_t x_strid
   if (x8 != nullptr) a.codes = packed(x8);
   const bool whole = rows_aligned(a.x, xdt) && rows_aligned(a.y, xsdt);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int cols = whole ? kCols : xdt == MUON_F32 && xsdt == MUON_F32 ? 4 : 8;   // kColsOf
+  const int cols = dispatch_cols(xsdt, whole, width);
   return by_tokens(a, r->tokens, xdt, cols, [&](const RowArgs& b) {
     prof_begin(kKindMoe, st);
     by_types(xdt, xsdt, [&](auto tx, auto ty) {
-      launch_dispatch<decltype(tx), decltype(ty)>(b, whole, x8 != nullptr, st);
+      launch_dispatch<decltype(tx), decltype(ty)>(b, whole, x8 != nullptr, cols, st);
     });
     prof_end(kKindMoe, st, 0.0, static_cast<double>(b.tokens) * width *
                                     (esize(xdt) + r->topk * (esize(xsdt) + (x8 != nullptr ? kCodeBytes : 0.0))));
@@ -852,12 +1016,9 @@ muon_status_t muon_moe_combine_backward(const void* dout, muon_dtype_t ddt, int6
   const bool whole = rows_aligned(a.x, ddt) && rows_aligned(a.y, ydt) && rows_aligned(a.z, ydt);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return by_tokens(a, r->tokens, ddt, kCols, [&](const RowArgs& b) {
-    prof_begin(kKindMoe, st);
     by_types(ddt, ydt, [&](auto tx, auto ty) {
       launch_combine_backward<decltype(tx), decltype(ty)>(b, whole, st);
     });
-    prof_end(kKindMoe, st, 0.0,
-             static_cast<double>(b.tokens) * width * (esize(ddt) + 2.0 * r->topk * esize(ydt)));
   });
 }
 

@@ -174,6 +174,31 @@ def test_dispatch(outer, inner, how, T, E, K, D):
 
 
 @pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("D", [127, 128, 129, 130, 255, 256, 257, 263, 511, 513, 1023, 1025, 1031, 2049])
+def test_dispatch_rows_at_every_offset(outer, inner, D):
+    """Rows whose stride runs through all offsets from a 16-byte boundary, inside a
+    buffer whose every other value has to stay."""
+    T, E, K = 5, 3, 4
+    r, place = routed(D, T, E, K, drop=0.1)
+    x = put(np.random.default_rng(D).normal(size=(T, D)), DT[outer], "shifted")
+    want = R.dispatch(f64(x), place, r.rows)
+    held = ~np.isnan(want[:, 0])
+    for stride, lead in ((D + 1, 0), (D + 3, 1), (D + 2, 2)):
+        buf = torch.full((r.rows * stride + 16,), 7.0, dtype=DT[inner], device=DEV)
+        xs = buf[lead:].as_strided((r.rows, D), (stride, 1))
+        x8 = m.act8_empty(r.rows, D)
+        m.muon_moe_dispatch(x, r, xs, x8)
+        got = f64(xs)
+        within(got[held], want[held], HALF[inner] * np.abs(want[held]))
+        assert (got[~held] == 7.0).all() and untouched(buf, xs)
+        first = torch.as_tensor(np.where(held)[0], device=DEV)
+        packed = m.act8_empty(len(first), D)
+        m.muon_act8_pack(x[r.order[first].long() // K].contiguous(), packed)
+        nb = (D + 31) // 32
+        assert torch.equal(x8.codes[first], packed.codes) and torch.equal(x8.exps[first, :nb], packed.exps[:, :nb])
+
+
+@pytest.mark.parametrize("outer,inner", TYPES)
 @pytest.mark.parametrize("how", ["dense", "padded", "shifted"])
 @pytest.mark.parametrize("T,E,K,D", SIZES)
 def test_combine_and_dispatch_gradient(outer, inner, how, T, E, K, D):
@@ -410,3 +435,33 @@ def test_from_the_choice_to_the_weight_gradient():
         rows = f64(xv[order[a:b] // K])
         want, mass = f64(dy[a:b]).T @ rows, np.abs(f64(dy[a:b])).T @ np.abs(rows)
         within(f64(G[e]), want, (b - a + 64) * U * mass)
+
+
+def test_example_layer_gives_back_the_gradient_of_its_input():
+    """dx of the example layer against automatic differentiation: 8-bit activations and bf16
+    products as in its weights' gradients, 3 % of the norm; and the clipped step is that of
+    the gradients times the factor."""
+    from tests.test_gpu_example import load
+    ex = load()
+    layer = ex.MoeLayer(500)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x, dy = (torch.randn(500, ex.WIDTH, generator=g, device=DEV) for _ in range(2))
+    y = layer.forward(x)
+    dx = layer.backward(dy)
+    xd = x.double().requires_grad_()
+    gate, up, down, router = (t.double() for t in (layer.gate, layer.up, layer.down, layer.router))
+    p = (xd @ router.T).softmax(dim=1)
+    w = p.gather(1, layer.chosen)
+    want = torch.zeros_like(xd)
+    for k in range(ex.TOPK):
+        for e in range(ex.EXPERTS):
+            t = torch.nonzero(layer.chosen[:, k] == e).flatten()
+            h = torch.nn.functional.silu(xd[t] @ gate[e].T) * (xd[t] @ up[e].T)
+            want = want.index_add(0, t, w[t, k, None] * (h @ down[e].T))
+    assert (y - want).norm() <= 0.03 * want.norm()
+    f = layer.counts.double() * ex.EXPERTS / (ex.TOPK * 500)
+    ((want * dy.double()).sum() + 1e-2 * (f * p.mean(dim=0)).sum()).backward()
+    assert (dx - xd.grad).norm() <= 0.03 * xd.grad.norm()
+    layer.step(1, max_norm=0.5)
+    n, s = R.grad_norm([f64(t) for t in layer.grads.values()], 0.5)
+    assert abs(layer.grad_norm.item() - n) <= 7 * U * n and abs(layer.grad_scale.item() - s) <= 9 * U * s
