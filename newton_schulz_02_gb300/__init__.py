@@ -994,13 +994,17 @@ class Grads:
             _dtype(t, "a gradient", self.device)
             if not t.is_contiguous():
                 raise ValueError("a gradient outside a group has to be contiguous")
-        self.ptrs = torch.tensor([t.data_ptr() for t in free], dtype=torch.int64).to(
+        same = {}   # tensors of one size and dtype are one group, as an AdamWGroup's
+        for t in free:
+            same.setdefault((t.numel(), _DT[t.dtype]), []).append(t.data_ptr())
+        self.ptrs = torch.tensor([p for ptrs in same.values() for p in ptrs], dtype=torch.int64).to(
             free[0].device if free else "cpu")
         at, descs = self.ptrs.data_ptr(), []
+        for (numel, dt), ptrs in same.items():
+            descs.append(muon_grads_t(len(ptrs), 1, numel, numel, dt, at))
+            at += 8 * len(ptrs)
         for g in self.items:
             if isinstance(g, torch.Tensor):
-                descs.append(muon_grads_t(1, 1, g.numel(), g.numel(), _DT[g.dtype], at))
-                at += 8
                 continue
             if g.ptrs.get_device() != self.device or self.device < 0:
                 raise _elsewhere("a group", self.device)

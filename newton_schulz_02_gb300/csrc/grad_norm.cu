@@ -32,7 +32,7 @@ constexpr int kVec = 8;                                       // values of a vec
 constexpr int kUnroll = 4;                                    // vectors of a thread in a piece
 constexpr int64_t kPiece = int64_t{kThreads} * kVec * kUnroll;
 constexpr int kMaxGroups = 64;                                // groups of a launch
-constexpr int kFinThreads = 1024;
+constexpr int kFinThreads = 256;
 constexpr size_t kHeader = 256;
 
 struct NormGroup {
@@ -49,14 +49,25 @@ struct NormArgs {
   int groups;
   int64_t begin[kMaxGroups + 1];   // first piece of a group
   NormGroup g[kMaxGroups];
-  double* sums;                    // [blocks] of this launch
-  uint32_t* flags;                 // [blocks]
+  float2* sums;                    // [blocks] of this launch: the pairs,
+  double* wide;                    // [blocks] what is not in them,
+  uint32_t* flags;                 // [blocks] and conditions
 };
 
+constexpr uint32_t kFlagWide = 1u << 31;   // of a block: there is something in its `wide`
+
 struct Sum {
-  float hi, lo;
-  double wide;
+  float hi, lo;    // hi + lo
+  double wide;     // what does not fit there
 };
+
+// (hi, lo) += (h, l); |lo| stays within a rounding of hi.
+__device__ __forceinline__ void add_pair(Sum& s, float h, float l) {
+  const float t = s.hi + h, b = t - s.hi;
+  const float e = (s.hi - (t - b)) + (h - b) + (s.lo + l);
+  s.hi = t + e;
+  s.lo = e - (s.hi - t);
+}
 
 __device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -98,21 +109,22 @@ __device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kV
     }
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
-  griddep_launch_dependents();
+// Pieces first, first + step, ... of all tensors, thread tid of the kThreads that
+// take a piece; sets *flags.
+__device__ __forceinline__ Sum sum_pieces(const NormArgs& a, int64_t first, int64_t step, int tid,
+                                          uint32_t* flags) {
   const int64_t total = a.begin[a.groups];
   Sum s{0.f, 0.f, 0.0};
-  uint32_t flags = 0;
   int gi = 0;
-  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+  for (int64_t item = first; item < total; item += step) {
     while (item >= a.begin[gi + 1]) ++gi;
     const NormGroup& G = a.g[gi];
     const int64_t local = item - a.begin[gi];
     const int64_t tensor = local / G.pieces;
     const int64_t piece = local - tensor * G.pieces;
     const char* p = static_cast<const char*>(G.ptrs[tensor]);
-    if (!((reinterpret_cast<uintptr_t>(p) & 15u) == 0)) {
-      flags |= MUON_FLAG_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) {
+      *flags |= MUON_FLAG_MISALIGNED;
       continue;   // the tensor is left out
     }
     const int64_t v0 = piece * (kPiece / kVec);
@@ -121,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
     if (G.stride == 0) {
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
-        const int64_t v = v0 + r * kThreads + threadIdx.x;
+        const int64_t v = v0 + r * kThreads + tid;
         at[r] = v < G.vecs ? v : -1;
       }
     } else {
@@ -129,9 +141,9 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
       const uint32_t col0 = static_cast<uint32_t>(v0 - row0 * G.per_row.d);
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
-        const uint32_t c = col0 + r * kThreads + threadIdx.x;
+        const uint32_t c = col0 + r * kThreads + tid;
         const uint32_t down = quotient(c, G.per_row);
-        at[r] = v0 + r * kThreads + threadIdx.x < G.vecs ? (row0 + down) * G.stride + (c - down * G.per_row.d) : -1;
+        at[r] = v0 + r * kThreads + tid < G.vecs ? (row0 + down) * G.stride + (c - down * G.per_row.d) : -1;
       }
     }
     if (G.dtype == MUON_BF16) {
@@ -155,32 +167,68 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
         x[r][4] = q[1].x; x[r][5] = q[1].y; x[r][6] = q[1].z; x[r][7] = q[1].w;
       }
     }
-    if (G.tail > 0 && piece == G.pieces - 1 && threadIdx.x < G.tail) {   // fewer than 8 values
-      const int64_t i = G.vecs * kVec + threadIdx.x;
+    if (G.tail > 0 && piece == G.pieces - 1 && tid < G.tail) {   // fewer than 8 values
+      const int64_t i = G.vecs * kVec + tid;
       const float v = G.dtype == MUON_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
                                            : reinterpret_cast<const float*>(p)[i];
       s.wide = fma(static_cast<double>(v), static_cast<double>(v), s.wide);
     }
     add_squares(s, x);
   }
-  // the block's sum, in a fixed order
-  __shared__ double red[kThreads / 32];
-  double d = (static_cast<double>(s.hi) + static_cast<double>(s.lo)) + s.wide;
+  return s;
+}
+
+// The sum over a block of THREADS, in a fixed order, in thread 0; *all: the flags of
+// all threads.  In fp32 pairs: an fp64 addition of every thread of a warp takes 16
+// clocks of an SM, and made 1.9 us of a small call.
+template <int THREADS>
+__device__ __forceinline__ Sum block_sum(Sum s, uint32_t flags, uint32_t* all) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ float2 red[kWarps];
+  __shared__ double red_wide[kWarps];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
-  const int any = __syncthreads_or(flags != 0);
+  for (int o = 16; o > 0; o >>= 1)
+    add_pair(s, __shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o));
+  if (lane == 0) red[w] = make_float2(s.hi, s.lo);
+  const int bad = __syncthreads_or(flags & MUON_FLAG_MISALIGNED);
+  const int wide = __syncthreads_or(!(s.wide == 0.0));   // or NaN
+  *all = (bad ? MUON_FLAG_MISALIGNED : 0u) | (wide ? kFlagWide : 0u);
+  if (wide) {   // rare: the same for all threads
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.wide += __shfl_xor_sync(0xffffffffu, s.wide, o);
+    if (lane == 0) red_wide[w] = s.wide;
+    __syncthreads();
+  }
+  if (w == 0) {
+    const float2 v = lane < kWarps ? red[lane] : make_float2(0.f, 0.f);
+    s.hi = v.x;
+    s.lo = v.y;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1)
+      add_pair(s, __shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o));
+    s.wide = 0.0;
+    if (wide)
+      for (int k = 0; k < kWarps; ++k) s.wide += red_wide[k];
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
+  griddep_launch_dependents();
+  uint32_t flags = 0;
+  const Sum mine = sum_pieces(a, blockIdx.x, gridDim.x, threadIdx.x, &flags);
+  const Sum s = block_sum<kThreads>(mine, flags, &flags);
   if (threadIdx.x == 0) {
-    d = red[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) d += red[w];
-    a.sums[blockIdx.x] = d;
-    a.flags[blockIdx.x] = any ? MUON_FLAG_MISALIGNED : 0u;
+    a.sums[blockIdx.x] = make_float2(s.hi, s.lo);
+    a.wide[blockIdx.x] = s.wide;
+    a.flags[blockIdx.x] = flags;
   }
 }
 
 struct FinishArgs {
-  const double* sums;
+  const float2* sums;
+  const double* wide;
   const uint32_t* flags;
   int blocks;
   float max_norm;
@@ -189,29 +237,42 @@ struct FinishArgs {
   uint32_t* status;
 };
 
-__global__ void __launch_bounds__(kFinThreads) k_grad_norm_finish(FinishArgs a) {
-  griddep_wait();
-  __shared__ double red[kFinThreads / 32];
-  double d = 0.0;
-  uint32_t f = 0;
-  for (int i = threadIdx.x; i < a.blocks; i += kFinThreads) {
-    d += a.sums[i];
-    f |= a.flags[i];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = d;
-  const int any = __syncthreads_or(f != 0);
-  if (threadIdx.x == 0) {
-    d = red[0];
-    for (int w = 1; w < kFinThreads / 32; ++w) d += red[w];
-    const double n = sqrt(d);
+// The norm and the factor.  From the pair alone in fp32 pairs, too: a root and a quotient
+// with what their first values leave over: in fp64 they take 0.7 us of a call's 4.
+__device__ __forceinline__ void write_norm(const FinishArgs& a, const Sum& s, uint32_t flags) {
+  uint32_t status = flags & MUON_FLAG_MISALIGNED;
+  if (flags & kFlagWide) {
+    const double n = sqrt((static_cast<double>(s.hi) + static_cast<double>(s.lo)) + s.wide);
     const bool finite = isfinite(n);
+    if (!finite) status |= MUON_FLAG_NONFINITE;
     *a.norm = static_cast<float>(n);
     *a.scale = finite ? static_cast<float>(fmin(1.0, static_cast<double>(a.max_norm) / (n + 1e-6)))
                       : __uint_as_float(0x7FC00000u);
-    *a.status = (any ? MUON_FLAG_MISALIGNED : 0u) | (finite ? 0u : MUON_FLAG_NONFINITE);
+  } else {
+    const float n = sqrtf(s.hi);
+    const float rest = s.hi > 0.f ? (fmaf(-n, n, s.hi) + s.lo) / (2.f * n) : 0.f;   // n + rest is the norm
+    const float d = n + 1e-6f, big = fmaxf(n, 1e-6f);
+    const float low = rest + (fminf(n, 1e-6f) - (d - big));                         // d + low divides
+    const float q = a.max_norm / d;
+    *a.norm = n + rest;
+    *a.scale = q >= 1.f + 0x1p-20f ? 1.f : fminf(1.f, q + (fmaf(-q, d, a.max_norm) - q * low) / d);
   }
+  *a.status = status;
+}
+
+__global__ void __launch_bounds__(kFinThreads) k_grad_norm_finish(FinishArgs a) {
+  griddep_wait();
+  Sum s{0.f, 0.f, 0.0};
+  uint32_t flags = 0;
+  for (int i = threadIdx.x; i < a.blocks; i += kFinThreads) {
+    const float2 v = a.sums[i];
+    add_pair(s, v.x, v.y);
+    const uint32_t f = a.flags[i];
+    if (f & kFlagWide) s.wide += a.wide[i];
+    flags |= f;
+  }
+  s = block_sum<kFinThreads>(s, flags, &flags);
+  if (threadIdx.x == 0) write_norm(a, s, flags);
 }
 
 // Blocks of a launch: every resident block of the current device, at most one a piece.
@@ -225,7 +286,8 @@ cudaError_t resident_blocks(int* out) {
   return cudaSuccess;
 }
 
-constexpr int kMaxBlocks = 2048;   // of a launch: SMs x 8 blocks of 256 threads, and more
+constexpr int kMaxBlocks = 2048;    // of a launch: SMs x 8 blocks of 256 threads, and more
+constexpr size_t kBlockBytes = 20;  // a pair, a double and the conditions
 
 bool empty(const muon_grads_t& g) { return g.count == 0 || g.rows == 0 || g.cols == 0; }
 
@@ -251,8 +313,6 @@ muon_status_t check_grads(const muon_grads_t* g, int n_groups, int* used) {
   return MUON_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 int launches_of(int used) { return (used + kMaxGroups - 1) / kMaxGroups; }
 
 }  // namespace
@@ -267,7 +327,7 @@ muon_status_t muon_grad_norm_workspace_size(const muon_grads_t* groups, int n_gr
   int used = 0;
   const muon_status_t s = check_grads(groups, n_groups, &used);
   if (s != MUON_OK) return s;
-  *bytes = kHeader + align256(static_cast<size_t>(launches_of(used)) * kMaxBlocks * 12);
+  *bytes = kHeader + static_cast<size_t>(launches_of(used)) * kMaxBlocks * kBlockBytes;
   return MUON_OK;
 }
 
@@ -288,13 +348,15 @@ muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  double* sums = reinterpret_cast<double*>(ws + kHeader);
-  uint32_t* flags = reinterpret_cast<uint32_t*>(sums + static_cast<size_t>(launches_of(used)) * kMaxBlocks);
+  const size_t most = static_cast<size_t>(launches_of(used)) * kMaxBlocks;
+  double* wide = reinterpret_cast<double*>(ws + kHeader);
+  float2* sums = reinterpret_cast<float2*>(wide + most);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(sums + most);
+  FinishArgs f{sums, wide, flags, 0, max_norm, norm, scale, reinterpret_cast<uint32_t*>(ws)};
   int resident = 0;
   if (resident_blocks(&resident) != cudaSuccess) return MUON_ERR_CUDA;
   if (resident > kMaxBlocks) resident = kMaxBlocks;
-  int blocks = 0, next = 0;
-  while (next < n_groups) {
+  for (int next = 0; next < n_groups;) {
     NormArgs a{};
     double bytes = 0.0;
     for (; next < n_groups && a.groups < kMaxGroups; ++next) {
@@ -317,15 +379,16 @@ muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max
     const int64_t items = a.begin[a.groups];
     if (items == 0) break;
     const int grid = static_cast<int>(items < resident ? items : resident);
-    a.sums = sums + blocks;
-    a.flags = flags + blocks;
-    blocks += grid;
+    a.sums = sums + f.blocks;
+    a.wide = wide + f.blocks;
+    a.flags = flags + f.blocks;
+    f.blocks += grid;
     prof_begin(kKindGradNorm, st);
     k_grad_norm<<<grid, kThreads, 0, st>>>(a);
     prof_end(kKindGradNorm, st, 0.0, bytes);
     if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
   }
-  FinishArgs f{sums, flags, blocks, max_norm, norm, scale, reinterpret_cast<uint32_t*>(ws)};
+  // a programmatic dependent of the last kernel before (it waits for the sums)
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -334,10 +397,10 @@ muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max
   cfg.blockDim = dim3(kFinThreads);
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = blocks > 0 ? 1 : 0;
+  cfg.numAttrs = f.blocks > 0 ? 1 : 0;
   prof_begin(kKindGradNorm, st);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_grad_norm_finish, f);
-  prof_end(kKindGradNorm, st, 0.0, 12.0 * blocks);
+  prof_end(kKindGradNorm, st, 0.0, 12.0 * f.blocks);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
