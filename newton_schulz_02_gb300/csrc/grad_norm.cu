@@ -12,7 +12,7 @@
 // fp32 (the rounding error of each addition is kept in the second), which
 // costs 7 additions for 32 values and holds 48 bits; an fp64 addition for each
 // value would take five times as long as the reads.  Squares outside fp32's
-// comfortable range (the sum of 32 below 2^-96 or above 2^90, infinite or NaN)
+// comfortable range (the sum of 32 below 2^-96 or above 2^80, infinite or NaN)
 // are added up in fp64 instead, value by value.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -86,7 +86,7 @@ __device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kV
     for (int k = 1; k < kVec; ++k) part[r] = fmaf(x[r][k], x[r][k], part[r]);
   }
   const float sq = (part[0] + part[1]) + (part[2] + part[3]);
-  if (sq >= 0x1p-96f && sq <= 0x1p90f) {
+  if (sq >= 0x1p-96f && sq <= 0x1p80f) {
     const float t = s.hi + sq, b = t - s.hi;
     s.lo += (s.hi - (t - b)) + (sq - b);
     s.hi = t;
