@@ -584,7 +584,8 @@ muon_status_t muon_moe_sort_workspace_size(int64_t tokens, int experts, int topk
 /* chosen, chosen_bytes, chosen_stride, token_mask: as in muon_balance_t (-1 = not
  * sent anywhere; any other value outside [0, experts) is taken as that and sets
  * MUON_FLAG_INDEX; the choices of masked tokens do not matter).  Two equal choices
- * of a token are two copies.  Status word in the workspace. */
+ * of a token are two copies.  chosen and place may not overlap.  Status word in the
+ * workspace. */
 muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen_stride,
                             const uint8_t* token_mask, const muon_routing_t* routing,
                             void* workspace, size_t workspace_bytes, muon_stream_t stream);
@@ -610,7 +611,7 @@ muon_status_t muon_moe_dispatch_backward(const void* dxs, muon_dtype_t dxsdt, in
 
 /* out[t] = sum_k weights[t][k] * ys[place[t][k]]; accumulate: 1 = added to what out
  * holds (a residual).  weights: device [tokens][topk] of wdt, row stride w_stride;
- * those of copies without a row are not read. */
+ * those of copies without a row do not matter. */
 muon_status_t muon_moe_combine(const void* ys, muon_dtype_t ydt, int64_t y_stride,
                                const muon_routing_t* routing, const void* weights,
                                muon_dtype_t wdt, int64_t w_stride, int width, void* out,

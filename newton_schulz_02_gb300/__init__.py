@@ -992,8 +992,8 @@ class Grads:
         self.device = (first if isinstance(first, torch.Tensor) else first.ptrs).get_device()
         for t in free:
             _dtype(t, "a gradient", self.device)
-            if not t.is_contiguous():
-                raise ValueError("a gradient outside a group has to be contiguous")
+            if not t.is_contiguous() or t.data_ptr() % 16 != 0:
+                raise ValueError("a gradient outside a group has to be contiguous and 16-byte aligned")
         same = {}   # tensors of one size and dtype are one group, as an AdamWGroup's
         for t in free:
             same.setdefault((t.numel(), _DT[t.dtype]), []).append(t.data_ptr())

@@ -137,7 +137,7 @@ def routed(seed, T, E, K, drop=0.15, rows=None):
 
 
 SIZES = [(1, 1, 1, 1), (1, 3, 8, 16), (5, 4, 2, 31), (70, 8, 2, 512), (33, 60, 6, 1111), (19, 16, 9, 77),
-         (40, 5, 3, 8), (9, 4, 17, 4100), (6, 3, 2, 8193)]
+         (40, 5, 3, 8), (9, 4, 17, 4100), (6, 3, 2, 8193), (3, 1024, 1024, 40)]
 TYPES = [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")]
 
 
@@ -380,6 +380,32 @@ def test_calls_in_a_graph():
         torch.cuda.synchronize()
         for p, q in zip(got, (out, dx, dw)):
             assert torch.equal(p, q)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured sorts (one block, and many) over one workspace, replayed in turn: each
+    replay gives what its own inputs give."""
+    E, K = 30, 3
+    ws = m.workspace(max(m.muon_moe_sort_workspace_size(T, E, K) for T in (100, 9000)))
+    work = []
+    for T in (100, 9000):
+        chosen = torch.as_tensor(choices(T, T, E, K, 0.1), device=DEV)
+        r = m.Routing.empty(T, K, E)
+        m.muon_moe_sort(chosen, r, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.muon_moe_sort(chosen, r, ws)
+        work.append((g, chosen, r))
+    for turn in range(4):
+        g, chosen, r = work[turn % 2]
+        c = choices(50 + turn, chosen.shape[0], E, K, 0.2)
+        chosen.copy_(torch.as_tensor(c))
+        g.replay()
+        torch.cuda.synchronize()
+        offsets, order, place, _ = R.sort(c, E)
+        assert r.offsets.tolist() == offsets.tolist() and np.array_equal(r.place.cpu().numpy(), place)
+        assert np.array_equal(r.order.cpu().numpy()[:len(order)], order)
 
 
 def test_gradients_against_differences():

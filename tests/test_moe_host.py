@@ -12,7 +12,7 @@ import torch
 import newton_schulz_02_gb300 as m
 from newton_schulz_02_gb300 import build as nbuild
 from tests.conftest import ROOT
-from tests.test_train_host import act8, changed, placed
+from tests.test_train_host import Placed, act8, changed, placed
 
 OK, INVALID, MISALIGNED, UNSUPPORTED, SMALL = (m.MUON_OK, m.MUON_ERR_INVALID_ARG, m.MUON_ERR_MISALIGNED,
                                                m.MUON_ERR_UNSUPPORTED, m.MUON_ERR_WORKSPACE_TOO_SMALL)
@@ -247,6 +247,10 @@ def test_gradient_list_refuses_what_it_cannot_hold(lib):
         m.Grads([])
     with pytest.raises(ValueError, match="GPU"):
         m.Grads([torch.zeros(8)])
+    off = torch.zeros(9)[1:].as_subclass(Placed)
+    off.gpu = 0
+    with pytest.raises(ValueError, match="aligned"):
+        m.Grads([off])
     t = [[torch.zeros(8)] for _ in range(4)]
     with pytest.raises(ValueError, match="GPU"):
         m.Grads(m.adamw_groups(*t))
