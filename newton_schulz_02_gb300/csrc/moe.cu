@@ -33,8 +33,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxPer = 8;       // copies a thread holds at a time
-// Copies a thread, up to which one block does it: 2048 copies take it 4.7 us, as two
-// kernels would; 4096 take it 7.0, the two kernels 5.7.
+// Copies a thread, up to which one block does it: 2048 copies take it 4.3 us, one launch
+// less; 4096 took it 7.0, the two kernels 5.7.
 constexpr int64_t kAlonePer = 2;
 constexpr int kSortBlocks = 152;
 constexpr size_t kHeader = 256;
@@ -81,21 +81,64 @@ struct SortArgs {
   uint32_t* status;
 };
 
-// Expert of copy i, or -1; a number that is neither sets *bad.
-__device__ __forceinline__ int key_of(const SortArgs& a, uint32_t i, bool* bad) {
-  if (i >= a.copies) return -1;
-  uint32_t t = 0;
-  int64_t at = i;
-  if (!a.dense) {   // rows apart from each other, or a mask: the token is needed
-    t = quotient(i, a.topk);
-    at = t * a.chosen_stride + (i - t * a.topk.d);
+// Experts of copies begin, begin + 32, ..., -1 where there is none; a number that is
+// neither sets *bad.  All loads are on their way before one is looked at, without a
+// branch between them (131072 x 8 of 256 13.7 -> 12.5 us): from the first or the last copy
+// where there is none.  PER is a.per up to 2, which is loads fewer (16384 x 8 8.6 -> 7.2 us),
+// else 8 (a form for 4 took 65536 x 8 11.8 us, this 10.5).
+template <int PER>
+__device__ __forceinline__ void load_keys(const SortArgs& a, uint32_t begin, int (&key)[PER], bool* bad) {
+  int64_t e[PER];
+  uint32_t valid = 0xFFFFFFFFu;
+  const uint32_t last = a.copies - 1;
+  if (a.copies == 0) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = -1;
+    return;
   }
-  const int64_t e = a.chosen_bytes == 8 ? static_cast<const int64_t*>(a.chosen)[at]
-                                        : static_cast<const int32_t*>(a.chosen)[at];
-  const bool valid = a.mask == nullptr || a.mask[t] != 0;   // read beside e, not before it
-  if (valid && static_cast<uint64_t>(e) < static_cast<uint64_t>(a.experts)) return static_cast<int>(e);
-  if (valid && e != -1) *bad = true;
-  return -1;
+  if (a.dense && a.chosen_bytes == 8) {
+    const int64_t* p = static_cast<const int64_t*>(a.chosen);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) e[j] = p[min(begin + (j < a.per ? 32 * j : 0), last)];
+  } else if (a.dense) {
+    const int32_t* p = static_cast<const int32_t*>(a.chosen);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) e[j] = p[min(begin + (j < a.per ? 32 * j : 0), last)];
+  } else {   // rows apart from each other, or a mask: the token is needed
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t i = min(begin + (j < a.per ? 32 * j : 0), last);
+      const uint32_t t = quotient(i, a.topk);
+      const int64_t at = t * a.chosen_stride + (i - t * a.topk.d);
+      const char* p = static_cast<const char*>(a.chosen) + at * a.chosen_bytes;
+      // both halves of an int64, or the int32 twice
+      const int32_t low = *reinterpret_cast<const int32_t*>(p);
+      const int32_t high = *reinterpret_cast<const int32_t*>(p + a.chosen_bytes - 4);
+      e[j] = a.chosen_bytes == 8 ? static_cast<int64_t>(high) << 32 | static_cast<uint32_t>(low) : low;
+    }
+    if (a.mask != nullptr) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const uint32_t i = min(begin + (j < a.per ? 32 * j : 0), last);
+        if (a.mask[quotient(i, a.topk)] == 0) valid &= ~(1u << j);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool on = j < a.per && begin + 32 * j < a.copies && (valid >> j & 1);
+    const bool known = static_cast<uint64_t>(e[j]) < static_cast<uint64_t>(a.experts);
+    key[j] = on && known ? static_cast<int>(e[j]) : -1;
+    if (on && !known && e[j] != -1) *bad = true;
+  }
+}
+
+// Ranks that k_moe_rank left for copies begin, begin + 32, ... (for no copy: any).
+template <int PER>
+__device__ __forceinline__ void load_ranks(const SortArgs& a, uint32_t begin, int (&rank)[PER]) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    rank[j] = a.place[min(begin + (j < a.per ? 32 * j : 0), a.copies - 1)];
 }
 
 // First of a lane's copies in a round: a block's copies are consecutive, and so
@@ -149,11 +192,13 @@ __device__ __forceinline__ void write_copy(const SortArgs& a, uint32_t i, bool k
 // expert's word of `lanes`, and its rank is the count so far plus the bits below its
 // own; the lowest lane clears the word and moves the count on.  Then the counts are
 // summed up over the warps.  Both kernels for
-// 131072 x 8 of 256 take 13.6 us; finding the lanes of one expert with a match over the
-// warp took 6.3 us more, with a vote for each bit of its number 3.7.
+// 131072 x 8 of 256 take 12.5 us; finding the lanes of one expert with a match over the
+// warp took 6.3 us more, with a vote for each bit of its number 3.7.  Half of each
+// kernel is its first loads: choices in the one; ranks and counts, 147 KB that
+// every SM reads, in the other.
 // ALONE: the block holds all copies, and its ranks become rows at once; else they
 // are left in `place` for k_moe_place, with the block's counts.
-template <bool ALONE>
+template <bool ALONE, int PER>
 __global__ void __launch_bounds__(kSortThreads) k_moe_rank(const __grid_constant__ SortArgs a) {
   extern __shared__ int sm[];
   int* base = sm;                                              // [experts]: ALONE: first row
@@ -168,16 +213,15 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_rank(const __grid_constant
   int total = 0;                               // of this thread's expert, over the rounds
   for (int round = 0; round < a.rounds; ++round) {
     const uint32_t begin = lane_begin(a, round);
-    int key[kMaxPer], rank[kMaxPer];
-#pragma unroll
-    for (int j = 0; j < kMaxPer; ++j) key[j] = j < a.per ? key_of(a, begin + 32 * j, &bad) : -1;
+    int key[PER], rank[PER];
+    load_keys(a, begin, key, &bad);
     for (int e = lane; e < a.experts; e += 32) {
       mine[e] = 0;
       my_lanes[e] = 0;
     }
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kMaxPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       if (j >= a.per) break;   // the same for all threads
       const bool on = key[j] >= 0;
       if (on) atomicOr(&my_lanes[key[j]], 1u << lane);
@@ -211,7 +255,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_rank(const __grid_constant
     if (tid < a.experts) base[tid] = ALONE ? first : rounds_before;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kMaxPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       if (j >= a.per) break;
       const uint32_t i = begin + 32 * j;
       int r = key[j] >= 0 ? mine[key[j]] + rank[j] : -1;
@@ -234,6 +278,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_rank(const __grid_constant
 // Ranks to rows: the block's first row of each expert is the expert's plus what the
 // blocks before this one have of it.  The copies of a block that has one round go out
 // sorted, so that runs of `order` are written together: 131072 x 8 of 256 17.2 -> 13.7 us.
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constant__ SortArgs a) {
   extern __shared__ int sm[];                  // [8 threads]: sums by thread, then the sorted copies
   int4* part = reinterpret_cast<int4*>(sm);    // totals, then counts of the blocks before
@@ -243,13 +288,10 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
   const int tid = threadIdx.x;
   const bool sorted = a.rounds == 1;
   bool bad = false;
-  int key[kMaxPer], rank[kMaxPer];
-#pragma unroll
-  for (int j = 0; j < kMaxPer; ++j)            // on their way during the wait
-    key[j] = j < a.per ? key_of(a, lane_begin(a, 0) + 32 * j, &bad) : -1;
+  int key[PER], rank[PER];
+  load_keys(a, lane_begin(a, 0), key, &bad);   // before the wait
   griddep_wait();
-#pragma unroll
-  for (int j = 0; j < kMaxPer; ++j) rank[j] = key[j] >= 0 ? a.place[lane_begin(a, 0) + 32 * j] : -1;
+  load_ranks(a, lane_begin(a, 0), rank);
   const bool bad_choice = blockIdx.x == 0 && tid < a.blocks && a.flags[tid] != 0;
   const int own = tid < a.experts ? a.counts[blockIdx.x * a.stride + tid] : 0;
   const int quads = 1 << a.quad_bits;          // threads of a row of counts, four experts each
@@ -287,7 +329,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
     const uint32_t block_first = blockIdx.x * a.per * kSortThreads;
     uint32_t* stage = reinterpret_cast<uint32_t*>(sm);   // expert and copy of the block
 #pragma unroll
-    for (int j = 0; j < kMaxPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       if (key[j] < 0) continue;
       const uint32_t i = lane_begin(a, 0) + 32 * j;
       const int at = local[key[j]] + rank[j];
@@ -305,13 +347,11 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
     for (int round = 0; round < a.rounds; ++round) {
       const uint32_t begin = lane_begin(a, round);
       if (round > 0) {
-#pragma unroll
-        for (int j = 0; j < kMaxPer; ++j) key[j] = j < a.per ? key_of(a, begin + 32 * j, &bad) : -1;
-#pragma unroll
-        for (int j = 0; j < kMaxPer; ++j) rank[j] = key[j] >= 0 ? a.place[begin + 32 * j] : -1;
+        load_keys(a, begin, key, &bad);
+        load_ranks(a, begin, rank);
       }
 #pragma unroll
-      for (int j = 0; j < kMaxPer; ++j)
+      for (int j = 0; j < PER; ++j)
         if (key[j] >= 0)
           write_copy(a, begin + 32 * j, true, static_cast<uint32_t>(base[key[j]] + rank[j]));
     }
@@ -711,6 +751,37 @@ muon_status_t row_args(const muon_routing_t* r, int width, RowArgs* a) {
   return MUON_OK;
 }
 
+template <bool ALONE, int PER>
+cudaError_t run_sort(const SortArgs& a, double bytes, cudaStream_t st) {
+  const size_t smem = rank_smem(a.experts);
+  if (smem > 48 * 1024) {   // per device, so with every call that needs it
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_moe_rank<ALONE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(rank_smem(kMaxExperts)));
+    if (e != cudaSuccess) return e;
+  }
+  prof_begin(kKindMoe, st);
+  k_moe_rank<ALONE, PER><<<a.blocks, kSortThreads, smem, st>>>(a);
+  prof_end(kKindMoe, st, 0.0, bytes);
+  const cudaError_t e = cudaGetLastError();
+  if (ALONE || e != cudaSuccess) return e;
+  // a programmatic dependent of the kernel before (it waits for the ranks)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.blocks);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = place_smem(a.experts);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  prof_begin(kKindMoe, st);
+  const cudaError_t p = cudaLaunchKernelEx(&cfg, k_moe_place<PER>, a);
+  prof_end(kKindMoe, st, 0.0, 0.0);
+  return p;
+}
+
 // `launch` for every token, `cols` columns an item, in pieces of fewer than 2^30 items.
 template <class F>
 muon_status_t by_tokens(RowArgs a, int64_t tokens, int xdt, int cols, F launch) {
@@ -922,33 +993,10 @@ muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen
   a.counts = reinterpret_cast<int*>(ws + kHeader + align256(static_cast<size_t>(plan.blocks) * 4));
   const double bytes = static_cast<double>(a.copies) * (chosen_bytes + 8);
   const bool alone = plan.blocks == 1;
-  const size_t smem = rank_smem(r->experts);
-  // per device, so with every call that needs it
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(alone ? k_moe_rank<true> : k_moe_rank<false>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(rank_smem(kMaxExperts))) != cudaSuccess)
-    return MUON_ERR_CUDA;
-  prof_begin(kKindMoe, st);
-  if (alone) k_moe_rank<true><<<1, kSortThreads, smem, st>>>(a);
-  else k_moe_rank<false><<<plan.blocks, kSortThreads, smem, st>>>(a);
-  prof_end(kKindMoe, st, 0.0, bytes);
-  if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
-  if (alone) return MUON_OK;
-  // a programmatic dependent of the kernel before (it waits for the ranks)
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(plan.blocks);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = place_smem(r->experts);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  prof_begin(kKindMoe, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_moe_place, a);
-  prof_end(kKindMoe, st, 0.0, 0.0);
+  cudaError_t e;
+  if (plan.per == 1) e = alone ? run_sort<true, 1>(a, bytes, st) : run_sort<false, 1>(a, bytes, st);
+  else if (plan.per == 2) e = alone ? run_sort<true, 2>(a, bytes, st) : run_sort<false, 2>(a, bytes, st);
+  else e = run_sort<false, 8>(a, bytes, st);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
