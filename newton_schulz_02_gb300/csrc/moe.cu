@@ -409,13 +409,15 @@ __device__ __forceinline__ float weight_at(const void* w, int wdt, int64_t i) {
 template <typename TX, typename TY, bool WHOLE, bool CODES>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant__ RowArgs a) {
   const Item p = item_of<kCols>(a);
+  const int32_t* at = a.place + static_cast<int64_t>(p.token) * a.topk;
+  uint32_t next = static_cast<uint32_t>(at[0]);   // a row ahead
   float x[kCols];
   load_values<TX, WHOLE>(a.x, p.token, p.col, p.n, x);
   Codes<kCols> c;
   if constexpr (CODES) c = encode(x);
-  const int32_t* at = a.place + static_cast<int64_t>(p.token) * a.topk;
   for (int k = 0; k < a.topk; ++k) {
-    const uint32_t row = static_cast<uint32_t>(at[k]);
+    const uint32_t row = next;
+    if (k + 1 < a.topk) next = static_cast<uint32_t>(at[k + 1]);
     const bool in = p.on && row < a.rows;
     store_values<TY, WHOLE>(a.y, in ? row : 0, p.col, in ? p.n : 0, x);
     if constexpr (CODES) {
@@ -625,8 +627,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 // x = dout, y = ys, z = dys.  blockDim.x threads take one token (whole warps, or a
 // part of one: SUB) and blockDim.y tokens share a block.  kDots choices are taken in
 // a pass over the columns.  Without ROWS only the weights' gradient is formed.
+template <typename TY, bool ROWS, int kDots>
+constexpr int kBackwardThreads = ROWS ? (kDots > 2 ? 512 : 768) : sizeof(TY) == 2 ? 1024 : 768;   // of an SM
+
 template <typename TX, typename TY, bool WHOLE, bool SUB, bool ROWS, int kDots>
-__global__ void __launch_bounds__(kThreads, !ROWS && sizeof(TY) == 2 ? 4 : kDots > 2 && ROWS ? 2 : 3)
+__global__ void __maxnreg__((65536 / kBackwardThreads<TY, ROWS, kDots> / 8 * 8))
     k_moe_combine_backward(const __grid_constant__ RowArgs a) {
   constexpr int kAhead = kDots > 2 && ROWS && sizeof(TY) == 2 ? 4 : 2;   // rows in flight
   constexpr int N = kCols;
@@ -647,12 +652,21 @@ __global__ void __launch_bounds__(kThreads, !ROWS && sizeof(TY) == 2 ? 4 : kDots
       const int col = c0 + threadIdx.x * N;
       const int n = on ? a.cols - col : 0;
       float d[N];
-      load_values<TX, WHOLE>(a.x, token, col, n, d);
+      Fetched<TX, WHOLE, N> d_raw;
+      if constexpr (ROWS) fetch(a.x, token, col, n, d_raw);   // on its way beside the rows
+      else load_values<TX, WHOLE>(a.x, token, col, n, d);     // (too many registers)
 #pragma unroll
       for (int j0 = 0; j0 < kDots; j0 += kAhead) {
         if (k0 + j0 >= a.topk) break;   // the same for all threads
         Fetched<TY, WHOLE, N> y[kAhead];
         uint32_t row[kAhead];
+        float w[kAhead];
+        if constexpr (ROWS) {   // all that is read is asked for before any of it is looked at:
+                                // 16384 tokens, 8 rows of 7168 bf16 639 -> 609 us
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            w[j] = k0 + j0 + j < a.topk ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const int k = k0 + j0 + j;
@@ -661,15 +675,17 @@ __global__ void __launch_bounds__(kThreads, !ROWS && sizeof(TY) == 2 ? 4 : kDots
           fetch(a.y, in ? row[j] : 0, col, in ? n : 0, y[j]);
         }
         if constexpr (ROWS) {
+          if (j0 == 0) values_of(d_raw, n, d);
+        }
+        if constexpr (ROWS) {
           if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads come first
           // dys needs nothing of ys: written while that is on its way
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
             const bool in = row[j] < a.rows;
-            const float w = in ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
             float g[N];
 #pragma unroll
-            for (int c = 0; c < N; ++c) g[c] = w * d[c];
+            for (int c = 0; c < N; ++c) g[c] = w[j] * d[c];
             store_values<TY, WHOLE>(a.z, in ? row[j] : 0, col, in ? n : 0, g);
           }
         }
@@ -862,7 +878,12 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaS
     const unsigned passes = (items + kThreads - 1) / kThreads;
     threads = ((items + passes - 1) / passes + 31) / 32 * 32;
   }
-  const unsigned tokens = kThreads / threads;
+  // as many tokens a block as fill an SM's threads best (4752 tokens, 6 rows of 1472
+  // bf16, 96 threads a token: 49 us with one a block, 56 with two)
+  const unsigned most = whole || narrow ? kBackwardThreads<TY, true, DOTS> : kBackwardThreads<TY, false, DOTS>;
+  unsigned tokens = kThreads / threads;
+  for (unsigned n = tokens; n > 0; --n)
+    if (most / (n * threads) * n > most / (tokens * threads) * tokens) tokens = n;
   const dim3 block(threads, tokens);   // a token's threads are lanes side by side
   const unsigned grid = (a.tokens + tokens - 1) / tokens;
   const bool sub = threads < 32;
