@@ -8,11 +8,11 @@
 // read rate is the bound.  Tensors of any number and size share a launch: a
 // persistent grid strides over fixed pieces of every tensor.
 //
-// A thread adds the squares of 32 values in fp32 and those sums in a pair of
+// A thread adds the squares of 32 values (64 of bf16) in fp32 and those sums in a pair of
 // fp32 (the rounding error of each addition is kept in the second), which
 // costs 7 additions for 32 values and holds 48 bits; an fp64 addition for each
 // value would take five times as long as the reads.  Squares outside fp32's
-// comfortable range (the sum of 32 below 2^-96 or above 2^80, infinite or NaN)
+// comfortable range (that sum below 2^-96 or above 2^80, infinite or NaN)
 // are added up in fp64 instead, value by value.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,8 +29,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                                       // values of a vector
-constexpr int kUnroll = 4;                                    // vectors of a thread in a piece
-constexpr int64_t kPiece = int64_t{kThreads} * kVec * kUnroll;
+// Vectors of a thread in a piece, 128 bytes of either type (0.54 G values of bf16: 154 us,
+// with 64 bytes 159).
+constexpr int kUnrollBf16 = 8, kUnrollF32 = 4;
+int64_t piece_values(int dtype) {
+  return int64_t{kThreads} * kVec * (dtype == MUON_BF16 ? kUnrollBf16 : kUnrollF32);
+}
 constexpr int kMaxGroups = 64;                                // groups of a launch
 constexpr int kFinThreads = 256;
 constexpr size_t kHeader = 256;
@@ -69,23 +73,31 @@ __device__ __forceinline__ void add_pair(Sum& s, float h, float l) {
   s.lo = e - (s.hi - t);
 }
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < kVec; ++k)
-    x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+// Value k of a vector as it was loaded.
+__device__ __forceinline__ float value(const uint4 (&u)[1], int k) {   // bf16
+  const uint32_t w = k < 2 ? u[0].x : k < 4 ? u[0].y : k < 6 ? u[0].z : u[0].w;
+  return __uint_as_float(k % 2 ? w & 0xFFFF0000u : w << 16);
+}
+__device__ __forceinline__ float value(const uint4 (&u)[2], int k) {   // fp32
+  const uint4& v = u[k / 4];
+  return __uint_as_float(k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w);
 }
 
-// Adds the squares of a thread's values of a piece.
-__device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kVec]) {
-  float part[kUnroll];
+// Adds the squares of a thread's values of a piece, WORDS 16-byte words a vector.
+template <int WORDS, int N>
+__device__ __forceinline__ void add_squares(Sum& s, const uint4 (&u)[N][WORDS]) {
+  float part[N];
 #pragma unroll
-  for (int r = 0; r < kUnroll; ++r) {
-    part[r] = x[r][0] * x[r][0];
+  for (int r = 0; r < N; ++r) {
+    part[r] = value(u[r], 0) * value(u[r], 0);
 #pragma unroll
-    for (int k = 1; k < kVec; ++k) part[r] = fmaf(x[r][k], x[r][k], part[r]);
+    for (int k = 1; k < kVec; ++k) part[r] = fmaf(value(u[r], k), value(u[r], k), part[r]);
   }
-  const float sq = (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+  for (int half = N / 2; half >= 1; half /= 2)
+#pragma unroll
+    for (int r = 0; r < half; ++r) part[r] += part[r + half];
+  const float sq = part[0];
   if (sq >= 0x1p-96f && sq <= 0x1p80f) {
     const float t = s.hi + sq, b = t - s.hi;
     s.lo += (s.hi - (t - b)) + (sq - b);
@@ -95,18 +107,50 @@ __device__ __forceinline__ void add_squares(Sum& s, const float (&x)[kUnroll][kV
   if (sq == 0.f) {   // nearly always nothing but zeros: an expert without tokens
     uint32_t any = 0;
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r)
+    for (int r = 0; r < N; ++r)
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) any |= __float_as_uint(x[r][k]);
-    if ((any & 0x7FFFFFFFu) == 0) return;
+      for (int w = 0; w < WORDS; ++w) any |= u[r][w].x | u[r][w].y | u[r][w].z | u[r][w].w;
+    if ((any & 0x7FFF7FFFu) == 0 && (WORDS == 1 || (any & 0x7FFFFFFFu) == 0)) return;
   }
-#pragma unroll 1
-  for (int r = 0; r < kUnroll; ++r)
+#pragma unroll
+  for (int r = 0; r < N; ++r)
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
-      const float v = r == 0 ? x[0][k] : r == 1 ? x[1][k] : r == 2 ? x[2][k] : x[3][k];
-      if (v != 0.f) s.wide = fma(static_cast<double>(v), static_cast<double>(v), s.wide);
+      const double v = value(u[r], k);
+      s.wide = fma(v, v, s.wide);
     }
+}
+
+// Loads a thread's vectors of a piece, which begins at vector v0 of the tensor at p (0
+// where there is none), and adds their squares.
+template <int WORDS, int N>
+__device__ __forceinline__ void add_piece(Sum& s, const NormGroup& G, const char* p, int64_t v0, int tid) {
+  int64_t at[N];   // vectors from the tensor's start; -1: none
+  if (G.stride == 0) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const int64_t v = v0 + r * kThreads + tid;
+      at[r] = v < G.vecs ? v : -1;
+    }
+  } else {
+    const int64_t row0 = v0 / G.per_row.d;
+    const uint32_t col0 = static_cast<uint32_t>(v0 - row0 * G.per_row.d);
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const uint32_t c = col0 + r * kThreads + tid;
+      const uint32_t down = quotient(c, G.per_row);
+      at[r] = v0 + r * kThreads + tid < G.vecs ? (row0 + down) * G.stride + (c - down * G.per_row.d) : -1;
+    }
+  }
+  uint4 u[N][WORDS];
+#pragma unroll
+  for (int r = 0; r < N; ++r)
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) {
+      u[r][w] = make_uint4(0, 0, 0, 0);
+      if (at[r] >= 0) u[r][w] = reinterpret_cast<const uint4*>(p)[WORDS * at[r] + w];
+    }
+  add_squares(s, u);
 }
 
 // Pieces first, first + step, ... of all tensors, thread tid of the kThreads that
@@ -127,53 +171,16 @@ __device__ __forceinline__ Sum sum_pieces(const NormArgs& a, int64_t first, int6
       *flags |= MUON_FLAG_MISALIGNED;
       continue;   // the tensor is left out
     }
-    const int64_t v0 = piece * (kPiece / kVec);
-    float x[kUnroll][kVec];
-    int64_t at[kUnroll];   // vectors from the tensor's start; -1: none
-    if (G.stride == 0) {
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        const int64_t v = v0 + r * kThreads + tid;
-        at[r] = v < G.vecs ? v : -1;
-      }
-    } else {
-      const int64_t row0 = v0 / G.per_row.d;
-      const uint32_t col0 = static_cast<uint32_t>(v0 - row0 * G.per_row.d);
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        const uint32_t c = col0 + r * kThreads + tid;
-        const uint32_t down = quotient(c, G.per_row);
-        at[r] = v0 + r * kThreads + tid < G.vecs ? (row0 + down) * G.stride + (c - down * G.per_row.d) : -1;
-      }
-    }
-    if (G.dtype == MUON_BF16) {
-      uint4 u[kUnroll];
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        u[r] = make_uint4(0, 0, 0, 0);
-        if (at[r] >= 0) u[r] = reinterpret_cast<const uint4*>(p)[at[r]];
-      }
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) unpack(u[r], x[r]);
-    } else {
-#pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        float4 q[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (at[r] >= 0) {
-          q[0] = reinterpret_cast<const float4*>(p)[2 * at[r]];
-          q[1] = reinterpret_cast<const float4*>(p)[2 * at[r] + 1];
-        }
-        x[r][0] = q[0].x; x[r][1] = q[0].y; x[r][2] = q[0].z; x[r][3] = q[0].w;
-        x[r][4] = q[1].x; x[r][5] = q[1].y; x[r][6] = q[1].z; x[r][7] = q[1].w;
-      }
-    }
+    if (G.dtype == MUON_BF16)
+      add_piece<1, kUnrollBf16>(s, G, p, piece * kThreads * kUnrollBf16, tid);
+    else
+      add_piece<2, kUnrollF32>(s, G, p, piece * kThreads * kUnrollF32, tid);
     if (G.tail > 0 && piece == G.pieces - 1 && tid < G.tail) {   // fewer than 8 values
       const int64_t i = G.vecs * kVec + tid;
       const float v = G.dtype == MUON_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
                                            : reinterpret_cast<const float*>(p)[i];
       s.wide = fma(static_cast<double>(v), static_cast<double>(v), s.wide);
     }
-    add_squares(s, x);
   }
   return s;
 }
@@ -214,7 +221,9 @@ __device__ __forceinline__ Sum block_sum(Sum s, uint32_t flags, uint32_t* all) {
   return s;
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ NormArgs a) {
+// Three blocks an SM: without the bound the fp64 path takes 124 registers and two fit
+// (0.54 G bf16 169 us); four spill (353).
+__global__ void __launch_bounds__(kThreads, 3) k_grad_norm(const __grid_constant__ NormArgs a) {
   griddep_launch_dependents();
   uint32_t flags = 0;
   const Sum mine = sum_pieces(a, blockIdx.x, gridDim.x, threadIdx.x, &flags);
@@ -368,7 +377,7 @@ muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max
       g.ptrs = src.ptrs;
       g.vecs = values / kVec;
       g.tail = static_cast<int>(values % kVec);
-      g.pieces = (values + kPiece - 1) / kPiece;
+      g.pieces = (values + piece_values(src.dtype) - 1) / piece_values(src.dtype);
       g.stride = strided ? src.row_stride / kVec : 0;
       g.per_row = divider(strided ? static_cast<uint32_t>(src.cols / kVec) : 1);
       g.dtype = src.dtype;

@@ -65,7 +65,7 @@ SortPlan sort_plan(int64_t copies) {
 struct SortArgs {
   uint32_t copies, rows;
   int experts, per, rounds, blocks;
-  int dense;                 // copy i's choice is chosen[i], and there is no mask
+  int dense;                 // copy i's choice is chosen[i]
   int quad_bits;             // log2 of the threads that read one row of counts
   int stride;                // of the rows of counts, a multiple of 4
   Divider topk;
@@ -81,64 +81,70 @@ struct SortArgs {
   uint32_t* status;
 };
 
-// Experts of copies begin, begin + 32, ..., -1 where there is none; a number that is
-// neither sets *bad.  All loads are on their way before one is looked at, without a
-// branch between them (131072 x 8 of 256 13.7 -> 12.5 us): from the first or the last copy
-// where there is none.  PER is a.per up to 2, which is loads fewer (16384 x 8 8.6 -> 7.2 us),
-// else 8 (a form for 4 took 65536 x 8 11.8 us, this 10.5).
+// Copy j of a thread's, or one that is there: loads from it need no branch between them, so
+// that all are on their way before one is looked at (131072 x 8 of 256 13.7 -> 12.5 us).
+__device__ __forceinline__ uint32_t some_copy(const SortArgs& a, uint32_t begin, int j) {
+  return min(begin + (j < a.per ? 32 * j : 0), a.copies - 1);
+}
+
+// Choices of copies begin, begin + 32, ... as they are.  PER is a.per up to 2, which is
+// loads fewer (16384 x 8 8.6 -> 7.2 us), else 8 (a form for 4 took 65536 x 8 11.8 us, this
+// 10.5).  There are copies.
 template <int PER>
-__device__ __forceinline__ void load_keys(const SortArgs& a, uint32_t begin, int (&key)[PER], bool* bad) {
-  int64_t e[PER];
-  uint32_t valid = 0xFFFFFFFFu;
-  const uint32_t last = a.copies - 1;
-  if (a.copies == 0) {
+__device__ __forceinline__ void load_choices(const SortArgs& a, uint32_t begin, int64_t (&e)[PER]) {
+  int64_t at[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) key[j] = -1;
-    return;
-  }
-  if (a.dense && a.chosen_bytes == 8) {
-    const int64_t* p = static_cast<const int64_t*>(a.chosen);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) e[j] = p[min(begin + (j < a.per ? 32 * j : 0), last)];
-  } else if (a.dense) {
-    const int32_t* p = static_cast<const int32_t*>(a.chosen);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) e[j] = p[min(begin + (j < a.per ? 32 * j : 0), last)];
-  } else {   // rows apart from each other, or a mask: the token is needed
+  for (int j = 0; j < PER; ++j) at[j] = some_copy(a, begin, j);
+  if (!a.dense) {   // rows apart from each other
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const uint32_t i = min(begin + (j < a.per ? 32 * j : 0), last);
-      const uint32_t t = quotient(i, a.topk);
-      const int64_t at = t * a.chosen_stride + (i - t * a.topk.d);
-      const char* p = static_cast<const char*>(a.chosen) + at * a.chosen_bytes;
-      // both halves of an int64, or the int32 twice
-      const int32_t low = *reinterpret_cast<const int32_t*>(p);
-      const int32_t high = *reinterpret_cast<const int32_t*>(p + a.chosen_bytes - 4);
-      e[j] = a.chosen_bytes == 8 ? static_cast<int64_t>(high) << 32 | static_cast<uint32_t>(low) : low;
+      const uint32_t i = static_cast<uint32_t>(at[j]), t = quotient(i, a.topk);
+      at[j] = t * a.chosen_stride + (i - t * a.topk.d);
     }
-    if (a.mask != nullptr) {
+  }
+  if (a.chosen_bytes == 8) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const uint32_t i = min(begin + (j < a.per ? 32 * j : 0), last);
-        if (a.mask[quotient(i, a.topk)] == 0) valid &= ~(1u << j);
-      }
-    }
+    for (int j = 0; j < PER; ++j) e[j] = static_cast<const int64_t*>(a.chosen)[at[j]];
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) e[j] = static_cast<const int32_t*>(a.chosen)[at[j]];
+  }
+}
+
+// Their experts, -1 where there is none; a number that is neither sets *bad.
+template <int PER>
+__device__ __forceinline__ void load_keys(const SortArgs& a, uint32_t begin, int (&key)[PER], bool* bad) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) key[j] = -1;
+  if (a.copies == 0) return;
+  int64_t e[PER];
+  uint32_t valid[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) valid[j] = 1;
+  load_choices(a, begin, e);
+  if (a.mask != nullptr) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) valid[j] = a.mask[quotient(some_copy(a, begin, j), a.topk)];
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const bool on = j < a.per && begin + 32 * j < a.copies && (valid >> j & 1);
+    const bool on = j < a.per && begin + 32 * j < a.copies && valid[j] != 0;
     const bool known = static_cast<uint64_t>(e[j]) < static_cast<uint64_t>(a.experts);
-    key[j] = on && known ? static_cast<int>(e[j]) : -1;
+    if (on && known) key[j] = static_cast<int>(e[j]);
     if (on && !known && e[j] != -1) *bad = true;
   }
 }
 
-// Ranks that k_moe_rank left for copies begin, begin + 32, ... (for no copy: any).
+// Ranks that k_moe_rank left, -1 for a copy without an expert; key gets the choice of the
+// others.
 template <int PER>
-__device__ __forceinline__ void load_ranks(const SortArgs& a, uint32_t begin, int (&rank)[PER]) {
+__device__ __forceinline__ void load_ranks(const SortArgs& a, uint32_t begin, const int64_t (&e)[PER],
+                                           int (&key)[PER], int (&rank)[PER]) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j) rank[j] = a.place[some_copy(a, begin, j)];
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    rank[j] = a.place[min(begin + (j < a.per ? 32 * j : 0), a.copies - 1)];
+    key[j] = j < a.per && begin + 32 * j < a.copies && rank[j] >= 0 ? static_cast<int>(e[j]) : -1;
 }
 
 // First of a lane's copies in a round: a block's copies are consecutive, and so
@@ -287,11 +293,11 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
   const bool sorted = a.rounds == 1;
-  bool bad = false;
+  int64_t choice[PER];
   int key[PER], rank[PER];
-  load_keys(a, lane_begin(a, 0), key, &bad);   // before the wait
+  load_choices(a, lane_begin(a, 0), choice);   // before the wait
   griddep_wait();
-  load_ranks(a, lane_begin(a, 0), rank);
+  load_ranks(a, lane_begin(a, 0), choice, key, rank);
   const bool bad_choice = blockIdx.x == 0 && tid < a.blocks && a.flags[tid] != 0;
   const int own = tid < a.experts ? a.counts[blockIdx.x * a.stride + tid] : 0;
   const int quads = 1 << a.quad_bits;          // threads of a row of counts, four experts each
@@ -347,8 +353,8 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const __grid_constan
     for (int round = 0; round < a.rounds; ++round) {
       const uint32_t begin = lane_begin(a, round);
       if (round > 0) {
-        load_keys(a, begin, key, &bad);
-        load_ranks(a, begin, rank);
+        load_choices(a, begin, choice);
+        load_ranks(a, begin, choice, key, rank);
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j)
@@ -999,7 +1005,7 @@ muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen
   a.rounds = plan.rounds;
   a.blocks = plan.blocks;
   while (4 << a.quad_bits < r->experts) ++a.quad_bits;
-  a.dense = token_mask == nullptr && chosen_stride == r->topk;
+  a.dense = chosen_stride == r->topk;
   a.stride = static_cast<int>(round_up(r->experts, 4));
   a.topk = divider(static_cast<uint32_t>(r->topk));
   a.chosen = chosen;

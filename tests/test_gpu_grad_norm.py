@@ -2,9 +2,9 @@
 GPU against the float64 oracle.
 
 Tolerance of the norm: 32 squares are added in fp32 (at most 10 roundings in a
-chain and one for the square: 11 U relative, all terms positive), the rest in 48
-bits; a root halves that, and the result is rounded: 7 U.  The factor: the same and
-two roundings."""
+chain and one for the square: 11 U relative, all terms positive; 64 of bf16, whose
+squares are exact, with 11), the rest in 48 bits; a root halves that, and the result
+is rounded: 7 U.  The factor: the same and two roundings."""
 import math
 
 import numpy as np
