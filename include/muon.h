@@ -61,12 +61,14 @@ typedef enum {
 } muon_status_t;
 
 /* Bits of the device status word (muon_get_status). */
-#define MUON_FLAG_NONFINITE 0x1u   /* some matrix had a non-finite Frobenius norm */
+#define MUON_FLAG_NONFINITE 0x1u   /* some matrix had a non-finite Frobenius norm; the norm of all
+                                      gradients, or a factor on them, was not finite */
 #define MUON_FLAG_TIMEOUT 0x2u     /* a bounded device wait ran out; results are invalid */
 #define MUON_FLAG_MISALIGNED 0x4u  /* a pointer in a device pointer array was not 16 B aligned;
                                       that matrix was left untouched */
 #define MUON_FLAG_INDEX 0x8u       /* an expert number or an offset in a device array was out of
-                                      range or out of order; it was ignored or cut to the range */
+                                      range or out of order; it was ignored or cut to the range;
+                                      or there were fewer rows than copies to put there */
 
 typedef enum { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype_t;
 

@@ -1084,6 +1084,7 @@ muon_status_t muon_moe_combine_backward(const void* dout, muon_dtype_t ddt, int6
   if (s == MUON_OK) s = check_rows(weights, r->tokens, wdt, w_stride, r->topk);
   if (s == MUON_OK) s = check_rows(dweights, r->tokens, wdt, dw_stride, r->topk);
   if (s != MUON_OK) return s;
+  if (dys == ys && r->rows > 1 && dys_stride != y_stride) return MUON_ERR_INVALID_ARG;
   a.x = plane(dout, dout_stride);
   a.y = plane(ys, y_stride);
   a.z = plane(dys, dys_stride);

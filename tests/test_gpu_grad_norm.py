@@ -183,6 +183,19 @@ def test_muon_step_with_a_factor_is_the_step_of_the_scaled_gradient(style, shape
     assert torch.equal(W, W2) and torch.equal(M, M2) and torch.equal(G, keep)
 
 
+@pytest.mark.parametrize("shape", [(2, 256, 384), (2, 384, 256), (2, 128, 512)])
+def test_muon_step_scales_bf16_gradients_in_fp32(shape):
+    """bf16 G: the product is not rounded to bf16, as in a step whose G is fp32."""
+    W, G, M = muon_case(torch.bfloat16, shape)
+    scale = torch.tensor([0.0377], device=DEV)
+    W2, M2, G2 = W.clone(), M.clone(), G.float() * scale
+    a, b = m.Group.stacked(W, G, M), m.Group.stacked(W2, G2, M2)
+    ws = m.workspace(m.muon_step_workspace_size([a]))
+    m.muon_step_batched([a], m.hparams(), ws, grad_scale=scale)
+    m.muon_step_batched([b], m.hparams(), ws)
+    assert torch.equal(W, W2) and torch.equal(M, M2)
+
+
 def test_steps_with_factor_one_are_the_steps_without():
     one = torch.ones(1, device=DEV)
     W, G, M = muon_case(torch.bfloat16, (2, 256, 384))

@@ -314,6 +314,65 @@ def test_row_offsets_past_32_bits():
     assert torch.equal(xs[rowsat], (0.5 * x).repeat_interleave(K, 0))
 
 
+def test_more_items_than_one_launch_takes():
+    """Over 2^30 pieces of columns: the tokens are taken in several launches."""
+    T = (1 << 29) + 5
+    r = m.Routing.empty(T, 1, 2, rows=6)
+    r.place.fill_(-1)
+    held = torch.tensor([0, 7, (1 << 29) - 1, 1 << 29, (1 << 29) + 3, T - 1], device=DEV)
+    r.place[held, 0] = torch.arange(6, dtype=torch.int32, device=DEV)
+    x = torch.full((T, 1), 3.0, dtype=torch.bfloat16, device=DEV)
+    x[held, 0] = torch.arange(1, 7, device=DEV).bfloat16()
+    xs = torch.zeros(6, 1, device=DEV)
+    m.muon_moe_dispatch(x, r, xs)
+    assert xs[:, 0].tolist() == [1, 2, 3, 4, 5, 6]
+    w = torch.full((T, 1), 0.5, dtype=torch.bfloat16, device=DEV)
+    dys, dw = torch.zeros_like(xs), torch.full_like(w, 9.0)
+    m.muon_moe_combine_backward(x, xs, w, r, dys, dw)
+    assert dys[:, 0].tolist() == [0.5, 1, 1.5, 2, 2.5, 3]
+    assert dw[held, 0].tolist() == [1, 4, 9, 16, 25, 36] and int((dw != 0).sum()) == 6
+    m.muon_moe_combine(xs, w, r, x)
+    assert x[held, 0].tolist() == [0.5, 1, 1.5, 2, 2.5, 3] and int((x != 0).sum()) == 6
+
+
+def test_two_streams_at_once():
+    """Two batches on two streams, each with buffers of its own, interleaved call by call."""
+    def batch(seed):
+        T, E, K, D = 3000 + seed, 20, 4, 515
+        chosen = torch.as_tensor(choices(seed, T, E, K, 0.1), device=DEV)
+        r = m.Routing.empty(T, K, E)
+        ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+        x, w = torch.randn(T, D, device=DEV), torch.rand(T, K, device=DEV)
+        xs = torch.zeros(r.rows, D, dtype=torch.bfloat16, device=DEV)
+        dys = torch.zeros_like(xs)
+        out, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+        calls = [lambda s: m.muon_moe_sort(chosen, r, ws, stream=s),
+                 lambda s: m.muon_moe_dispatch(x, r, xs, stream=s),
+                 lambda s: m.muon_moe_combine(xs, w, r, out, stream=s),
+                 lambda s: m.muon_moe_combine_backward(x, xs, w, r, dys, dw, stream=s),
+                 lambda s: m.muon_moe_dispatch_backward(dys, r, dx, stream=s)]
+        return calls, (r.offsets, r.place, xs, out, dys, dw, dx)
+
+    both, streams = [batch(1), batch(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    alone = []
+    for calls, results in both:
+        for c in calls:
+            c(streams[0])
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in results])
+        for t in results:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for first, second in zip(both[0][0], both[1][0]):
+            first(streams[0])
+            second(streams[1])
+    torch.cuda.synchronize()
+    for (_, results), want in zip(both, alone):
+        assert all(torch.equal(a, b) for a, b in zip(results, want))
+
+
 def test_repeats_its_bits_and_runs_on_another_stream():
     T, E, K, D = 700, 16, 4, 1111
     chosen = torch.as_tensor(choices(2, T, E, K, 0.1), device=DEV)

@@ -116,6 +116,7 @@ def test_row_pass_refusals(lib):
     for bad in (dict(z=None), dict(zst=99), dict(dw=None), dict(dwst=1)):
         assert combine_b(**bad) == INVALID, bad
     assert combine_b(z=z + 1) == MISALIGNED and combine_b(dw=dw + 2) == MISALIGNED
+    assert combine_b(z=y, zst=104) == INVALID     # ys itself, but not its rows
     for bad in (act8(rows=7), act8(cols=99), act8(codes=None)):
         assert dispatch(x8=bad) == INVALID
     assert dispatch(x8=act8(exps=0x20001)) == MISALIGNED
