@@ -433,15 +433,13 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const __grid_constant
 }
 
 // The same for rows that start anywhere, and are wide enough for a warp: a warp takes
-// kPieces x 32 pieces of 16 bytes of a token, side by side.  All of a warp's
+// 32 x kPieces pieces of 16 bytes of a token, side by side.  All of a warp's
 // pieces are off a row's 16-byte boundaries by the same amount, so a shift is a choice
 // of registers in a branch that all lanes take together, with the next lane's first words
 // behind the own ones; what is before the first boundary and after the last goes out one
 // value a lane.  8 rows of 7001 columns a token take 313 us (8192 tokens, fp32) and 312
 // (16384, bf16), 97% of the copy rate; with 16 columns a thread, whose sectors go out in
 // two halves, 661 and 467.
-constexpr int kPieces = 4;
-
 // Words Q .. Q + 3 of a lane's four and the next lane's (HALF: from the middle of word
 // Q on); lane 31's next is lane 0 of `after`.
 template <int Q, bool HALF>
@@ -516,8 +514,9 @@ __device__ __forceinline__ void load_piece(const T* p, int n, int j, int lane, f
 }
 
 // WEIGHTS: a row gets w times the values (the rows' gradient in combine's).
-template <typename TX, typename TY, bool CODES, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, sizeof(TY) == 4 ? 4 : 3) k_moe_dispatch_wide(const __grid_constant__ RowArgs a) {
+template <typename TX, typename TY, bool CODES, bool WEIGHTS, int kPieces>
+__global__ void __launch_bounds__(kThreads, sizeof(TY) == 4 || kPieces == 2 ? 4 : 3)
+    k_moe_dispatch_wide(const __grid_constant__ RowArgs a) {
   constexpr int N = 16 / sizeof(TY);        // columns of a piece
   constexpr int kSpan = 32 * kPieces * N;   // columns of a warp
   const int lane = threadIdx.x & 31;
@@ -526,6 +525,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(TY) == 4 ? 4 : 3) k_moe_dispa
   const uint32_t token = quotient(item, a.per_row);
   const int col = static_cast<int>(item - token * a.per_row.d) * kSpan;
   const int n = min(a.cols - col, kSpan);   // columns of this warp
+  const int32_t* at = a.place + static_cast<int64_t>(token) * a.topk;
+  uint32_t next = static_cast<uint32_t>(at[0]);   // a row ahead, and its weight
+  float next_w = WEIGHTS ? weight_at(a.w, a.wdt, token * a.w_stride) : 1.f;
   const TX* x = static_cast<const TX*>(a.x.p) + token * a.x.stride + col;
   float v[kPieces][N];
   uint32_t w[kPieces + 1][4];
@@ -540,13 +542,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(TY) == 4 ? 4 : 3) k_moe_dispa
   for (int k = 0; k < 4; ++k) w[kPieces][k] = 0;   // behind the last: never written
   const int edge = edge_column(n, lane);
   const float end = edge >= 0 ? static_cast<float>(x[edge]) : 0.f;
-  const int32_t* at = a.place + static_cast<int64_t>(token) * a.topk;
   for (int k = 0; k < a.topk; ++k) {
-    const uint32_t row = static_cast<uint32_t>(at[k]);
+    const uint32_t row = next;
+    const float by = next_w;
+    if (k + 1 < a.topk) {
+      next = static_cast<uint32_t>(at[k + 1]);
+      if constexpr (WEIGHTS) next_w = weight_at(a.w, a.wdt, token * a.w_stride + k + 1);
+    }
     if (row >= a.rows) continue;   // the same for all lanes
-    float by = 1.f;
     if constexpr (WEIGHTS) {
-      by = weight_at(a.w, a.wdt, token * a.w_stride + k);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float g[N];
@@ -831,18 +835,28 @@ unsigned grid_of(const RowArgs& a) { return (a.items + kThreads - 1) / kThreads;
 
 // Columns of an item of the dispatch: a warp's where rows start anywhere and hold a warp's
 // pieces, else a thread's.  (65536 tokens, 8 rows each: 257 columns of bf16 80 us by
-// warps, 97 by threads; 801 155 and 236; 129 of fp32 64 and 128.)
+// warps, 97 by threads; 801 155 and 236; 129 of fp32 64 and 128.)  A lane takes two
+// pieces where that is the whole row, else four (257 columns of bf16 62 us with two, 77
+// with four; 257 of fp32, a column more than two hold, 120 and 101).
 int dispatch_cols(int xsdt, bool whole, int width) {
-  const int piece = 16 / esize(xsdt);
-  return whole || width < 32 * piece ? kCols : 32 * kPieces * piece;
+  const int warp = 32 * 16 / esize(xsdt);
+  return whole || width < warp ? kCols : width <= 2 * warp ? 2 * warp : 4 * warp;
+}
+
+template <typename TX, typename TY, bool CODES, bool WEIGHTS>
+void launch_dispatch_wide(const RowArgs& a, int cols, cudaStream_t st) {
+  const unsigned grid = (a.items + kThreads / 32 - 1) / (kThreads / 32);
+  if (cols == 2 * 32 * 16 / static_cast<int>(sizeof(TY)))
+    k_moe_dispatch_wide<TX, TY, CODES, WEIGHTS, 2><<<grid, kThreads, 0, st>>>(a);
+  else
+    k_moe_dispatch_wide<TX, TY, CODES, WEIGHTS, 4><<<grid, kThreads, 0, st>>>(a);
 }
 
 template <typename TX, typename TY>
 void launch_dispatch(const RowArgs& a, bool whole, bool codes, int cols, cudaStream_t st) {
   if (cols > kCols) {
-    const unsigned grid = (a.items + kThreads / 32 - 1) / (kThreads / 32);
-    if (codes) k_moe_dispatch_wide<TX, TY, true, false><<<grid, kThreads, 0, st>>>(a);
-    else k_moe_dispatch_wide<TX, TY, false, false><<<grid, kThreads, 0, st>>>(a);
+    if (codes) launch_dispatch_wide<TX, TY, true, false>(a, cols, st);
+    else launch_dispatch_wide<TX, TY, false, false>(a, cols, st);
     return;
   }
   const unsigned grid = grid_of(a);
@@ -902,8 +916,8 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaS
 
 // Rows that start anywhere and hold a warp's pieces are written by the dispatch, after
 // the weights' gradient has read ys (which may be dys): one more read of dout, and 8
-// rows of 7001 bf16 columns, 16384 tokens, take 722 us
-// for 889 (8192 tokens, fp32: 669 for 748).
+// rows of 7001 bf16 columns, 16384 tokens, take 682 us
+// for 889 (8192 tokens, fp32: 662 for 748).
 template <typename TX, typename TY>
 void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
   const int cols = dispatch_cols(sizeof(TY) == 2 ? MUON_BF16 : MUON_F32, whole, a.cols);
@@ -921,8 +935,7 @@ void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
   b.y = a.z;
   b.per_row = divider(static_cast<uint32_t>((a.cols + cols - 1) / cols));
   b.items = a.tokens * b.per_row.d;
-  k_moe_dispatch_wide<TX, TY, false, true>
-      <<<(b.items + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, st>>>(b);
+  launch_dispatch_wide<TX, TY, false, true>(b, cols, st);
   prof_end(kKindMoe, st, 0.0, tokens * row);
 }
 
