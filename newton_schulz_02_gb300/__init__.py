@@ -917,9 +917,20 @@ def muon_moe_sort(chosen: torch.Tensor, routing: Routing, ws: torch.Tensor,
 
 
 def _width(t: torch.Tensor, what: str) -> int:
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} needs two dimensions")
-    return t.shape[1]
+    return shape[1]
+
+
+def _operand(t: torch.Tensor, what: str, shape: tuple, dev: int) -> tuple:
+    """Pointer, dtype and row stride of a matrix of `shape` on GPU `dev`."""
+    dt = _DT.get(t.dtype)
+    if dt is None or t.get_device() != dev:
+        dt = _dtype(t, what, dev)
+    if t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), dt, shape[1]
+    return t.data_ptr(), dt, _rows2d(t, what, shape)
 
 
 def muon_moe_dispatch(x: torch.Tensor, routing: Routing, xs: torch.Tensor,
@@ -930,9 +941,9 @@ def muon_moe_dispatch(x: torch.Tensor, routing: Routing, xs: torch.Tensor,
     if x8 is not None and x8.device != dev:
         raise _elsewhere("x8", dev)
     _check(load_library().muon_moe_dispatch(
-        x.data_ptr(), _dtype(x, "x", dev), _rows2d(x, "x", (routing.tokens, width)), routing.ref, width,
-        xs.data_ptr(), _dtype(xs, "xs", dev), _rows2d(xs, "xs", (routing.rows, width)),
-        None if x8 is None else x8.ref, _stream_of(stream, dev)), "muon_moe_dispatch")
+        *_operand(x, "x", (routing.tokens, width), dev), routing.ref, width,
+        *_operand(xs, "xs", (routing.rows, width), dev), None if x8 is None else x8.ref,
+        _stream_of(stream, dev)), "muon_moe_dispatch")
 
 
 def muon_moe_dispatch_backward(dxs: torch.Tensor, routing: Routing, dx: torch.Tensor,
@@ -940,9 +951,9 @@ def muon_moe_dispatch_backward(dxs: torch.Tensor, routing: Routing, dx: torch.Te
     """dx[t] (+)= the sum of dxs at the token's rows."""
     dev, width = routing.device, _width(dx, "dx")
     _check(load_library().muon_moe_dispatch_backward(
-        dxs.data_ptr(), _dtype(dxs, "dxs", dev), _rows2d(dxs, "dxs", (routing.rows, width)), routing.ref,
-        width, dx.data_ptr(), _dtype(dx, "dx", dev), _rows2d(dx, "dx", (routing.tokens, width)),
-        int(bool(accumulate)), _stream_of(stream, dev)), "muon_moe_dispatch_backward")
+        *_operand(dxs, "dxs", (routing.rows, width), dev), routing.ref, width,
+        *_operand(dx, "dx", (routing.tokens, width), dev), 1 if accumulate else 0,
+        _stream_of(stream, dev)), "muon_moe_dispatch_backward")
 
 
 def muon_moe_combine(ys: torch.Tensor, weights: torch.Tensor, routing: Routing, out: torch.Tensor,
@@ -950,10 +961,9 @@ def muon_moe_combine(ys: torch.Tensor, weights: torch.Tensor, routing: Routing, 
     """out[t] (+)= sum_k weights[t, k] * ys[place[t, k]].  weights [tokens, topk] (bf16 or fp32)."""
     dev, width = routing.device, _width(out, "out")
     _check(load_library().muon_moe_combine(
-        ys.data_ptr(), _dtype(ys, "ys", dev), _rows2d(ys, "ys", (routing.rows, width)), routing.ref,
-        weights.data_ptr(), _dtype(weights, "weights", dev),
-        _rows2d(weights, "weights", (routing.tokens, routing.topk)), width, out.data_ptr(),
-        _dtype(out, "out", dev), _rows2d(out, "out", (routing.tokens, width)), int(bool(accumulate)),
+        *_operand(ys, "ys", (routing.rows, width), dev), routing.ref,
+        *_operand(weights, "weights", (routing.tokens, routing.topk), dev), width,
+        *_operand(out, "out", (routing.tokens, width), dev), 1 if accumulate else 0,
         _stream_of(stream, dev)), "muon_moe_combine")
 
 
@@ -965,15 +975,13 @@ def muon_moe_combine_backward(dout: torch.Tensor, ys: torch.Tensor, weights: tor
     dev, width = routing.device, _width(dout, "dout")
     if dys.dtype != ys.dtype or dweights.dtype != weights.dtype:
         raise ValueError("dys needs the dtype of ys, dweights that of weights")
-    _dtype(dys, "dys", dev)
-    _dtype(dweights, "dweights", dev)
     rows, choices = (routing.rows, width), (routing.tokens, routing.topk)
+    dys_ptr, _, dys_stride = _operand(dys, "dys", rows, dev)
+    dw_ptr, _, dw_stride = _operand(dweights, "dweights", choices, dev)
     _check(load_library().muon_moe_combine_backward(
-        dout.data_ptr(), _dtype(dout, "dout", dev), _rows2d(dout, "dout", (routing.tokens, width)),
-        ys.data_ptr(), _dtype(ys, "ys", dev), _rows2d(ys, "ys", rows), routing.ref, weights.data_ptr(),
-        _dtype(weights, "weights", dev), _rows2d(weights, "weights", choices), width, dys.data_ptr(),
-        _rows2d(dys, "dys", rows), dweights.data_ptr(), _rows2d(dweights, "dweights", choices),
-        _stream_of(stream, dev)), "muon_moe_combine_backward")
+        *_operand(dout, "dout", (routing.tokens, width), dev), *_operand(ys, "ys", rows, dev),
+        routing.ref, *_operand(weights, "weights", choices, dev), width, dys_ptr, dys_stride, dw_ptr,
+        dw_stride, _stream_of(stream, dev)), "muon_moe_combine_backward")
 
 
 # ---------------------------------------------------------------------------

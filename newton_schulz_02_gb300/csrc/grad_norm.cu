@@ -37,6 +37,7 @@ int64_t piece_values(int dtype) {
 }
 constexpr int kMaxGroups = 64;                                // groups of a launch
 constexpr int kFinThreads = 256;
+constexpr int kBlocksPerSm = 3;
 constexpr size_t kHeader = 256;
 
 struct NormGroup {
@@ -223,7 +224,7 @@ __device__ __forceinline__ Sum block_sum(Sum s, uint32_t flags, uint32_t* all) {
 
 // Three blocks an SM: without the bound the fp64 path takes 124 registers and two fit
 // (0.54 G bf16 169 us); four spill (353).
-__global__ void __launch_bounds__(kThreads, 3) k_grad_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_grad_norm(const __grid_constant__ NormArgs a) {
   griddep_launch_dependents();
   uint32_t flags = 0;
   const Sum mine = sum_pieces(a, blockIdx.x, gridDim.x, threadIdx.x, &flags);
@@ -284,18 +285,16 @@ __global__ void __launch_bounds__(kFinThreads) k_grad_norm_finish(FinishArgs a) 
   if (threadIdx.x == 0) write_norm(a, s, flags);
 }
 
-// Blocks of a launch: every resident block of the current device, at most one a piece.
+// Blocks of a launch: as many as run at once on the current device, at most one a piece.
 cudaError_t resident_blocks(int* out) {
-  int dev = 0, sms = 0, per_sm = 0;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_grad_norm, kThreads, 0);
-  if (e != cudaSuccess) return e;
-  *out = sms * (per_sm > 0 ? per_sm : 1);
-  return cudaSuccess;
+  *out = sms * kBlocksPerSm;
+  return e;
 }
 
-constexpr int kMaxBlocks = 2048;    // of a launch: SMs x 8 blocks of 256 threads, and more
+constexpr int kMaxBlocks = 2048;    // of a launch
 constexpr size_t kBlockBytes = 20;  // a pair, a double and the conditions
 
 bool empty(const muon_grads_t& g) { return g.count == 0 || g.rows == 0 || g.cols == 0; }
