@@ -890,7 +890,7 @@ void launch_combine(const RowArgs& a, bool whole, cudaStream_t st) {
 // Threads of a token: up to 256, as many as make the passes over its columns
 // equally long; narrow tokens share a block and, below a warp's columns, a warp.
 template <typename TX, typename TY, int DOTS>
-void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaStream_t st) {
+void launch_combine_backward_of(const RowArgs& a, bool whole, bool rows, cudaStream_t st) {
   const unsigned items = a.per_row.d;
   unsigned threads = 2;
   while (threads < items && threads < 32) threads *= 2;
@@ -900,7 +900,7 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaS
   }
   // as many tokens a block as fill an SM's threads best (4752 tokens, 6 rows of 1472
   // bf16, 96 threads a token: 49 us with one a block, 56 with two)
-  const unsigned most = whole || narrow ? kBackwardThreads<TY, true, DOTS> : kBackwardThreads<TY, false, DOTS>;
+  const unsigned most = rows ? kBackwardThreads<TY, true, DOTS> : kBackwardThreads<TY, false, DOTS>;
   unsigned tokens = kThreads / threads;
   for (unsigned n = tokens; n > 0; --n)
     if (most / (n * threads) * n > most / (tokens * threads) * tokens) tokens = n;
@@ -909,7 +909,8 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaS
   const bool sub = threads < 32;
   if (whole && sub) k_moe_combine_backward<TX, TY, true, true, true, DOTS><<<grid, block, 0, st>>>(a);
   else if (whole) k_moe_combine_backward<TX, TY, true, false, true, DOTS><<<grid, block, 0, st>>>(a);
-  else if (narrow) k_moe_combine_backward<TX, TY, false, true, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (rows && sub) k_moe_combine_backward<TX, TY, false, true, true, DOTS><<<grid, block, 0, st>>>(a);
+  else if (rows) k_moe_combine_backward<TX, TY, false, false, true, DOTS><<<grid, block, 0, st>>>(a);
   else if (sub) k_moe_combine_backward<TX, TY, false, true, false, DOTS><<<grid, block, 0, st>>>(a);
   else k_moe_combine_backward<TX, TY, false, false, false, DOTS><<<grid, block, 0, st>>>(a);
 }
@@ -917,17 +918,19 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool narrow, cudaS
 // Rows that start anywhere and hold a warp's pieces are written by the dispatch, after
 // the weights' gradient has read ys (which may be dys): one more read of dout, and 8
 // rows of 7001 bf16 columns, 16384 tokens, take 682 us
-// for 889 (8192 tokens, fp32: 662 for 748).
+// for 889 (8192 tokens, fp32: 662 for 748).  Up to kOneKernelBytes of rows the second launch
+// costs more than that: 64 tokens, 6 rows of 1111 fp32 12.4 us in two, 7.5 in one, 1023
+// tokens, 6 of 1111 bf16 (14 MB) 16.5 and 14.5; 27 MB 20.7 and 20.9, 43 MB 26.8 and 33.7.
+constexpr double kOneKernelBytes = 16e6;
+
 template <typename TX, typename TY>
 void launch_combine_backward(const RowArgs& a, bool whole, cudaStream_t st) {
   const int cols = dispatch_cols(sizeof(TY) == 2 ? MUON_BF16 : MUON_F32, whole, a.cols);
-  const bool narrow = !whole && cols == kCols;
-  static_assert(32 * 8 <= 16 * kCols, "narrow rows take a part of a warp");
-  const bool rows = whole || narrow;   // by the same kernel
   const double tokens = static_cast<double>(a.tokens) * a.cols, row = sizeof(TY) * static_cast<double>(a.topk);
+  const bool rows = whole || cols == kCols || tokens * row <= kOneKernelBytes;   // by the same kernel
   prof_begin(kKindMoe, st);
-  if (a.topk <= 2) launch_combine_backward_of<TX, TY, 2>(a, whole, narrow, st);
-  else launch_combine_backward_of<TX, TY, 8>(a, whole, narrow, st);
+  if (a.topk <= 2) launch_combine_backward_of<TX, TY, 2>(a, whole, rows, st);
+  else launch_combine_backward_of<TX, TY, 8>(a, whole, rows, st);
   prof_end(kKindMoe, st, 0.0, tokens * (sizeof(TX) + (rows ? 2 : 1) * row));
   if (rows) return;
   prof_begin(kKindMoe, st);

@@ -256,6 +256,34 @@ def test_combine_gradient(outer, inner, how, T, E, K, D):
                 assert torch.equal(torch.nan_to_num(ys), torch.nan_to_num(y0))
 
 
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("T,E,K,D", [(4200, 60, 8, 257), (2100, 16, 4, 1111), (1700, 16, 2, 2501),
+                                     (330, 9, 3, 8193)])
+def test_combine_gradient_of_many_odd_rows(outer, inner, T, E, K, D):
+    """Over 16 MB of rows off 16-byte boundaries, which two kernels take one after the other;
+    over the rows themselves, too."""
+    rng = np.random.default_rng(D)
+    r, place = routed(D, T, E, K, drop=0.05)
+    assert r.rows * D * 2 > 16e6
+    dout = put(rng.normal(size=(T, D)), DT[outer])
+    y0 = put(rng.normal(size=(r.rows, D)), DT[inner], "shifted")
+    y0[r.offsets[-1]:] = float("nan")
+    w = put(rng.random((T, K)), torch.float32)
+    want, dw_want, mass = R.combine_grad(f64(dout), f64(y0), f64(w), place)
+    held = ~np.isnan(want[:, 0])
+    for inplace in (False, True):
+        bufy, ys = framed(r.rows, D, DT[inner], "shifted")
+        ys.copy_(y0)
+        buf, dys = (bufy, ys) if inplace else framed(r.rows, D, DT[inner], "shifted")
+        dw = torch.full_like(w, 9.0)
+        m.muon_moe_combine_backward(dout, ys, w, r, dys, dw)
+        got = f64(dys)
+        within(got[held], want[held], 2 * HALF[inner] * np.abs(want[held]))
+        assert np.isnan(got[~held]).all() if inplace else (got[~held] == 7.0).all()
+        within(f64(dw), dw_want, (D + 3) * U * mass)
+        assert untouched(buf, dys)
+
+
 def test_not_finite_values_reach_their_own_columns_only():
     T, E, K, D = 12, 4, 3, 130
     r, place = routed(3, T, E, K, drop=0.0)
