@@ -98,10 +98,12 @@ __device__ __forceinline__ bool misaligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) != 0;
 }
 
+// SCALED: there is a factor on the gradients.
+template <bool SCALED>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamWLaunch p) {
   const int64_t total = p.item_begin[p.n_groups];
-  const float gscale = p.grad_scale == nullptr ? 1.f : *p.grad_scale;
-  if (!isfinite(gscale)) {   // nothing is updated
+  const float gscale = SCALED ? *p.grad_scale : 1.f;
+  if (SCALED && !isfinite(gscale)) {   // nothing is updated
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags != nullptr) atomicOr(p.flags, MUON_FLAG_NONFINITE);
     return;
   }
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
       if (full[r]) {
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-          Elem e{W[r][k], Gv[r][k] * gscale, Mv[r][k], Vv[r][k]};
+          Elem e{W[r][k], SCALED ? Gv[r][k] * gscale : Gv[r][k], Mv[r][k], Vv[r][k]};
           adamw_elem(p, decay, e);
           W[r][k] = e.w; Mv[r][k] = e.m; Vv[r][k] = e.v;
         }
@@ -168,11 +170,12 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Adam
 int64_t chunks(int64_t numel) { return numel <= 0 ? 0 : (numel + kChunk - 1) / kChunk; }
 
 // Resident blocks of k_adamw on the current device (SMs x blocks per SM).
+template <bool SCALED>
 cudaError_t resident_blocks(int* out) {
   int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_adamw, kThreads, 0);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_adamw<SCALED>, kThreads, 0);
   if (e != cudaSuccess) return e;
   *out = sms * (per_sm > 0 ? per_sm : 1);
   return cudaSuccess;
@@ -183,7 +186,8 @@ cudaError_t resident_blocks(int* out) {
 cudaError_t launch_adamw(AdamWGroupArgs* groups, int n_groups, const AdamWScalars& s,
                          uint32_t* flags, cudaStream_t st) {
   int resident = 0;
-  cudaError_t e0 = resident_blocks(&resident);
+  const bool scaled = s.grad_scale != nullptr;
+  cudaError_t e0 = scaled ? resident_blocks<true>(&resident) : resident_blocks<false>(&resident);
   if (e0 != cudaSuccess) return e0;
   for (int i = 0; i < n_groups; ++i) groups[i].chunks_per_tensor = chunks(groups[i].numel);
   for (int base = 0; base < n_groups; base += kAdamWMaxGroups) {
@@ -207,7 +211,8 @@ cudaError_t launch_adamw(AdamWGroupArgs* groups, int n_groups, const AdamWScalar
     // persistent grid: every resident block (a multiple of the SM count)
     const int grid = static_cast<int>(items < resident ? items : resident);
     prof_begin(kKindAdamW, st);
-    k_adamw<<<grid, kThreads, 0, st>>>(p);
+    if (scaled) k_adamw<true><<<grid, kThreads, 0, st>>>(p);
+    else k_adamw<false><<<grid, kThreads, 0, st>>>(p);
     prof_end(kKindAdamW, st, 0.0, bytes);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
