@@ -688,8 +688,11 @@ __global__ void __maxnreg__((65536 / kBackwardThreads<TY, ROWS, kDots> / 8 * 8))
           if (j0 == 0) values_of(d_raw, n, d);
         }
         if constexpr (ROWS) {
-          if constexpr (!WHOLE) __syncwarp();   // dys may be ys: the warp's reads come first
-          // dys needs nothing of ys: written while that is on its way
+          // dys needs nothing of ys: written while that is on its way.  It may be ys, so the
+          // reads come first: the warp's, or (WHOLE) the thread's own, which the compiler
+          // must not move a plain store in front of (fetch does not tell it what it reads)
+          if constexpr (!WHOLE) __syncwarp();
+          else asm volatile("" ::: "memory");
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
             const bool in = row[j] < a.rows;

@@ -284,6 +284,30 @@ def test_combine_gradient_of_many_odd_rows(outer, inner, T, E, K, D):
         assert untouched(buf, dys)
 
 
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("T,E,K", [(50, 8, 2), (21, 16, 6), (9, 30, 17)])
+def test_combine_gradient_over_its_own_aligned_rows(outer, inner, T, E, K):
+    """Rows on 32-byte boundaries whose last columns fill no 16: dys in the place of ys is
+    what it is beside it, bit for bit, and so is the weights' gradient, which needs the
+    values that were there."""
+    for D in list(range(1, 34)) + [130, 1034, 4111]:
+        rng = np.random.default_rng(D + K)
+        r, place = routed(D, T, E, K, drop=0.1)
+        dout = put(rng.normal(size=(T, D)), DT[outer], "padded")
+        w = torch.rand(T, K, device=DEV)
+        y0 = rng.normal(size=(r.rows, D))
+        bufy, ys = framed(r.rows, D, DT[inner], "padded")
+        ys.copy_(torch.as_tensor(y0))
+        beside, dw, dw2 = put(y0, DT[inner], "padded"), torch.full_like(w, 9.0), torch.full_like(w, 8.0)
+        _, dys = framed(r.rows, D, DT[inner], "padded")
+        m.muon_moe_combine_backward(dout, beside, w, r, dys, dw)
+        m.muon_moe_combine_backward(dout, ys, w, r, ys, dw2)
+        held = torch.as_tensor(place[place >= 0], device=DEV)
+        assert torch.equal(dw, dw2) and torch.equal(ys[held], dys[held]) and untouched(bufy, ys)
+        _, dw_want, mass = R.combine_grad(f64(dout), f64(beside), f64(w), place)
+        within(f64(dw), dw_want, (D + 2) * U * mass)
+
+
 def test_not_finite_values_reach_their_own_columns_only():
     T, E, K, D = 12, 4, 3, 130
     r, place = routed(3, T, E, K, drop=0.0)
