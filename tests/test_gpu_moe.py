@@ -129,6 +129,52 @@ def test_sort_bad_numbers_and_too_few_rows_are_flagged(T):
     assert flags == 0
 
 
+def stable_sort(chosen, E, mask, rows):
+    """R.sort of many copies at once: (offsets, order, place, bad)."""
+    T, K = chosen.shape
+    on = np.ones((T, K), dtype=bool) if mask is None else np.repeat(mask[:, None], K, axis=1)
+    known = (chosen >= 0) & (chosen < E)
+    key = np.where(on & known, chosen, E).ravel()
+    n = int((key < E).sum())
+    order = np.argsort(key, kind="stable")[:n]
+    ends = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=E + 1)[:E])])
+    bad = bool((on & ~known & (chosen != -1)).any()) or n > rows
+    order = order[:rows]
+    place = np.full(T * K, -1, dtype=np.int64)
+    place[order] = np.arange(len(order))
+    return np.minimum(ends, rows), order, place.reshape(T, K), bad
+
+
+# Copies at the borders between the forms: one block of one or two copies a thread (2048),
+# blocks of one, two and three to eight copies a thread (up to 155648, 311296, 1245184),
+# and several rounds of those.
+@pytest.mark.parametrize("T,E,K", [(1025, 9, 1), (2047, 300, 1), (1024, 1024, 2), (683, 60, 3), (19456, 256, 8),
+                                   (51883, 31, 3), (38912, 256, 8), (44471, 1000, 7), (65536, 256, 8),
+                                   (131071, 256, 8), (131071, 1024, 8), (155648, 64, 8), (249037, 257, 5),
+                                   (400000, 128, 8)])
+def test_sort_in_each_of_its_forms(T, E, K):
+    rng = np.random.default_rng(T + E)
+    chosen = choices(T, T, E, K, drop=0.05)
+    mask = rng.random(T) > 0.1
+    mask[-1] = mask[T // 2] = True
+    ways = ((torch.int64, None, None, T * K, None), (torch.int32, K + 3, mask, T * K, None),
+            (torch.int64, K + 1, mask, T * K * 2 // 3, None), (torch.int32, None, None, T * K + 3, E),
+            (torch.int64, None, mask, T * K // 2 + 1, 2 ** 32 + 3), (torch.int32, K + 2, None, T * K - 1, -2))
+    for idx, stride, mk, rows, bad in ways:
+        c = chosen.copy()
+        if bad is not None:
+            c[T // 2 if bad > 0 else -1, K - 1] = bad
+        r, flags = run_sort(c, E, mk, rows, idx, stride)
+        offsets, order, place, flagged = stable_sort(c, E, mk, rows)
+        assert np.array_equal(r.offsets.cpu().numpy(), offsets)
+        got = r.order.cpu().numpy()
+        assert np.array_equal(got[:len(order)], order) and (got[len(order):] == -77).all()
+        assert np.array_equal(r.place.cpu().numpy(), place)
+        assert flags == (m.MUON_FLAG_INDEX if flagged else 0)
+        if T * K < 2100:
+            check_sort(r, flags, c, E, mk, rows)
+
+
 # ---- activations ------------------------------------------------------------
 def routed(seed, T, E, K, drop=0.15, rows=None):
     chosen = choices(seed, T, E, K, drop)
