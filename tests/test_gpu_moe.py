@@ -354,6 +354,54 @@ def test_combine_gradient_over_its_own_aligned_rows(outer, inner, T, E, K):
         within(f64(dw), dw_want, (D + 2) * U * mass)
 
 
+@pytest.mark.parametrize("wdt", ["f32", "bf16"])
+@pytest.mark.parametrize("outer,inner,T,E,K,D", [
+    ("f32", "f32", 4100, 60, 8, 129), ("bf16", "f32", 2700, 60, 8, 200), ("f32", "f32", 10300, 8, 2, 200),
+    ("f32", "f32", 2100, 60, 8, 255), ("bf16", "bf16", 4000, 60, 8, 256), ("f32", "bf16", 16300, 8, 2, 256),
+    ("f32", "bf16", 5500, 16, 6, 256), ("bf16", "bf16", 850, 16, 9, 1111), ("f32", "f32", 500, 32, 17, 515),
+    ("f32", "bf16", 620, 32, 17, 801)])
+def test_combine_gradient_by_two_kernels(outer, inner, wdt, T, E, K, D):
+    """Over 16 MB of rows off 16-byte boundaries: widths of part of a warp in the kernel of the
+    weights' gradient, and more choices than that takes at a time.  dys is one product in
+    fp32 rounded to the rows' type, to the bit."""
+    r, place = routed(D, T, E, K, drop=0.02)
+    assert T * K * D * DT[inner].itemsize > 16e6
+    g = torch.Generator(device=DEV).manual_seed(D)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    dout = rand(T, D).to(DT[outer])
+    y0 = rand(r.rows, D).to(DT[inner])
+    w = rand(T, K).to(DT[wdt])
+    held = torch.as_tensor(place, device=DEV) >= 0
+    at = torch.as_tensor(place, device=DEV)[held]
+    rows = (w.float()[:, :, None] * dout.float()[:, None, :])[held].to(DT[inner])
+    _, dw_want, mass = R.combine_grad(f64(dout), f64(y0), f64(w), place)
+    for inplace in (False, True):
+        bufy, ys = framed(r.rows, D, DT[inner], "shifted")
+        ys.copy_(y0)
+        buf, dys = (bufy, ys) if inplace else framed(r.rows, D, DT[inner], "shifted")
+        dw = torch.full_like(w, 9.0)
+        m.muon_moe_combine_backward(dout, ys, w, r, dys, dw)
+        assert torch.equal(dys[at], rows) and untouched(buf, dys)
+        within(f64(dw), dw_want, (D + 3) * U * mass + HALF[wdt] * np.abs(dw_want) * (1 + 2.0 ** -7))
+
+
+@pytest.mark.parametrize("outer,inner", TYPES)
+@pytest.mark.parametrize("wdt", ["f32", "bf16"])
+@pytest.mark.parametrize("how", ["dense", "padded", "shifted"])
+def test_rows_gradient_is_one_product_rounded_once(outer, inner, wdt, how):
+    for T, E, K, D in ((70, 8, 2, 512), (33, 60, 6, 1111), (19, 16, 9, 77), (9, 4, 17, 4100)):
+        g = torch.Generator(device=DEV).manual_seed(D)
+        r, place = routed(D, T, E, K)
+        dout = put(torch.randn(T, D, generator=g, device=DEV), DT[outer], how)
+        w = torch.randn(T, K, generator=g, device=DEV).to(DT[wdt])
+        ys = put(torch.randn(r.rows, D, generator=g, device=DEV), DT[inner], how)
+        _, dys = framed(r.rows, D, DT[inner], how)
+        m.muon_moe_combine_backward(dout, ys, w, r, dys, torch.empty_like(w))
+        held = torch.as_tensor(place, device=DEV) >= 0
+        rows = (w.float()[:, :, None] * dout.float()[:, None, :])[held].to(DT[inner])
+        assert torch.equal(dys[torch.as_tensor(place, device=DEV)[held]], rows)
+
+
 def test_not_finite_values_reach_their_own_columns_only():
     T, E, K, D = 12, 4, 3, 130
     r, place = routed(3, T, E, K, drop=0.0)
