@@ -586,8 +586,8 @@ muon_status_t muon_moe_sort_workspace_size(int64_t tokens, int experts, int topk
 /* chosen, chosen_bytes, chosen_stride, token_mask: as in muon_balance_t (-1 = not
  * sent anywhere; any other value outside [0, experts) is taken as that and sets
  * MUON_FLAG_INDEX; the choices of masked tokens do not matter).  Two equal choices
- * of a token are two copies.  chosen and place may not overlap.  Status word in the
- * workspace. */
+ * of a token are two copies.  chosen and token_mask may not overlap offsets, order or
+ * place (MUON_ERR_INVALID_ARG).  Status word in the workspace. */
 muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen_stride,
                             const uint8_t* token_mask, const muon_routing_t* routing,
                             void* workspace, size_t workspace_bytes, muon_stream_t stream);

@@ -761,6 +761,29 @@ muon_status_t check_routing(const muon_routing_t* r) {
   return at_multiple(r->place, 4) ? MUON_OK : MUON_ERR_MISALIGNED;
 }
 
+// Whether one of `runs` runs of `bytes` bytes, each `step` (>= bytes) behind the one before,
+// holds a byte of [q, q + size).
+bool runs_overlap(const void* p, int64_t runs, uint64_t bytes, uint64_t step, const void* q, uint64_t size) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (runs <= 0 || size == 0 || a >= b + size) return false;
+  uint64_t last = (b + size - 1 - a) / step;   // of the runs that begin in front of the end
+  if (last >= static_cast<uint64_t>(runs)) last = static_cast<uint64_t>(runs) - 1;
+  return a + last * step + bytes > b;
+}
+
+// Whether the choices or the mask share memory with what the sort writes: its second kernel
+// reads the choices again while other blocks write, and so does the first the mask.
+bool sort_overlaps(const void* chosen, int bytes, int64_t stride, const uint8_t* mask, const muon_routing_t& r) {
+  const uint64_t apart = static_cast<uint64_t>(stride < (int64_t{1} << 48) ? stride : int64_t{1} << 48) * bytes;
+  const uint64_t row = static_cast<uint64_t>(r.topk) * bytes;
+  const auto with = [&](const void* q, int64_t n) {
+    const uint64_t size = static_cast<uint64_t>(n) * 4;
+    return runs_overlap(chosen, r.tokens, row, apart, q, size) ||
+           (mask != nullptr && runs_overlap(mask, r.tokens, 1, 1, q, size));
+  };
+  return with(r.offsets, r.experts + 1) || with(r.order, r.rows) || with(r.place, r.tokens * r.topk);
+}
+
 muon_status_t check_rows(const void* p, int64_t rows, int dtype, int64_t stride, int width) {
   if (dtype != MUON_BF16 && dtype != MUON_F32) return MUON_ERR_INVALID_ARG;
   if (stride < width || (rows > 0 && p == nullptr)) return MUON_ERR_INVALID_ARG;
@@ -1008,6 +1031,7 @@ muon_status_t muon_moe_sort(const void* chosen, int chosen_bytes, int64_t chosen
   if (!at_multiple(chosen, chosen_bytes) || !at_multiple(r->offsets, 4) || !at_multiple(r->order, 4) ||
       !at_multiple(workspace, 256))
     return MUON_ERR_MISALIGNED;
+  if (sort_overlaps(chosen, chosen_bytes, chosen_stride, token_mask, *r)) return MUON_ERR_INVALID_ARG;
   size_t need = 0;
   s = muon_moe_sort_workspace_size(r->tokens, r->experts, r->topk, &need);
   if (s != MUON_OK) return s;

@@ -71,6 +71,28 @@ def test_sort_refusals(lib):
         m.muon_moe_sort_workspace_size(1, 2000, 1)
 
 
+def test_sort_refuses_choices_and_masks_that_share_memory_with_its_outputs(lib):
+    """offsets, order and place are [0x10000, 0x10014), [0x20000, 0x20020), [0x30000,
+    0x30050).  A workspace that is too small ends the calls that are in order."""
+    def sort(chosen, size=4, stride=2, mask=None, **kw):
+        return lib.muon_moe_sort(chosen, size, stride, mask, R(routing(**kw)), 0x100000, 0, None)
+
+    for chosen in (0x10000, 0x20000, 0x30000, 0x2001C, 0x10010, 0x3004C, 0x20000 - 0x4C, 0x30000 - 0x4C):
+        assert sort(chosen) == INVALID, hex(chosen)
+    for chosen in (0x10014, 0x20020, 0x30050, 0x10000 - 0x50, 0x20000 - 0x50, 0x30000 - 0x50):
+        assert sort(chosen) == SMALL, hex(chosen)
+    assert sort(0x30000 - 0x98, size=8) == INVALID and sort(0x30000 - 0xA0, size=8) == SMALL
+    # rows apart: the outputs may lie between two of them
+    assert sort(0x1FFF8, stride=16) == SMALL and sort(0x1FFF8, stride=8) == INVALID
+    assert sort(0x20000 - 9 * 64 - 4, stride=16) == INVALID and sort(0x20000 - 9 * 64 - 8, stride=16) == SMALL
+    assert sort(0x30000 - 8, stride=1 << 62) == SMALL and sort(0x30000 - 4, stride=1 << 62) == INVALID
+    for mask in (0x10013, 0x2001F, 0x3004F, 0x20000 - 9, 0x30000 - 9):
+        assert sort(0x40000, mask=mask) == INVALID, hex(mask)
+    for mask in (0x10014, 0x20020, 0x30050, 0x20000 - 10, 0x30000 - 10):
+        assert sort(0x40000, mask=mask) == SMALL, hex(mask)
+    assert sort(0x30000, tokens=0) == SMALL and sort(0x20000, rows=0) == SMALL
+
+
 @pytest.mark.parametrize("tokens,experts,topk", [(1, 1, 1), (4096, 8, 2), (4097, 8, 2), (131072, 256, 8),
                                                  (1 << 21, 1024, 8), (2 ** 31 - 1, 64, 1)])
 def test_sort_workspace_is_one_row_of_counts_a_block(lib, tokens, experts, topk):
