@@ -61,7 +61,7 @@ typedef enum {
 } muon_status_t;
 
 /* Bits of the device status word (muon_get_status). */
-#define MUON_FLAG_NONFINITE 0x1u   /* some matrix had a non-finite Frobenius norm; the norm of all
+#define MUON_FLAG_NONFINITE 0x1u   /* some matrix had a non-finite Frobenius norm; one of all
                                       gradients, or a factor on them, was not finite */
 #define MUON_FLAG_TIMEOUT 0x2u     /* a bounded device wait ran out; results are invalid */
 #define MUON_FLAG_MISALIGNED 0x4u  /* a pointer in a device pointer array was not 16 B aligned;
@@ -351,7 +351,7 @@ muon_status_t muon_adamw_step_scaled(const muon_adamw_group_t* groups, int n_gro
 
 /* ---- Norm of all gradients, and clipping ------------------------------------
  *   norm  = sqrt(sum over all tensors of g^2)
- *   scale = min(1, max_norm / (norm + 1e-6)),  NaN where norm is not finite
+ *   scale = min(1, max_norm / (norm + 1e-6)),  NaN where a gradient is infinite or NaN
  * The gradients are only read: the optimizer steps above take `scale` and
  * multiply where they read G, so that clipping costs no pass of its own. */
 
@@ -374,9 +374,13 @@ muon_status_t muon_grad_norm_workspace_size(const muon_grads_t* groups, int n_gr
 
 /* groups: host array [n_groups] (a tensor that is in two counts twice; no tensors:
  * norm 0).  max_norm: >= 0 (infinity: only the norm; scale is 1).  norm, scale: device, 1 fp32 each.
- * The sum holds 48 bits or more, whatever the gradients' size: squares do not
- * overflow or vanish.  Its order is fixed by the sizes and the GPU.  Status word
- * in the workspace (muon_get_status): MUON_FLAG_NONFINITE, MUON_FLAG_MISALIGNED. */
+ * Squares are added 32 (64 of bf16) at a time in fp32, and those sums in 48 bits or
+ * more: norm is within 7 * 2^-24, and scale within 9 * 2^-24, of its exact value,
+ * whatever the gradients' size (squares do not overflow or vanish).  A norm
+ * beyond fp32's range reads as infinity; its scale is finite and no flag is set, so it
+ * is scale that tells a batch to be skipped.  The order of the sum is fixed by the sizes
+ * and the GPU.  Status word in the workspace (muon_get_status): MUON_FLAG_NONFINITE,
+ * MUON_FLAG_MISALIGNED. */
 muon_status_t muon_grad_norm(const muon_grads_t* groups, int n_groups, float max_norm, float* norm,
                              float* scale, void* workspace, size_t workspace_bytes,
                              muon_stream_t stream);

@@ -1034,7 +1034,9 @@ def muon_grad_norm_workspace_size(grads: Grads) -> int:
 def muon_grad_norm(grads: Grads, norm: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
                    max_norm: float = float("inf"), stream=None) -> None:
     """norm (fp32, one element) = the norm of all gradients together; scale (the same) =
-    min(1, max_norm / (norm + 1e-6)), what the steps take as grad_scale."""
+    min(1, max_norm / (norm + 1e-6)), what the steps take as grad_scale: NaN where a
+    gradient is infinite or NaN.  (A norm beyond fp32's range reads as infinity and has
+    its finite scale.)"""
     dev = grads.device
     _check(load_library().muon_grad_norm(
         grads.c, len(grads.c), float(max_norm), _vector(norm, "norm", torch.float32, 1, dev),

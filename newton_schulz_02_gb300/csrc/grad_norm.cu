@@ -8,10 +8,12 @@
 // read rate is the bound.  Tensors of any number and size share a launch: a
 // persistent grid strides over fixed pieces of every tensor.
 //
-// A thread adds the squares of 32 values (64 of bf16) in fp32 and those sums in a pair of
-// fp32 (the rounding error of each addition is kept in the second), which
-// costs 7 additions for 32 values and holds 48 bits; an fp64 addition for each
-// value would take five times as long as the reads.  Squares outside fp32's
+// A thread adds the squares of 32 values (64 of bf16) in fp32, which leaves at most 11
+// roundings in a chain (11 x 2^-24 of the sum, half of that of the norm; 1.1e-8 of the sum
+// was seen for Gaussian bf16, whose squares end in few bits and round down more often than
+// up).  Those sums are added in a pair of fp32 (the rounding error of each addition is kept in
+// the second), which costs 7 additions for 32 values and holds 48 bits; an fp64 addition
+// for each value would take five times as long as the reads.  Squares outside fp32's
 // comfortable range (that sum below 2^-96 or above 2^80, infinite or NaN)
 // are added up in fp64 instead, value by value.
 #include <cuda_bf16.h>

@@ -102,6 +102,39 @@ def test_squares_neither_overflow_nor_vanish(size):
     check([mixed], [mixed]) if size < 1e30 else None
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e-3, 0.0217])
+def test_norm_of_many_values_keeps_its_bound(dtype, size):
+    """Half a million partial sums, whose roundings might all go one way."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    t = torch.empty(1 << 25, dtype=dtype, device=DEV).normal_(0.0, size, generator=g)
+    n = math.sqrt(sum(torch.dot(p, p).item() for p in (q.double() for q in t.split(1 << 22))))
+    norm, scale, flags = run([t], max_norm=1.0)
+    assert flags == 0 and abs(norm.item() - n) <= 7 * U * n
+    assert abs(scale.item() - min(1.0, 1.0 / (n + 1e-6))) <= 9 * U * min(1.0, 1.0 / (n + 1e-6))
+
+
+def test_a_norm_beyond_the_range_of_fp32_still_clips():
+    """The norm reads as infinity; the factor is finite, and the steps take it."""
+    G = torch.full((4, 1024), 3e38, device=DEV)
+    G[1, ::2] = -2.5e38
+    W, mom, var = torch.rand_like(G), torch.rand_like(G), torch.rand_like(G)
+    norm, scale, flags = run([G], max_norm=1.0)
+    n, s = R.grad_norm([f64(G)], 1.0)
+    assert n > 3.5e38 and norm.item() == math.inf and flags == 0
+    assert abs(scale.item() - s) <= 9 * U * s + 2.0 ** -150
+    W2, m2, v2 = W.clone(), mom.clone(), var.clone()
+    m.muon_adamw_step(m.adamw_groups([W], [G], [mom], [var]), m.adamw_hparams(), grad_scale=scale)
+    m.muon_adamw_step(m.adamw_groups([W2], [G * scale], [m2], [v2]), m.adamw_hparams())
+    assert torch.equal(W, W2) and torch.equal(mom, m2) and torch.equal(var, v2)
+    M, start = torch.zeros_like(G), W.clone()
+    group = m.Group([W], [G], [M])
+    ws = m.workspace(m.muon_step_workspace_size([group]))
+    m.muon_step_batched([group], m.hparams(), ws, grad_scale=scale)
+    assert m.muon_get_status(ws) == (m.MUON_OK, 0)
+    assert torch.equal(M, G * scale) and not torch.equal(W, start)
+
+
 def test_zero_gradients_and_the_border_of_clipping():
     z = torch.zeros(5000, device=DEV)
     norm, scale, flags = run([z], max_norm=0.0)
