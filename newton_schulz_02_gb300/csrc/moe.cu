@@ -10,8 +10,9 @@
 //
 // Every pass over activations goes by token, not by row: a token's values are
 // read (or written) once and its K rows are whole rows wherever they are, so
-// the traffic is what the definition has, and a token's sum is a loop over k
-// in one thread, in that order, with no atomics.  Going by row would read a
+// the traffic is what the definition has (but for dout in combine's gradient, which is
+// read once for every 8 choices, and once more where two kernels take it), and a
+// token's sum is a loop over k in one thread, in that order, with no atomics.  Going by row would read a
 // token's values once for each expert, from HBM where they do not fit in L2.
 // A copy without a row has place -1; a place outside [0, rows) is taken as that.
 #include <cuda_bf16.h>
@@ -33,8 +34,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxPer = 8;       // copies a thread holds at a time
-// Copies a thread, up to which one block does it: 2048 copies take it 4.3 us, one launch
-// less; 4096 took it 7.0, the two kernels 5.7.
+// Copies a thread, up to which one block does it: 2048 copies take it 4.6 us in a graph, one
+// launch less; 4096 took it 7.0, the two kernels 5.1.
 constexpr int64_t kAlonePer = 2;
 constexpr int kSortBlocks = 152;
 constexpr size_t kHeader = 256;
@@ -672,7 +673,7 @@ __global__ void __maxnreg__((65536 / kBackwardThreads<TY, ROWS, kDots> / 8 * 8))
         uint32_t row[kAhead];
         float w[kAhead];
         if constexpr (ROWS) {   // all that is read is asked for before any of it is looked at:
-                                // 16384 tokens, 8 rows of 7168 bf16 639 -> 609 us
+                                // 16384 tokens, 8 rows of 7168 bf16 639 -> 602 us
 #pragma unroll
           for (int j = 0; j < kAhead; ++j)
             w[j] = k0 + j0 + j < a.topk ? weight_at(a.w, a.wdt, token * a.w_stride + k0 + j0 + j) : 0.f;
@@ -924,8 +925,8 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool rows, cudaStr
     const unsigned passes = (items + kThreads - 1) / kThreads;
     threads = ((items + passes - 1) / passes + 31) / 32 * 32;
   }
-  // as many tokens a block as fill an SM's threads best (4752 tokens, 6 rows of 1472
-  // bf16, 96 threads a token: 49 us with one a block, 56 with two)
+  // as many tokens a block as fill an SM's threads best (6 rows of 1472 bf16, 96 threads a
+  // token, in a graph: 4752 tokens 40 us with one a block, 45 with two; 19008 142 and 166)
   const unsigned most = rows ? kBackwardThreads<TY, true, DOTS> : kBackwardThreads<TY, false, DOTS>;
   unsigned tokens = kThreads / threads;
   for (unsigned n = tokens; n > 0; --n)
@@ -947,6 +948,14 @@ void launch_combine_backward_of(const RowArgs& a, bool whole, bool rows, cudaStr
 // for 889 (8192 tokens, fp32: 662 for 748).  Up to kOneKernelBytes of rows the second launch
 // costs more than that: 64 tokens, 6 rows of 1111 fp32 12.4 us in two, 7.5 in one, 1023
 // tokens, 6 of 1111 bf16 (14 MB) 16.5 and 14.5; 27 MB 20.7 and 20.9, 43 MB 26.8 and 33.7.
+// In a graph, in two and in one, at 8, 16, 32 and 64 MB of rows:
+//   2 rows of 1111 bf16   9.1  8.8   18.0 16.4   30.6 30.2   59.1 56.2
+//   2 of 4099 bf16        8.9  8.4   16.6 16.0   25.8 27.3   47.8 48.6
+//   2 of 1111 fp32        7.8  8.2   15.3 17.4   23.4 27.4   43.5 51.4
+//   8 of 257 bf16        10.6  9.5   18.6 18.0   30.0 32.9   51.7 59.4
+//   8 of 1111 fp32       10.7  8.2   14.5  9.9   20.4 21.9   36.3 34.7
+// so the border is about the same however few the choices are; fp32 with one or two would
+// take two kernels from 8 MB on.
 constexpr double kOneKernelBytes = 16e6;
 
 template <typename TX, typename TY>
