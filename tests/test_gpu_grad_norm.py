@@ -135,6 +135,48 @@ def test_a_norm_beyond_the_range_of_fp32_still_clips():
     assert torch.equal(M, G * scale) and not torch.equal(W, start)
 
 
+def test_norm_of_tensors_of_more_than_32_bits_of_values():
+    """Values and rows behind 2^32, dense and as columns of a wider matrix."""
+    rows, width = (1 << 19) + 3, 8208
+    big = torch.zeros(rows, width, dtype=torch.bfloat16, device=DEV)
+    assert big.numel() > 1 << 32
+    big[0, 0], big[rows - 1, width - 1], big[rows - 1, 8], big[rows // 2, 8199] = 3.0, 5.0, 2.0, 4.0
+    big[rows - 1, 8200], big[7, 7] = 16.0, 1.0
+    norm, _, flags = run([big])
+    assert flags == 0 and abs(norm.item() - math.sqrt(9 + 25 + 4 + 16 + 256 + 1)) <= 7 * U * 18
+    g = m.Grads([big])
+    g.c[0] = m.muon_grads_t(1, rows, 8192, width, m.MUON_BF16, g.c[0].ptrs)
+    norm, scale = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    ws = m.workspace(m.muon_grad_norm_workspace_size(g))
+    m.muon_grad_norm(g, norm, scale, ws)
+    assert abs(norm.item() - math.sqrt(9 + 4 + 1)) <= 7 * U * 4
+    g.ptrs += 16
+    m.muon_grad_norm(g, norm, scale, ws)
+    assert abs(norm.item() - math.sqrt(4 + 16)) <= 7 * U * 5
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured norms over one workspace, replayed in turn on other gradients."""
+    sets = [[torch.randn(n, device=DEV) for n in sizes] for sizes in ((9, 70001), (1 << 20, 3, 5000001))]
+    grads = [m.Grads(ts) for ts in sets]
+    ws = m.workspace(max(m.muon_grad_norm_workspace_size(g) for g in grads))
+    out = [(torch.empty(1, device=DEV), torch.empty(1, device=DEV)) for _ in sets]
+    graphs = []
+    for g, (norm, scale) in zip(grads, out):
+        m.muon_grad_norm(g, norm, scale, ws, max_norm=1.0)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            m.muon_grad_norm(g, norm, scale, ws, max_norm=1.0)
+    for turn in range(4):
+        ts, (norm, scale) = sets[turn % 2], out[turn % 2]
+        ts[0].normal_()
+        ts[1][0] = 1e30 if turn == 2 else 0.5
+        graphs[turn % 2].replay()
+        n, s = R.grad_norm([f64(t) for t in ts], 1.0)
+        assert abs(norm.item() - n) <= 7 * U * n and abs(scale.item() - s) <= 9 * U * s + 2.0 ** -149
+
+
 def test_zero_gradients_and_the_border_of_clipping():
     z = torch.zeros(5000, device=DEV)
     norm, scale, flags = run([z], max_norm=0.0)

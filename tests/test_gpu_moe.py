@@ -175,6 +175,38 @@ def test_sort_in_each_of_its_forms(T, E, K):
             check_sort(r, flags, c, E, mk, rows)
 
 
+@pytest.mark.parametrize("T,K,stride", [(2 ** 31 - 1, 1, 1), ((2 ** 31 - 1) // 7, 7, 8)])
+def test_sort_of_as_many_copies_as_it_takes(T, K, stride):
+    """Copy i chooses expert i mod 5, or none where i mod 5 = 4: its row is i // 5 behind the
+    expert's first."""
+    E, n = 4, T * K
+    chosen = torch.empty(T, stride, dtype=torch.int32, device=DEV)[:, :K]
+    step = (1 << 26) // K
+    for t in range(0, T, step):     # a part of the tokens at a time
+        i = torch.arange(t * K, min(T, t + step) * K, device=DEV)
+        e = i % 5
+        chosen[t:t + step] = torch.where(e == 4, -1, e).to(torch.int32).view(-1, K)
+    r = m.Routing.empty(T, K, E)
+    r.order.fill_(-77)
+    ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+    m.muon_moe_sort(chosen, r, ws)
+    assert m.muon_get_status(ws) == (m.MUON_OK, 0)
+    sizes = [(n - e + 4) // 5 for e in range(E)]
+    assert r.offsets.tolist() == [sum(sizes[:e]) for e in range(E + 1)]
+    first = r.offsets.long()
+    for t in range(0, T, step):
+        i = torch.arange(t * K, min(T, t + step) * K, device=DEV)
+        e = i % 5
+        want = torch.where(e == 4, -1, first[e] + i // 5)
+        assert torch.equal(r.place[t:t + step].flatten().long(), want)
+    for e in range(E):
+        for a in range(0, sizes[e], 1 << 26):
+            b = min(sizes[e], a + (1 << 26))
+            rows = r.order[int(first[e]) + a:int(first[e]) + b]
+            assert torch.equal(rows.long(), 5 * torch.arange(a, b, device=DEV) + e)
+    assert bool((r.order[int(first[E]):] == -77).all())
+
+
 # ---- activations ------------------------------------------------------------
 def routed(seed, T, E, K, drop=0.15, rows=None):
     chosen = choices(seed, T, E, K, drop)
@@ -400,6 +432,38 @@ def test_rows_gradient_is_one_product_rounded_once(outer, inner, wdt, how):
         held = torch.as_tensor(place, device=DEV) >= 0
         rows = (w.float()[:, :, None] * dout.float()[:, None, :])[held].to(DT[inner])
         assert torch.equal(dys[torch.as_tensor(place, device=DEV)[held]], rows)
+
+
+@pytest.mark.parametrize("D", [1, 48, 301, 515])
+@pytest.mark.parametrize("outer,inner", TYPES)
+def test_no_tokens_and_no_rows(outer, inner, D):
+    """Without tokens nothing happens; with tokens but no rows (buffers of none, too) sums and
+    weights' gradients are 0, or what was there where it is added to."""
+    for T, rows in ((0, 0), (0, 5), (6, 0), (6, 4)):
+        E, K = 3, 2
+        chosen = torch.full((T, K), -1, device=DEV)
+        r = m.Routing.empty(T, K, E, rows=rows)
+        ws = m.workspace(m.muon_moe_sort_workspace_size(T, E, K))
+        m.muon_moe_sort(chosen, r, ws)
+        assert m.muon_get_status(ws) == (m.MUON_OK, 0) and r.offsets.tolist() == [0] * (E + 1)
+        x = torch.randn(T, D, device=DEV).to(DT[outer])
+        xs = torch.full((rows, D), 7.0, dtype=DT[inner], device=DEV)
+        x8 = m.act8_empty(rows, D)
+        codes = x8.codes.clone()
+        m.muon_moe_dispatch(x, r, xs, x8)
+        m.muon_moe_dispatch(x, r, xs)
+        assert bool((xs == 7.0).all()) and torch.equal(x8.codes, codes)
+        w, out = torch.full((T, K), float("nan"), device=DEV), torch.full_like(x, 9.0)
+        for call in (lambda acc: m.muon_moe_combine(xs, w, r, out, accumulate=acc),
+                     lambda acc: m.muon_moe_dispatch_backward(xs, r, out, accumulate=acc)):
+            out.fill_(9.0)
+            call(True)
+            assert bool((out == 9.0).all())
+            call(False)
+            assert bool((out == 0.0).all())
+        dw = torch.full_like(w, 9.0)
+        m.muon_moe_combine_backward(x, xs, w, r, xs, dw)
+        assert bool((xs == 7.0).all()) and bool((dw == 0.0).all())
 
 
 def test_not_finite_values_reach_their_own_columns_only():
