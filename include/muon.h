@@ -375,8 +375,9 @@ muon_status_t muon_grad_norm_workspace_size(const muon_grads_t* groups, int n_gr
 /* groups: host array [n_groups] (a tensor that is in two counts twice; no tensors:
  * norm 0).  max_norm: >= 0 (infinity: only the norm; scale is 1).  norm, scale: device, 1 fp32 each.
  * Squares are added 32 (64 of bf16) at a time in fp32, and those sums in 48 bits or
- * more: norm is within 7 * 2^-24, and scale within 9 * 2^-24, of its exact value,
- * whatever the gradients' size (squares do not overflow or vanish).  A norm
+ * more: norm is within 7 * 2^-24, and scale within 9 * 2^-24, of its exact value (below
+ * fp32's normal numbers within 2^-149), whatever the gradients' size (squares do not
+ * overflow or vanish).  A norm
  * beyond fp32's range reads as infinity; its scale is finite and no flag is set, so it
  * is scale that tells a batch to be skipped.  The order of the sum is fixed by the sizes
  * and the GPU.  Status word in the workspace (muon_get_status): MUON_FLAG_NONFINITE,
